@@ -51,8 +51,9 @@ enum {
                                        that does not fit one launch                     */
     GEMMF32_ERR_BAD_CONFIG = -7,    /* unknown variant or tile configuration id          */
     GEMMF32_ERR_HIP = -8,           /* the HIP launch failed                             */
-    GEMMF32_ERR_SCRATCH_LIMIT = -9  /* gemm_f32_splitk_noalloc: the split needs more than
+    GEMMF32_ERR_SCRATCH_LIMIT = -9, /* gemm_f32_splitk_noalloc: the split needs more than
                                        GEMMF32_SCRATCH_FLOATS floats of scratch         */
+    GEMMF32_ERR_BAD_TYPE = -10      /* an element type that gemm_lp.h does not name     */
 };
 
 /* Floats of the static device scratch array behind gemm_f32_splitk_noalloc (32 MiB). */

@@ -1,0 +1,407 @@
+"""The low-precision and expert-grouped products on the GPU against plain 64-bit forms
+(tests/lowp_oracle.py, which derives the bounds)."""
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import tiled_double_buffered_amd as tdb  # noqa: E402
+import lowp_oracle as lo  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+DEV = torch.device("cuda:0")
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+NAN = float("nan")
+
+
+def _say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g)
+
+
+# ------------------------------------------------------------------------------ quantization
+def _wide(rows, cols, dtype, seed):
+    """Values of very different sizes, zero blocks, halves of a step, 448 and just above."""
+    g = _gen(seed)
+    x = _randn(g, rows, cols) * torch.exp2(torch.randint(-9, 5, (rows, cols), generator=g).float())
+    if dtype != torch.float16:
+        x *= torch.exp2(torch.randint(-60, 60, (rows, 1), generator=g).float())
+    x[rows // 2] = 0.0
+    x[0, 0] = 448.0
+    x[0, cols - 1] = 449.0
+    x[rows - 1, 0] = 1.0625
+    return x.to(dtype)
+
+
+def _same(q, s, v, sc):
+    assert q.dtype == lo.F8 and s.dtype == torch.float32
+    assert tuple(q.shape) == tuple(v.shape) and tuple(s.shape) == tuple(sc.shape)
+    assert torch.equal(s.double().cpu(), sc)
+    assert torch.equal(q.float().double().cpu().nan_to_num(9e9), v.nan_to_num(9e9))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 128), (3, 129), (16, 512), (130, 257), (257, 136),
+                                   (64, 1000)], ids=str)
+def test_quantize(shape, block, dtype):
+    x = _wide(*shape, TYPES[dtype], 11 + shape[0] + shape[1])
+    xd = x.to(DEV)
+    _say("[quantize]", shape, block, dtype)
+    v, s = lo.quantize(x, block)
+    vt, st = lo.quantize(x.t(), block)
+    _same(*tdb.quantize_fp8(xd, block=(block, 128)), v, s)
+    q, sq, qt, sqt = tdb.quantize_fp8_pair(xd, block=(block, 128))
+    _same(q, sq, v, s)
+    _same(qt, sqt, vt, st)
+
+
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_not_finite_and_tiny(block):
+    x = _randn(_gen(5), 140, 300)
+    x[3, 5] = float("inf")
+    x[3, 200] = -float("inf")
+    x[139, 299] = NAN
+    x[7, :128] = NAN              # a block of nothing else
+    x[9] = 2.0 ** -140            # subnormal values: the smallest scale, and zeros
+    x[10, :128] = 2.0 ** -126 * 1.75
+    x[11, 0] = torch.finfo(torch.float32).max
+    v, s = lo.quantize(x, block)
+    vt, st = lo.quantize(x.t(), block)
+    q, sq, qt, sqt = tdb.quantize_fp8_pair(x.to(DEV), block=(block, 128))
+    _same(q, sq, v, s)
+    _same(qt, sqt, vt, st)
+    _same(*tdb.quantize_fp8(x.to(DEV), block=(block, 128)), v, s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_views(dtype):
+    """Rows that start at any element and do not fill their stride."""
+    big = _randn(_gen(6), 70, 421).to(TYPES[dtype])
+    x, xd = big[3:67, 5:398], big.to(DEV)[3:67, 5:398]
+    v, s = lo.quantize(x, 1)
+    _same(*tdb.quantize_fp8(xd), v, s)
+    vt, st = lo.quantize(x.t(), 1)
+    _same(*tdb.quantize_fp8_pair(xd)[2:], vt, st)
+
+
+# ------------------------------------------------------------------------------ 8-bit products
+def _scaled(rows, cols, block, seed, lead=()):
+    """8-bit values and scales of any size, as a checkpoint holds them."""
+    g = _gen(seed)
+    q = (_randn(g, *lead, rows, cols) * 60).to(lo.F8)
+    s = torch.exp(_randn(g, *lead, -(-rows // block), lo.blocks(cols)))
+    return q, s
+
+
+def _aligned(q):
+    """The same values in rows that start at multiples of 16 bytes; the rest of each is NaN."""
+    ld = (q.shape[-1] + 15) // 16 * 16
+    p = torch.full((*q.shape[:-1], ld), NAN, device=q.device).to(lo.F8)
+    p[..., :q.shape[-1]] = q
+    return p[..., :q.shape[-1]]
+
+
+FP8_SHAPES = [(1, 1, 1), (1, 64, 128), (5, 33, 127), (16, 256, 1024), (33, 130, 129),
+              (127, 193, 61), (129, 257, 400), (200, 520, 2053), (300, 384, 896), (7, 1000, 4096),
+              (512, 512, 640)]
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("b_block", [1, 128])
+@pytest.mark.parametrize("shape", FP8_SHAPES, ids=str)
+def test_matmul_fp8(shape, b_block, out):
+    M, N, K = shape
+    a, sa = _scaled(M, K, 1, 21 + M)
+    b, sb = _scaled(N, K, b_block, 22 + N)
+    ref, mag = lo.product(lo.values(a, sa, 1), lo.values(b, sb, b_block).t())
+    if out == "f16":  # into its range
+        f = 2.0 ** -12
+        sa, ref, mag = sa * f, ref * f, mag * f
+    ad, sad, bd, sbd = (t.to(DEV) for t in (a, sa, b, sb))
+    for how, (p, r) in dict(plain=(ad, bd), aligned=(_aligned(ad), _aligned(bd)),
+                            mixed=(ad, _aligned(bd))).items():
+        _say("[matmul_fp8]", shape, b_block, out, how)
+        c = tdb.matmul_fp8(p, sad, r, sbd, out_dtype=TYPES[out])
+        assert c.dtype == TYPES[out]
+        lo.check(c, ref, mag, K, how)
+
+
+def test_matmul_fp8_no_depth_and_no_rows():
+    z = torch.empty(5, 0, device=DEV, dtype=lo.F8)
+    s = torch.empty(5, 0, device=DEV)
+    c = tdb.matmul_fp8(z, s, z[:3], s[:1])
+    assert c.shape == (5, 3) and not c.any()
+    a, sa = (t.to(DEV) for t in _scaled(4, 256, 1, 3))
+    b, sb = (t.to(DEV) for t in _scaled(4, 256, 128, 3))
+    assert tdb.matmul_fp8(a[:0], sa[:0], b, sb).shape == (0, 4)
+    assert tdb.matmul_fp8(a, sa, b[:0], sb[:0]).shape == (4, 0)
+
+
+def _split(sizes, lead, tail):
+    """Offsets of groups of these sizes after `lead` rows of no expert; rows with the tail."""
+    o = [lead]
+    for n in sizes:
+        o.append(o[-1] + n)
+    return o, o[-1] + tail
+
+
+# sizes, rows of no expert before and after
+GROUPS = [([5], 0, 0), ([1, 0, 3, 0, 0, 7], 0, 0), ([0, 0, 0], 2, 3), ([130, 1, 0, 64], 1, 5),
+          ([300, 5, 257], 0, 70), ([0, 17, 33, 0, 1, 1, 1, 128, 16, 0], 0, 1),
+          ([1] * 20 + [0] * 50 + [2] * 30, 3, 0)]
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{len(g[0])}e-{sum(g[0])}")
+@pytest.mark.parametrize("NK", [(64, 128), (130, 400), (257, 261)], ids=str)
+def test_matmul_fp8_grouped(groups, NK, out):
+    N, K = NK
+    off, rows = _split(*groups)
+    E = len(groups[0])
+    a, sa = _scaled(rows, K, 1, 31)
+    b, sb = _scaled(N, K, 128, 32, (E,))
+    sa *= 2.0 ** -12
+    ref = torch.zeros(rows, N, dtype=torch.float64)
+    mag = torch.zeros_like(ref)
+    av = lo.values(a, sa, 1)
+    for e, (i, j) in enumerate(lo.ranges(off)):
+        ref[i:j], mag[i:j] = lo.product(av[i:j], lo.values(b[e], sb[e], 128).t())
+    a.view(torch.uint8)[:off[0]] = 0x7f  # NaN in the rows of no expert stays out
+    a.view(torch.uint8)[off[-1]:] = 0x7f
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    ad, sad, bd, sbd = (t.to(DEV) for t in (a, sa, b, sb))
+    for how, (p, r) in dict(plain=(ad, bd), aligned=(_aligned(ad), _aligned(bd))).items():
+        _say("[matmul_fp8_grouped]", E, rows, NK, out, how)
+        lo.check(tdb.matmul_fp8_grouped(p, sad, r, sbd, offd, out_dtype=TYPES[out]), ref, mag, K,
+                 how)
+
+
+# ------------------------------------------------------------------------- expert products
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tw", [False, True])
+@pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{len(g[0])}e-{sum(g[0])}")
+@pytest.mark.parametrize("KN", [(1, 1), (64, 128), (136, 264), (321, 131), (400, 72)], ids=str)
+def test_grouped_step(groups, KN, tw, dtype):
+    """y, dx and dw of a step, NaN in the rows of no expert (which must not leak)."""
+    K, N = KN
+    off, rows = _split(*groups)
+    E = len(groups[0])
+    g = _gen(41 + K)
+    x = _randn(g, rows, K).to(TYPES[dtype])
+    w = (0.1 * _randn(g, *((E, N, K) if tw else (E, K, N)))).to(TYPES[dtype])
+    dy = _randn(g, rows, N).to(TYPES[dtype])
+    x64, w64, dy64 = x.double(), w.double(), dy.double()
+    ref = [torch.zeros(rows, N).double(), torch.zeros(rows, K).double(), torch.zeros_like(w64)]
+    mag = [torch.zeros_like(t) for t in ref]
+    for e, (i, j) in enumerate(lo.ranges(off)):
+        we = w64[e].t() if tw else w64[e]
+        ref[0][i:j], mag[0][i:j] = lo.product(x64[i:j], we)
+        ref[1][i:j], mag[1][i:j] = lo.product(dy64[i:j], we.t())
+        l, r = (dy64[i:j], x64[i:j]) if tw else (x64[i:j], dy64[i:j])
+        ref[2][e], mag[2][e] = lo.product(l.t(), r)
+    for t in (x, dy):
+        t[:off[0]] = NAN
+        t[off[-1]:] = NAN
+    _say("[grouped_step]", E, rows, KN, tw, dtype)
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    xd, wd = x.to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+    y = tdb.linear_grouped(xd, wd, offd, transpose_w=tw)
+    assert y.dtype == x.dtype
+    dx, dw = torch.autograd.grad(y, (xd, wd), dy.to(DEV))
+    lo.check(y, ref[0], mag[0], K, "y")
+    lo.check(dx, ref[1], mag[1], N, "dx")
+    lo.check(dw, ref[2], mag[2], max(rows, 1), "dw")
+    assert torch.equal(tdb.matmul_grouped(xd.detach(), wd.detach(), offd, transpose_w=tw),
+                       y.detach())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tw", [False, True])
+def test_grouped_views(dtype, tw):
+    """Operands whose rows and experts do not fill their strides."""
+    K, N, E = 96, 80, 3
+    off, rows = _split([9, 0, 40], 0, 2)
+    g = _gen(51)
+    bigx = _randn(g, rows, K + 9).to(TYPES[dtype]).to(DEV)
+    bigw = _randn(g, E + 2, (N if tw else K) + 3, (K if tw else N) + 5).to(TYPES[dtype]).to(DEV)
+    x = bigx[:, 3:3 + K]
+    w = bigw[1:1 + E, 2:-1, 3:-2]
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    y = tdb.matmul_grouped(x, w, offd, transpose_w=tw)
+    ref = torch.zeros(rows, N, dtype=torch.float64)
+    mag = torch.zeros_like(ref)
+    for e, (i, j) in enumerate(lo.ranges(off)):
+        we = w[e].double().cpu()
+        ref[i:j], mag[i:j] = lo.product(x[i:j].double().cpu(), we.t() if tw else we)
+    lo.check(y, ref, mag, K)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_inf_and_nan_stay_in_their_rows_and_experts(dtype):
+    """An Inf or NaN of one expert's rows reaches that expert's results and no others."""
+    K, N, E = 128, 128, 3
+    off = [0, 20, 40, 60]
+    g = _gen(52)
+    x = _randn(g, 60, K).to(TYPES[dtype]).to(DEV)
+    w = _randn(g, E, K, N).to(TYPES[dtype]).to(DEV)
+    dy = _randn(g, 60, N).to(TYPES[dtype]).to(DEV)
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    x[19, 3] = float("inf")
+    x[40, 5] = NAN
+    dy[20, 0] = NAN
+    y = tdb.matmul_grouped(x, w, offd)
+    bad = ~torch.isfinite(y).all(1)
+    assert bad.nonzero().flatten().tolist() == [19, 40]
+    dw = tdb.matmul_grouped_wgrad(x, dy, offd)
+    finite = torch.isfinite(dw)
+    assert not finite[0, 3].any() and finite[0].sum() == (K - 1) * N
+    assert not finite[1, :, 0].any() and finite[1].sum() == K * (N - 1)
+    assert not finite[2, 5].any() and finite[2].sum() == (K - 1) * N
+
+
+def test_wrong_offsets_stay_in_bounds():
+    """Offsets past the rows, negative and decreasing ones: the values are undefined, the call
+    ends, and what lies around the outputs keeps its values."""
+    K, N, E, rows = 64, 64, 4, 50
+    g = _gen(53)
+    x = _randn(g, rows, K).bfloat16().to(DEV)
+    w = _randn(g, E, K, N).bfloat16().to(DEV)
+    for off in ([0, 60, 70, 80, 90], [-5, -3, 10, 20, 1 << 30], [50, 40, 30, 20, 10],
+                [0, 50, 0, 50, 0], [-(1 << 31), (1 << 31) - 1, 0, 50, -1]):
+        offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+        _say("[wrong offsets]", off)
+        guard = torch.full((rows + 20, N), 7.0, device=DEV).bfloat16()
+        rc = tdb.gemm_grouped(rows, N, K, E, offd.data_ptr(), x.data_ptr(), K, w.data_ptr(), N,
+                              K * N, 0, guard[10:].data_ptr(), N, 0,
+                              torch.cuda.current_stream().cuda_stream)
+        assert rc == tdb.OK
+        torch.cuda.synchronize()
+        assert (guard[:10] == 7).all() and (guard[10 + rows:] == 7).all()
+        dw = tdb.matmul_grouped_wgrad(x, x, offd)
+        torch.cuda.synchronize()
+        assert dw.shape == (E, K, K)
+
+
+# ------------------------------------------------------------------------------ training steps
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(1, 1, 1), (5, 130, 70), (128, 128, 128), (200, 384, 264),
+                                   (257, 129, 513)], ids=str)
+def test_linear_fp8(shape, dtype):
+    M, N, K = shape
+    g = _gen(61 + M)
+    x = _randn(g, M, K).to(TYPES[dtype])
+    w = (0.05 * _randn(g, N, K)).to(TYPES[dtype])
+    dy = _randn(g, M, N).to(TYPES[dtype])
+
+    def v(t, b):
+        return lo.values(*lo.quantize(t, b), b)
+
+    y64 = lo.product(v(x, 1), v(w, 128).t())
+    dx64 = lo.product(v(dy, 1), v(w, 128))
+    dw64 = lo.product(v(dy.t(), 1), v(x.t(), 1).t())
+    xd, wd = x.to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+    _say("[linear_fp8]", shape, dtype)
+    y = tdb.linear_fp8(xd, wd)
+    dx, dw = torch.autograd.grad(y, (xd, wd), dy.to(DEV))
+    assert y.dtype == dx.dtype == dw.dtype == x.dtype
+    lo.check(y, *y64, K, "y")
+    lo.check(dx, *dx64, N, "dx")
+    lo.check(dw, *dw64, M, "dw")
+
+
+def test_linear_fp8_leading_axes_and_missing_gradients():
+    g = _gen(62)
+    x = _randn(g, 3, 5, 64).bfloat16().to(DEV)
+    w = _randn(g, 32, 64).bfloat16().to(DEV).requires_grad_()
+    y = tdb.linear_fp8(x, w)
+    assert y.shape == (3, 5, 32)
+    y.sum().backward()  # the gradient of a sum comes as one broadcast value
+    assert x.grad is None and w.grad.shape == w.shape
+    flat = tdb.linear_fp8(x.view(15, 64), w.detach())
+    assert torch.equal(flat.view(3, 5, 32), y.detach()) and not flat.requires_grad
+    x.requires_grad_()
+    tdb.linear_fp8(x, w.detach()).sum().backward()
+    assert x.grad.shape == x.shape
+
+
+@pytest.mark.parametrize("op", ["fp8", "grouped"])
+def test_gradients_against_differences(op):
+    """Both layers are linear wherever the 8-bit values are exact (whole numbers up to 15 are),
+    so that differences of the loss are exact too: along any direction of whole numbers,
+    loss(x + d) - loss(x) = <dx, d>, and the same in w."""
+    g = _gen(63)
+
+    def whole(*shape):
+        return torch.randint(-3, 4, shape, generator=g).float().to(DEV)
+
+    x, dy = whole(24, 96), whole(24, 40)
+    off = torch.tensor([0, 10, 10, 23], dtype=torch.int32, device=DEV)
+    w = whole(40, 96) if op == "fp8" else whole(3, 96, 40)
+    f = tdb.linear_fp8 if op == "fp8" else lambda a, b: tdb.linear_grouped(a, b, off)
+    xr, wr = x.clone().requires_grad_(), w.clone().requires_grad_()
+    dx, dw = torch.autograd.grad(f(xr, wr), (xr, wr), dy)
+    loss = lambda a, b: (f(a, b).double() * dy.double()).sum()  # noqa: E731
+    for _ in range(3):
+        d, v = whole(*x.shape), whole(*w.shape)
+        assert loss(x + d, w) - loss(x, w) == (dx.double() * d.double()).sum()
+        assert loss(x, w + v) - loss(x, w) == (dw.double() * v.double()).sum()
+
+
+# -------------------------------------------------------------------- streams and graphs
+def test_other_stream():
+    x = _randn(_gen(71), 64, 256).bfloat16().to(DEV)
+    w = _randn(_gen(72), 128, 256).bfloat16().to(DEV)
+    ref = tdb.matmul_fp8(*tdb.quantize_fp8(x), *tdb.quantize_fp8(w, block=(128, 128)))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(DEV)
+    q = tdb.quantize_fp8(x, stream=s)
+    p = tdb.quantize_fp8(w, block=(128, 128), stream=s)
+    c = tdb.matmul_fp8(*q, *p, stream=s)
+    s.synchronize()
+    assert torch.equal(c, ref)
+
+
+def test_graph_replays_follow_their_inputs():
+    """Captured calls read the offsets and values that the buffers hold at each replay."""
+    K, N, E, rows = 192, 160, 4, 90
+    x = torch.zeros(rows, K, device=DEV, dtype=torch.bfloat16)
+    w = _randn(_gen(73), E, K, N).bfloat16().to(DEV)
+    wq, ws = tdb.quantize_fp8(w.view(E * K, N), block=(128, 128))
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    bq = _randn(_gen(75), E, N, K).to(lo.F8).to(DEV)
+    bs = torch.ones(E, lo.blocks(N), lo.blocks(K), device=DEV)
+
+    def step():
+        q, s, qt, st = tdb.quantize_fp8_pair(x)
+        return (tdb.matmul_grouped(x, w, off), tdb.matmul_grouped_wgrad(x, x, off),
+                tdb.matmul_fp8_grouped(q, s, bq, bs, off), tdb.matmul_fp8(qt, st, qt, st))
+
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed, o in enumerate(([0, 30, 30, 60, 90], [0, 0, 0, 0, 0], [5, 6, 80, 85, 88],
+                              [0, 90, 90, 90, 90])):
+        x.copy_(_randn(_gen(80 + seed), rows, K).bfloat16())
+        off.copy_(torch.tensor(o, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(held, step()):
+            assert torch.equal(got, ref)
+    del wq, ws

@@ -24,6 +24,7 @@ ERR_TOO_LARGE = -6
 ERR_BAD_CONFIG = -7
 ERR_HIP = -8
 ERR_SCRATCH_LIMIT = -9
+ERR_BAD_TYPE = -10
 SCRATCH_FLOATS = 8 * 1024 * 1024  # GEMMF32_SCRATCH_FLOATS
 
 VARIANT_AUTO = 0

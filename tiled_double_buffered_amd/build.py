@@ -26,11 +26,13 @@ INCLUDE = os.path.join(ROOT, "include")
 MAIN_SOURCE = os.path.join(CSRC, "gemm_f32.hip")
 CFG_SOURCE = os.path.join(CSRC, "cfg_kernels.hip")
 NUM_CONFIGS = 20  # configs.h: kNumConfigs
-SOURCES = [MAIN_SOURCE, CFG_SOURCE]
+LP_SOURCE = os.path.join(CSRC, "gemm_lp.hip")  # low-precision and expert-grouped products
+SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",
-                                            "dispatch_table.h", "mfma_peak.h")]
-DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, "gemmf32.h")]
+                                            "dispatch_table.h", "mfma_peak.h",
+                                            "lp_common.h", "lp_quantize.h", "lp_tile.h")]
+DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h")]
 LIB = os.path.join(PKG, "libgemmf32.so")
 LIB_POISON = os.path.join(PKG, "libgemmf32_lds_poison.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
@@ -50,8 +52,8 @@ def _run(cmd, **kw):
 
 def _units():
     """(name, source, extra flags) of every translation unit: the host code and reduction
-    kernels, then one unit per tile configuration."""
-    units = [("gemm_f32", MAIN_SOURCE, [])]
+    kernels, one unit per tile configuration, and the low-precision products."""
+    units = [("gemm_f32", MAIN_SOURCE, []), ("gemm_lp", LP_SOURCE, [])]
     units += [(f"cfg{i}", CFG_SOURCE, [f"-DGEMMF32_CFG_ID={i}"]) for i in range(NUM_CONFIGS)]
     return units
 

@@ -73,6 +73,7 @@ namespace gemmf32 {
 // Host side: validation, dispatch, launch.
 // ------------------------------------------------------------------------------------
 static thread_local int g_last_hip_error = 0;
+void set_last_hip_error(int code) { g_last_hip_error = code; }  // for gemm_lp.hip
 
 constexpr int64_t kMaxDim = 2147483647LL - 1024;  // keeps tile-end arithmetic in int32
 constexpr int64_t kMaxLd = kMaxDim * 64;           // leading dimensions (elements)
@@ -618,6 +619,7 @@ const char* gemm_f32_strerror(int code) {
     case GEMMF32_ERR_BAD_CONFIG: return "unknown variant or tile configuration";
     case GEMMF32_ERR_HIP: return "HIP kernel launch failed";
     case GEMMF32_ERR_SCRATCH_LIMIT: return "split needs more than the static scratch holds";
+    case GEMMF32_ERR_BAD_TYPE: return "unknown element type";
     default: return "unknown error code";
   }
 }

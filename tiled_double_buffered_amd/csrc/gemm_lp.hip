@@ -1,0 +1,286 @@
+// Host side of the low-precision and expert-grouped products: argument checks, the choice of
+// a kernel, launches, and the C ABI of include/gemm_lp.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gemm_lp.h"
+#include "lp_common.h"
+#include "lp_quantize.h"
+#include "lp_tile.h"
+
+namespace gemmlp {
+
+constexpr int64_t kMaxDim = 2147483647LL - 1024;  // keeps tile-end arithmetic in int32
+constexpr int64_t kMaxExtent = (int64_t)1 << 61;   // bytes one operand may span
+
+// Byte range [lo, hi) of `count` blocks of rows x cols values of `bytes` bytes, row stride ld
+// and block stride `stride` (elements).  False where it passes kMaxExtent or wraps.
+struct Range {
+  uintptr_t lo = 0, hi = 0;
+};
+static bool byte_range(const void* p, int64_t count, int64_t stride, int64_t rows, int64_t cols,
+                       int64_t ld, int64_t bytes, Range* r) {
+  int64_t e, s;
+  if (__builtin_mul_overflow(rows - 1, ld, &e) || __builtin_add_overflow(e, cols, &e) ||
+      __builtin_mul_overflow(count - 1, stride, &s) || __builtin_add_overflow(e, s, &e) ||
+      __builtin_mul_overflow(e, bytes, &e) || e > kMaxExtent)
+    return false;
+  r->lo = (uintptr_t)p;
+  return !__builtin_add_overflow(r->lo, (uintptr_t)e, &r->hi);
+}
+static bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+static bool known_type(int t) { return t == GEMM_LP_BF16 || t == GEMM_LP_F16 || t == GEMM_LP_F32; }
+static bool misaligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) != 0; }
+static int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
+static int64_t at_least_1(int64_t n) { return n > 1 ? n : 1; }
+
+static int launch(const void* fn, dim3 grid, int threads, void* args, void* stream) {
+  void* list[] = {args};
+  const hipError_t err =
+      hipLaunchKernel(fn, grid, dim3((unsigned)threads), list, 0, (hipStream_t)stream);
+  if (err != hipSuccess) {
+    gemmf32::set_last_hip_error((int)err);
+    return GEMMF32_ERR_HIP;
+  }
+  return GEMMF32_OK;
+}
+
+// Workgroups of a row product with BM x BN tiles: the most tiles that any offsets give.  A
+// group adds at most one partly filled tile to its rows' whole ones, and a group without
+// rows none.
+static int64_t row_tiles(const LpArgs& a, int64_t BM, int64_t BN) {
+  const int64_t m = a.offsets == nullptr
+                        ? (a.rows + BM - 1) / BM
+                        : a.rows / BM + std::min<int64_t>((int64_t)a.E + 2, a.rows);
+  return m * ((a.N + BN - 1) / BN);
+}
+
+static int launch_rows(LpKernel fn, LpArgs a, int BM, int BN, int threads, void* stream) {
+  const int64_t wgs = row_tiles(a, BM, BN);
+  if (wgs * threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  return launch((const void*)fn, dim3((unsigned)wgs), threads, &a, stream);
+}
+
+static int launch_wgrad(LpKernel fn, LpArgs a, int BM, int BN, int threads, void* stream) {
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  int64_t wgs;
+  if (__builtin_mul_overflow(tm * tn, (int64_t)a.E, &wgs) || wgs > kMaxDim ||
+      wgs * threads > 0xFFFFFFFFLL)
+    return GEMMF32_ERR_TOO_LARGE;
+  a.tiles_n = (int)tn;
+  return launch((const void*)fn, dim3((unsigned)wgs), threads, &a, stream);
+}
+
+template <bool AKC, bool BKC, bool WGRAD>
+static LpKernel tile_kernel(int type) {
+  switch (type) {
+    case GEMM_LP_BF16: return &lp_tile_kernel<Bf16, AKC, BKC, WGRAD>;
+    case GEMM_LP_F16: return &lp_tile_kernel<F16, AKC, BKC, WGRAD>;
+    default: return &lp_tile_kernel<F32, AKC, BKC, WGRAD>;
+  }
+}
+
+static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
+                        int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* QT,
+                        int64_t ldqt, float* ST, int64_t ldst, void* stream) {
+  if (rows < 0 || cols < 0) return GEMMF32_ERR_NEGATIVE_DIM;
+  if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
+  if (block_rows != 1 && block_rows != kBlock) return GEMMF32_ERR_BAD_CONFIG;
+  if ((Q == nullptr) != (S == nullptr) || (QT == nullptr) != (ST == nullptr))
+    return GEMMF32_ERR_NULL_PTR;
+  const int64_t kb = blocks(cols), mb = blocks(rows);
+  if (ldx < at_least_1(cols) || (Q && (ldq < at_least_1(cols) || lds < at_least_1(kb))) ||
+      (QT && (ldqt < at_least_1(rows) || ldst < at_least_1(mb))))
+    return GEMMF32_ERR_BAD_LD;
+  if (rows > kMaxDim || cols > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (rows == 0 || cols == 0) return GEMMF32_OK;
+  if (X == nullptr || (Q == nullptr && QT == nullptr)) return GEMMF32_ERR_NULL_PTR;
+  const int xb = type_bytes(type);
+  if (misaligned(X, xb) || misaligned(S, 4) || misaligned(ST, 4)) return GEMMF32_ERR_MISALIGNED;
+  Range x, out[4];
+  const int64_t s_rows = block_rows == 1 ? rows : mb, st_rows = block_rows == 1 ? cols : kb;
+  if (!byte_range(X, 1, 0, rows, cols, ldx, xb, &x)) return GEMMF32_ERR_TOO_LARGE;
+  if (Q && (!byte_range(Q, 1, 0, rows, cols, ldq, 1, &out[0]) ||
+            !byte_range(S, 1, 0, s_rows, kb, lds, 4, &out[1])))
+    return GEMMF32_ERR_TOO_LARGE;
+  if (QT && (!byte_range(QT, 1, 0, cols, rows, ldqt, 1, &out[2]) ||
+             !byte_range(ST, 1, 0, st_rows, mb, ldst, 4, &out[3])))
+    return GEMMF32_ERR_TOO_LARGE;
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(out[i], x)) return GEMMF32_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return GEMMF32_ERR_ALIAS;
+  }
+  QuantArgs a{X,   (uint8_t*)Q, S,    (uint8_t*)QT, ST,       ldx,
+              ldq, lds,         ldqt, ldst,         (int)rows, (int)cols};
+  if (QT == nullptr && block_rows == 1) {
+    const int64_t wgs = (rows * kb + 15) / 16;
+    if (wgs > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
+    const void* fn = type == GEMM_LP_BF16 ? (const void*)&lp_quantize_rows_kernel<Bf16>
+                     : type == GEMM_LP_F16 ? (const void*)&lp_quantize_rows_kernel<F16>
+                                           : (const void*)&lp_quantize_rows_kernel<F32>;
+    return launch(fn, dim3((unsigned)wgs), 256, &a, stream);
+  }
+  if (mb > 65535 || kb > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
+  const bool r1 = block_rows == 1;
+  const void* fn = type == GEMM_LP_BF16
+                       ? (r1 ? (const void*)&lp_quantize_tile_kernel<Bf16, 1>
+                             : (const void*)&lp_quantize_tile_kernel<Bf16, kBlock>)
+                   : type == GEMM_LP_F16
+                       ? (r1 ? (const void*)&lp_quantize_tile_kernel<F16, 1>
+                             : (const void*)&lp_quantize_tile_kernel<F16, kBlock>)
+                       : (r1 ? (const void*)&lp_quantize_tile_kernel<F32, 1>
+                             : (const void*)&lp_quantize_tile_kernel<F32, kBlock>);
+  return launch(fn, dim3((unsigned)kb, (unsigned)mb), 256, &a, stream);
+}
+
+static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                   const void* A, int64_t lda, const float* SA, int64_t ldsa, const void* B,
+                   int64_t ldb, int64_t stride_b, const float* SB, int64_t ldsb,
+                   int64_t stride_sb, int b_block, void* C, int64_t ldc, int c_type,
+                   void* stream) {
+  if (M < 0 || N < 0 || K < 0 || E < 0) return GEMMF32_ERR_NEGATIVE_DIM;
+  if (!known_type(c_type)) return GEMMF32_ERR_BAD_TYPE;
+  if ((b_block != 1 && b_block != kBlock) || (offsets == nullptr && E != 1))
+    return GEMMF32_ERR_BAD_CONFIG;
+  const int64_t kb = blocks(K), nb = b_block == 1 ? N : blocks(N);
+  if (lda < at_least_1(K) || ldb < at_least_1(K) || ldc < at_least_1(N) ||
+      ldsa < at_least_1(kb) || ldsb < at_least_1(kb) || stride_b < 0 || stride_sb < 0)
+    return GEMMF32_ERR_BAD_LD;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (M == 0 || N == 0) return GEMMF32_OK;
+  if (C == nullptr) return GEMMF32_ERR_NULL_PTR;
+  const bool reads = K > 0 && E > 0;
+  if (reads && (A == nullptr || B == nullptr || SA == nullptr || SB == nullptr))
+    return GEMMF32_ERR_NULL_PTR;
+  const int cb = type_bytes(c_type);
+  if (misaligned(C, cb) || misaligned(offsets, 4) ||
+      (reads && (misaligned(SA, 4) || misaligned(SB, 4))))
+    return GEMMF32_ERR_MISALIGNED;
+  Range c, in[5];
+  if (!byte_range(C, 1, 0, M, N, ldc, cb, &c)) return GEMMF32_ERR_TOO_LARGE;
+  if (reads && (!byte_range(A, 1, 0, M, K, lda, 1, &in[0]) ||
+                !byte_range(SA, 1, 0, M, kb, ldsa, 4, &in[1]) ||
+                !byte_range(B, E, stride_b, N, K, ldb, 1, &in[2]) ||
+                !byte_range(SB, E, stride_sb, nb, kb, ldsb, 4, &in[3])))
+    return GEMMF32_ERR_TOO_LARGE;
+  if (offsets && !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[4]))
+    return GEMMF32_ERR_TOO_LARGE;
+  for (const Range& r : in)
+    if (overlap(c, r)) return GEMMF32_ERR_ALIAS;
+  LpArgs a{};
+  a.A = A, a.B = B, a.C = C, a.SA = SA, a.SB = SB, a.offsets = offsets;
+  a.lda = lda, a.ldb = ldb, a.ldc = ldc, a.stride_b = stride_b;
+  a.ldsa = ldsa, a.ldsb = ldsb, a.stride_sb = stride_sb;
+  a.rows = a.M = (int)M, a.N = (int)N, a.K = (int)K, a.E = (int)E;
+  a.sb_shift = b_block == 1 ? 0 : 7, a.c_type = c_type;
+  return launch_rows(&lp_tile_kernel<F8, true, true, false>, a, 64, 64, 256, stream);
+}
+
+static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                       const void* X, int64_t ldx, const void* W, int64_t ldw,
+                       int64_t stride_w, int transpose_w, void* Y, int64_t ldy, int type,
+                       void* stream) {
+  if (rows < 0 || N < 0 || K < 0 || E < 0) return GEMMF32_ERR_NEGATIVE_DIM;
+  if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
+  const int64_t wr = transpose_w ? N : K, wc = transpose_w ? K : N;
+  if (ldx < at_least_1(K) || ldw < at_least_1(wc) || ldy < at_least_1(N) || stride_w < 0)
+    return GEMMF32_ERR_BAD_LD;
+  if (rows > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (rows == 0 || N == 0) return GEMMF32_OK;
+  const bool reads = K > 0 && E > 0;
+  if (Y == nullptr || offsets == nullptr || (reads && (X == nullptr || W == nullptr)))
+    return GEMMF32_ERR_NULL_PTR;
+  const int b = type_bytes(type);
+  if (misaligned(Y, b) || misaligned(offsets, 4) || (reads && (misaligned(X, b) || misaligned(W, b))))
+    return GEMMF32_ERR_MISALIGNED;
+  Range y, in[3];
+  if (!byte_range(Y, 1, 0, rows, N, ldy, b, &y) ||
+      !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[2]) ||
+      (reads && (!byte_range(X, 1, 0, rows, K, ldx, b, &in[0]) ||
+                 !byte_range(W, E, stride_w, wr, wc, ldw, b, &in[1]))))
+    return GEMMF32_ERR_TOO_LARGE;
+  for (const Range& r : in)
+    if (overlap(y, r)) return GEMMF32_ERR_ALIAS;
+  LpArgs a{};
+  a.A = X, a.B = W, a.C = Y, a.offsets = offsets;
+  a.lda = ldx, a.ldb = ldw, a.ldc = ldy, a.stride_b = stride_w;
+  a.rows = a.M = (int)rows, a.N = (int)N, a.K = (int)K, a.E = (int)E;
+  a.c_type = type;
+  const LpKernel fn = transpose_w ? tile_kernel<true, true, false>(type)
+                                  : tile_kernel<true, false, false>(type);
+  return launch_rows(fn, a, 64, 64, 256, stream);
+}
+
+static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_t* offsets,
+                     const void* A, int64_t lda, const void* B, int64_t ldb, void* dW,
+                     int64_t ldw, int64_t stride_w, int type, void* stream) {
+  if (rows < 0 || M < 0 || N < 0 || E < 0) return GEMMF32_ERR_NEGATIVE_DIM;
+  if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
+  if (lda < at_least_1(M) || ldb < at_least_1(N) || ldw < at_least_1(N)) return GEMMF32_ERR_BAD_LD;
+  if (rows > kMaxDim || M > kMaxDim || N > kMaxDim || E > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (M == 0 || N == 0 || E == 0) return GEMMF32_OK;
+  const bool reads = rows > 0;
+  if (dW == nullptr || offsets == nullptr || (reads && (A == nullptr || B == nullptr)))
+    return GEMMF32_ERR_NULL_PTR;
+  const int b = type_bytes(type);
+  if (misaligned(dW, b) || misaligned(offsets, 4) || (reads && (misaligned(A, b) || misaligned(B, b))))
+    return GEMMF32_ERR_MISALIGNED;
+  Range w, in[3], one;
+  if (!byte_range(dW, E, stride_w, M, N, ldw, b, &w) ||
+      !byte_range(dW, 1, 0, M, N, ldw, b, &one) ||
+      !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[2]) ||
+      (reads && (!byte_range(A, 1, 0, rows, M, lda, b, &in[0]) ||
+                 !byte_range(B, 1, 0, rows, N, ldb, b, &in[1]))))
+    return GEMMF32_ERR_TOO_LARGE;
+  // each expert's dW has to end where the next begins, or it would be written twice
+  if (E > 1 && (stride_w < 0 || (uint64_t)stride_w * b < (uint64_t)(one.hi - one.lo)))
+    return GEMMF32_ERR_BAD_LD;
+  for (const Range& r : in)
+    if (overlap(w, r)) return GEMMF32_ERR_ALIAS;
+  LpArgs a{};
+  a.A = A, a.B = B, a.C = dW, a.offsets = offsets;
+  a.lda = lda, a.ldb = ldb, a.ldc = ldw, a.stride_c = stride_w;
+  a.rows = a.K = (int)rows, a.M = (int)M, a.N = (int)N, a.E = (int)E;
+  a.c_type = type;
+  return launch_wgrad(tile_kernel<false, false, true>(type), a, 64, 64, 256, stream);
+}
+
+}  // namespace gemmlp
+
+extern "C" {
+
+int gemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
+                      int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* QT,
+                      int64_t ldqt, float* ST, int64_t ldst, void* stream) {
+  return gemmlp::run_quantize(rows, cols, X, ldx, type, block_rows, Q, ldq, S, lds, QT, ldqt,
+                              ST, ldst, stream);
+}
+
+int gemm_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* offsets, const void* A,
+             int64_t lda, const float* SA, int64_t ldsa, const void* B, int64_t ldb,
+             int64_t stride_b, const float* SB, int64_t ldsb, int64_t stride_sb, int b_block,
+             void* C, int64_t ldc, int c_type, void* stream) {
+  return gemmlp::run_fp8(M, N, K, E, offsets, A, lda, SA, ldsa, B, ldb, stride_b, SB, ldsb,
+                         stride_sb, b_block, C, ldc, c_type, stream);
+}
+
+int gemm_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                 const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t stride_w,
+                 int transpose_w, void* Y, int64_t ldy, int type, void* stream) {
+  return gemmlp::run_grouped(rows, N, K, E, offsets, X, ldx, W, ldw, stride_w, transpose_w, Y,
+                             ldy, type, stream);
+}
+
+int gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_t* offsets,
+                       const void* A, int64_t lda, const void* B, int64_t ldb, void* dW,
+                       int64_t ldw, int64_t stride_w, int type, void* stream) {
+  return gemmlp::run_wgrad(rows, M, N, E, offsets, A, lda, B, ldb, dW, ldw, stride_w, type,
+                           stream);
+}
+
+}  // extern "C"

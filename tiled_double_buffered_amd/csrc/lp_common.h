@@ -1,0 +1,248 @@
+// Shared parts of the low-precision and expert-grouped products: element types, the matrix
+// instructions, kernel arguments, the search for a workgroup's tile in ragged groups of rows,
+// and the epilogue's stores.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_lp.h"
+
+namespace gemmlp {
+
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef __bf16 bf168v __attribute__((ext_vector_type(8)));
+
+constexpr int kBlock = 128;   // columns (along K) that share a scale
+constexpr int kRowBytes = 128;  // bytes of one operand row in a K step, every type
+constexpr int kXcds = 8;
+
+struct Bf16 {
+  using type = __bf16;
+  static constexpr int BYTES = 2;
+  static constexpr int CODE = GEMM_LP_BF16;
+};
+struct F16 {
+  using type = _Float16;
+  static constexpr int BYTES = 2;
+  static constexpr int CODE = GEMM_LP_F16;
+};
+struct F32 {
+  using type = float;
+  static constexpr int BYTES = 4;
+  static constexpr int CODE = GEMM_LP_F32;
+};
+struct F8 {
+  using type = uint8_t;
+  static constexpr int BYTES = 1;
+  static constexpr int CODE = -1;
+};
+
+static inline __host__ __device__ int type_bytes(int code) { return code == GEMM_LP_F32 ? 4 : 2; }
+
+// The product of two 16-row operands over one K step of 128 bytes a row (128 8-bit values,
+// 64 16-bit, 32 32-bit).  Lane l holds of row l % 16 the two 16-byte groups lo and hi that
+// its lane group l / 16 stands for; both operands use the same groups, so that the order of
+// k inside the step does not matter.  D's row index comes from `a`, its column from `b`:
+// lane l, register r hold row 4 (l / 16) + r, column l % 16.
+// 8-bit values go through the 16-bit instruction here, which every e4m3 number and product
+// fits exactly: the 8-bit instruction aligns its 128 products to the largest and cuts what
+// falls below (measured: up to 2^-12.2 of the sum of magnitudes, 2^-16 on average), so its
+// sums hold fewer than 32 bits.
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ half8v fp8x8_to_half(int w0, int w1) {
+  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
+  const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true);
+  const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false);
+  const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true);
+  return half8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <class T>
+__device__ __forceinline__ float4v mma_step(int4v alo, int4v ahi, int4v blo, int4v bhi,
+                                            float4v c) {
+  if constexpr (T::BYTES == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int4v a = i ? ahi : alo, b = i ? bhi : blo;
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[0], a[1]),
+                                                 fp8x8_to_half(b[0], b[1]), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[2], a[3]),
+                                                 fp8x8_to_half(b[2], b[3]), c, 0, 0, 0);
+    }
+    return c;
+  } else if constexpr (T::CODE == GEMM_LP_BF16) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf168v, alo),
+                                                __builtin_bit_cast(bf168v, blo), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf168v, ahi),
+                                                   __builtin_bit_cast(bf168v, bhi), c, 0, 0, 0);
+  } else if constexpr (T::CODE == GEMM_LP_F16) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, alo),
+                                               __builtin_bit_cast(half8v, blo), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, ahi),
+                                                  __builtin_bit_cast(half8v, bhi), c, 0, 0, 0);
+  } else {
+    const float4v a0 = __builtin_bit_cast(float4v, alo), a1 = __builtin_bit_cast(float4v, ahi);
+    const float4v b0 = __builtin_bit_cast(float4v, blo), b1 = __builtin_bit_cast(float4v, bhi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a0[i], b0[i], c, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[i], b1[i], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// Arguments of every product kernel.  Row products: C rows m0.. of group e from A's rows and
+// B_e.  Weight gradients: the group's rows are the contraction, M x N the size of one C_e.
+struct LpArgs {
+  const void* A;
+  const void* B;
+  void* C;
+  const float* SA;
+  const float* SB;
+  const int32_t* offsets;  // NULL: one group of all rows
+  int64_t lda, ldb, ldc;   // elements
+  int64_t stride_b;        // elements from one expert's B to the next's (row products)
+  int64_t stride_c;        // elements from one expert's C to the next's (weight gradients)
+  int64_t ldsa, ldsb, stride_sb;
+  int rows;                // rows of A: M of a row product, the contraction of a gradient
+  int M, N, K;             // row products: M = rows; gradients: K = rows
+  int E;
+  int tiles_n;
+  int sb_shift;            // log2 of the rows of B that share a scale: 7 or 0
+  int c_type;
+};
+
+// One expert's rows, from the offsets: clamped to [0, rows], empty where they decrease.
+__device__ __forceinline__ int clamped_offset(const int32_t* off, int i, int rows) {
+  return min(max(off[i], 0), rows);
+}
+
+struct TileAt {
+  int e;         // expert (0 where there are no offsets); -1: rows of no expert
+  int row0;      // first row of the tile
+  int row_end;   // end of the group's rows
+  int tn;        // tile column
+};
+
+// Consecutive ids for the workgroups of one XCD: workgroup w runs on XCD w mod 8, and
+// XCD x gets ids x q + min(x, r) .. of n = 8 q + r, a permutation of 0 .. n - 1.
+__device__ __forceinline__ int xcd_order(int w, int n) {
+  const int q = n / kXcds, r = n % kXcds, x = w % kXcds;
+  return x * q + min(x, r) + w / kXcds;
+}
+
+// Tiles of one group are walked in bands of kBand tile rows, column by column, so that the
+// workgroups of one XCD that run together share rows of A and of B in its L2.
+constexpr int kBand = 8;
+__device__ __forceinline__ void band_order(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int band = id / (kBand * tiles_n);
+  const int rest = id - band * kBand * tiles_n;
+  const int h = min(kBand, tiles_m - band * kBand);
+  tn = rest / h;
+  tm = band * kBand + rest - tn * h;
+}
+
+// Which tile workgroup `wg` of `nwg` computes.  The launch has a workgroup for the largest
+// number of tiles that any offsets can give; the count that these give is found here, by
+// every wave for itself, 64 groups at a time, and the workgroups past it return false.
+// Group 0 is the rows before offsets[0], group E + 1 the ones from offsets[E] on.
+__device__ inline bool find_tile(const LpArgs& p, int BM, int wg, int nwg, TileAt& t) {
+  int tm;
+  if (p.offsets == nullptr) {
+    const int tiles_m = (p.rows + BM - 1) / BM, n = tiles_m * p.tiles_n;
+    if (wg >= n) return false;
+    band_order(xcd_order(wg, n), tiles_m, p.tiles_n, tm, t.tn);
+    t.e = 0;
+    t.row0 = tm * BM;
+    t.row_end = p.rows;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  const int groups = p.E + 2;
+  int total = 0, lo = 0, hi = 0, incl = 0;
+  auto load = [&](int base) {  // this lane's group and the running tile count up to it
+    const int g = base + lane;
+    lo = hi = 0;
+    if (g < groups) {
+      lo = g == 0 ? 0 : clamped_offset(p.offsets, g - 1, p.rows);
+      hi = g == p.E + 1 ? p.rows : clamped_offset(p.offsets, g, p.rows);
+    }
+    incl = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(incl, d);
+      if (lane >= d) incl += up;
+    }
+  };
+  for (int base = 0; base < groups; base += 64) {
+    load(base);
+    total += __shfl(incl, 63);
+  }
+  const int n = (int)min((int64_t)total * p.tiles_n, (int64_t)nwg);
+  if (wg >= n) return false;
+  int id = xcd_order(wg, n);
+  for (int base = 0; base < groups; base += 64) {
+    if (groups > 64) load(base);
+    const uint64_t past = __ballot((int64_t)incl * p.tiles_n > id);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int before = l ? __shfl(incl, l - 1) : 0;
+      const int count = __shfl(incl, l) - before;
+      const int g = base + l;
+      band_order(id - before * p.tiles_n, count, p.tiles_n, tm, t.tn);
+      t.e = g == 0 || g == p.E + 1 ? -1 : g - 1;
+      t.row0 = __shfl(lo, l) + tm * BM;
+      t.row_end = __shfl(hi, l);
+      return true;
+    }
+    id -= __shfl(incl, 63) * p.tiles_n;
+  }
+  return false;
+}
+
+// Store four neighbouring values of one row: at most `n` of them are inside it.  `vec`: the
+// row's address and stride allow one store.  One rounding to the nearest, ties to even.
+__device__ __forceinline__ void store4(void* C, int64_t at, int n, bool vec, int type,
+                                       float4v v) {
+  if (type == GEMM_LP_F32) {
+    float* p = (float*)C + at;
+    if (vec && n >= 4) {
+      *(float4v*)p = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = v[i];
+    }
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = type == GEMM_LP_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v[i])
+                                : __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+  uint16_t* p = (uint16_t*)C + at;
+  if (vec && n >= 4) {
+    *(uint2*)p = make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16,
+                            (uint32_t)h[2] | (uint32_t)h[3] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = h[i];
+  }
+}
+
+// Host: a kernel and how it is launched.
+using LpKernel = void (*)(LpArgs);
+
+}  // namespace gemmlp
+
+namespace gemmf32 {
+void set_last_hip_error(int code);  // what gemm_f32_last_hip_error reports (gemm_f32.hip)
+}
