@@ -21,6 +21,14 @@ def _say(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
+@pytest.fixture(params=["", "256", "128", "64"], ids=lambda v: f"tile{v or '-auto'}")
+def tile(request, monkeypatch):
+    """Every tile's kernel, wherever it takes the operands, besides the one that is chosen."""
+    if request.param:
+        monkeypatch.setenv("GEMM_LP_TILE", request.param)
+    return request.param
+
+
 def _gen(seed):
     return torch.Generator().manual_seed(seed)
 
@@ -114,13 +122,13 @@ def _aligned(q):
 
 FP8_SHAPES = [(1, 1, 1), (1, 64, 128), (5, 33, 127), (16, 256, 1024), (33, 130, 129),
               (127, 193, 61), (129, 257, 400), (200, 520, 2053), (300, 384, 896), (7, 1000, 4096),
-              (512, 512, 640)]
+              (512, 512, 640), (260, 264, 1024), (131, 300, 2500)]
 
 
 @pytest.mark.parametrize("out", TYPES)
 @pytest.mark.parametrize("b_block", [1, 128])
 @pytest.mark.parametrize("shape", FP8_SHAPES, ids=str)
-def test_matmul_fp8(shape, b_block, out):
+def test_matmul_fp8(shape, b_block, out, tile):
     M, N, K = shape
     a, sa = _scaled(M, K, 1, 21 + M)
     b, sb = _scaled(N, K, b_block, 22 + N)
@@ -164,8 +172,8 @@ GROUPS = [([5], 0, 0), ([1, 0, 3, 0, 0, 7], 0, 0), ([0, 0, 0], 2, 3), ([130, 1, 
 
 @pytest.mark.parametrize("out", TYPES)
 @pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{len(g[0])}e-{sum(g[0])}")
-@pytest.mark.parametrize("NK", [(64, 128), (130, 400), (257, 261)], ids=str)
-def test_matmul_fp8_grouped(groups, NK, out):
+@pytest.mark.parametrize("NK", [(64, 128), (130, 400), (257, 261), (132, 1300)], ids=str)
+def test_matmul_fp8_grouped(groups, NK, out, tile):
     N, K = NK
     off, rows = _split(*groups)
     E = len(groups[0])
@@ -192,7 +200,7 @@ def test_matmul_fp8_grouped(groups, NK, out):
 @pytest.mark.parametrize("tw", [False, True])
 @pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{len(g[0])}e-{sum(g[0])}")
 @pytest.mark.parametrize("KN", [(1, 1), (64, 128), (136, 264), (321, 131), (400, 72)], ids=str)
-def test_grouped_step(groups, KN, tw, dtype):
+def test_grouped_step(groups, KN, tw, dtype, tile):
     """y, dx and dw of a step, NaN in the rows of no expert (which must not leak)."""
     K, N = KN
     off, rows = _split(*groups)
@@ -228,7 +236,7 @@ def test_grouped_step(groups, KN, tw, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tw", [False, True])
-def test_grouped_views(dtype, tw):
+def test_grouped_views(dtype, tw, tile):
     """Operands whose rows and experts do not fill their strides."""
     K, N, E = 96, 80, 3
     off, rows = _split([9, 0, 40], 0, 2)
@@ -248,7 +256,7 @@ def test_grouped_views(dtype, tw):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_inf_and_nan_stay_in_their_rows_and_experts(dtype):
+def test_inf_and_nan_stay_in_their_rows_and_experts(dtype, tile):
     """An Inf or NaN of one expert's rows reaches that expert's results and no others."""
     K, N, E = 128, 128, 3
     off = [0, 20, 40, 60]
@@ -270,7 +278,7 @@ def test_inf_and_nan_stay_in_their_rows_and_experts(dtype):
     assert not finite[2, 5].any() and finite[2].sum() == (K - 1) * N
 
 
-def test_wrong_offsets_stay_in_bounds():
+def test_wrong_offsets_stay_in_bounds(tile):
     """Offsets past the rows, negative and decreasing ones: the values are undefined, the call
     ends, and what lies around the outputs keeps its values."""
     K, N, E, rows = 64, 64, 4, 50
@@ -296,8 +304,8 @@ def test_wrong_offsets_stay_in_bounds():
 # ------------------------------------------------------------------------------ training steps
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("shape", [(1, 1, 1), (5, 130, 70), (128, 128, 128), (200, 384, 264),
-                                   (257, 129, 513)], ids=str)
-def test_linear_fp8(shape, dtype):
+                                   (257, 129, 513), (1100, 260, 1027)], ids=str)
+def test_linear_fp8(shape, dtype, tile):
     M, N, K = shape
     g = _gen(61 + M)
     x = _randn(g, M, K).to(TYPES[dtype])

@@ -27,11 +27,14 @@ MAIN_SOURCE = os.path.join(CSRC, "gemm_f32.hip")
 CFG_SOURCE = os.path.join(CSRC, "cfg_kernels.hip")
 NUM_CONFIGS = 20  # configs.h: kNumConfigs
 LP_SOURCE = os.path.join(CSRC, "gemm_lp.hip")  # low-precision and expert-grouped products
-SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE]
+LP_UNIT_SOURCE = os.path.join(CSRC, "lp_kernels.hip")
+NUM_LP_UNITS = 11  # lp_units.h: kUnits
+SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",
                                             "dispatch_table.h", "mfma_peak.h",
-                                            "lp_common.h", "lp_quantize.h", "lp_tile.h")]
+                                            "lp_common.h", "lp_quantize.h", "lp_tile.h",
+                                            "lp_pipe.h", "lp_units.h")]
 DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h")]
 LIB = os.path.join(PKG, "libgemmf32.so")
 LIB_POISON = os.path.join(PKG, "libgemmf32_lds_poison.so")
@@ -52,9 +55,11 @@ def _run(cmd, **kw):
 
 def _units():
     """(name, source, extra flags) of every translation unit: the host code and reduction
-    kernels, one unit per tile configuration, and the low-precision products."""
+    kernels, one unit per tile configuration, and the low-precision and expert-grouped
+    products, their pipelined kernels one unit per element type and operand order."""
     units = [("gemm_f32", MAIN_SOURCE, []), ("gemm_lp", LP_SOURCE, [])]
     units += [(f"cfg{i}", CFG_SOURCE, [f"-DGEMMF32_CFG_ID={i}"]) for i in range(NUM_CONFIGS)]
+    units += [(f"lp{i}", LP_UNIT_SOURCE, [f"-DLP_UNIT={i}"]) for i in range(NUM_LP_UNITS)]
     return units
 
 

@@ -4,11 +4,13 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "gemm_lp.h"
 #include "lp_common.h"
 #include "lp_quantize.h"
 #include "lp_tile.h"
+#include "lp_units.h"
 
 namespace gemmlp {
 
@@ -82,6 +84,50 @@ static LpKernel tile_kernel(int type) {
     case GEMM_LP_F16: return &lp_tile_kernel<F16, AKC, BKC, WGRAD>;
     default: return &lp_tile_kernel<F32, AKC, BKC, WGRAD>;
   }
+}
+
+static LpKernel pipe_kernel(int unit, int tile) {
+  switch (unit) {
+    case 0: return pipe_kernel_0(tile);
+    case 1: return pipe_kernel_1(tile);
+    case 2: return pipe_kernel_2(tile);
+    case 3: return pipe_kernel_3(tile);
+    case 4: return pipe_kernel_4(tile);
+    case 5: return pipe_kernel_5(tile);
+    case 6: return pipe_kernel_6(tile);
+    case 7: return pipe_kernel_7(tile);
+    case 8: return pipe_kernel_8(tile);
+    case 9: return pipe_kernel_9(tile);
+    default: return pipe_kernel_10(tile);
+  }
+}
+
+// Whether an operand can be copied in words: rows and experts that start at multiples of four
+// bytes, and 256 rows (or k rows) within the 32-bit offsets of a copy.
+static bool word_rows(const void* p, int64_t ld, int64_t stride, int bytes) {
+  return misaligned(p, 4) == false && ld * bytes % 4 == 0 && stride * bytes % 4 == 0 &&
+         ld <= (int64_t)0xFFFF0000u / 256 / bytes;
+}
+
+// The tile of the pipelined kernel for a product of `tiles(BM, BN)` tiles, or -1: the general
+// kernel.
+//
+// GEMM_LP_TILE=<256|128|64> forces a tile where its kernel takes the operands, for tests and
+// measurement, as GEMMF32_VARIANT does for the FP32 product.
+static int env_tile() {
+  const char* v = std::getenv("GEMM_LP_TILE");
+  return v == nullptr ? 0 : std::atoi(v);
+}
+template <class F>
+static int pick_tile(int unit, F tiles) {
+  if (const int forced = env_tile()) {
+    for (int t : {kTile256, kTile128})
+      if (kTiles[t].bm == forced && pipe_kernel(unit, t) != nullptr) return t;
+    return -1;
+  }
+  for (int t : {kTile256, kTile128})
+    if (pipe_kernel(unit, t) != nullptr && tiles(kTiles[t].bm, kTiles[t].bn) >= 128) return t;
+  return -1;
 }
 
 static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
@@ -178,6 +224,18 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   a.ldsa = ldsa, a.ldsb = ldsb, a.stride_sb = stride_sb;
   a.rows = a.M = (int)M, a.N = (int)N, a.K = (int)K, a.E = (int)E;
   a.sb_shift = b_block == 1 ? 0 : 7, a.c_type = c_type;
+  // The 8-bit instruction cuts up to 2^-12.2 of its 128 products' magnitudes S (2^-16 on
+  // average, lp_common.h).  It is taken for bf16 results, which keep 8 bits, of contractions
+  // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
+  // themselves; other results go through the 16-bit instruction, which cuts nothing.
+  const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? 9 : 10;
+  if (word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1) && ldsa <= (1 << 22) &&
+      ldsb <= (1 << 22)) {
+    const int t = pick_tile(unit, [&](int bm, int bn) { return row_tiles(a, bm, bn); });
+    if (t >= 0)
+      return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
+                         stream);
+  }
   return launch_rows(&lp_tile_kernel<F8, true, true, false>, a, 64, 64, 256, stream);
 }
 
@@ -211,6 +269,13 @@ static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int3
   a.lda = ldx, a.ldb = ldw, a.ldc = ldy, a.stride_b = stride_w;
   a.rows = a.M = (int)rows, a.N = (int)N, a.K = (int)K, a.E = (int)E;
   a.c_type = type;
+  const int unit = 3 * type + (transpose_w ? 0 : 1);
+  if (word_rows(X, ldx, 0, b) && word_rows(W, ldw, stride_w, b)) {
+    const int t = pick_tile(unit, [&](int bm, int bn) { return row_tiles(a, bm, bn); });
+    if (t >= 0)
+      return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
+                         stream);
+  }
   const LpKernel fn = transpose_w ? tile_kernel<true, true, false>(type)
                                   : tile_kernel<true, false, false>(type);
   return launch_rows(fn, a, 64, 64, 256, stream);
@@ -247,6 +312,15 @@ static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_
   a.lda = lda, a.ldb = ldb, a.ldc = ldw, a.stride_c = stride_w;
   a.rows = a.K = (int)rows, a.M = (int)M, a.N = (int)N, a.E = (int)E;
   a.c_type = type;
+  const int unit = 3 * type + 2;
+  if (word_rows(A, lda, 0, b) && word_rows(B, ldb, 0, b)) {
+    const int t = pick_tile(unit, [&](int64_t bm, int64_t bn) {
+      return (M + bm - 1) / bm * ((N + bn - 1) / bn) * E;
+    });
+    if (t >= 0)
+      return launch_wgrad(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
+                          stream);
+  }
   return launch_wgrad(tile_kernel<false, false, true>(type), a, 64, 64, 256, stream);
 }
 

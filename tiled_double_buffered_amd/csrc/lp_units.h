@@ -1,0 +1,50 @@
+// The units that the pipelined product kernels are compiled in: an element type and the order
+// of the operands (does k, the contraction, lie contiguous in A and in B).
+#pragma once
+
+#include "lp_common.h"
+
+namespace gemmlp {
+
+// Tiles of the pipelined kernel.
+enum { kTile256 = 0, kTile128 = 1 };
+struct TileSize {
+  int bm, bn, threads;
+};
+constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}};
+
+template <class T, bool A, bool B, bool W, bool F>
+struct Unit {
+  using type = T;
+  static constexpr bool AKC = A, BKC = B, WGRAD = W, FAST8 = F;
+};
+template <int UNIT>
+struct UnitOf;
+// 16- and 32-bit: X W^T, X W, and the weight gradient
+template <> struct UnitOf<0> : Unit<Bf16, true, true, false, false> {};
+template <> struct UnitOf<1> : Unit<Bf16, true, false, false, false> {};
+template <> struct UnitOf<2> : Unit<Bf16, false, false, true, false> {};
+template <> struct UnitOf<3> : Unit<F16, true, true, false, false> {};
+template <> struct UnitOf<4> : Unit<F16, true, false, false, false> {};
+template <> struct UnitOf<5> : Unit<F16, false, false, true, false> {};
+template <> struct UnitOf<6> : Unit<F32, true, true, false, false> {};
+template <> struct UnitOf<7> : Unit<F32, true, false, false, false> {};
+template <> struct UnitOf<8> : Unit<F32, false, false, true, false> {};
+// 8-bit: through the 8-bit instruction, and through the 16-bit one
+template <> struct UnitOf<9> : Unit<F8, true, true, false, true> {};
+template <> struct UnitOf<10> : Unit<F8, true, true, false, false> {};
+constexpr int kUnits = 11;
+
+LpKernel pipe_kernel_0(int tile);
+LpKernel pipe_kernel_1(int tile);
+LpKernel pipe_kernel_2(int tile);
+LpKernel pipe_kernel_3(int tile);
+LpKernel pipe_kernel_4(int tile);
+LpKernel pipe_kernel_5(int tile);
+LpKernel pipe_kernel_6(int tile);
+LpKernel pipe_kernel_7(int tile);
+LpKernel pipe_kernel_8(int tile);
+LpKernel pipe_kernel_9(int tile);
+LpKernel pipe_kernel_10(int tile);
+
+}  // namespace gemmlp
