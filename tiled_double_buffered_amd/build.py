@@ -28,13 +28,13 @@ CFG_SOURCE = os.path.join(CSRC, "cfg_kernels.hip")
 NUM_CONFIGS = 20  # configs.h: kNumConfigs
 LP_SOURCE = os.path.join(CSRC, "gemm_lp.hip")  # low-precision and expert-grouped products
 LP_UNIT_SOURCE = os.path.join(CSRC, "lp_kernels.hip")
-NUM_LP_UNITS = 11  # lp_units.h: kUnits
+NUM_LP_UNITS = 12  # lp_units.h: kUnits
 SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",
                                             "dispatch_table.h", "mfma_peak.h",
                                             "lp_common.h", "lp_quantize.h", "lp_tile.h",
-                                            "lp_pipe.h", "lp_units.h")]
+                                            "lp_pipe.h", "lp_deep.h", "lp_units.h")]
 DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h")]
 LIB = os.path.join(PKG, "libgemmf32.so")
 LIB_POISON = os.path.join(PKG, "libgemmf32_lds_poison.so")

@@ -98,7 +98,8 @@ static LpKernel pipe_kernel(int unit, int tile) {
     case 7: return pipe_kernel_7(tile);
     case 8: return pipe_kernel_8(tile);
     case 9: return pipe_kernel_9(tile);
-    default: return pipe_kernel_10(tile);
+    case 10: return pipe_kernel_10(tile);
+    default: return pipe_kernel_11(tile);
   }
 }
 
@@ -228,7 +229,7 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   // average, lp_common.h).  It is taken for bf16 results, which keep 8 bits, of contractions
   // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
   // themselves; other results go through the 16-bit instruction, which cuts nothing.
-  const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? 9 : 10;
+  const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? (b_block == 1 ? 11 : 10) : 9;
   if (word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1) && ldsa <= (1 << 22) &&
       ldsb <= (1 << 22)) {
     const int t = pick_tile(unit, [&](int bm, int bn) { return row_tiles(a, bm, bn); });

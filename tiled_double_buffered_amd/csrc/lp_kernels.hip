@@ -2,6 +2,7 @@
 // (LP_UNIT) so that they build in parallel.
 #include <hip/hip_runtime.h>
 
+#include "lp_deep.h"
 #include "lp_pipe.h"
 #include "lp_units.h"
 
@@ -15,12 +16,15 @@ template <int UNIT>
 static LpKernel pick(int tile) {
   using U = UnitOf<UNIT>;
   using T = typename U::type;
-  // (8-bit values through the 16-bit instruction need more registers than a wave of the
-  // large tile has)
-  constexpr bool kLarge = U::FAST8 || T::BYTES != 1;
-  if constexpr (kLarge)
-    if (tile == kTile256) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 256, 256, 2, 4, U::FAST8>;
-  if (tile == kTile128) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 128, 128, 2, 2, U::FAST8>;
+  if (tile == kTile256) {
+    // 8-bit values through the 16-bit instruction, or with a scale for each column, need more
+    // registers than a wave of the deep kernel has
+    if constexpr (T::BYTES != 1 || U::HOW == kFast8Blocks)
+      return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD, U::HOW>;
+    else if constexpr (U::HOW == kFast8Rows)
+      return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 256, 256, 2, 4, U::HOW>;
+  }
+  if (tile == kTile128) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 128, 128, 2, 2, U::HOW>;
   return nullptr;
 }
 

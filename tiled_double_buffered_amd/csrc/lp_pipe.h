@@ -68,8 +68,9 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// One operand: R rows (of A or columns of B) a tile, WT of them a wave.
-template <class T, bool KC, int R, int WT, int WAVES>
+// One operand: R rows (of A or columns of B) a tile, WT of them a wave.  GAP: the part holds WT
+// rows of every WT + GAP of the tile's (half of an operand, the same half for every wave).
+template <class T, bool KC, int R, int WT, int WAVES, int GAP = 0>
 struct PipeOperand {
   static constexpr int BYTES = R * kRowBytes;  // of a slot, either order
   static constexpr int COPIES = R / 8 / WAVES;
@@ -78,6 +79,8 @@ struct PipeOperand {
   static constexpr int K_ROW = R * T::BYTES;   // bytes of a k row (rows contiguous)
   static_assert(COPIES * WAVES * 8 == R, "whole copies");
   static_assert(KC || T::BYTES == 4 || R >= 128, "f(k) needs eight positions");
+
+  static __device__ __forceinline__ int tile_row(int r) { return r + r / WT * GAP; }
 
   uint32_t off[COPIES];  // of this lane's 16 bytes from the tile's first
   const char* base;
@@ -103,14 +106,15 @@ struct PipeOperand {
       const int j = wave + i * WAVES;
       if constexpr (KC) {
         const int row = j * 8 + lane / 8;
-        off[i] = (uint32_t)(row * ldb) + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+        off[i] = (uint32_t)(tile_row(row) * ldb) +
+                 (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
       } else {
         const int at = j * 1024 + lane * 16, k = at / K_ROW, in = at % K_ROW;
-        if constexpr (T::BYTES == 4)
-          off[i] = (uint32_t)(k * ldb) + (uint32_t)in;
-        else
-          off[i] = (uint32_t)(k * ldb) +
-                   (uint32_t)((((in >> 5) ^ ((k & 3) | ((k >> 3) & 1) << 2)) << 5) | (in & 31));
+        const int from = T::BYTES == 4
+                             ? in
+                             : ((((in >> 5) ^ ((k & 3) | ((k >> 3) & 1) << 2)) << 5) | (in & 31));
+        off[i] = (uint32_t)(k * ldb) +
+                 (uint32_t)(tile_row(from / T::BYTES) * T::BYTES + from % T::BYTES);
       }
     }
     const int l16 = lane & 15, g = lane >> 4;
@@ -128,39 +132,49 @@ struct PipeOperand {
     }
   }
 
+  __device__ __forceinline__ int4v words(int kt) const {
+    return buffer_words(base + kt * step, left - kt * step);
+  }
+  __device__ __forceinline__ void copy(int i, int4v r, uint32_t lds, int wave) const {
+    copy16(__builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave + i * WAVES) * 1024u), r, off[i]);
+  }
   __device__ __forceinline__ void issue(int kt, uint32_t lds, int wave) const {
-    const int4v r = buffer_words(base + kt * step, left - kt * step);
+    const int4v r = words(kt);
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i)
-      copy16(__builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave + i * WAVES) * 1024u), r, off[i]);
+    for (int i = 0; i < COPIES; ++i) copy(i, r, lds, wave);
   }
 
-  // Half h of a K step: 16 bytes of k a lane for each 16-row fragment.
-  __device__ __forceinline__ void read(const char* slot, int h, int4v* f) const {
+  // Both halves of a K step, 16 bytes of k a lane each, for fragment i (of 16 rows), or for
+  // the four fragments from i on where a lane reads four columns at once.
+  static constexpr int READ = KC || T::BYTES != 4 ? 1 : 4;
+  __device__ __forceinline__ void read(const char* slot, int i, int8v* f) const {
     if constexpr (KC) {
-#pragma unroll
-      for (int i = 0; i < SUB; ++i)
-        f[i] = *(const int4v*)(slot + lane_at[h] + i * 16 * kRowBytes);
+      f[0] = both(*(const int4v*)(slot + lane_at[0] + i * 16 * kRowBytes),
+                  *(const int4v*)(slot + lane_at[1] + i * 16 * kRowBytes));
     } else if constexpr (T::BYTES == 4) {
 #pragma unroll
-      for (int j = 0; j < SUB / 4; ++j)
+      for (int q = 0; q < 4; ++q) {
+        const char* at = slot + lane_at[0] + q * K_ROW + 64 * i;
+        const int4v u = *(const int4v*)at, v = *(const int4v*)(at + 16 * K_ROW);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int4v v = *(const int4v*)(slot + lane_at[0] + (16 * h + q) * K_ROW + 256 * j);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[4 * j + i][q] = v[i];
+        for (int x = 0; x < 4; ++x) {
+          f[x][q] = u[x];
+          f[x][4 + q] = v[x];
         }
-    } else {
-#pragma unroll
-      for (int j = 0; j < SUB; ++j) {
-        const char* at = slot + lane_at[j] + h * 32 * K_ROW;
-        typedef __attribute__((address_space(3))) short4v lds_short4;
-        const short4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds_char*)at);
-        const short4v b =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds_char*)(at + 4 * K_ROW));
-        f[j] = __builtin_bit_cast(int4v, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
       }
+    } else {
+      f[0] = both(turned(slot + lane_at[i]), turned(slot + lane_at[i] + 32 * K_ROW));
     }
+  }
+  static __device__ __forceinline__ int8v both(int4v lo, int4v hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  static __device__ __forceinline__ int4v turned(const char* at) {
+    typedef __attribute__((address_space(3))) short4v lds_short4;
+    const short4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds_char*)at);
+    const short4v b =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds_char*)(at + 4 * K_ROW));
+    return __builtin_bit_cast(int4v, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   // The row that fragment i's row x of the wave's is.
   static __device__ __forceinline__ int row_of(int i, int x) {
@@ -188,6 +202,10 @@ struct PipeOperand {
   }
 };
 
+__device__ __forceinline__ int4v half_of(int8v f, int h) {
+  return h ? __builtin_shufflevector(f, f, 4, 5, 6, 7) : __builtin_shufflevector(f, f, 0, 1, 2, 3);
+}
+
 // 16 bytes of k a lane from each side.
 template <class T>
 __device__ __forceinline__ float4v mma_half(int4v a, int4v b, float4v c) {
@@ -205,8 +223,112 @@ __device__ __forceinline__ float4v mma_half(int4v a, int4v b, float4v c) {
   }
 }
 
-// FAST8: 8-bit values through the 8-bit instruction; otherwise through the 16-bit one.
-template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, bool FAST8>
+// What one workgroup computes: C's rows m0 .. m_end and columns n0 .. from A's and B's rows.
+struct TileOf {
+  const char* A;
+  const char* B;
+  int64_t c_base;
+  int m0, m_end, n0, e, k_end;
+};
+template <class T, bool WGRAD, int BM, int BN>
+__device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
+  w.A = (const char*)p.A;
+  w.B = (const char*)p.B;
+  w.c_base = 0;
+  if constexpr (WGRAD) {
+    const int tiles_m = (p.M + BM - 1) / BM, per = tiles_m * p.tiles_n;
+    const int id = xcd_order(blockIdx.x, gridDim.x);
+    w.e = id / per;
+    int tm, tn;
+    band_order(id - w.e * per, tiles_m, p.tiles_n, tm, tn);
+    const int lo = clamped_offset(p.offsets, w.e, p.rows);
+    const int hi = clamped_offset(p.offsets, w.e + 1, p.rows);
+    w.A += (int64_t)lo * p.lda * T::BYTES;
+    w.B += (int64_t)lo * p.ldb * T::BYTES;
+    w.k_end = max(hi - lo, 0);
+    w.m0 = tm * BM;
+    w.m_end = p.M;
+    w.n0 = tn * BN;
+    w.c_base = w.e * p.stride_c;
+  } else {
+    TileAt t;
+    if (!find_tile(p, BM, blockIdx.x, gridDim.x, t)) return false;
+    w.e = __builtin_amdgcn_readfirstlane(t.e);
+    w.k_end = w.e < 0 ? 0 : p.K;
+    if (w.e > 0) w.B += w.e * p.stride_b * T::BYTES;
+    w.m0 = __builtin_amdgcn_readfirstlane(t.row0);
+    w.m_end = __builtin_amdgcn_readfirstlane(t.row_end);
+    w.n0 = __builtin_amdgcn_readfirstlane(t.tn) * BN;
+  }
+  return true;
+}
+
+// The copies of a K step's scales (8-bit values): one for each row of A and column of B of the
+// tile, 64 a wave.
+struct ScaleCopy {
+  const char* base;
+  int64_t left;
+  uint32_t off;
+  template <int BM>
+  __device__ __forceinline__ void init(const LpArgs& p, const TileOf& w, int steps, int wave,
+                                       int lane) {
+    const int r = wave * 64 + lane;
+    if (wave < BM / 64) {
+      const int rows = w.m_end - w.m0;
+      base = (const char*)(p.SA + (int64_t)w.m0 * p.ldsa);
+      off = (uint32_t)(min(r, rows - 1) * p.ldsa * 4);
+      left = ((int64_t)(rows - 1) * p.ldsa + steps) * 4;
+    } else {
+      const int first = w.n0 >> p.sb_shift;
+      const int n = min(w.n0 + r - BM, p.N - 1) >> p.sb_shift;
+      base = (const char*)(p.SB + w.e * p.stride_sb + (int64_t)first * p.ldsb);
+      off = (uint32_t)((n - first) * p.ldsb * 4);
+      left = ((int64_t)(((p.N - 1) >> p.sb_shift) - first) * p.ldsb + steps) * 4;
+    }
+  }
+  __device__ __forceinline__ int4v words(int kt) const {
+    return buffer_words(base + kt * 4, left - kt * 4);
+  }
+  __device__ __forceinline__ void copy(int4v r, uint32_t lds, int wave) const {
+    copy4(__builtin_amdgcn_readfirstlane(lds + (uint32_t)wave * 256u), r, off);
+  }
+  __device__ __forceinline__ void issue(int kt, uint32_t lds, int wave) const {
+    copy(words(kt), lds, wave);
+  }
+};
+
+// One wave's accumulators into C.  m: C's row of fragment i for this lane.
+template <class T, bool BKC, int SM, int SN, class F>
+__device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int wn, int g,
+                                           const float4v (&acc)[SM][SN], F row) {
+  const int cb = type_bytes(p.c_type);
+  const bool vec = (((uintptr_t)p.C | (uintptr_t)(p.ldc * cb) | (uintptr_t)(w.c_base * cb)) &
+                    (uintptr_t)(4 * cb - 1)) == 0;
+#pragma unroll
+  for (int i = 0; i < SM; ++i) {
+    const int m = row(i);
+    if (m >= w.m_end) continue;
+    const int64_t at = w.c_base + (int64_t)m * p.ldc;
+#pragma unroll
+    for (int j = 0; j < SN; ++j) {
+      if constexpr (!BKC && T::BYTES == 4) {
+        // fragments 4 q .. 4 q + 3, register r: columns 64 q + 16 g + 4 r .. + 3
+        const int q = j >> 2, r = j & 3, n = w.n0 + wn + 64 * q + 16 * g + 4 * r;
+        const float4v v = {acc[i][4 * q][r], acc[i][4 * q + 1][r], acc[i][4 * q + 2][r],
+                           acc[i][4 * q + 3][r]};
+        store4(p.C, at + n, p.N - n, vec, p.c_type, v);
+      } else {
+        const int n = w.n0 + wn + 16 * j + 4 * g;
+        store4(p.C, at + n, p.N - n, vec, p.c_type, acc[i][j]);
+      }
+    }
+  }
+}
+
+// HOW (8-bit values): through the 16-bit instruction; or through the 8-bit one, with B's scales
+// by blocks of 128 columns or column by column.
+enum { kExact8 = 0, kFast8Blocks = 1, kFast8Rows = 2 };
+template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW>
 __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
@@ -220,78 +342,32 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
-  const char* A = (const char*)p.A;
-  const char* B = (const char*)p.B;
-  int64_t c_base = 0;
-  int m0, m_end, n0, e, k_end, a_rows;
-  if constexpr (WGRAD) {
-    const int tiles_m = (p.M + BM - 1) / BM, per = tiles_m * p.tiles_n;
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    e = id / per;
-    int tm, tn;
-    band_order(id - e * per, tiles_m, p.tiles_n, tm, tn);
-    const int lo = clamped_offset(p.offsets, e, p.rows);
-    const int hi = clamped_offset(p.offsets, e + 1, p.rows);
-    A += (int64_t)lo * p.lda * T::BYTES;
-    B += (int64_t)lo * p.ldb * T::BYTES;
-    k_end = max(hi - lo, 0);
-    m0 = tm * BM;
-    m_end = a_rows = p.M;
-    n0 = tn * BN;
-    c_base = e * p.stride_c;
-  } else {
-    TileAt t;
-    if (!find_tile(p, BM, blockIdx.x, gridDim.x, t)) return;
-    e = __builtin_amdgcn_readfirstlane(t.e);
-    k_end = e < 0 ? 0 : p.K;
-    if (e > 0) B += e * p.stride_b * T::BYTES;
-    m0 = __builtin_amdgcn_readfirstlane(t.row0);
-    m_end = __builtin_amdgcn_readfirstlane(t.row_end);
-    n0 = __builtin_amdgcn_readfirstlane(t.tn) * BN;
-    a_rows = m_end;
-  }
+  TileOf w;
+  if (!locate<T, WGRAD, BM, BN>(p, w)) return;
   const int wm = (wave / WN) * WTM, wn = (wave % WN) * WTN;
 
   float4v acc[SM][SN] = {};
-  const int steps = (k_end + OA::KS - 1) / OA::KS;
+  const int steps = (w.k_end + OA::KS - 1) / OA::KS;
   if (steps > 0) {
     OA oa;
     OB ob;
-    oa.init(A, p.lda, m0, a_rows, k_end, wave, lane, wm);
-    ob.init(B, p.ldb, n0, p.N, k_end, wave, lane, wn);
+    oa.init(w.A, p.lda, w.m0, w.m_end, w.k_end, wave, lane, wm);
+    ob.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane, wn);
     const uint32_t lds0 =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
-    // 8-bit: a K step's scales, one for each row of A and column of B, one copy of 64 a wave
-    uint32_t s_off = 0;
-    const char* s_base = nullptr;
-    int64_t s_left = 0;
+    ScaleCopy os;
     constexpr int S_WAVES = (BM + BN) / 64;
-    if constexpr (F8T) {
-      static_assert(S_WAVES <= WAVES, "a wave copies 64 scales at most");
-      const int r = wave * 64 + lane;
-      if (wave < BM / 64) {
-        s_base = (const char*)(p.SA + (int64_t)m0 * p.ldsa);
-        const int rows = a_rows - m0;
-        s_off = (uint32_t)(min(r, rows - 1) * p.ldsa * 4);
-        s_left = ((int64_t)(rows - 1) * p.ldsa + steps) * 4;
-      } else {
-        const int n = min(n0 + r - BM, p.N - 1);
-        s_base = (const char*)(p.SB + e * p.stride_sb + (int64_t)(n0 >> p.sb_shift) * p.ldsb);
-        s_off = (uint32_t)(((n >> p.sb_shift) - (n0 >> p.sb_shift)) * p.ldsb * 4);
-        s_left = ((int64_t)(((p.N - 1) >> p.sb_shift) - (n0 >> p.sb_shift)) * p.ldsb + steps) * 4;
-      }
-    }
+    static_assert(S_WAVES <= WAVES, "a wave copies 64 scales at most");
+    if constexpr (F8T) os.init<BM>(p, w, steps, wave, lane);
     auto issue = [&](int kt, int slot) {
       const uint32_t at = lds0 + (uint32_t)(slot * SLOT);
       oa.issue(kt, at, wave);
       ob.issue(kt, at + OA::BYTES, wave);
       if constexpr (F8T) {
-        if (wave < S_WAVES)
-          copy4(__builtin_amdgcn_readfirstlane(at + OA::BYTES + OB::BYTES + (uint32_t)wave * 256u),
-                buffer_words(s_base + kt * 4, s_left - kt * 4), s_off);
+        if (wave < S_WAVES) os.issue(kt, at + OA::BYTES + OB::BYTES, wave);
       }
     };
-    const int tail = (k_end % OA::KS) * T::BYTES;  // bytes of k in the last step, 0: all
+    const int tail = (w.k_end % OA::KS) * T::BYTES;  // bytes of k in the last step, 0: all
 
     issue(0, 0);
     for (int kt = 0; kt < steps; ++kt) {
@@ -305,69 +381,78 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
         __syncthreads();
       }
       if constexpr (!F8T) {
+        int8v a[SM], b[SN];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int4v fa[SM], fb[SN];
-          ob.read(sb, h, fb);
-          oa.read(sa, h, fa);
+        for (int j = 0; j < SN; j += OB::READ) ob.read(sb, j, b + j);
+#pragma unroll
+        for (int i = 0; i < SM; i += OA::READ) oa.read(sa, i, a + i);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < SM; ++i)
 #pragma unroll
-            for (int j = 0; j < SN; ++j) acc[i][j] = mma_half<T>(fb[j], fa[i], acc[i][j]);
-        }
+            for (int j = 0; j < SN; ++j) 
+              acc[i][j] = mma_half<T>(half_of(b[j], h), half_of(a[i], h), acc[i][j]);
       } else {
         const float* scales = (const float*)(sb + OB::BYTES);
-        int4v b0[SN], b1[SN];
-        ob.read(sb, 0, b0);
-        ob.read(sb, 1, b1);
+        int8v b[SN], a[2];
+#pragma unroll
+        for (int j = 0; j < SN; ++j) ob.read(sb, j, b + j);
+        oa.read(sa, 0, a);
         float4v s_b[SN];
+        float s_a[SM];
+        if constexpr (HOW != kFast8Blocks) {
 #pragma unroll
-        for (int j = 0; j < SN; ++j)
-          s_b[j] = *(const float4v*)(scales + BM + wn + 16 * j + 4 * g);
+          for (int j = 0; j < SN; ++j)
+            s_b[j] = *(const float4v*)(scales + BM + wn + 16 * j + 4 * g);
+        }
 #pragma unroll
-        for (int i = 0; i < SM; ++i) {
-          const int4v a0 = *(const int4v*)(sa + oa.lane_at[0] + i * 16 * kRowBytes);
-          const int4v a1 = *(const int4v*)(sa + oa.lane_at[1] + i * 16 * kRowBytes);
-          const float s_a = scales[wm + 16 * i + l16];
+        for (int i = 0; i < SM; ++i) s_a[i] = scales[wm + 16 * i + l16];
+        if constexpr (HOW == kFast8Blocks) {
+          // the wave's columns lie in one block of 128: one factor a row
+          static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
+          const float block = scales[BM + wn];
 #pragma unroll
-          for (int j = 0; j < SN; ++j) {
+          for (int i = 0; i < SM; ++i) s_a[i] *= block;
+        }
+        // The sums of a step are scaled and added kLag products behind, while the matrix
+        // cores work on the next ones; the order is pinned, since the compiler would put each
+        // addition right behind its product and wait.
+        constexpr int kLag = HOW == kExact8 ? 1 : 2, kRing = kLag + 1;
+        float4v d[kRing];
+#pragma unroll
+        for (int s = 0; s < SM * SN + kLag; ++s) {
+          if (s < SM * SN) {
+            const int i = s / SN, j = s % SN;
+            if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
             const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-            float4v d;
-            if constexpr (FAST8)
-              d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  __builtin_shufflevector(b0[j], b1[j], 0, 1, 2, 3, 4, 5, 6, 7),
-                  __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7), z, 0, 0, 0, 0, 0, 0);
+            if constexpr (HOW == kExact8)
+              d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
+                                         half_of(a[i & 1], 1), z);
             else
-              d = mma_step<T>(b0[j], b1[j], a0, a1, z);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] += d[r] * (s_a * s_b[j][r]);
+              d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
           }
+          if constexpr (HOW != kExact8) __builtin_amdgcn_sched_barrier(0);
+          if (s >= kLag) {
+            const int i = (s - kLag) / SN, j = (s - kLag) % SN;
+            const float4v v = d[(s - kLag) % kRing];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (HOW == kFast8Blocks)
+                acc[i][j][r] += v[r] * s_a[i];
+              else
+                acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
+            }
+          }
+          if constexpr (HOW != kExact8) __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
   }
 
-  const int cb = type_bytes(p.c_type);
-  const bool vec = (((uintptr_t)p.C | (uintptr_t)(p.ldc * cb) | (uintptr_t)(c_base * cb)) &
-                    (uintptr_t)(4 * cb - 1)) == 0;
-#pragma unroll
-  for (int i = 0; i < SM; ++i) {
-    const int m = m0 + wm + OA::row_of(i, l16);
-    if (m >= m_end) continue;
-#pragma unroll
-    for (int j = 0; j < SN; ++j) {
-      if constexpr (!BKC && T::BYTES == 4) {
-        // fragments 4 q .. 4 q + 3, register r: columns 64 q + 16 g + 4 r .. + 3
-        const int q = j >> 2, r = j & 3, n = n0 + wn + 64 * q + 16 * g + 4 * r;
-        const float4v v = {acc[i][4 * q][r], acc[i][4 * q + 1][r], acc[i][4 * q + 2][r],
-                           acc[i][4 * q + 3][r]};
-        store4(p.C, c_base + (int64_t)m * p.ldc + n, p.N - n, vec, p.c_type, v);
-      } else {
-        const int n = n0 + wn + 16 * j + 4 * g;
-        store4(p.C, c_base + (int64_t)m * p.ldc + n, p.N - n, vec, p.c_type, acc[i][j]);
-      }
-    }
-  }
+  store_tile<T, BKC>(p, w, wn, g, acc,
+                     [&](int i) { return w.m0 + wm + OA::row_of(i, l16); });
 }
 
 }  // namespace gemmlp

@@ -13,27 +13,30 @@ struct TileSize {
 };
 constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}};
 
-template <class T, bool A, bool B, bool W, bool F>
+template <class T, bool A, bool B, bool W, int H>
 struct Unit {
   using type = T;
-  static constexpr bool AKC = A, BKC = B, WGRAD = W, FAST8 = F;
+  static constexpr bool AKC = A, BKC = B, WGRAD = W;
+  static constexpr int HOW = H;
 };
 template <int UNIT>
 struct UnitOf;
 // 16- and 32-bit: X W^T, X W, and the weight gradient
-template <> struct UnitOf<0> : Unit<Bf16, true, true, false, false> {};
-template <> struct UnitOf<1> : Unit<Bf16, true, false, false, false> {};
-template <> struct UnitOf<2> : Unit<Bf16, false, false, true, false> {};
-template <> struct UnitOf<3> : Unit<F16, true, true, false, false> {};
-template <> struct UnitOf<4> : Unit<F16, true, false, false, false> {};
-template <> struct UnitOf<5> : Unit<F16, false, false, true, false> {};
-template <> struct UnitOf<6> : Unit<F32, true, true, false, false> {};
-template <> struct UnitOf<7> : Unit<F32, true, false, false, false> {};
-template <> struct UnitOf<8> : Unit<F32, false, false, true, false> {};
-// 8-bit: through the 8-bit instruction, and through the 16-bit one
-template <> struct UnitOf<9> : Unit<F8, true, true, false, true> {};
-template <> struct UnitOf<10> : Unit<F8, true, true, false, false> {};
-constexpr int kUnits = 11;
+template <> struct UnitOf<0> : Unit<Bf16, true, true, false, 0> {};
+template <> struct UnitOf<1> : Unit<Bf16, true, false, false, 0> {};
+template <> struct UnitOf<2> : Unit<Bf16, false, false, true, 0> {};
+template <> struct UnitOf<3> : Unit<F16, true, true, false, 0> {};
+template <> struct UnitOf<4> : Unit<F16, true, false, false, 0> {};
+template <> struct UnitOf<5> : Unit<F16, false, false, true, 0> {};
+template <> struct UnitOf<6> : Unit<F32, true, true, false, 0> {};
+template <> struct UnitOf<7> : Unit<F32, true, false, false, 0> {};
+template <> struct UnitOf<8> : Unit<F32, false, false, true, 0> {};
+// 8-bit: through the 16-bit instruction, and through the 8-bit one with B's scales by blocks
+// and by rows (lp_pipe.h: HOW)
+template <> struct UnitOf<9> : Unit<F8, true, true, false, 0> {};
+template <> struct UnitOf<10> : Unit<F8, true, true, false, 1> {};
+template <> struct UnitOf<11> : Unit<F8, true, true, false, 2> {};
+constexpr int kUnits = 12;
 
 LpKernel pipe_kernel_0(int tile);
 LpKernel pipe_kernel_1(int tile);
@@ -46,5 +49,6 @@ LpKernel pipe_kernel_7(int tile);
 LpKernel pipe_kernel_8(int tile);
 LpKernel pipe_kernel_9(int tile);
 LpKernel pipe_kernel_10(int tile);
+LpKernel pipe_kernel_11(int tile);
 
 }  // namespace gemmlp
