@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 
@@ -113,23 +114,55 @@ static bool word_rows(const void* p, int64_t ld, int64_t stride, int bytes) {
 // The tile of the pipelined kernel for a product of `tiles(BM, BN)` tiles, or -1: the general
 // kernel.
 //
-// GEMM_LP_TILE=<256|128|64> forces a tile where its kernel takes the operands, for tests and
-// measurement, as GEMMF32_VARIANT does for the FP32 product.
+// GEMM_LP_TILE=<256|128|64|1> forces a tile where its kernel takes the operands (1: the general
+// kernel), for tests and measurement, as GEMMF32_VARIANT does for the FP32 product.
 static int env_tile() {
   const char* v = std::getenv("GEMM_LP_TILE");
   return v == nullptr ? 0 : std::atoi(v);
 }
+// Time of one 128-byte K step of a tile, in us, measured on MI355X: `alone` with one workgroup
+// on the CU, `full` a CU's time for each with as many as fit (and the chip as warm as it gets).
+// A CU works through n = ceil(tiles / 256) tiles in n * full or, where that is more, in rounds
+// of `fit` tiles of `alone`; a launch, its first loads and last stores add about 4 us to all.
+struct StepCost {
+  double alone, full;
+};
+constexpr int kFit[kTileCount] = {1, 2, 4};
+constexpr StepCost kStep16[kTileCount] = {{1.40, 1.75}, {0.80, 0.56}, {0.45, 0.24}};
+constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.58}};
+constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}};
+constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.30, 1.10}, {0.60, 0.36}};
+
+// The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number.
 template <class F>
-static int pick_tile(int unit, F tiles) {
+static int pick_tile(int unit, double steps, F tiles) {
   if (const int forced = env_tile()) {
-    for (int t : {kTile256, kTile128})
+    for (int t = 0; t < kTileCount; ++t)
       if (kTiles[t].bm == forced && pipe_kernel(unit, t) != nullptr) return t;
     return -1;
   }
-  for (int t : {kTile256, kTile128})
-    if (pipe_kernel(unit, t) != nullptr && tiles(kTiles[t].bm, kTiles[t].bn) >= 128) return t;
-  return -1;
+  const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 ? kStep8Exact : kStep8;
+  int best = -1;
+  double least = 0;
+  for (int t = 0; t < kTileCount; ++t) {
+    if (pipe_kernel(unit, t) == nullptr) continue;
+    const double n = std::ceil(tiles(kTiles[t].bm, kTiles[t].bn) / 256.0);
+    // every tile's own prologue and epilogue cost it about two steps
+    const double us = (steps + 2) * std::max(n * cost[t].full,
+                                             std::ceil(n / kFit[t]) * cost[t].alone);
+    if (best < 0 || us < least) best = t, least = us;
+  }
+  return best;
 }
+
+// Tiles of a row product to expect: every group with rows leaves half a tile row unused.
+static double expected_rows(const LpArgs& a, double bm, double bn) {
+  const double m = a.offsets == nullptr
+                       ? std::ceil(a.rows / bm)
+                       : std::max<double>(a.rows / bm + 0.5 * std::min(a.E, a.rows), 1.0);
+  return m * std::ceil(a.N / bn);
+}
+static double k_steps(int64_t k, int bytes) { return std::ceil((double)k * bytes / kRowBytes); }
 
 static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
                         int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* QT,
@@ -232,7 +265,8 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? (b_block == 1 ? 11 : 10) : 9;
   if (word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1) && ldsa <= (1 << 22) &&
       ldsb <= (1 << 22)) {
-    const int t = pick_tile(unit, [&](int bm, int bn) { return row_tiles(a, bm, bn); });
+    const int t = pick_tile(unit, k_steps(K, 1),
+                            [&](int bm, int bn) { return expected_rows(a, bm, bn); });
     if (t >= 0)
       return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
                          stream);
@@ -272,7 +306,8 @@ static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int3
   a.c_type = type;
   const int unit = 3 * type + (transpose_w ? 0 : 1);
   if (word_rows(X, ldx, 0, b) && word_rows(W, ldw, stride_w, b)) {
-    const int t = pick_tile(unit, [&](int bm, int bn) { return row_tiles(a, bm, bn); });
+    const int t = pick_tile(unit, k_steps(K, b),
+                            [&](int bm, int bn) { return expected_rows(a, bm, bn); });
     if (t >= 0)
       return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
                          stream);
@@ -315,8 +350,8 @@ static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_
   a.c_type = type;
   const int unit = 3 * type + 2;
   if (word_rows(A, lda, 0, b) && word_rows(B, ldb, 0, b)) {
-    const int t = pick_tile(unit, [&](int64_t bm, int64_t bn) {
-      return (M + bm - 1) / bm * ((N + bn - 1) / bn) * E;
+    const int t = pick_tile(unit, k_steps((rows + E - 1) / E, b), [&](int64_t bm, int64_t bn) {
+      return (double)((M + bm - 1) / bm * ((N + bn - 1) / bn) * E);
     });
     if (t >= 0)
       return launch_wgrad(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,

@@ -21,11 +21,6 @@
 
 namespace gemmlp {
 
-template <int OPEN>  // copies that may still be open
-__device__ __forceinline__ void part_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(OPEN) : "memory");
-}
-
 template <class T, bool AKC, bool BKC, bool WGRAD, int HOW>
 __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
@@ -218,7 +213,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     if (steps > 1) step(One{}, steps - 2);
     step(None{}, steps - 1);
   }
-  store_tile<T, BKC>(p, w, wn, g, acc, [&](int i) {
+  store_tile<OB>(p, w, wn, g, acc, [&](int i) {
     return w.m0 + wm * WTM + (i / SH) * HALF + OA::row_of(i % SH, l16);
   });
 }

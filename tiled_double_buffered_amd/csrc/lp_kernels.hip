@@ -25,6 +25,7 @@ static LpKernel pick(int tile) {
       return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 256, 256, 2, 4, U::HOW>;
   }
   if (tile == kTile128) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 128, 128, 2, 2, U::HOW>;
+  if (tile == kTile64) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 64, 64, 2, 2, U::HOW>;
   return nullptr;
 }
 

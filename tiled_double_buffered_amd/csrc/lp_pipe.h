@@ -1,6 +1,6 @@
 // The product kernel for operands whose rows start at multiples of 4 bytes: tiles go from
 // memory straight into LDS (gfx950's direct-to-LDS loads), two slots in turn, one barrier a
-// K step.
+// K step.  (Three or four slots, with fewer workgroups on a CU, were 1.1 to 1.4 times slower.)
 //
 // A K step is 128 bytes of every row where k is contiguous (128 8-bit, 64 16-bit, 32 32-bit
 // values), so that all types share one LDS layout:
@@ -8,11 +8,11 @@
 //     so that the 16 rows a fragment reads at one c fall into 16 different groups of banks;
 //   rows contiguous (the operand's k is the slow axis), 16-bit: k rows of R values, read
 //     through the transposing LDS load, which hands each lane four k of one column; the 32
-//     bytes of 16 columns at position j lie at j ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2), so
-//     that the eight k rows that half a wave reads fall into different banks;
-//   rows contiguous, 32-bit: k rows of R values as they are; a lane reads four neighbouring
-//     columns of one k, which are four 16-column fragments, column 4 i + q the i-th of the
-//     q-th, and the epilogue undoes that order.
+//     bytes of 16 columns at position j lie at j ^ f(k), so that the eight k rows that half a
+//     wave reads (k mod 4 and k / 8 mod 2 vary) fall into different banks;
+//   rows contiguous, 32-bit: k rows of R values as they are; a lane reads four (two)
+//     neighbouring columns of one k, which are as many 16-column fragments, column 4 i + q the
+//     i-th of the q-th, and the epilogue undoes that order.
 // The copies write LDS in lane order, so each lane fetches what belongs at its place.
 //
 // Accumulators are transposed (D's rows are columns of C): a lane holds four neighbouring
@@ -63,9 +63,10 @@ __device__ __forceinline__ void copy4(uint32_t lds, int4v r, uint32_t off) {
 }
 #pragma clang diagnostic pop
 
-// This wave's copies have landed and its reads are done; then all waves' are.
-__device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// All but OPEN of this wave's copies have landed and its reads are done; then all waves' are.
+template <int OPEN>
+__device__ __forceinline__ void part_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(OPEN) : "memory");
 }
 
 // One operand: R rows (of A or columns of B) a tile, WT of them a wave.  GAP: the part holds WT
@@ -75,10 +76,16 @@ struct PipeOperand {
   static constexpr int BYTES = R * kRowBytes;  // of a slot, either order
   static constexpr int COPIES = R / 8 / WAVES;
   static constexpr int SUB = WT / 16;
+  static constexpr int READ = KC || T::BYTES != 4 ? 1 : SUB >= 4 ? 4 : 2;  // see read()
+  static_assert(SUB % READ == 0, "whole groups of columns");
   static constexpr int KS = kRowBytes / T::BYTES;
   static constexpr int K_ROW = R * T::BYTES;   // bytes of a k row (rows contiguous)
   static_assert(COPIES * WAVES * 8 == R, "whole copies");
-  static_assert(KC || T::BYTES == 4 || R >= 128, "f(k) needs eight positions");
+  static_assert(KC || T::BYTES == 4 || R >= 64, "f(k) needs four positions");
+  static __device__ __forceinline__ int swizzle(int k) {
+    if constexpr (R >= 128) return (k & 3) | ((k >> 3) & 1) << 2;
+    return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;  // two k rows share the 256 bytes of the banks
+  }
 
   static __device__ __forceinline__ int tile_row(int r) { return r + r / WT * GAP; }
 
@@ -112,7 +119,7 @@ struct PipeOperand {
         const int at = j * 1024 + lane * 16, k = at / K_ROW, in = at % K_ROW;
         const int from = T::BYTES == 4
                              ? in
-                             : ((((in >> 5) ^ ((k & 3) | ((k >> 3) & 1) << 2)) << 5) | (in & 31));
+                             : ((((in >> 5) ^ swizzle(k)) << 5) | (in & 31));
         off[i] = (uint32_t)(k * ldb) +
                  (uint32_t)(tile_row(from / T::BYTES) * T::BYTES + from % T::BYTES);
       }
@@ -123,9 +130,9 @@ struct PipeOperand {
       lane_at[0] = (uint32_t)((w0 + l16) * kRowBytes + ((g ^ sw) << 4));
       lane_at[1] = (uint32_t)((w0 + l16) * kRowBytes + (((g + 4) ^ sw) << 4));
     } else if constexpr (T::BYTES == 4) {
-      lane_at[0] = (uint32_t)(4 * g * K_ROW + (w0 + 4 * l16) * 4);
+      lane_at[0] = (uint32_t)(4 * g * K_ROW + (w0 + READ * l16) * 4);
     } else {
-      const int k = 8 * g + (l16 >> 2), f = (k & 3) | ((k >> 3) & 1) << 2;
+      const int k = 8 * g + (l16 >> 2), f = swizzle(k);
 #pragma unroll
       for (int j = 0; j < SUB; ++j)
         lane_at[j] = (uint32_t)(k * K_ROW + ((((w0 >> 4) + j) ^ f) << 5) + (l16 & 3) * 8);
@@ -145,8 +152,7 @@ struct PipeOperand {
   }
 
   // Both halves of a K step, 16 bytes of k a lane each, for fragment i (of 16 rows), or for
-  // the four fragments from i on where a lane reads four columns at once.
-  static constexpr int READ = KC || T::BYTES != 4 ? 1 : 4;
+  // the READ fragments from i on where a lane reads several columns at once.
   __device__ __forceinline__ void read(const char* slot, int i, int8v* f) const {
     if constexpr (KC) {
       f[0] = both(*(const int4v*)(slot + lane_at[0] + i * 16 * kRowBytes),
@@ -155,9 +161,10 @@ struct PipeOperand {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const char* at = slot + lane_at[0] + q * K_ROW + 64 * i;
-        const int4v u = *(const int4v*)at, v = *(const int4v*)(at + 16 * K_ROW);
+        typedef int group __attribute__((ext_vector_type(READ)));
+        const group u = *(const group*)at, v = *(const group*)(at + 16 * K_ROW);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < READ; ++x) {
           f[x][q] = u[x];
           f[x][4 + q] = v[x];
         }
@@ -178,8 +185,7 @@ struct PipeOperand {
   }
   // The row that fragment i's row x of the wave's is.
   static __device__ __forceinline__ int row_of(int i, int x) {
-    if constexpr (!KC && T::BYTES == 4) return 64 * (i >> 2) + 4 * x + (i & 3);
-    return 16 * i + x;
+    return 16 * (i - i % READ) + READ * x + i % READ;
   }
   // The last K step holds k_bytes of each row: clear the rest, which came from beyond the row.
   static __device__ __forceinline__ void clear_tail(char* slot, int k_bytes, int tid, int threads) {
@@ -237,10 +243,8 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
   w.c_base = 0;
   if constexpr (WGRAD) {
     const int tiles_m = (p.M + BM - 1) / BM, per = tiles_m * p.tiles_n;
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    w.e = id / per;
     int tm, tn;
-    band_order(id - w.e * per, tiles_m, p.tiles_n, tm, tn);
+    wgrad_tile(blockIdx.x, per, tiles_m, p.tiles_n, w.e, tm, tn);
     const int lo = clamped_offset(p.offsets, w.e, p.rows);
     const int hi = clamped_offset(p.offsets, w.e + 1, p.rows);
     w.A += (int64_t)lo * p.lda * T::BYTES;
@@ -298,7 +302,7 @@ struct ScaleCopy {
 };
 
 // One wave's accumulators into C.  m: C's row of fragment i for this lane.
-template <class T, bool BKC, int SM, int SN, class F>
+template <class OB, int SM, int SN, class F>
 __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int wn, int g,
                                            const float4v (&acc)[SM][SN], F row) {
   const int cb = type_bytes(p.c_type);
@@ -311,16 +315,15 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
     const int64_t at = w.c_base + (int64_t)m * p.ldc;
 #pragma unroll
     for (int j = 0; j < SN; ++j) {
-      if constexpr (!BKC && T::BYTES == 4) {
-        // fragments 4 q .. 4 q + 3, register r: columns 64 q + 16 g + 4 r .. + 3
-        const int q = j >> 2, r = j & 3, n = w.n0 + wn + 64 * q + 16 * g + 4 * r;
-        const float4v v = {acc[i][4 * q][r], acc[i][4 * q + 1][r], acc[i][4 * q + 2][r],
-                           acc[i][4 * q + 3][r]};
-        store4(p.C, at + n, p.N - n, vec, p.c_type, v);
-      } else {
-        const int n = w.n0 + wn + 16 * j + 4 * g;
-        store4(p.C, at + n, p.N - n, vec, p.c_type, acc[i][j]);
-      }
+      // of READ fragments from j0 on, a lane has 4 READ neighbouring columns, fragment by
+      // fragment in each register: the j - j0 th four of them
+      constexpr int READ = OB::READ;
+      const int q = j % READ, j0 = j - q;
+      float4v v;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = acc[i][j0 + (4 * q + x) % READ][(4 * q + x) / READ];
+      const int n = w.n0 + wn + 16 * j0 + 4 * READ * g + 4 * q;
+      store4(p.C, at + n, p.N - n, vec, p.c_type, v);
     }
   }
 }
@@ -371,7 +374,7 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
 
     issue(0, 0);
     for (int kt = 0; kt < steps; ++kt) {
-      step_barrier();
+      part_barrier<0>();
       if (kt + 1 < steps) issue(kt + 1, (kt + 1) & 1);
       char* sa = lds + (kt & 1) * SLOT;
       char* sb = sa + OA::BYTES;
@@ -451,7 +454,7 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
     }
   }
 
-  store_tile<T, BKC>(p, w, wn, g, acc,
+  store_tile<OB>(p, w, wn, g, acc,
                      [&](int i) { return w.m0 + wm + OA::row_of(i, l16); });
 }
 

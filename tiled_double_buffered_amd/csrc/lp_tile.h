@@ -85,10 +85,8 @@ __global__ __launch_bounds__(256) void lp_tile_kernel(LpArgs p) {
   int m0, m_end, n0, e, k_end;
   if constexpr (WGRAD) {
     const int tiles_m = (p.M + 63) / 64, per = tiles_m * p.tiles_n;
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    e = id / per;
     int tm, tn;
-    band_order(id - e * per, tiles_m, p.tiles_n, tm, tn);
+    wgrad_tile(blockIdx.x, per, tiles_m, p.tiles_n, e, tm, tn);
     const int lo = clamped_offset(p.offsets, e, p.rows);
     const int hi = clamped_offset(p.offsets, e + 1, p.rows);
     A += (int64_t)lo * p.lda;

@@ -7,11 +7,11 @@
 namespace gemmlp {
 
 // Tiles of the pipelined kernel.
-enum { kTile256 = 0, kTile128 = 1 };
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileCount = 3 };
 struct TileSize {
   int bm, bn, threads;
 };
-constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}};
+constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}, {64, 64, 256}};
 
 template <class T, bool A, bool B, bool W, int H>
 struct Unit {
