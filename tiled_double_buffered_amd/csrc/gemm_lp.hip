@@ -155,11 +155,13 @@ static int pick_tile(int unit, double steps, F tiles) {
   return best;
 }
 
-// Tiles of a row product to expect: every group with rows leaves half a tile row unused.
+// Tiles of a row product to expect: every group with rows leaves half a tile row unused (a
+// quarter where the tile is computed in halves).
 static double expected_rows(const LpArgs& a, double bm, double bn) {
+  const double waste = bm == 256 ? 0.25 : 0.5;
   const double m = a.offsets == nullptr
                        ? std::ceil(a.rows / bm)
-                       : std::max<double>(a.rows / bm + 0.5 * std::min(a.E, a.rows), 1.0);
+                       : std::max<double>(a.rows / bm + waste * std::min(a.E, a.rows), 1.0);
   return m * std::ceil(a.N / bn);
 }
 static double k_steps(int64_t k, int bytes) { return std::ceil((double)k * bytes / kRowBytes); }

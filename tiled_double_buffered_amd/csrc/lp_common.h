@@ -163,7 +163,10 @@ __device__ __forceinline__ void wgrad_tile(int wg, int per, int tiles_m, int til
 // number of tiles that any offsets can give; the count that these give is found here, by
 // every wave for itself, 64 groups at a time, and the workgroups past it return false.
 // Group 0 is the rows before offsets[0], group E + 1 the ones from offsets[E] on.
-__device__ inline bool find_tile(const LpArgs& p, int BM, int wg, int nwg, TileAt& t) {
+// HALF > 0: a group's last tile costs half where it has HALF rows or fewer, and all such tiles
+// come after the others, to fill the last round.
+template <int BM, int HALF>
+__device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   int tm;
   if (p.offsets == nullptr) {
     const int tiles_m = (p.rows + BM - 1) / BM, n = tiles_m * p.tiles_n;
@@ -176,43 +179,56 @@ __device__ inline bool find_tile(const LpArgs& p, int BM, int wg, int nwg, TileA
   }
   const int lane = threadIdx.x & 63;
   const int groups = p.E + 2;
-  int total = 0, lo = 0, hi = 0, incl = 0;
-  auto load = [&](int base) {  // this lane's group and the running tile count up to it
+  int lo = 0, hi = 0, whole = 0, part = 0;  // this lane's group, running counts up to it
+  auto load = [&](int base) {
     const int g = base + lane;
     lo = hi = 0;
     if (g < groups) {
       lo = g == 0 ? 0 : clamped_offset(p.offsets, g - 1, p.rows);
       hi = g == p.E + 1 ? p.rows : clamped_offset(p.offsets, g, p.rows);
     }
-    incl = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    const int len = max(hi - lo, 0), rest = len % BM;
+    part = rest > 0 && rest <= HALF ? 1 : 0;
+    whole = len / BM + (rest > 0 ? 1 : 0) - part;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(incl, d);
-      if (lane >= d) incl += up;
+      const int w = __shfl_up(whole, d), q = __shfl_up(part, d);
+      if (lane >= d) whole += w, part += q;
     }
   };
+  int wholes = 0, parts = 0;
   for (int base = 0; base < groups; base += 64) {
     load(base);
-    total += __shfl(incl, 63);
+    wholes += __shfl(whole, 63);
+    parts += __shfl(part, 63);
   }
-  const int n = (int)min((int64_t)total * p.tiles_n, (int64_t)nwg);
-  if (wg >= n) return false;
-  int id = xcd_order(wg, n);
+  const int nw = (int)min((int64_t)wholes * p.tiles_n, (int64_t)nwg);
+  const int np = (int)min((int64_t)parts * p.tiles_n, (int64_t)(nwg - nw));
+  if (wg >= nw + np) return false;
+  const bool small = wg >= nw;
+  int id = small ? xcd_order(wg - nw, np) : xcd_order(wg, nw);
   for (int base = 0; base < groups; base += 64) {
     if (groups > 64) load(base);
-    const uint64_t past = __ballot((int64_t)incl * p.tiles_n > id);
+    const int upto = small ? part : whole;
+    const uint64_t past = __ballot((int64_t)upto * p.tiles_n > id);
     if (past) {
       const int l = __builtin_ctzll(past);
-      const int before = l ? __shfl(incl, l - 1) : 0;
-      const int count = __shfl(incl, l) - before;
+      const int before = l ? __shfl(upto, l - 1) : 0;
+      const int first = __shfl(lo, l);
       const int g = base + l;
-      band_order(id - before * p.tiles_n, count, p.tiles_n, tm, t.tn);
       t.e = g == 0 || g == p.E + 1 ? -1 : g - 1;
-      t.row0 = __shfl(lo, l) + tm * BM;
       t.row_end = __shfl(hi, l);
+      id -= before * p.tiles_n;
+      if (small) {
+        t.tn = id;
+        t.row0 = first + (t.row_end - first) / BM * BM;
+      } else {
+        band_order(id, __shfl(upto, l) - before, p.tiles_n, tm, t.tn);
+        t.row0 = first + tm * BM;
+      }
       return true;
     }
-    id -= __shfl(incl, 63) * p.tiles_n;
+    id -= __shfl(upto, 63) * p.tiles_n;
   }
   return false;
 }
@@ -245,6 +261,24 @@ __device__ __forceinline__ void store4(void* C, int64_t at, int n, bool vec, int
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < n) p[i] = h[i];
+  }
+}
+
+// Eight neighbouring 16-bit values.
+__device__ __forceinline__ void store8(void* C, int64_t at, int n, bool vec, int type, float4v u,
+                                       float4v v) {
+  if (vec && n >= 8) {
+    uint16_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = i < 4 ? u[i] : v[i - 4];
+      h[i] = type == GEMM_LP_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x)
+                                  : __builtin_bit_cast(uint16_t, (_Float16)x);
+    }
+    __builtin_memcpy(__builtin_assume_aligned((uint16_t*)C + at, 16), h, 16);
+  } else {
+    store4(C, at, n, false, type, u);
+    store4(C, at + 4, n - 4, false, type, v);
   }
 }
 

@@ -4,13 +4,14 @@
 // The kernel of lp_pipe.h starts a step's copies when the slot's last reader is done and needs
 // them one step later, and waits for them (8 bits: 40 % of all wave cycles).  Here each slot has
 // three parts that are freed at different times: B, which a wave holds in registers for the
-// whole step, the half A1 of A's rows that the step's first products read, and the other half
-// A2.  A step has two barriers:
+// whole step, the upper half A1 of A's rows, which the step's first products read, and the
+// lower half A2.  A step has two barriers:
 //   middle (before the products of the last A1 fragment): B, A1 of this step are read by all
 //     waves, A2 of this step has landed; the copies of B, A1 (and scales) two steps on start;
 //   end (before the products of the last A2 fragment): A2 of this step is read, B and A1 of
 //     the next have landed; the copies of A2 two steps on start, and the next step's first
 //     fragments are read while this step's last products run.
+// A tile of 128 rows or fewer leaves A2 and its products out.
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
 #pragma once
@@ -27,8 +28,9 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
   constexpr bool F8T = T::BYTES == 1;
   static_assert(!F8T || HOW != kExact8, "not enough registers");
-  using OA = PipeOperand<T, AKC, BM / 2, HALF, WAVES, HALF>;
-  using OB = PipeOperand<T, BKC, BN, WTN, WAVES>;
+  constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
+  using OA = PipeOperand<T, AKC, BM / 2, HALF, WAVES>;
+  using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
   constexpr int SCALES = F8T ? (BM + BN) * 4 : 0;
   constexpr int A1 = 0, A2 = OA::BYTES, B0 = 2 * OA::BYTES, S0 = B0 + OB::BYTES;
   constexpr int SLOT = S0 + SCALES;
@@ -39,8 +41,10 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   const int l16 = lane & 15, g = lane >> 4;
 
   TileOf w;
-  if (!locate<T, WGRAD, BM, BN>(p, w)) return;
+  if (!locate<T, WGRAD, BM, BN, BM / 2>(p, w)) return;
   const int wm = wave / WN, wn = (wave % WN) * WTN;
+  // the tile's row of this lane in fragment i
+  auto row_of = [&](int i) { return (i / SH) * (BM / 2) + wm * HALF + OA::row_of(i % SH, l16); };
 
   float4v acc[SM][SN] = {};
   const int steps = (w.k_end + OA::KS - 1) / OA::KS;
@@ -48,7 +52,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     OA oa1, oa2;
     OB ob;
     oa1.init(w.A, p.lda, w.m0, w.m_end, w.k_end, wave, lane, wm * HALF);
-    oa2.init(w.A, p.lda, w.m0 + HALF, w.m_end, w.k_end, wave, lane, wm * HALF);
+    oa2.init(w.A, p.lda, w.m0 + BM / 2, w.m_end, w.k_end, wave, lane, wm * HALF);
     ob.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane, wn);
     const uint32_t lds0 =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
@@ -89,14 +93,14 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       if constexpr (F8T) {
         const float* s = (const float*)(slot + S0);
 #pragma unroll
-        for (int i = 0; i < SM; ++i) s_a[i] = s[wm * WTM + 16 * i + l16];
+        for (int i = 0; i < SM; ++i) s_a[i] = s[row_of(i)];
         if constexpr (HOW == kFast8Blocks) {
           const float block = s[BM + wn];
 #pragma unroll
           for (int i = 0; i < SM; ++i) s_a[i] *= block;
         } else {
 #pragma unroll
-          for (int j = 0; j < SN; ++j) s_b[j] = *(const float4v*)(s + BM + wn + 16 * j + 4 * g);
+          for (int j = 0; j < SN; ++j) s_b[j] = *(const float4v*)(s + BM + wn + OB::row_of(j, 4 * g));
         }
       }
     };
@@ -104,18 +108,19 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     // matrix cores work on the next ones.
     constexpr int kLag = 2, kRing = 3;
     float4v d[kRing];
-    auto product = [&](int s) {  // product s = i * SN + j of the step
-      const int i = s / SN, j = s % SN, f = set_of(i);
+    auto product_of = [&](int s, const int8v& fa) {  // product s = i * SN + j of the step
+      const int i = s / SN, j = s % SN;
       if constexpr (F8T) {
         const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
         d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            b[j], a[f], z, 0, 0, 0, 0, 0, 0);
+            b[j], fa, z, 0, 0, 0, 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       } else {
-        acc[i][j] = mma_half<T>(half_of(b[j], 0), half_of(a[f], 0), acc[i][j]);
-        acc[i][j] = mma_half<T>(half_of(b[j], 1), half_of(a[f], 1), acc[i][j]);
+        acc[i][j] = mma_half<T>(half_of(b[j], 0), half_of(fa, 0), acc[i][j]);
+        acc[i][j] = mma_half<T>(half_of(b[j], 1), half_of(fa, 1), acc[i][j]);
       }
     };
+    auto product = [&](int s) { product_of(s, a[set_of(s / SN)]); };
     auto add = [&](int s) {
       if constexpr (F8T) {
         if (s < 0) return;
@@ -196,6 +201,42 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     using One = std::integral_constant<int, 1>;
     using None = std::integral_constant<int, 0>;
 
+    if (w.m_end - w.m0 <= BM / 2) {
+      // Half a tile: the step's fragments go into registers at once, which frees the slot.
+      issue_first(0);
+      if (steps > 1) issue_first(1);
+      int8v h[SH];
+      for (int kt = 0; kt < steps; ++kt) {
+        const char* slot = lds + (kt & 1) * SLOT;
+        if (kt + 1 < steps) part_barrier<FIRST>();
+        else part_barrier<0>();
+#pragma unroll
+        for (int j = 0; j < SN; j += OB::READ) ob.read(slot + B0, j, b + j);
+#pragma unroll
+        for (int i = 0; i < SH; i += OA::READ) oa1.read(slot + A1, i, h + i);
+        read_scales(slot);
+        part_barrier<63>();  // (the copies stay open)
+        if (kt + 2 < steps) issue_first(kt + 2);
+        if (kt + 1 == steps) {
+          if constexpr (AKC) {
+#pragma unroll
+            for (int i = 0; i < SH; ++i) h[i] &= last_mask;
+          }
+          if constexpr (BKC) {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) b[j] &= last_mask;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < SH * SN + kLag; ++s) {
+          if (s < SH * SN) product_of(s, h[s / SN]);
+          if (s >= kLag) add(s - kLag);
+        }
+      }
+      store_tile<OB>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
+      return;
+    }
+
     issue_first(0);
     issue_second(0);
     if (steps > 1) {
@@ -213,9 +254,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     if (steps > 1) step(One{}, steps - 2);
     step(None{}, steps - 1);
   }
-  store_tile<OB>(p, w, wn, g, acc, [&](int i) {
-    return w.m0 + wm * WTM + (i / SH) * HALF + OA::row_of(i % SH, l16);
-  });
+  store_tile<OB>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
 }
 
 }  // namespace gemmlp

@@ -4,8 +4,7 @@
 //
 // A K step is 128 bytes of every row where k is contiguous (128 8-bit, 64 16-bit, 32 32-bit
 // values), so that all types share one LDS layout:
-//   k contiguous: rows of 128 bytes; the 16-byte group c of row r lies at c ^ (r / 2 mod 8),
-//     so that the 16 rows a fragment reads at one c fall into 16 different groups of banks;
+//   k contiguous: rows of 128 bytes whose 16-byte groups change places from row to row;
 //   rows contiguous (the operand's k is the slow axis), 16-bit: k rows of R values, read
 //     through the transposing LDS load, which hands each lane four k of one column; the 32
 //     bytes of 16 columns at position j lie at j ^ f(k), so that the eight k rows that half a
@@ -69,15 +68,18 @@ __device__ __forceinline__ void part_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(OPEN) : "memory");
 }
 
-// One operand: R rows (of A or columns of B) a tile, WT of them a wave.  GAP: the part holds WT
-// rows of every WT + GAP of the tile's (half of an operand, the same half for every wave).
-template <class T, bool KC, int R, int WT, int WAVES, int GAP = 0>
+// One operand: R rows (of A or columns of B) a tile, WT of them a wave.
+// PACK (B, where C has 16 bits): the columns are spread over the fragments so that a lane's
+// accumulators of two fragments are eight neighbouring columns, one 16-byte store.
+template <class T, bool KC, int R, int WT, int WAVES, bool PACK = false>
 struct PipeOperand {
   static constexpr int BYTES = R * kRowBytes;  // of a slot, either order
   static constexpr int COPIES = R / 8 / WAVES;
   static constexpr int SUB = WT / 16;
   static constexpr int READ = KC || T::BYTES != 4 ? 1 : SUB >= 4 ? 4 : 2;  // see read()
   static_assert(SUB % READ == 0, "whole groups of columns");
+  static constexpr bool PACKED = PACK;
+  static_assert(!PACK || (READ == 1 && SUB % 2 == 0), "pairs of fragments");
   static constexpr int KS = kRowBytes / T::BYTES;
   static constexpr int K_ROW = R * T::BYTES;   // bytes of a k row (rows contiguous)
   static_assert(COPIES * WAVES * 8 == R, "whole copies");
@@ -86,8 +88,6 @@ struct PipeOperand {
     if constexpr (R >= 128) return (k & 3) | ((k >> 3) & 1) << 2;
     return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;  // two k rows share the 256 bytes of the banks
   }
-
-  static __device__ __forceinline__ int tile_row(int r) { return r + r / WT * GAP; }
 
   uint32_t off[COPIES];  // of this lane's 16 bytes from the tile's first
   const char* base;
@@ -113,29 +113,31 @@ struct PipeOperand {
       const int j = wave + i * WAVES;
       if constexpr (KC) {
         const int row = j * 8 + lane / 8;
-        off[i] = (uint32_t)(tile_row(row) * ldb) +
-                 (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+        off[i] = (uint32_t)(row * ldb) + (uint32_t)(((lane & 7) ^ place(row)) * 16);
       } else {
         const int at = j * 1024 + lane * 16, k = at / K_ROW, in = at % K_ROW;
         const int from = T::BYTES == 4
                              ? in
                              : ((((in >> 5) ^ swizzle(k)) << 5) | (in & 31));
-        off[i] = (uint32_t)(k * ldb) +
-                 (uint32_t)(tile_row(from / T::BYTES) * T::BYTES + from % T::BYTES);
+        off[i] = (uint32_t)(k * ldb) + (uint32_t)from;
       }
     }
     const int l16 = lane & 15, g = lane >> 4;
     if constexpr (KC) {
-      const int sw = (l16 >> 1) & 7;
-      lane_at[0] = (uint32_t)((w0 + l16) * kRowBytes + ((g ^ sw) << 4));
-      lane_at[1] = (uint32_t)((w0 + l16) * kRowBytes + (((g + 4) ^ sw) << 4));
+      const int r = w0 + row_of(0, l16), sw = place(r);
+      lane_at[0] = (uint32_t)(r * kRowBytes + ((g ^ sw) << 4));
+      lane_at[1] = (uint32_t)(r * kRowBytes + (((g + 4) ^ sw) << 4));
     } else if constexpr (T::BYTES == 4) {
       lane_at[0] = (uint32_t)(4 * g * K_ROW + (w0 + READ * l16) * 4);
     } else {
       const int k = 8 * g + (l16 >> 2), f = swizzle(k);
 #pragma unroll
       for (int j = 0; j < SUB; ++j)
-        lane_at[j] = (uint32_t)(k * K_ROW + ((((w0 >> 4) + j) ^ f) << 5) + (l16 & 3) * 8);
+      {
+        // lane l16 fetches columns row_of(j, 4 (l16 mod 4)) .. + 3 of its k row
+        const int c = w0 + row_of(j, 4 * (l16 & 3));
+        lane_at[j] = (uint32_t)(k * K_ROW + (((c >> 4) ^ f) << 5) + (c & 15) * 2);
+      }
     }
   }
 
@@ -155,8 +157,9 @@ struct PipeOperand {
   // the READ fragments from i on where a lane reads several columns at once.
   __device__ __forceinline__ void read(const char* slot, int i, int8v* f) const {
     if constexpr (KC) {
-      f[0] = both(*(const int4v*)(slot + lane_at[0] + i * 16 * kRowBytes),
-                  *(const int4v*)(slot + lane_at[1] + i * 16 * kRowBytes));
+      // (the same place in every fragment: place() has row_of(i, 0)'s bits out)
+      f[0] = both(*(const int4v*)(slot + lane_at[0] + row_of(i, 0) * kRowBytes),
+                  *(const int4v*)(slot + lane_at[1] + row_of(i, 0) * kRowBytes));
     } else if constexpr (T::BYTES == 4) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -185,14 +188,21 @@ struct PipeOperand {
   }
   // The row that fragment i's row x of the wave's is.
   static __device__ __forceinline__ int row_of(int i, int x) {
+    if constexpr (PACK) return 32 * (i >> 1) + 8 * (x >> 2) + 4 * (i & 1) + (x & 3);
     return 16 * (i - i % READ) + READ * x + i % READ;
+  }
+  // Where k is contiguous: the 16-byte group c of row r lies at c ^ place(r).  The 16 rows of a
+  // fragment at one c then fall into 16 different groups of banks (two rows share 256 bytes).
+  static __device__ __forceinline__ int place(int r) {
+    if constexpr (PACK) return ((r >> 1) & 1) | ((r >> 3) & 3) << 1;
+    return (r >> 1) & 7;
   }
   // The last K step holds k_bytes of each row: clear the rest, which came from beyond the row.
   static __device__ __forceinline__ void clear_tail(char* slot, int k_bytes, int tid, int threads) {
     for (int t = tid; t < R * 8; t += threads) {
       const int row = t >> 3, c = t & 7, n = k_bytes - 16 * c;
       if (n >= 16) continue;
-      int4v* at = (int4v*)(slot + row * kRowBytes + ((c ^ ((row >> 1) & 7)) << 4));
+      int4v* at = (int4v*)(slot + row * kRowBytes + ((c ^ place(row)) << 4));
       int4v v = {0, 0, 0, 0};
       if (n > 0) {
         v = *at;
@@ -236,7 +246,7 @@ struct TileOf {
   int64_t c_base;
   int m0, m_end, n0, e, k_end;
 };
-template <class T, bool WGRAD, int BM, int BN>
+template <class T, bool WGRAD, int BM, int BN, int HALF = 0>
 __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
   w.A = (const char*)p.A;
   w.B = (const char*)p.B;
@@ -256,7 +266,7 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
     w.c_base = w.e * p.stride_c;
   } else {
     TileAt t;
-    if (!find_tile(p, BM, blockIdx.x, gridDim.x, t)) return false;
+    if (!find_tile<BM, HALF>(p, blockIdx.x, gridDim.x, t)) return false;
     w.e = __builtin_amdgcn_readfirstlane(t.e);
     w.k_end = w.e < 0 ? 0 : p.K;
     if (w.e > 0) w.B += w.e * p.stride_b * T::BYTES;
@@ -306,24 +316,33 @@ template <class OB, int SM, int SN, class F>
 __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int wn, int g,
                                            const float4v (&acc)[SM][SN], F row) {
   const int cb = type_bytes(p.c_type);
+  constexpr int PER = OB::PACKED ? 8 : 4;
   const bool vec = (((uintptr_t)p.C | (uintptr_t)(p.ldc * cb) | (uintptr_t)(w.c_base * cb)) &
-                    (uintptr_t)(4 * cb - 1)) == 0;
+                    (uintptr_t)(PER * cb - 1)) == 0;
 #pragma unroll
   for (int i = 0; i < SM; ++i) {
     const int m = row(i);
     if (m >= w.m_end) continue;
     const int64_t at = w.c_base + (int64_t)m * p.ldc;
+    if constexpr (OB::PACKED) {
 #pragma unroll
-    for (int j = 0; j < SN; ++j) {
-      // of READ fragments from j0 on, a lane has 4 READ neighbouring columns, fragment by
-      // fragment in each register: the j - j0 th four of them
-      constexpr int READ = OB::READ;
-      const int q = j % READ, j0 = j - q;
-      float4v v;
+      for (int j = 0; j < SN; j += 2) {
+        const int n = w.n0 + wn + 16 * j + 8 * g;
+        store8(p.C, at + n, p.N - n, vec, p.c_type, acc[i][j], acc[i][j + 1]);
+      }
+    } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[x] = acc[i][j0 + (4 * q + x) % READ][(4 * q + x) / READ];
-      const int n = w.n0 + wn + 16 * j0 + 4 * READ * g + 4 * q;
-      store4(p.C, at + n, p.N - n, vec, p.c_type, v);
+      for (int j = 0; j < SN; ++j) {
+        // of READ fragments from j0 on, a lane has 4 READ neighbouring columns, fragment by
+        // fragment in each register: the j - j0 th four of them
+        constexpr int READ = OB::READ;
+        const int q = j % READ, j0 = j - q;
+        float4v v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = acc[i][j0 + (4 * q + x) % READ][(4 * q + x) / READ];
+        const int n = w.n0 + wn + 16 * j0 + 4 * READ * g + 4 * q;
+        store4(p.C, at + n, p.N - n, vec, p.c_type, v);
+      }
     }
   }
 }
@@ -337,7 +356,8 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
   constexpr bool F8T = T::BYTES == 1;
   using OA = PipeOperand<T, AKC, BM, WTM, WAVES>;
-  using OB = PipeOperand<T, BKC, BN, WTN, WAVES>;
+  constexpr bool PACK = T::BYTES == 2 || (F8T && HOW != kExact8);  // C has 16 bits
+  using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
   constexpr int SCALES = F8T ? (BM + BN) * 4 : 0;
   constexpr int SLOT = OA::BYTES + OB::BYTES + SCALES;
   __shared__ __align__(1024) char lds[2 * SLOT];
@@ -407,7 +427,7 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
         if constexpr (HOW != kFast8Blocks) {
 #pragma unroll
           for (int j = 0; j < SN; ++j)
-            s_b[j] = *(const float4v*)(scales + BM + wn + 16 * j + 4 * g);
+            s_b[j] = *(const float4v*)(scales + BM + wn + OB::row_of(j, 4 * g));
         }
 #pragma unroll
         for (int i = 0; i < SM; ++i) s_a[i] = scales[wm + 16 * i + l16];

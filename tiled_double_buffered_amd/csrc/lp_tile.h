@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void lp_tile_kernel(LpArgs p) {
     c_base = e * p.stride_c;
   } else {
     TileAt t;
-    if (!find_tile(p, 64, blockIdx.x, gridDim.x, t)) return;
+    if (!find_tile<64, 0>(p, blockIdx.x, gridDim.x, t)) return;
     e = t.e;
     k_end = e < 0 ? 0 : p.K;
     if (e > 0) B += e * p.stride_b;
