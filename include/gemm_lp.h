@@ -56,7 +56,8 @@ int gemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int64_t ldx, in
  * A: M x K e4m3fn, row stride lda; SA: M x ceil(K/128), row stride ldsa.
  * B: N x K e4m3fn, row stride ldb; SB: ceil(N/b_block) x ceil(K/128), row stride ldsb;
  * b_block is 1 or 128.  C: M x N of c_type, row stride ldc.  Any alignment of A and B.
- * The product sa * sb of two scales has to lie in FP32's normal range.
+ * The product sa * sb of two scales has to lie in FP32's normal range; ldsa and ldsb are below
+ * 2^22.
  * offsets == NULL: one product (E must be 1).  Otherwise E experts: expert e's B and SB
  * start e * stride_b bytes and e * stride_sb floats after the first's, and rows of no
  * expert are zeroed in C. */

@@ -77,6 +77,7 @@ def _fp8(M=4, N=200, K=300, E=1, off=None, A=PA, lda=300, SA=PS, ldsa=3, B=PB, l
     (dict(off=PO + 2), tdb.ERR_MISALIGNED), (dict(C=PB), tdb.ERR_ALIAS),
     (dict(C=PS), tdb.ERR_ALIAS), (dict(off=PC + 4), tdb.ERR_ALIAS),
     (dict(M=1 << 31), tdb.ERR_TOO_LARGE), (dict(lda=1 << 61), tdb.ERR_TOO_LARGE),
+    (dict(ldsa=1 << 22), tdb.ERR_TOO_LARGE), (dict(ldsb=1 << 22), tdb.ERR_TOO_LARGE),
     (dict(E=1 << 30, off=PO, sB=1 << 40), tdb.ERR_TOO_LARGE),
 ])
 def test_fp8_refusals(change, code):

@@ -33,7 +33,7 @@ SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",
                                             "dispatch_table.h", "mfma_peak.h",
-                                            "lp_common.h", "lp_quantize.h", "lp_tile.h",
+                                            "lp_common.h", "lp_quantize.h",
                                             "lp_pipe.h", "lp_deep.h", "lp_units.h")]
 DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h")]
 LIB = os.path.join(PKG, "libgemmf32.so")

@@ -10,13 +10,13 @@
 #include "gemm_lp.h"
 #include "lp_common.h"
 #include "lp_quantize.h"
-#include "lp_tile.h"
 #include "lp_units.h"
 
 namespace gemmlp {
 
 constexpr int64_t kMaxDim = 2147483647LL - 1024;  // keeps tile-end arithmetic in int32
 constexpr int64_t kMaxExtent = (int64_t)1 << 61;   // bytes one operand may span
+constexpr int64_t kMaxScaleLd = (int64_t)1 << 22;  // 256 rows of scales in 32-bit offsets
 
 // Byte range [lo, hi) of `count` blocks of rows x cols values of `bytes` bytes, row stride ld
 // and block stride `stride` (elements).  False where it passes kMaxExtent or wraps.
@@ -61,47 +61,42 @@ static int64_t row_tiles(const LpArgs& a, int64_t BM, int64_t BN) {
   return m * ((a.N + BN - 1) / BN);
 }
 
-static int launch_rows(LpKernel fn, LpArgs a, int BM, int BN, int threads, void* stream) {
-  const int64_t wgs = row_tiles(a, BM, BN);
-  if (wgs * threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
-  a.tiles_n = (a.N + BN - 1) / BN;
-  return launch((const void*)fn, dim3((unsigned)wgs), threads, &a, stream);
+static LpKernel pipe_kernel(int unit, int tile, bool staged) {
+  switch (unit) {
+    case 0: return pipe_kernel_0(tile, staged);
+    case 1: return pipe_kernel_1(tile, staged);
+    case 2: return pipe_kernel_2(tile, staged);
+    case 3: return pipe_kernel_3(tile, staged);
+    case 4: return pipe_kernel_4(tile, staged);
+    case 5: return pipe_kernel_5(tile, staged);
+    case 6: return pipe_kernel_6(tile, staged);
+    case 7: return pipe_kernel_7(tile, staged);
+    case 8: return pipe_kernel_8(tile, staged);
+    case 9: return pipe_kernel_9(tile, staged);
+    case 10: return pipe_kernel_10(tile, staged);
+    default: return pipe_kernel_11(tile, staged);
+  }
 }
 
-static int launch_wgrad(LpKernel fn, LpArgs a, int BM, int BN, int threads, void* stream) {
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+static int launch_rows(int unit, int tile, bool staged, LpArgs a, void* stream) {
+  const TileSize& s = kTiles[tile];
+  const int64_t wgs = row_tiles(a, s.bm, s.bn);
+  if (wgs * s.threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  a.tiles_n = (a.N + s.bn - 1) / s.bn;
+  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
+                stream);
+}
+
+static int launch_wgrad(int unit, int tile, bool staged, LpArgs a, void* stream) {
+  const TileSize& s = kTiles[tile];
+  const int64_t tm = (a.M + s.bm - 1) / s.bm, tn = (a.N + s.bn - 1) / s.bn;
   int64_t wgs;
   if (__builtin_mul_overflow(tm * tn, (int64_t)a.E, &wgs) || wgs > kMaxDim ||
-      wgs * threads > 0xFFFFFFFFLL)
+      wgs * s.threads > 0xFFFFFFFFLL)
     return GEMMF32_ERR_TOO_LARGE;
   a.tiles_n = (int)tn;
-  return launch((const void*)fn, dim3((unsigned)wgs), threads, &a, stream);
-}
-
-template <bool AKC, bool BKC, bool WGRAD>
-static LpKernel tile_kernel(int type) {
-  switch (type) {
-    case GEMM_LP_BF16: return &lp_tile_kernel<Bf16, AKC, BKC, WGRAD>;
-    case GEMM_LP_F16: return &lp_tile_kernel<F16, AKC, BKC, WGRAD>;
-    default: return &lp_tile_kernel<F32, AKC, BKC, WGRAD>;
-  }
-}
-
-static LpKernel pipe_kernel(int unit, int tile) {
-  switch (unit) {
-    case 0: return pipe_kernel_0(tile);
-    case 1: return pipe_kernel_1(tile);
-    case 2: return pipe_kernel_2(tile);
-    case 3: return pipe_kernel_3(tile);
-    case 4: return pipe_kernel_4(tile);
-    case 5: return pipe_kernel_5(tile);
-    case 6: return pipe_kernel_6(tile);
-    case 7: return pipe_kernel_7(tile);
-    case 8: return pipe_kernel_8(tile);
-    case 9: return pipe_kernel_9(tile);
-    case 10: return pipe_kernel_10(tile);
-    default: return pipe_kernel_11(tile);
-  }
+  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
+                stream);
 }
 
 // Whether an operand can be copied in words: rows and experts that start at multiples of four
@@ -111,11 +106,8 @@ static bool word_rows(const void* p, int64_t ld, int64_t stride, int bytes) {
          ld <= (int64_t)0xFFFF0000u / 256 / bytes;
 }
 
-// The tile of the pipelined kernel for a product of `tiles(BM, BN)` tiles, or -1: the general
-// kernel.
-//
-// GEMM_LP_TILE=<256|128|64|1> forces a tile where its kernel takes the operands (1: the general
-// kernel), for tests and measurement, as GEMMF32_VARIANT does for the FP32 product.
+// GEMM_LP_TILE=<256|128|64> forces a tile where it has a kernel, for tests and measurement, as
+// GEMMF32_VARIANT does for the FP32 product.
 static int env_tile() {
   const char* v = std::getenv("GEMM_LP_TILE");
   return v == nullptr ? 0 : std::atoi(v);
@@ -133,23 +125,24 @@ constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.5
 constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}};
 constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.30, 1.10}, {0.60, 0.36}};
 
-// The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number.
+// The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number,
+// and the longest of them has `skew` times the average's K steps.
 template <class F>
-static int pick_tile(int unit, double steps, F tiles) {
+static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) {
   if (const int forced = env_tile()) {
     for (int t = 0; t < kTileCount; ++t)
-      if (kTiles[t].bm == forced && pipe_kernel(unit, t) != nullptr) return t;
-    return -1;
+      if (kTiles[t].bm == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
   }
   const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 ? kStep8Exact : kStep8;
   int best = -1;
   double least = 0;
   for (int t = 0; t < kTileCount; ++t) {
-    if (pipe_kernel(unit, t) == nullptr) continue;
+    if (pipe_kernel(unit, t, staged) == nullptr) continue;
     const double n = std::ceil(tiles(kTiles[t].bm, kTiles[t].bn) / 256.0);
     // every tile's own prologue and epilogue cost it about two steps
-    const double us = (steps + 2) * std::max(n * cost[t].full,
-                                             std::ceil(n / kFit[t]) * cost[t].alone);
+    const double us = std::max({(steps + 2) * n * cost[t].full,
+                                (steps + 2) * std::ceil(n / kFit[t]) * cost[t].alone,
+                                (skew * steps + 2) * cost[t].alone});
     if (best < 0 || us < least) best = t, least = us;
   }
   return best;
@@ -233,7 +226,9 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   if (lda < at_least_1(K) || ldb < at_least_1(K) || ldc < at_least_1(N) ||
       ldsa < at_least_1(kb) || ldsb < at_least_1(kb) || stride_b < 0 || stride_sb < 0)
     return GEMMF32_ERR_BAD_LD;
-  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim || ldsa >= kMaxScaleLd ||
+      ldsb >= kMaxScaleLd)
+    return GEMMF32_ERR_TOO_LARGE;
   if (M == 0 || N == 0) return GEMMF32_OK;
   if (C == nullptr) return GEMMF32_ERR_NULL_PTR;
   const bool reads = K > 0 && E > 0;
@@ -265,15 +260,10 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
   // themselves; other results go through the 16-bit instruction, which cuts nothing.
   const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? (b_block == 1 ? 11 : 10) : 9;
-  if (word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1) && ldsa <= (1 << 22) &&
-      ldsb <= (1 << 22)) {
-    const int t = pick_tile(unit, k_steps(K, 1),
-                            [&](int bm, int bn) { return expected_rows(a, bm, bn); });
-    if (t >= 0)
-      return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
-                         stream);
-  }
-  return launch_rows(&lp_tile_kernel<F8, true, true, false>, a, 64, 64, 256, stream);
+  const bool staged = !(word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1));
+  const int t = pick_tile(unit, staged, k_steps(K, 1), 1.0,
+                          [&](int bm, int bn) { return expected_rows(a, bm, bn); });
+  return launch_rows(unit, t, staged, a, stream);
 }
 
 static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
@@ -307,16 +297,10 @@ static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int3
   a.rows = a.M = (int)rows, a.N = (int)N, a.K = (int)K, a.E = (int)E;
   a.c_type = type;
   const int unit = 3 * type + (transpose_w ? 0 : 1);
-  if (word_rows(X, ldx, 0, b) && word_rows(W, ldw, stride_w, b)) {
-    const int t = pick_tile(unit, k_steps(K, b),
-                            [&](int bm, int bn) { return expected_rows(a, bm, bn); });
-    if (t >= 0)
-      return launch_rows(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
-                         stream);
-  }
-  const LpKernel fn = transpose_w ? tile_kernel<true, true, false>(type)
-                                  : tile_kernel<true, false, false>(type);
-  return launch_rows(fn, a, 64, 64, 256, stream);
+  const bool staged = !(word_rows(X, ldx, 0, b) && word_rows(W, ldw, stride_w, b));
+  const int t = pick_tile(unit, staged, k_steps(K, b), 1.0,
+                          [&](int bm, int bn) { return expected_rows(a, bm, bn); });
+  return launch_rows(unit, t, staged, a, stream);
 }
 
 static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_t* offsets,
@@ -351,15 +335,13 @@ static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_
   a.rows = a.K = (int)rows, a.M = (int)M, a.N = (int)N, a.E = (int)E;
   a.c_type = type;
   const int unit = 3 * type + 2;
-  if (word_rows(A, lda, 0, b) && word_rows(B, ldb, 0, b)) {
-    const int t = pick_tile(unit, k_steps((rows + E - 1) / E, b), [&](int64_t bm, int64_t bn) {
-      return (double)((M + bm - 1) / bm * ((N + bn - 1) / bn) * E);
-    });
-    if (t >= 0)
-      return launch_wgrad(pipe_kernel(unit, t), a, kTiles[t].bm, kTiles[t].bn, kTiles[t].threads,
-                          stream);
-  }
-  return launch_wgrad(tile_kernel<false, false, true>(type), a, 64, 64, 256, stream);
+  const bool staged = !(word_rows(A, lda, 0, b) && word_rows(B, ldb, 0, b));
+  // (an expert with three times the average's rows is common)
+  const int t = pick_tile(unit, staged, k_steps((rows + E - 1) / E, b), E > 1 ? 3.0 : 1.0,
+                          [&](int64_t bm, int64_t bn) {
+                            return (double)((M + bm - 1) / bm * ((N + bn - 1) / bn) * E);
+                          });
+  return launch_wgrad(unit, t, staged, a, stream);
 }
 
 }  // namespace gemmlp

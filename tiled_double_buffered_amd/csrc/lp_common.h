@@ -233,52 +233,46 @@ __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   return false;
 }
 
-// Store four neighbouring values of one row: at most `n` of them are inside it.  `vec`: the
-// row's address and stride allow one store.  One rounding to the nearest, ties to even.
-__device__ __forceinline__ void store4(void* C, int64_t at, int n, bool vec, int type,
-                                       float4v v) {
+// Store neighbouring values of one row, of which `n` are inside it, in one store of any
+// alignment where all are.  One rounding to the nearest, ties to even.
+// OUT: the type, or -1 where it is only known as `any`.
+template <int COUNT, int OUT>
+__device__ __forceinline__ void store_row(void* C, int64_t at, int n, int any, const float* v) {
+  const int type = OUT >= 0 ? OUT : any;
   if (type == GEMM_LP_F32) {
+    typedef float group __attribute__((ext_vector_type(4), aligned(4)));
     float* p = (float*)C + at;
-    if (vec && n >= 4) {
-      *(float4v*)p = v;
+    if (n >= COUNT) {
+#pragma unroll
+      for (int i = 0; i < COUNT; i += 4) *(group*)(p + i) = group{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < COUNT; ++i)
         if (i < n) p[i] = v[i];
     }
     return;
   }
-  uint16_t h[4];
+  typedef uint32_t group __attribute__((ext_vector_type(COUNT / 2), aligned(2)));
+  group h;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = type == GEMM_LP_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v[i])
-                                : __builtin_bit_cast(uint16_t, (_Float16)v[i]);
-  uint16_t* p = (uint16_t*)C + at;
-  if (vec && n >= 4) {
-    *(uint2*)p = make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16,
-                            (uint32_t)h[2] | (uint32_t)h[3] << 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = h[i];
-  }
-}
-
-// Eight neighbouring 16-bit values.
-__device__ __forceinline__ void store8(void* C, int64_t at, int n, bool vec, int type, float4v u,
-                                       float4v v) {
-  if (vec && n >= 8) {
-    uint16_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = i < 4 ? u[i] : v[i - 4];
-      h[i] = type == GEMM_LP_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x)
-                                  : __builtin_bit_cast(uint16_t, (_Float16)x);
+  for (int i = 0; i < COUNT; i += 2) {
+    uint16_t lo, hi;
+    if (type == GEMM_LP_BF16) {
+      lo = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+      hi = __builtin_bit_cast(uint16_t, (__bf16)v[i + 1]);
+    } else {
+      lo = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+      hi = __builtin_bit_cast(uint16_t, (_Float16)v[i + 1]);
     }
-    __builtin_memcpy(__builtin_assume_aligned((uint16_t*)C + at, 16), h, 16);
+    h[i / 2] = (uint32_t)lo | (uint32_t)hi << 16;
+  }
+  uint16_t* p = (uint16_t*)C + at;
+  if (n >= COUNT) {
+    *(group*)p = h;
   } else {
-    store4(C, at, n, false, type, u);
-    store4(C, at + 4, n - 4, false, type, v);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      if (i < n) p[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
   }
 }
 

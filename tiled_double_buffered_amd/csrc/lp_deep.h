@@ -233,7 +233,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           if (s >= kLag) add(s - kLag);
         }
       }
-      store_tile<OB>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
+      store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
       return;
     }
 
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     if (steps > 1) step(One{}, steps - 2);
     step(None{}, steps - 1);
   }
-  store_tile<OB>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
+  store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
 }
 
 }  // namespace gemmlp

@@ -12,25 +12,34 @@
 
 namespace gemmlp {
 
-template <int UNIT>
-static LpKernel pick(int tile) {
-  using U = UnitOf<UNIT>;
+template <class U, int BM, int BN, int WM, int WN, bool STAGED>
+constexpr LpKernel pipe() {
+  return &lp_pipe_kernel<typename U::type, U::AKC, U::BKC, U::WGRAD, BM, BN, WM, WN, U::HOW,
+                         STAGED>;
+}
+
+template <class U>
+static LpKernel pick(int tile, bool staged) {
   using T = typename U::type;
-  if (tile == kTile256) {
+  if (tile == kTile256 && !staged) {
     // 8-bit values through the 16-bit instruction, or with a scale for each column, need more
     // registers than a wave of the deep kernel has
     if constexpr (T::BYTES != 1 || U::HOW == kFast8Blocks)
       return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD, U::HOW>;
     else if constexpr (U::HOW == kFast8Rows)
-      return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 256, 256, 2, 4, U::HOW>;
+      return pipe<U, 256, 256, 2, 4, false>();
   }
-  if (tile == kTile128) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 128, 128, 2, 2, U::HOW>;
-  if (tile == kTile64) return &lp_pipe_kernel<T, U::AKC, U::BKC, U::WGRAD, 64, 64, 2, 2, U::HOW>;
+  if (tile == kTile128)
+    return staged ? pipe<U, 128, 128, 2, 2, true>() : pipe<U, 128, 128, 2, 2, false>();
+  if (tile == kTile64)
+    return staged ? pipe<U, 64, 64, 2, 2, true>() : pipe<U, 64, 64, 2, 2, false>();
   return nullptr;
 }
 
 #define LP_CAT2(a, b) a##b
 #define LP_CAT(a, b) LP_CAT2(a, b)
-LpKernel LP_CAT(pipe_kernel_, LP_UNIT)(int tile) { return pick<LP_UNIT>(tile); }
+LpKernel LP_CAT(pipe_kernel_, LP_UNIT)(int tile, bool staged) {
+  return pick<UnitOf<LP_UNIT>>(tile, staged);
+}
 
 }  // namespace gemmlp

@@ -1,6 +1,7 @@
-// The product kernel for operands whose rows start at multiples of 4 bytes: tiles go from
+// The product kernel: tiles of operands whose rows start at multiples of 4 bytes go from
 // memory straight into LDS (gfx950's direct-to-LDS loads), two slots in turn, one barrier a
 // K step.  (Three or four slots, with fewer workgroups on a CU, were 1.1 to 1.4 times slower.)
+// Tiles of other operands pass through registers (STAGED) on the way.
 //
 // A K step is 128 bytes of every row where k is contiguous (128 8-bit, 64 16-bit, 32 32-bit
 // values), so that all types share one LDS layout:
@@ -110,17 +111,9 @@ struct PipeOperand {
     }
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-      const int j = wave + i * WAVES;
-      if constexpr (KC) {
-        const int row = j * 8 + lane / 8;
-        off[i] = (uint32_t)(row * ldb) + (uint32_t)(((lane & 7) ^ place(row)) * 16);
-      } else {
-        const int at = j * 1024 + lane * 16, k = at / K_ROW, in = at % K_ROW;
-        const int from = T::BYTES == 4
-                             ? in
-                             : ((((in >> 5) ^ swizzle(k)) << 5) | (in & 31));
-        off[i] = (uint32_t)(k * ldb) + (uint32_t)from;
-      }
+      int row, at;
+      place_of(wave + i * WAVES, lane, row, at);
+      off[i] = (uint32_t)(row * ldb) + (uint32_t)at;
     }
     const int l16 = lane & 15, g = lane >> 4;
     if constexpr (KC) {
@@ -141,6 +134,18 @@ struct PipeOperand {
     }
   }
 
+  // Which row (k contiguous) or k row, and which byte of it in the step, lane `lane` of copy j
+  // moves.
+  static __device__ __forceinline__ void place_of(int j, int lane, int& row, int& at) {
+    if constexpr (KC) {
+      row = j * 8 + lane / 8;
+      at = ((lane & 7) ^ place(row)) * 16;
+    } else {
+      const int b = j * 1024 + lane * 16, in = b % K_ROW;
+      row = b / K_ROW;
+      at = T::BYTES == 4 ? in : ((((in >> 5) ^ swizzle(row)) << 5) | (in & 31));
+    }
+  }
   __device__ __forceinline__ int4v words(int kt) const {
     return buffer_words(base + kt * step, left - kt * step);
   }
@@ -221,6 +226,71 @@ struct PipeOperand {
 __device__ __forceinline__ int4v half_of(int8v f, int h) {
   return h ? __builtin_shufflevector(f, f, 4, 5, 6, 7) : __builtin_shufflevector(f, f, 0, 1, 2, 3);
 }
+
+// 16 bytes at p of any alignment, of which the first n bytes (whole elements) may be read; the
+// others are zero.
+template <class T>
+__device__ __forceinline__ int4v load_group(const char* p, int64_t n) {
+  constexpr int PER = 16 / T::BYTES;
+  int4v v = {0, 0, 0, 0};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (n > 0) {
+    typename T::type e[PER] = {};
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * T::BYTES < n) __builtin_memcpy(e + i, p + i * T::BYTES, T::BYTES);
+    __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+// The copies of an operand of any alignment and leading dimension, through registers: the
+// same groups at the same places as PipeOperand's.
+template <class T, class O, bool KC, int WAVES>
+struct StagedCopy {
+  int4v v[O::COPIES];
+  const char* base;
+  int64_t off[O::COPIES];
+  int64_t left, step;
+  int k_of[O::COPIES];  // KC: the group's first byte of k in a step; else its k row
+  int inside;           // KC: bit i: group i's row is one of the operand's
+  int64_t k_len;        // KC: bytes of k; else k rows
+
+  __device__ __forceinline__ void init(const char* p, int64_t ld, int first, int rows, int k,
+                                       int wave, int lane) {
+    const int64_t ldb = ld * T::BYTES;
+    base = p + (KC ? (int64_t)first * ldb : (int64_t)first * T::BYTES);
+    left = (int64_t)(k - 1) * ldb + (int64_t)(rows - first) * T::BYTES;  // (not KC)
+    step = KC ? kRowBytes : O::KS * ldb;
+    k_len = KC ? (int64_t)k * T::BYTES : k;
+    inside = 0;
+#pragma unroll
+    for (int i = 0; i < O::COPIES; ++i) {
+      int row, at;
+      O::place_of(wave + i * WAVES, lane, row, at);
+      off[i] = row * ldb + at;
+      k_of[i] = KC ? at : row;
+      if (first + row < rows) inside |= 1 << i;
+    }
+  }
+  __device__ __forceinline__ void load(int kt) {
+#pragma unroll
+    for (int i = 0; i < O::COPIES; ++i) {
+      int64_t n;  // bytes that may be read
+      if constexpr (KC)
+        n = inside >> i & 1 ? k_len - (int64_t)kt * kRowBytes - k_of[i] : 0;
+      else  // past the last column a group holds the next row's values, which go nowhere
+        n = kt * O::KS + k_of[i] < k_len ? left - kt * step - off[i] : 0;
+      v[i] = load_group<T>(base + kt * step + off[i], n);
+    }
+  }
+  __device__ __forceinline__ void store(char* part, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < O::COPIES; ++i)
+      *(int4v*)(part + (wave + i * WAVES) * 1024 + lane * 16) = v[i];
+  }
+};
 
 // 16 bytes of k a lane from each side.
 template <class T>
@@ -312,13 +382,9 @@ struct ScaleCopy {
 };
 
 // One wave's accumulators into C.  m: C's row of fragment i for this lane.
-template <class OB, int SM, int SN, class F>
+template <class OB, int OUT, int SM, int SN, class F>
 __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int wn, int g,
                                            const float4v (&acc)[SM][SN], F row) {
-  const int cb = type_bytes(p.c_type);
-  constexpr int PER = OB::PACKED ? 8 : 4;
-  const bool vec = (((uintptr_t)p.C | (uintptr_t)(p.ldc * cb) | (uintptr_t)(w.c_base * cb)) &
-                    (uintptr_t)(PER * cb - 1)) == 0;
 #pragma unroll
   for (int i = 0; i < SM; ++i) {
     const int m = row(i);
@@ -328,7 +394,10 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
 #pragma unroll
       for (int j = 0; j < SN; j += 2) {
         const int n = w.n0 + wn + 16 * j + 8 * g;
-        store8(p.C, at + n, p.N - n, vec, p.c_type, acc[i][j], acc[i][j + 1]);
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = acc[i][j + x / 4][x % 4];
+        store_row<8, OUT>(p.C, at + n, p.N - n, p.c_type, v);
       }
     } else {
 #pragma unroll
@@ -337,11 +406,11 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
         // fragment in each register: the j - j0 th four of them
         constexpr int READ = OB::READ;
         const int q = j % READ, j0 = j - q;
-        float4v v;
+        float v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) v[x] = acc[i][j0 + (4 * q + x) % READ][(4 * q + x) / READ];
         const int n = w.n0 + wn + 16 * j0 + 4 * READ * g + 4 * q;
-        store4(p.C, at + n, p.N - n, vec, p.c_type, v);
+        store_row<4, OUT>(p.C, at + n, p.N - n, p.c_type, v);
       }
     }
   }
@@ -350,7 +419,9 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
 // HOW (8-bit values): through the 16-bit instruction; or through the 8-bit one, with B's scales
 // by blocks of 128 columns or column by column.
 enum { kExact8 = 0, kFast8Blocks = 1, kFast8Rows = 2 };
-template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW>
+// STAGED: operands of any alignment, through registers.
+template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW,
+          bool STAGED>
 __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
@@ -382,23 +453,42 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
     constexpr int S_WAVES = (BM + BN) / 64;
     static_assert(S_WAVES <= WAVES, "a wave copies 64 scales at most");
     if constexpr (F8T) os.init<BM>(p, w, steps, wave, lane);
+    StagedCopy<T, OA, AKC, WAVES> ca;
+    StagedCopy<T, OB, BKC, WAVES> cb;
+    if constexpr (STAGED) {
+      ca.init(w.A, p.lda, w.m0, w.m_end, w.k_end, wave, lane);
+      cb.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane);
+    }
     auto issue = [&](int kt, int slot) {
       const uint32_t at = lds0 + (uint32_t)(slot * SLOT);
-      oa.issue(kt, at, wave);
-      ob.issue(kt, at + OA::BYTES, wave);
+      if constexpr (STAGED) {
+        ca.load(kt);
+        cb.load(kt);
+      } else {
+        oa.issue(kt, at, wave);
+        ob.issue(kt, at + OA::BYTES, wave);
+      }
       if constexpr (F8T) {
         if (wave < S_WAVES) os.issue(kt, at + OA::BYTES + OB::BYTES, wave);
       }
     };
     const int tail = (w.k_end % OA::KS) * T::BYTES;  // bytes of k in the last step, 0: all
 
+    auto settle = [&](int slot) {  // what issue() left in registers
+      if constexpr (STAGED) {
+        ca.store(lds + slot * SLOT, wave, lane);
+        cb.store(lds + slot * SLOT + OA::BYTES, wave, lane);
+      }
+    };
+
     issue(0, 0);
+    settle(0);
     for (int kt = 0; kt < steps; ++kt) {
       part_barrier<0>();
       if (kt + 1 < steps) issue(kt + 1, (kt + 1) & 1);
       char* sa = lds + (kt & 1) * SLOT;
       char* sb = sa + OA::BYTES;
-      if ((AKC || BKC) && tail != 0 && kt + 1 == steps) {
+      if (!STAGED && (AKC || BKC) && tail != 0 && kt + 1 == steps) {
         if constexpr (AKC) OA::clear_tail(sa, tail, tid, THREADS);
         if constexpr (BKC) OB::clear_tail(sb, tail, tid, THREADS);
         __syncthreads();
@@ -471,10 +561,12 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
           if constexpr (HOW != kExact8) __builtin_amdgcn_sched_barrier(0);
         }
       }
+      if (kt + 1 < steps) settle((kt + 1) & 1);
     }
   }
 
-  store_tile<OB>(p, w, wn, g, acc,
+  constexpr int OUT = !F8T ? T::CODE : HOW != kExact8 ? GEMM_LP_BF16 : -1;
+  store_tile<OB, OUT>(p, w, wn, g, acc,
                      [&](int i) { return w.m0 + wm + OA::row_of(i, l16); });
 }
 

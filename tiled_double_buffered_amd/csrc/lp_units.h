@@ -38,17 +38,18 @@ template <> struct UnitOf<10> : Unit<F8, true, true, false, 1> {};
 template <> struct UnitOf<11> : Unit<F8, true, true, false, 2> {};
 constexpr int kUnits = 12;
 
-LpKernel pipe_kernel_0(int tile);
-LpKernel pipe_kernel_1(int tile);
-LpKernel pipe_kernel_2(int tile);
-LpKernel pipe_kernel_3(int tile);
-LpKernel pipe_kernel_4(int tile);
-LpKernel pipe_kernel_5(int tile);
-LpKernel pipe_kernel_6(int tile);
-LpKernel pipe_kernel_7(int tile);
-LpKernel pipe_kernel_8(int tile);
-LpKernel pipe_kernel_9(int tile);
-LpKernel pipe_kernel_10(int tile);
-LpKernel pipe_kernel_11(int tile);
+// The kernel of a tile, or NULL where the unit has none; staged: for operands of any alignment.
+LpKernel pipe_kernel_0(int tile, bool staged);
+LpKernel pipe_kernel_1(int tile, bool staged);
+LpKernel pipe_kernel_2(int tile, bool staged);
+LpKernel pipe_kernel_3(int tile, bool staged);
+LpKernel pipe_kernel_4(int tile, bool staged);
+LpKernel pipe_kernel_5(int tile, bool staged);
+LpKernel pipe_kernel_6(int tile, bool staged);
+LpKernel pipe_kernel_7(int tile, bool staged);
+LpKernel pipe_kernel_8(int tile, bool staged);
+LpKernel pipe_kernel_9(int tile, bool staged);
+LpKernel pipe_kernel_10(int tile, bool staged);
+LpKernel pipe_kernel_11(int tile, bool staged);
 
 }  // namespace gemmlp
