@@ -5,8 +5,10 @@
  * Operators
  *   gemm_fp8_quantize   values -> 8-bit floating point (OCP e4m3fn), one power-of-two scale
  *                       for each 1 x 128 or 128 x 128 block; optionally the transpose too
+ *   gemm_fp8_quantize_exp  the same with the scales as exponent bytes
  *   gemm_fp8            C = (A sa)(B sb)^T for 8-bit A, B with a scale for each block of 128
  *                       along K; optionally one B per expert and ragged groups of rows
+ *   gemm_fp8_exp        one such product with exponent bytes for scales
  *   gemm_grouped        Y[t] = X[t] W_e for the rows t of expert e, in bf16, fp16 or fp32
  *   gemm_grouped_wgrad  dW_e = sum over the rows t of expert e of A[t]^T B[t]
  *
@@ -52,6 +54,13 @@ int gemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int64_t ldx, in
                       int block_rows, void *Q, int64_t ldq, float *S, int64_t lds,
                       void *QT, int64_t ldqt, float *ST, int64_t ldst, void *stream);
 
+/* The same with the scales as bytes e + 127 (2^e the scale), one for each row of Q and block of
+ * 128 columns, block by block: S is ceil(cols / 128) x rows with row stride lds, ST is
+ * ceil(rows / 128) x cols with row stride ldst.  The rows of a 128 x 128 block have one value. */
+int gemm_fp8_quantize_exp(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type,
+                          int block_rows, void *Q, int64_t ldq, uint8_t *S, int64_t lds,
+                          void *QT, int64_t ldqt, uint8_t *ST, int64_t ldst, void *stream);
+
 /* C[i][j] = sum_k A[i][k] sa[i][k/128] B[j][k] sb[j/b_block][k/128].
  * A: M x K e4m3fn, row stride lda; SA: M x ceil(K/128), row stride ldsa.
  * B: N x K e4m3fn, row stride ldb; SB: ceil(N/b_block) x ceil(K/128), row stride ldsb;
@@ -66,6 +75,13 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t *offsets,
              const void *B, int64_t ldb, int64_t stride_b,
              const float *SB, int64_t ldsb, int64_t stride_sb, int b_block,
              void *C, int64_t ldc, int c_type, void *stream);
+
+/* gemm_fp8 of one product whose scales are gemm_fp8_quantize_exp's bytes: SA is ceil(K/128) x M,
+ * SB ceil(K/128) x N, both 4-byte aligned with row strides that are multiples of 4.  The matrix
+ * cores apply such scales themselves. */
+int gemm_fp8_exp(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const uint8_t *SA,
+                 int64_t ldsa, const void *B, int64_t ldb, const uint8_t *SB, int64_t ldsb,
+                 void *C, int64_t ldc, int c_type, void *stream);
 
 /* Y (rows x N) = X (rows x K) W_e, all of `type`.  W_e starts e * stride_w elements after W:
  * K x N with row stride ldw, or with transpose_w N x K (Y = X W_e^T). */

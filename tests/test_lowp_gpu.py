@@ -6,6 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import tiled_double_buffered_amd as tdb  # noqa: E402
+from tiled_double_buffered_amd import lowp  # noqa: E402
 import lowp_oracle as lo  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -72,6 +73,25 @@ def test_quantize(shape, block, dtype):
     q, sq, qt, sqt = tdb.quantize_fp8_pair(xd, block=(block, 128))
     _same(q, sq, v, s)
     _same(qt, sqt, vt, st)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 129), (130, 257), (257, 136)], ids=str)
+def test_quantize_exponents(shape, block, dtype):
+    """The exponent bytes are the scales', one for each row; the 8-bit values are the same."""
+    rows, cols = shape
+    x = _wide(rows, cols, TYPES[dtype], 13 + rows).to(DEV)
+    x[rows - 1, cols // 2] = float("inf")
+    q, s, qt, st = tdb.quantize_fp8_pair(x, block=(block, 128))
+    pair = lowp._quantize_exp(x, block, True, True)
+    plain = lowp._quantize_exp(x, block, True, False)
+    for (e, ex), (v, sc), (r, c) in ((pair[:2], (q, s), shape), (plain[:2], (q, s), shape),
+                                     (pair[2:], (qt, st), (cols, rows))):
+        assert torch.equal(e[:, :c].view(torch.uint8), v.contiguous().view(torch.uint8))
+        exps = torch.log2(sc).to(torch.int32) + 127
+        by_row = exps if block == 1 else exps.repeat_interleave(128, 0)[:r]
+        assert torch.equal(ex[:, :r].t().to(torch.int32), by_row)
 
 
 @pytest.mark.parametrize("block", [1, 128])

@@ -50,9 +50,43 @@ def test_quantize_refusals(change, code):
     assert _quant(**change) == code
 
 
+def _quant_exp(rows=4, cols=200, X=PA, ldx=200, t=BF16, br=1, Q=PB, ldq=208, S=PS, lds=4, QT=None,
+               ldqt=0, ST=None, ldst=0):
+    return lowp.gemm_fp8_quantize_exp(rows, cols, X, ldx, t, br, Q, ldq, S, lds, QT, ldqt, ST,
+                                      ldst, None)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(rows=-1), tdb.ERR_NEGATIVE_DIM), (dict(t=3), tdb.ERR_BAD_TYPE),
+    (dict(br=2), tdb.ERR_BAD_CONFIG), (dict(lds=3), tdb.ERR_BAD_LD),
+    (dict(QT=PC, ldqt=4, ST=PT, ldst=199), tdb.ERR_BAD_LD), (dict(S=None), tdb.ERR_NULL_PTR),
+    (dict(S=PB + 4), tdb.ERR_ALIAS), (dict(X=PA + 1), tdb.ERR_MISALIGNED),
+])
+def test_quantize_exp_refusals(change, code):
+    assert _quant_exp(**change) == code
+
+
+def _fp8_exp(M=4, N=200, K=300, A=PA, lda=300, SA=PS, ldsa=4, B=PB, ldb=300, SB=PT, ldsb=200,
+             C=PC, ldc=200, t=BF16):
+    return lowp.gemm_fp8_exp(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, t, None)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(K=-1), tdb.ERR_NEGATIVE_DIM), (dict(t=-1), tdb.ERR_BAD_TYPE),
+    (dict(ldsa=3), tdb.ERR_BAD_LD), (dict(ldsa=6), tdb.ERR_BAD_LD),
+    (dict(ldsb=199), tdb.ERR_BAD_LD), (dict(ldb=299), tdb.ERR_BAD_LD),
+    (dict(SA=None), tdb.ERR_NULL_PTR), (dict(SB=PT + 1), tdb.ERR_MISALIGNED),
+    (dict(C=PT), tdb.ERR_ALIAS), (dict(N=1 << 31, ldc=1 << 31, ldsb=1 << 31), tdb.ERR_TOO_LARGE),
+])
+def test_fp8_exp_refusals(change, code):
+    assert _fp8_exp(**change) == code
+
+
 def test_empty_calls_launch_nothing():
     assert _quant(rows=0, X=None) == tdb.OK
     assert _fp8(M=0, A=None) == tdb.OK
+    assert _fp8_exp(M=0, A=None) == tdb.OK
+    assert _quant_exp(cols=0, X=None) == tdb.OK
     assert _fp8(N=0, C=None, ldc=1) == tdb.OK
     assert _grouped(rows=0, X=None) == tdb.OK
     assert _wgrad(E=0, D=None) == tdb.OK

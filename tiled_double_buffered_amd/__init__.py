@@ -19,7 +19,7 @@ from ._binding import (  # noqa: F401
     load, matmul, matmul_splitk,
 )
 
-_LOWP = ("gemm_fp8", "gemm_fp8_quantize", "gemm_grouped", "gemm_grouped_wgrad", "linear_fp8",
+_LOWP = ("gemm_fp8", "gemm_fp8_exp", "gemm_fp8_quantize", "gemm_fp8_quantize_exp", "gemm_grouped", "gemm_grouped_wgrad", "linear_fp8",
          "linear_grouped", "matmul_fp8", "matmul_fp8_grouped", "matmul_grouped",
          "matmul_grouped_wgrad", "quantize_fp8", "quantize_fp8_pair")
 

@@ -74,7 +74,9 @@ static LpKernel pipe_kernel(int unit, int tile, bool staged) {
     case 8: return pipe_kernel_8(tile, staged);
     case 9: return pipe_kernel_9(tile, staged);
     case 10: return pipe_kernel_10(tile, staged);
-    default: return pipe_kernel_11(tile, staged);
+    case 11: return pipe_kernel_11(tile, staged);
+    case 12: return pipe_kernel_12(tile, staged);
+    default: return pipe_kernel_13(tile, staged);
   }
 }
 
@@ -133,7 +135,7 @@ static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) 
     for (int t = 0; t < kTileCount; ++t)
       if (kTiles[t].bm == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
   }
-  const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 ? kStep8Exact : kStep8;
+  const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 || unit == 13 ? kStep8Exact : kStep8;
   int best = -1;
   double least = 0;
   for (int t = 0; t < kTileCount; ++t) {
@@ -159,31 +161,52 @@ static double expected_rows(const LpArgs& a, double bm, double bn) {
 }
 static double k_steps(int64_t k, int bytes) { return std::ceil((double)k * bytes / kRowBytes); }
 
+template <class T, bool EXP>
+static const void* quantize_kernel(bool rows_only, int block_rows) {
+  if (rows_only) return (const void*)&lp_quantize_rows_kernel<T, EXP>;
+  return block_rows == 1 ? (const void*)&lp_quantize_tile_kernel<T, 1, EXP>
+                         : (const void*)&lp_quantize_tile_kernel<T, kBlock, EXP>;
+}
+template <bool EXP>
+static const void* quantize_kernel(int type, bool rows_only, int block_rows) {
+  switch (type) {
+    case GEMM_LP_BF16: return quantize_kernel<Bf16, EXP>(rows_only, block_rows);
+    case GEMM_LP_F16: return quantize_kernel<F16, EXP>(rows_only, block_rows);
+    default: return quantize_kernel<F32, EXP>(rows_only, block_rows);
+  }
+}
+
+// EXP: scales as exponent bytes, [block][row]; otherwise FP32 numbers, [row block][block].
+template <bool EXP>
 static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
-                        int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* QT,
-                        int64_t ldqt, float* ST, int64_t ldst, void* stream) {
+                        int block_rows, void* Q, int64_t ldq, void* S, int64_t lds, void* QT,
+                        int64_t ldqt, void* ST, int64_t ldst, void* stream) {
   if (rows < 0 || cols < 0) return GEMMF32_ERR_NEGATIVE_DIM;
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
   if (block_rows != 1 && block_rows != kBlock) return GEMMF32_ERR_BAD_CONFIG;
   if ((Q == nullptr) != (S == nullptr) || (QT == nullptr) != (ST == nullptr))
     return GEMMF32_ERR_NULL_PTR;
   const int64_t kb = blocks(cols), mb = blocks(rows);
-  if (ldx < at_least_1(cols) || (Q && (ldq < at_least_1(cols) || lds < at_least_1(kb))) ||
-      (QT && (ldqt < at_least_1(rows) || ldst < at_least_1(mb))))
+  // rows and columns of the two arrays of scales, and the bytes of one
+  const int64_t s_rows = EXP ? kb : block_rows == 1 ? rows : mb, s_cols = EXP ? rows : kb;
+  const int64_t st_rows = EXP ? mb : block_rows == 1 ? cols : kb, st_cols = EXP ? cols : mb;
+  constexpr int sb = EXP ? 1 : 4;
+  if (ldx < at_least_1(cols) || (Q && (ldq < at_least_1(cols) || lds < at_least_1(s_cols))) ||
+      (QT && (ldqt < at_least_1(rows) || ldst < at_least_1(st_cols))))
     return GEMMF32_ERR_BAD_LD;
   if (rows > kMaxDim || cols > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
   if (rows == 0 || cols == 0) return GEMMF32_OK;
   if (X == nullptr || (Q == nullptr && QT == nullptr)) return GEMMF32_ERR_NULL_PTR;
   const int xb = type_bytes(type);
-  if (misaligned(X, xb) || misaligned(S, 4) || misaligned(ST, 4)) return GEMMF32_ERR_MISALIGNED;
+  if (misaligned(X, xb) || misaligned(S, sb) || misaligned(ST, sb))
+    return GEMMF32_ERR_MISALIGNED;
   Range x, out[4];
-  const int64_t s_rows = block_rows == 1 ? rows : mb, st_rows = block_rows == 1 ? cols : kb;
   if (!byte_range(X, 1, 0, rows, cols, ldx, xb, &x)) return GEMMF32_ERR_TOO_LARGE;
   if (Q && (!byte_range(Q, 1, 0, rows, cols, ldq, 1, &out[0]) ||
-            !byte_range(S, 1, 0, s_rows, kb, lds, 4, &out[1])))
+            !byte_range(S, 1, 0, s_rows, s_cols, lds, sb, &out[1])))
     return GEMMF32_ERR_TOO_LARGE;
   if (QT && (!byte_range(QT, 1, 0, cols, rows, ldqt, 1, &out[2]) ||
-             !byte_range(ST, 1, 0, st_rows, mb, ldst, 4, &out[3])))
+             !byte_range(ST, 1, 0, st_rows, st_cols, ldst, sb, &out[3])))
     return GEMMF32_ERR_TOO_LARGE;
   for (int i = 0; i < 4; ++i) {
     if (overlap(out[i], x)) return GEMMF32_ERR_ALIAS;
@@ -192,30 +215,22 @@ static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, 
   }
   QuantArgs a{X,   (uint8_t*)Q, S,    (uint8_t*)QT, ST,       ldx,
               ldq, lds,         ldqt, ldst,         (int)rows, (int)cols};
-  if (QT == nullptr && block_rows == 1) {
+  const bool rows_only = QT == nullptr && block_rows == 1;
+  const void* fn = quantize_kernel<EXP>(type, rows_only, block_rows);
+  if (rows_only) {
     const int64_t wgs = (rows * kb + 15) / 16;
     if (wgs > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
-    const void* fn = type == GEMM_LP_BF16 ? (const void*)&lp_quantize_rows_kernel<Bf16>
-                     : type == GEMM_LP_F16 ? (const void*)&lp_quantize_rows_kernel<F16>
-                                           : (const void*)&lp_quantize_rows_kernel<F32>;
     return launch(fn, dim3((unsigned)wgs), 256, &a, stream);
   }
   if (mb > 65535 || kb > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
-  const bool r1 = block_rows == 1;
-  const void* fn = type == GEMM_LP_BF16
-                       ? (r1 ? (const void*)&lp_quantize_tile_kernel<Bf16, 1>
-                             : (const void*)&lp_quantize_tile_kernel<Bf16, kBlock>)
-                   : type == GEMM_LP_F16
-                       ? (r1 ? (const void*)&lp_quantize_tile_kernel<F16, 1>
-                             : (const void*)&lp_quantize_tile_kernel<F16, kBlock>)
-                       : (r1 ? (const void*)&lp_quantize_tile_kernel<F32, 1>
-                             : (const void*)&lp_quantize_tile_kernel<F32, kBlock>);
   return launch(fn, dim3((unsigned)kb, (unsigned)mb), 256, &a, stream);
 }
 
+// EXP: the scales are exponent bytes, [block][row], as run_quantize writes them.
+template <bool EXP>
 static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
-                   const void* A, int64_t lda, const float* SA, int64_t ldsa, const void* B,
-                   int64_t ldb, int64_t stride_b, const float* SB, int64_t ldsb,
+                   const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* B,
+                   int64_t ldb, int64_t stride_b, const void* SB, int64_t ldsb,
                    int64_t stride_sb, int b_block, void* C, int64_t ldc, int c_type,
                    void* stream) {
   if (M < 0 || N < 0 || K < 0 || E < 0) return GEMMF32_ERR_NEGATIVE_DIM;
@@ -223,11 +238,14 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   if ((b_block != 1 && b_block != kBlock) || (offsets == nullptr && E != 1))
     return GEMMF32_ERR_BAD_CONFIG;
   const int64_t kb = blocks(K), nb = b_block == 1 ? N : blocks(N);
+  const int64_t sa_rows = EXP ? kb : M, sa_cols = EXP ? M : kb;
+  const int64_t sb_rows = EXP ? kb : nb, sb_cols = EXP ? N : kb;
   if (lda < at_least_1(K) || ldb < at_least_1(K) || ldc < at_least_1(N) ||
-      ldsa < at_least_1(kb) || ldsb < at_least_1(kb) || stride_b < 0 || stride_sb < 0)
+      ldsa < at_least_1(sa_cols) || ldsb < at_least_1(sb_cols) || stride_b < 0 || stride_sb < 0 ||
+      (EXP && (ldsa % 4 != 0 || ldsb % 4 != 0)))
     return GEMMF32_ERR_BAD_LD;
-  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim || ldsa >= kMaxScaleLd ||
-      ldsb >= kMaxScaleLd)
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxDim ||
+      (!EXP && (ldsa >= kMaxScaleLd || ldsb >= kMaxScaleLd)))
     return GEMMF32_ERR_TOO_LARGE;
   if (M == 0 || N == 0) return GEMMF32_OK;
   if (C == nullptr) return GEMMF32_ERR_NULL_PTR;
@@ -241,16 +259,17 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   Range c, in[5];
   if (!byte_range(C, 1, 0, M, N, ldc, cb, &c)) return GEMMF32_ERR_TOO_LARGE;
   if (reads && (!byte_range(A, 1, 0, M, K, lda, 1, &in[0]) ||
-                !byte_range(SA, 1, 0, M, kb, ldsa, 4, &in[1]) ||
+                !byte_range(SA, 1, 0, sa_rows, sa_cols, ldsa, EXP ? 1 : 4, &in[1]) ||
                 !byte_range(B, E, stride_b, N, K, ldb, 1, &in[2]) ||
-                !byte_range(SB, E, stride_sb, nb, kb, ldsb, 4, &in[3])))
+                !byte_range(SB, E, stride_sb, sb_rows, sb_cols, ldsb, EXP ? 1 : 4, &in[3])))
     return GEMMF32_ERR_TOO_LARGE;
   if (offsets && !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[4]))
     return GEMMF32_ERR_TOO_LARGE;
   for (const Range& r : in)
     if (overlap(c, r)) return GEMMF32_ERR_ALIAS;
   LpArgs a{};
-  a.A = A, a.B = B, a.C = C, a.SA = SA, a.SB = SB, a.offsets = offsets;
+  a.A = A, a.B = B, a.C = C, a.offsets = offsets;
+  a.SA = (const float*)SA, a.SB = (const float*)SB;
   a.lda = lda, a.ldb = ldb, a.ldc = ldc, a.stride_b = stride_b;
   a.ldsa = ldsa, a.ldsb = ldsb, a.stride_sb = stride_sb;
   a.rows = a.M = (int)M, a.N = (int)N, a.K = (int)K, a.E = (int)E;
@@ -259,7 +278,8 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   // average, lp_common.h).  It is taken for bf16 results, which keep 8 bits, of contractions
   // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
   // themselves; other results go through the 16-bit instruction, which cuts nothing.
-  const int unit = c_type == GEMM_LP_BF16 && K >= 1024 ? (b_block == 1 ? 11 : 10) : 9;
+  const bool fast = c_type == GEMM_LP_BF16 && K >= 1024;
+  const int unit = EXP ? (fast ? 12 : 13) : fast ? (b_block == 1 ? 11 : 10) : 9;
   const bool staged = !(word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1));
   const int t = pick_tile(unit, staged, k_steps(K, 1), 1.0,
                           [&](int bm, int bn) { return expected_rows(a, bm, bn); });
@@ -351,16 +371,30 @@ extern "C" {
 int gemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
                       int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* QT,
                       int64_t ldqt, float* ST, int64_t ldst, void* stream) {
-  return gemmlp::run_quantize(rows, cols, X, ldx, type, block_rows, Q, ldq, S, lds, QT, ldqt,
-                              ST, ldst, stream);
+  return gemmlp::run_quantize<false>(rows, cols, X, ldx, type, block_rows, Q, ldq, S, lds, QT,
+                                     ldqt, ST, ldst, stream);
+}
+
+int gemm_fp8_quantize_exp(int64_t rows, int64_t cols, const void* X, int64_t ldx, int type,
+                          int block_rows, void* Q, int64_t ldq, uint8_t* S, int64_t lds, void* QT,
+                          int64_t ldqt, uint8_t* ST, int64_t ldst, void* stream) {
+  return gemmlp::run_quantize<true>(rows, cols, X, ldx, type, block_rows, Q, ldq, S, lds, QT,
+                                    ldqt, ST, ldst, stream);
 }
 
 int gemm_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* offsets, const void* A,
              int64_t lda, const float* SA, int64_t ldsa, const void* B, int64_t ldb,
              int64_t stride_b, const float* SB, int64_t ldsb, int64_t stride_sb, int b_block,
              void* C, int64_t ldc, int c_type, void* stream) {
-  return gemmlp::run_fp8(M, N, K, E, offsets, A, lda, SA, ldsa, B, ldb, stride_b, SB, ldsb,
-                         stride_sb, b_block, C, ldc, c_type, stream);
+  return gemmlp::run_fp8<false>(M, N, K, E, offsets, A, lda, SA, ldsa, B, ldb, stride_b, SB,
+                                ldsb, stride_sb, b_block, C, ldc, c_type, stream);
+}
+
+int gemm_fp8_exp(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const uint8_t* SA,
+                 int64_t ldsa, const void* B, int64_t ldb, const uint8_t* SB, int64_t ldsb,
+                 void* C, int64_t ldc, int c_type, void* stream) {
+  return gemmlp::run_fp8<true>(M, N, K, 1, nullptr, A, lda, SA, ldsa, B, ldb, 0, SB, ldsb, 0, 1,
+                               C, ldc, c_type, stream);
 }
 
 int gemm_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,

@@ -27,11 +27,12 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
   constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
   constexpr bool F8T = T::BYTES == 1;
-  static_assert(!F8T || HOW != kExact8, "not enough registers");
+  static_assert(!F8T || !exact(HOW), "not enough registers");
   constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
   using OA = PipeOperand<T, AKC, BM / 2, HALF, WAVES>;
   using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
-  constexpr int SCALES = F8T ? (BM + BN) * 4 : 0;
+  using OS = ScaleCopy<HOW, BM, BN>;
+  constexpr int SCALES = F8T ? OS::BYTES : 0;
   constexpr int A1 = 0, A2 = OA::BYTES, B0 = 2 * OA::BYTES, S0 = B0 + OB::BYTES;
   constexpr int SLOT = S0 + SCALES;
   constexpr int FIRST = OA::COPIES + OB::COPIES + (F8T ? 1 : 0), SECOND = OA::COPIES;
@@ -56,13 +57,13 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     ob.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane, wn);
     const uint32_t lds0 =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
-    ScaleCopy os;
-    if constexpr (F8T) os.init<BM>(p, w, steps, wave, lane);
+    OS os;
+    if constexpr (F8T) os.init(p, w, steps, wave, lane);
     auto issue_first = [&](int kt) {
       const uint32_t at = lds0 + (uint32_t)((kt & 1) * SLOT);
       ob.issue(kt, at + B0, wave);
       oa1.issue(kt, at + A1, wave);
-      if constexpr (F8T) os.issue(kt, at + S0, wave);
+      if constexpr (F8T) os.issue(kt, at + S0);
     };
     auto issue_second = [&](int kt) {
       oa2.issue(kt, lds0 + (uint32_t)((kt & 1) * SLOT + A2), wave);
@@ -80,8 +81,9 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     }
 
     int8v b[SN], a[2 * OA::READ];
-    float s_a[F8T ? SM : 1];
-    float4v s_b[HOW == kFast8Rows ? SN : 1];
+    float s_a[SM];              // kFast8
+    float4v s_b[SN];
+    int x_a[SM], x_b[SN];       // kScaled8
     // fragments of A, READ of them at a time, into the two sets in turn
     auto read_a = [&](const char* slot, int i, bool masked) {
       const int at = (i / OA::READ & 1) * OA::READ;
@@ -91,16 +93,23 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     auto set_of = [](int i) { return (i / OA::READ & 1) * OA::READ + i % OA::READ; };
     auto read_scales = [&](const char* slot) {
       if constexpr (F8T) {
-        const float* s = (const float*)(slot + S0);
+        const char* table = slot + S0;
+        if constexpr (HOW == kScaled8) {
 #pragma unroll
-        for (int i = 0; i < SM; ++i) s_a[i] = s[row_of(i)];
-        if constexpr (HOW == kFast8Blocks) {
-          const float block = s[BM + wn];
+          for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, row_of(i));
 #pragma unroll
-          for (int i = 0; i < SM; ++i) s_a[i] *= block;
+          for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
         } else {
 #pragma unroll
-          for (int j = 0; j < SN; ++j) s_b[j] = *(const float4v*)(s + BM + wn + OB::row_of(j, 4 * g));
+          for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, row_of(i));
+          if constexpr (HOW == kFast8Blocks) {
+            const float block = OS::b(table, wn);
+#pragma unroll
+            for (int i = 0; i < SM; ++i) s_a[i] *= block;
+          } else {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
+          }
         }
       }
     };
@@ -110,7 +119,10 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     float4v d[kRing];
     auto product_of = [&](int s, const int8v& fa) {  // product s = i * SN + j of the step
       const int i = s / SN, j = s % SN;
-      if constexpr (F8T) {
+      if constexpr (HOW == kScaled8) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], fa, acc[i][j], 0, 0, 0,
+                                                                     x_b[j], 0, x_a[i]);
+      } else if constexpr (F8T) {
         const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
         d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
             b[j], fa, z, 0, 0, 0, 0, 0, 0);
@@ -122,7 +134,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     };
     auto product = [&](int s) { product_of(s, a[set_of(s / SN)]); };
     auto add = [&](int s) {
-      if constexpr (F8T) {
+      if constexpr (F8T && HOW != kScaled8) {
         if (s < 0) return;
         const int i = s / SN, j = s % SN;
         const float4v v = d[s % kRing];
@@ -179,7 +191,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
               while (done * SLOTS < (at + 1) * FIRST) {
                 if (done < OB::COPIES) ob.copy(done, rb, to + B0, wave);
                 else if (done < OB::COPIES + OA::COPIES) oa1.copy(done - OB::COPIES, ra, to + A1, wave);
-                else if constexpr (F8T) os.copy(rs, to + S0, wave);
+                else if constexpr (F8T) os.copy(rs, to + S0);
                 ++done;
               }
             } else if (i == SM - 1 && j * OA::COPIES / SN != (j + 1) * OA::COPIES / SN) {

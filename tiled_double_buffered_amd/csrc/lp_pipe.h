@@ -347,16 +347,45 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
   return true;
 }
 
-// The copies of a K step's scales (8-bit values): one for each row of A and column of B of the
-// tile, 64 a wave.
+// How 8-bit values are multiplied and scaled:
+//   kExact8: through the 16-bit instruction, FP32 scales (B's by blocks of 128 columns or column
+//     by column);
+//   kFast8Blocks, kFast8Rows: through the 8-bit instruction, B's scales by blocks, by columns;
+//   kScaled8: through the 8-bit instruction, which applies the scales itself: they are powers of
+//     two, one exponent byte for each row and column;
+//   kExactScaled8: such scales, through the 16-bit instruction.
+enum { kExact8 = 0, kFast8Blocks = 1, kFast8Rows = 2, kScaled8 = 3, kExactScaled8 = 4 };
+constexpr bool by_exponents(int how) { return how == kScaled8 || how == kExactScaled8; }
+constexpr bool exact(int how) { return how == kExact8 || how == kExactScaled8; }
+
+// The copies of a K step's scales (8-bit values) into the slot's table, A's rows first: FP32
+// numbers, 64 a wave, or exponent bytes, which every wave copies for A or for B (the same bytes:
+// a wave's copies of a step then have one count).
+template <int HOW, int BM, int BN>
 struct ScaleCopy {
+  static constexpr bool EXP = by_exponents(HOW);
+  static constexpr int B_AT = EXP ? 256 : BM * 4;       // B's part
+  static constexpr int BYTES = EXP ? 512 : (BM + BN) * 4;
+  static constexpr int WAVES = EXP ? 64 : (BM + BN) / 64;  // waves that copy
+  static_assert(!EXP || (BM <= 256 && BN <= 256), "64 words an operand");
   const char* base;
-  int64_t left;
+  int64_t left, step;
   uint32_t off;
-  template <int BM>
+  uint32_t to;
   __device__ __forceinline__ void init(const LpArgs& p, const TileOf& w, int steps, int wave,
                                        int lane) {
+    if constexpr (EXP) {
+      const bool b = wave & 1;
+      step = b ? p.ldsb : p.ldsa;
+      base = (const char*)(b ? p.SB : p.SA) + (b ? w.n0 : w.m0);
+      left = (int64_t)(steps - 1) * step + (b ? p.N - w.n0 : w.m_end - w.m0);
+      off = (uint32_t)lane * 4;
+      to = b ? B_AT : 0;
+      return;
+    }
     const int r = wave * 64 + lane;
+    step = 4;
+    to = (uint32_t)wave * 256;
     if (wave < BM / 64) {
       const int rows = w.m_end - w.m0;
       base = (const char*)(p.SA + (int64_t)w.m0 * p.ldsa);
@@ -371,13 +400,37 @@ struct ScaleCopy {
     }
   }
   __device__ __forceinline__ int4v words(int kt) const {
-    return buffer_words(base + kt * 4, left - kt * 4);
+    return buffer_words(base + kt * step, left - kt * step);
   }
-  __device__ __forceinline__ void copy(int4v r, uint32_t lds, int wave) const {
-    copy4(__builtin_amdgcn_readfirstlane(lds + (uint32_t)wave * 256u), r, off);
+  __device__ __forceinline__ void copy(int4v r, uint32_t table) const {
+    copy4(__builtin_amdgcn_readfirstlane(table + to), r, off);
   }
-  __device__ __forceinline__ void issue(int kt, uint32_t lds, int wave) const {
-    copy(words(kt), lds, wave);
+  __device__ __forceinline__ void issue(int kt, uint32_t table) const { copy(words(kt), table); }
+
+  // Scales from the table: of row r of A, of column c of B, of columns c .. c + 3.
+  static __device__ __forceinline__ float number(uint32_t byte) {
+    return __builtin_bit_cast(float, byte << 23);  // 2^(byte - 127)
+  }
+  static __device__ __forceinline__ int a_byte(const char* table, int r) {
+    return (uint8_t)table[r];
+  }
+  static __device__ __forceinline__ int b_byte(const char* table, int c) {
+    return (uint8_t)table[B_AT + c];
+  }
+  static __device__ __forceinline__ float a(const char* table, int r) {
+    if constexpr (EXP) return number((uint8_t)table[r]);
+    return ((const float*)table)[r];
+  }
+  static __device__ __forceinline__ float b(const char* table, int c) {
+    if constexpr (EXP) return number((uint8_t)table[B_AT + c]);
+    return ((const float*)(table + B_AT))[c];
+  }
+  static __device__ __forceinline__ float4v b4(const char* table, int c) {
+    if constexpr (EXP) {
+      const uint32_t x = *(const uint32_t*)(table + B_AT + c);
+      return float4v{number(x & 255), number(x >> 8 & 255), number(x >> 16 & 255), number(x >> 24)};
+    }
+    return *(const float4v*)(table + B_AT + 4 * c);
   }
 };
 
@@ -416,9 +469,6 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
   }
 }
 
-// HOW (8-bit values): through the 16-bit instruction; or through the 8-bit one, with B's scales
-// by blocks of 128 columns or column by column.
-enum { kExact8 = 0, kFast8Blocks = 1, kFast8Rows = 2 };
 // STAGED: operands of any alignment, through registers.
 template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW,
           bool STAGED>
@@ -427,9 +477,10 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
   constexpr bool F8T = T::BYTES == 1;
   using OA = PipeOperand<T, AKC, BM, WTM, WAVES>;
-  constexpr bool PACK = T::BYTES == 2 || (F8T && HOW != kExact8);  // C has 16 bits
+  constexpr bool PACK = T::BYTES == 2 || (F8T && !exact(HOW));  // C has 16 bits
   using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
-  constexpr int SCALES = F8T ? (BM + BN) * 4 : 0;
+  using OS = ScaleCopy<HOW, BM, BN>;
+  constexpr int SCALES = F8T ? OS::BYTES : 0;
   constexpr int SLOT = OA::BYTES + OB::BYTES + SCALES;
   __shared__ __align__(1024) char lds[2 * SLOT];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -449,10 +500,8 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
     ob.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane, wn);
     const uint32_t lds0 =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
-    ScaleCopy os;
-    constexpr int S_WAVES = (BM + BN) / 64;
-    static_assert(S_WAVES <= WAVES, "a wave copies 64 scales at most");
-    if constexpr (F8T) os.init<BM>(p, w, steps, wave, lane);
+    OS os;
+    if constexpr (F8T) os.init(p, w, steps, wave, lane);
     StagedCopy<T, OA, AKC, WAVES> ca;
     StagedCopy<T, OB, BKC, WAVES> cb;
     if constexpr (STAGED) {
@@ -469,7 +518,8 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
         ob.issue(kt, at + OA::BYTES, wave);
       }
       if constexpr (F8T) {
-        if (wave < S_WAVES) os.issue(kt, at + OA::BYTES + OB::BYTES, wave);
+        static_assert(OS::EXP || OS::WAVES <= WAVES, "a wave copies 64 scales");
+        if (wave < OS::WAVES) os.issue(kt, at + OA::BYTES + OB::BYTES);
       }
     };
     const int tail = (w.k_end % OA::KS) * T::BYTES;  // bytes of k in the last step, 0: all
@@ -507,31 +557,37 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
             for (int j = 0; j < SN; ++j) 
               acc[i][j] = mma_half<T>(half_of(b[j], h), half_of(a[i], h), acc[i][j]);
       } else {
-        const float* scales = (const float*)(sb + OB::BYTES);
+        const char* table = sb + OB::BYTES;
         int8v b[SN], a[2];
 #pragma unroll
         for (int j = 0; j < SN; ++j) ob.read(sb, j, b + j);
         oa.read(sa, 0, a);
         float4v s_b[SN];
         float s_a[SM];
-        if constexpr (HOW != kFast8Blocks) {
+        int x_a[SM], x_b[SN];
+        if constexpr (HOW == kScaled8) {
 #pragma unroll
-          for (int j = 0; j < SN; ++j)
-            s_b[j] = *(const float4v*)(scales + BM + wn + OB::row_of(j, 4 * g));
-        }
+          for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
 #pragma unroll
-        for (int i = 0; i < SM; ++i) s_a[i] = scales[wm + 16 * i + l16];
-        if constexpr (HOW == kFast8Blocks) {
-          // the wave's columns lie in one block of 128: one factor a row
-          static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
-          const float block = scales[BM + wn];
+          for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, wm + 16 * i + l16);
+        } else {
 #pragma unroll
-          for (int i = 0; i < SM; ++i) s_a[i] *= block;
+          for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
+          if constexpr (HOW == kFast8Blocks) {
+            // the wave's columns lie in one block of 128: one factor a row
+            static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
+            const float block = OS::b(table, wn);
+#pragma unroll
+            for (int i = 0; i < SM; ++i) s_a[i] *= block;
+          } else {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
+          }
         }
         // The sums of a step are scaled and added kLag products behind, while the matrix
         // cores work on the next ones; the order is pinned, since the compiler would put each
         // addition right behind its product and wait.
-        constexpr int kLag = HOW == kExact8 ? 1 : 2, kRing = kLag + 1;
+        constexpr int kLag = HOW == kScaled8 ? 0 : exact(HOW) ? 1 : 2, kRing = kLag + 1;
         float4v d[kRing];
 #pragma unroll
         for (int s = 0; s < SM * SN + kLag; ++s) {
@@ -539,15 +595,18 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
             const int i = s / SN, j = s % SN;
             if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
             const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (HOW == kExact8)
+            if constexpr (HOW == kScaled8)
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  b[j], a[i & 1], acc[i][j], 0, 0, 0, x_b[j], 0, x_a[i]);
+            else if constexpr (exact(HOW))
               d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
                                          half_of(a[i & 1], 1), z);
             else
               d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                   b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
           }
-          if constexpr (HOW != kExact8) __builtin_amdgcn_sched_barrier(0);
-          if (s >= kLag) {
+          if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
+          if (s >= kLag && HOW != kScaled8) {
             const int i = (s - kLag) / SN, j = (s - kLag) % SN;
             const float4v v = d[(s - kLag) % kRing];
 #pragma unroll
@@ -558,14 +617,14 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
                 acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
             }
           }
-          if constexpr (HOW != kExact8) __builtin_amdgcn_sched_barrier(0);
+          if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
         }
       }
       if (kt + 1 < steps) settle((kt + 1) & 1);
     }
   }
 
-  constexpr int OUT = !F8T ? T::CODE : HOW != kExact8 ? GEMM_LP_BF16 : -1;
+  constexpr int OUT = !F8T ? T::CODE : exact(HOW) ? -1 : GEMM_LP_BF16;
   store_tile<OB, OUT>(p, w, wn, g, acc,
                      [&](int i) { return w.m0 + wm + OA::row_of(i, l16); });
 }

@@ -8,63 +8,62 @@
 // conversion instruction's, to nearest with ties to even.
 #pragma once
 
+#include <type_traits>
+
 #include "lp_common.h"
 
 namespace gemmlp {
 
+// EXP: the scales as bytes e + 127, one for each row of Q and block of columns (the rows of a
+// block all get its exponent), block by block: S[block * lds + row].  Otherwise as FP32 numbers,
+// one for each block: S[row block * lds + block].
 struct QuantArgs {
   const void* X;
   uint8_t* Q;
-  float* S;
+  void* S;
   uint8_t* QT;
-  float* ST;
+  void* ST;
   int64_t ldx, ldq, lds, ldqt, ldst;
   int rows, cols;
 };
 
-__device__ __forceinline__ uint32_t finite_bits(float x) {  // |x| as bits, 0 for Inf and NaN
-  const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0u;
-}
-__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+__device__ __forceinline__ int scale_exponent(float top) {  // top: finite, not negative
+  const uint32_t bits = __builtin_bit_cast(uint32_t, top);
   const int e = (int)(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return max(e, -126);
 }
 __device__ __forceinline__ float power_of_two(int e) {
   return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
 }
-// Two values as 8-bit numbers in the low or high half of `old`.
-template <bool HIGH>
-__device__ __forceinline__ int to_fp8(float a, float b, float inv, int old) {
-  a = finite_bits(a) || a == 0.0f ? a * inv : __builtin_nanf("");
-  b = finite_bits(b) || b == 0.0f ? b * inv : __builtin_nanf("");
-  return __builtin_amdgcn_cvt_pk_fp8_f32(a, b, old, HIGH);
-}
+// Eight values as 8-bit numbers: the conversion rounds to nearest even, and turns Inf and NaN
+// into NaN.
 __device__ __forceinline__ uint2 to_fp8x8(const float* v, int step, float inv) {
   int lo = 0, hi = 0;
-  lo = to_fp8<false>(v[0], v[step], inv, lo);
-  lo = to_fp8<true>(v[2 * step], v[3 * step], inv, lo);
-  hi = to_fp8<false>(v[4 * step], v[5 * step], inv, hi);
-  hi = to_fp8<true>(v[6 * step], v[7 * step], inv, hi);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[step] * inv, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2 * step] * inv, v[3 * step] * inv, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * step] * inv, v[5 * step] * inv, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6 * step] * inv, v[7 * step] * inv, hi, true);
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
 // Eight neighbouring values of a row, the first `n` of them inside it.
 template <class T>
 __device__ __forceinline__ void load8(const typename T::type* p, int n, float* v) {
-  typename T::type e[8];
+  typedef typename T::type E;
+  typedef E group __attribute__((ext_vector_type(8), aligned(sizeof(E))));
   if (n >= 8) {
-    __builtin_memcpy(e, p, sizeof(e));
+    const group e = *(const group*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : (typename T::type)0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
 }
 __device__ __forceinline__ void store_bytes8(uint8_t* p, int n, uint2 q) {
+  typedef uint32_t group __attribute__((ext_vector_type(2), aligned(1)));
   if (n >= 8) {
-    __builtin_memcpy(p, &q, 8);
+    *(group*)p = group{q.x, q.y};
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -72,14 +71,46 @@ __device__ __forceinline__ void store_bytes8(uint8_t* p, int n, uint2 q) {
   }
 }
 
-__device__ __forceinline__ uint32_t max_over_16(uint32_t m) {
+// Maxima over lanes: over each 16 by rotations on the vector unit, and over the four 16s of a
+// wave.
+__device__ __forceinline__ float max_over_16(float m) {
+  auto turn = [&](auto ctrl) {
+    const int v = __builtin_bit_cast(int, m);
+    m = fmaxf(m, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                               v, v, decltype(ctrl)::value, 0xf, 0xf, false)));
+  };
+  turn(std::integral_constant<int, 0x121>{});  // row_ror:1
+  turn(std::integral_constant<int, 0x122>{});
+  turn(std::integral_constant<int, 0x124>{});
+  turn(std::integral_constant<int, 0x128>{});
+  return m;
+}
+__device__ __forceinline__ float max_over_rows(float m) {
+  m = fmaxf(m, __shfl_xor(m, 16));
+  return fmaxf(m, __shfl_xor(m, 32));
+}
+
+// The largest finite magnitude of values v[0], v[step], ...; NO_INF: it is known that none is
+// Inf (a maximum passes over NaN by itself).
+template <int N, bool NO_INF>
+__device__ __forceinline__ float top_of(const float* v, int step) {
+  float m = 0.0f;
 #pragma unroll
-  for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  for (int i = 0; i < N; ++i) {
+    const float a = fabsf(v[i * step]);
+    m = fmaxf(m, NO_INF || a < __builtin_inff() ? a : 0.0f);
+  }
   return m;
 }
 
+template <bool EXP>
+__device__ __forceinline__ void put_scale(void* S, int64_t ld, int row, int block, int e) {
+  if constexpr (EXP) ((uint8_t*)S)[block * ld + row] = (uint8_t)(e + 127);
+  else ((float*)S)[row * ld + block] = power_of_two(e);
+}
+
 // 1 x 128 blocks, no transpose: 16 lanes a block, 16 blocks a workgroup.
-template <class T>
+template <class T, bool EXP>
 __global__ __launch_bounds__(256) void lp_quantize_rows_kernel(QuantArgs p) {
   const int kb = (p.cols + kBlock - 1) / kBlock;
   const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -88,55 +119,37 @@ __global__ __launch_bounds__(256) void lp_quantize_rows_kernel(QuantArgs p) {
   const int c = b * kBlock + (threadIdx.x & 15) * 8;
   float v[8];
   load8<T>((const typename T::type*)p.X + row * p.ldx + c, p.cols - c, v);
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, finite_bits(v[i]));
-  const int e = scale_exponent(max_over_16(m));
+  float top = max_over_16(top_of<8, true>(v, 1));
+  if (top == __builtin_inff()) top = max_over_16(top_of<8, false>(v, 1));
+  const int e = scale_exponent(top);
   store_bytes8(p.Q + row * p.ldq + c, p.cols - c, to_fp8x8(v, 1, power_of_two(-e)));
-  if ((threadIdx.x & 15) == 0) p.S[row * p.lds + b] = power_of_two(e);
+  if ((threadIdx.x & 15) == 0) put_scale<EXP>(p.S, p.lds, row, b, e);
 }
 
-// 128 x 128 tiles: thread (ty, tx) of 16 x 16 holds rows 8 ty .. + 7, columns 8 tx .. + 7, so
-// that X is read once whatever is asked for.  ROWS: rows of a block (1 or 128).
-template <class T, int ROWS>
-__global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
-  __shared__ uint32_t part[4][kBlock];
-  constexpr int kStride = kBlock + 16;
-  __shared__ __align__(16) uint8_t turn[kBlock * kStride];
+// A 128 x 128 tile whose values the threads hold (lp_quantize_tile_kernel).
+constexpr int kTurnStride = kBlock + 16;
+template <int ROWS, bool EXP, bool NO_INF>
+__device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&v)[8][8],
+                                              float (&part)[4][kBlock], uint8_t* turn) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, wave = tid >> 6;
   const int r0 = blockIdx.y * kBlock, c0 = blockIdx.x * kBlock;
   const int c = c0 + tx * 8;
-  float v[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = r0 + ty * 8 + i;
-    load8<T>((const typename T::type*)p.X + r * p.ldx + c, r < p.rows ? p.cols - c : 0, v[i]);
-  }
   if constexpr (ROWS == 1) {
     if (p.Q != nullptr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = r0 + ty * 8 + i;
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, finite_bits(v[i][j]));
-        const int e = scale_exponent(max_over_16(m));
+        const int e = scale_exponent(max_over_16(top_of<8, NO_INF>(v[i], 1)));
         if (r < p.rows) {
           store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, power_of_two(-e)));
-          if (tx == 0) p.S[r * p.lds + blockIdx.x] = power_of_two(e);
+          if (tx == 0) put_scale<EXP>(p.S, p.lds, r, blockIdx.x, e);
         }
       }
     }
     if (p.QT == nullptr) return;
-    uint32_t m[8];
+    float m[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[j] = max(m[j], finite_bits(v[i][j]));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32));
-    }
+    for (int j = 0; j < 8; ++j) m[j] = max_over_rows(top_of<8, NO_INF>(&v[0][j], 8));
     if ((tid & 63) < 16) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) part[wave][tx * 8 + j] = m[j];
@@ -145,21 +158,20 @@ __global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int k = tx * 8 + j;
-      const int e = scale_exponent(max(max(part[0][k], part[1][k]), max(part[2][k], part[3][k])));
-      *(uint2*)(turn + k * kStride + ty * 8) = to_fp8x8(&v[0][j], 8, power_of_two(-e));
-      if (ty == 0 && c0 + k < p.cols) p.ST[(c0 + k) * p.ldst + blockIdx.y] = power_of_two(e);
+      const int e =
+          scale_exponent(fmaxf(fmaxf(part[0][k], part[1][k]), fmaxf(part[2][k], part[3][k])));
+      *(uint2*)(turn + k * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, power_of_two(-e));
+      if (ty == 0 && c0 + k < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + k, blockIdx.y, e);
     }
   } else {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, finite_bits(v[i][j]));
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, top_of<8, NO_INF>(v[i], 1));
+    m = max_over_rows(max_over_16(m));
     if ((tid & 63) == 0) part[0][wave] = m;
     __syncthreads();
-    const int e = scale_exponent(max(max(part[0][0], part[0][1]), max(part[0][2], part[0][3])));
+    const int e =
+        scale_exponent(fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3])));
     const float inv = power_of_two(-e);
     if (p.Q != nullptr) {
 #pragma unroll
@@ -167,28 +179,60 @@ __global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
         const int r = r0 + ty * 8 + i;
         if (r < p.rows) store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, inv));
       }
-      if (tid == 0) p.S[blockIdx.y * p.lds + blockIdx.x] = power_of_two(e);
+      if constexpr (EXP) {
+        if (tid < kBlock && r0 + tid < p.rows) put_scale<EXP>(p.S, p.lds, r0 + tid, blockIdx.x, e);
+      } else {
+        if (tid == 0) put_scale<EXP>(p.S, p.lds, blockIdx.y, blockIdx.x, e);
+      }
     }
     if (p.QT == nullptr) return;
-    if (tid == 0) p.ST[blockIdx.x * p.ldst + blockIdx.y] = power_of_two(e);
+    if constexpr (EXP) {
+      if (tid < kBlock && c0 + tid < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + tid, blockIdx.y, e);
+    } else {
+      if (tid == 0) put_scale<EXP>(p.ST, p.ldst, blockIdx.x, blockIdx.y, e);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      *(uint2*)(turn + (tx * 8 + j) * kStride + ty * 8) = to_fp8x8(&v[0][j], 8, inv);
+      *(uint2*)(turn + (tx * 8 + j) * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, inv);
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = i * 32 + (tid >> 3), r = r0 + (tid & 7) * 16;
     if (c0 + k >= p.cols) continue;
-    const uint4 q = *(const uint4*)(turn + k * kStride + (tid & 7) * 16);
+    const uint4 q = *(const uint4*)(turn + k * kTurnStride + (tid & 7) * 16);
     uint8_t* to = p.QT + (c0 + k) * p.ldqt + r;
     if (r + 16 <= p.rows) {
-      __builtin_memcpy(to, &q, 16);
+      typedef uint32_t group __attribute__((ext_vector_type(4), aligned(1)));
+      *(group*)to = group{q.x, q.y, q.z, q.w};
     } else {
       store_bytes8(to, p.rows - r, make_uint2(q.x, q.y));
       store_bytes8(to + 8, p.rows - r - 8, make_uint2(q.z, q.w));
     }
   }
+}
+
+// 128 x 128 tiles: thread (ty, tx) of 16 x 16 holds rows 8 ty .. + 7, columns 8 tx .. + 7, so
+// that X is read once whatever is asked for.  ROWS: rows of a block (1 or 128).
+template <class T, int ROWS, bool EXP>
+__global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
+  __shared__ float part[4][kBlock];
+  __shared__ __align__(16) uint8_t turn[kBlock * kTurnStride];
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.y * kBlock + (tid >> 4) * 8, c = blockIdx.x * kBlock + (tid & 15) * 8;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8<T>((const typename T::type*)p.X + (r0 + i) * p.ldx + c,
+             r0 + i < p.rows ? p.cols - c : 0, v[i]);
+  // one maximum decides for the workgroup whether Inf has to be looked for
+  float any = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) any = fmaxf(any, top_of<8, true>(v[i], 1));
+  if (__syncthreads_or(any == __builtin_inff()))
+    quantize_tile<ROWS, EXP, false>(p, v, part, turn);
+  else
+    quantize_tile<ROWS, EXP, true>(p, v, part, turn);
 }
 
 }  // namespace gemmlp

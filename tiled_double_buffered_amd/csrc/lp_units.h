@@ -36,7 +36,10 @@ template <> struct UnitOf<8> : Unit<F32, false, false, true, 0> {};
 template <> struct UnitOf<9> : Unit<F8, true, true, false, 0> {};
 template <> struct UnitOf<10> : Unit<F8, true, true, false, 1> {};
 template <> struct UnitOf<11> : Unit<F8, true, true, false, 2> {};
-constexpr int kUnits = 12;
+// 8-bit with exponents for scales: through the 8-bit instruction, and through the 16-bit one
+template <> struct UnitOf<12> : Unit<F8, true, true, false, 3> {};
+template <> struct UnitOf<13> : Unit<F8, true, true, false, 4> {};
+constexpr int kUnits = 14;
 
 // The kernel of a tile, or NULL where the unit has none; staged: for operands of any alignment.
 LpKernel pipe_kernel_0(int tile, bool staged);
@@ -51,5 +54,7 @@ LpKernel pipe_kernel_8(int tile, bool staged);
 LpKernel pipe_kernel_9(int tile, bool staged);
 LpKernel pipe_kernel_10(int tile, bool staged);
 LpKernel pipe_kernel_11(int tile, bool staged);
+LpKernel pipe_kernel_12(int tile, bool staged);
+LpKernel pipe_kernel_13(int tile, bool staged);
 
 }  // namespace gemmlp
