@@ -22,7 +22,7 @@ def _say(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
-@pytest.fixture(params=["", "256", "128", "64"], ids=lambda v: f"tile{v or '-auto'}")
+@pytest.fixture(params=["", "256", "128", "64", "644"], ids=lambda v: f"tile{v or '-auto'}")
 def tile(request, monkeypatch):
     """Every tile's kernel, wherever it takes the operands, besides the one that is chosen."""
     if request.param:

@@ -108,7 +108,7 @@ static bool word_rows(const void* p, int64_t ld, int64_t stride, int bytes) {
          ld <= (int64_t)0xFFFF0000u / 256 / bytes;
 }
 
-// GEMM_LP_TILE=<256|128|64> forces a tile where it has a kernel, for tests and measurement, as
+// GEMM_LP_TILE=<256|128|64|644> forces a tile where it has a kernel, for tests and measurement, as
 // GEMMF32_VARIANT does for the FP32 product.
 static int env_tile() {
   const char* v = std::getenv("GEMM_LP_TILE");
@@ -121,19 +121,20 @@ static int env_tile() {
 struct StepCost {
   double alone, full;
 };
-constexpr int kFit[kTileCount] = {1, 2, 4};
-constexpr StepCost kStep16[kTileCount] = {{1.40, 1.75}, {0.80, 0.56}, {0.45, 0.24}};
-constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.58}};
-constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}};
-constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.30, 1.10}, {0.60, 0.36}};
+constexpr int kFit[kTileCount] = {1, 2, 4, 1};
+constexpr StepCost kStep16[kTileCount] = {{1.40, 1.75}, {0.80, 0.60}, {0.45, 0.24}, {0.25, 0.25}};
+constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.58}, {0.58, 0.58}};
+constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}, {0.24, 0.24}};
+constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.30, 1.10}, {0.60, 0.36}, {0.37, 0.37}};
 
 // The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number,
 // and the longest of them has `skew` times the average's K steps.
+constexpr int kForced[kTileCount] = {256, 128, 64, 644};
 template <class F>
 static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) {
   if (const int forced = env_tile()) {
     for (int t = 0; t < kTileCount; ++t)
-      if (kTiles[t].bm == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
+      if (kForced[t] == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
   }
   const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 || unit == 13 ? kStep8Exact : kStep8;
   int best = -1;

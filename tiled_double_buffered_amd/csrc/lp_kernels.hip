@@ -12,10 +12,10 @@
 
 namespace gemmlp {
 
-template <class U, int BM, int BN, int WM, int WN, bool STAGED>
+template <class U, int BM, int BN, int WM, int WN, bool STAGED, int KG = 1>
 constexpr LpKernel pipe() {
   return &lp_pipe_kernel<typename U::type, U::AKC, U::BKC, U::WGRAD, BM, BN, WM, WN, U::HOW,
-                         STAGED>;
+                         STAGED, KG>;
 }
 
 template <class U>
@@ -33,6 +33,8 @@ static LpKernel pick(int tile, bool staged) {
     return staged ? pipe<U, 128, 128, 2, 2, true>() : pipe<U, 128, 128, 2, 2, false>();
   if (tile == kTile64)
     return staged ? pipe<U, 64, 64, 2, 2, true>() : pipe<U, 64, 64, 2, 2, false>();
+  if (tile == kTile64K4)
+    return staged ? pipe<U, 64, 64, 2, 2, true, 4>() : pipe<U, 64, 64, 2, 2, false, 4>();
   return nullptr;
 }
 

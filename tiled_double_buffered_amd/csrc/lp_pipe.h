@@ -470,9 +470,12 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
 }
 
 // STAGED: operands of any alignment, through registers.
+// KG: groups of waves that share the tile, each with slots of its own and every KG-th K step;
+// they add their sums through LDS in a fixed order.  With fewer tiles than CUs one group would
+// wait for memory most of the time.
 template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW,
-          bool STAGED>
-__global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
+          bool STAGED, int KG>
+__global__ __launch_bounds__(WM * WN * 64 * KG) void lp_pipe_kernel(LpArgs p) {
   constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
   constexpr bool F8T = T::BYTES == 1;
@@ -482,8 +485,10 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
   using OS = ScaleCopy<HOW, BM, BN>;
   constexpr int SCALES = F8T ? OS::BYTES : 0;
   constexpr int SLOT = OA::BYTES + OB::BYTES + SCALES;
-  __shared__ __align__(1024) char lds[2 * SLOT];
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ __align__(1024) char all_lds[KG * 2 * SLOT];
+  const int group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / THREADS);
+  char* lds = all_lds + group * 2 * SLOT;
+  const int tid = KG == 1 ? threadIdx.x : threadIdx.x % THREADS, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
@@ -531,18 +536,25 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
       }
     };
 
-    issue(0, 0);
-    settle(0);
-    for (int kt = 0; kt < steps; ++kt) {
+    if (group < steps) {
+      issue(group, 0);
+      settle(0);
+    }
+    const int rounds = (steps + KG - 1) / KG;
+    for (int it = 0; it < rounds; ++it) {
+      const int kt = it * KG + group;
       part_barrier<0>();
-      if (kt + 1 < steps) issue(kt + 1, (kt + 1) & 1);
-      char* sa = lds + (kt & 1) * SLOT;
+      if (kt + KG < steps) issue(kt + KG, (it + 1) & 1);
+      char* sa = lds + (it & 1) * SLOT;
       char* sb = sa + OA::BYTES;
-      if (!STAGED && (AKC || BKC) && tail != 0 && kt + 1 == steps) {
-        if constexpr (AKC) OA::clear_tail(sa, tail, tid, THREADS);
-        if constexpr (BKC) OB::clear_tail(sb, tail, tid, THREADS);
+      if (!STAGED && (AKC || BKC) && tail != 0 && it + 1 == rounds) {
+        if (KG == 1 || kt + 1 == steps) {
+          if constexpr (AKC) OA::clear_tail(sa, tail, tid, THREADS);
+          if constexpr (BKC) OB::clear_tail(sb, tail, tid, THREADS);
+        }
         __syncthreads();
       }
+      if (KG > 1 && kt >= steps) continue;
       if constexpr (!F8T) {
         int8v a[SM], b[SN];
 #pragma unroll
@@ -620,9 +632,31 @@ __global__ __launch_bounds__(WM * WN * 64) void lp_pipe_kernel(LpArgs p) {
           if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (kt + 1 < steps) settle((kt + 1) & 1);
+      if (kt + KG < steps) settle((it + 1) & 1);
+    }
+    if constexpr (KG > 1) {
+      // the groups' sums, in their order: lane by lane, 16 bytes at a time
+      static_assert(SM * SN * 16 * THREADS <= 2 * SLOT, "a group's sums in its slots");
+      __syncthreads();
+      if (group > 0) {
+#pragma unroll
+        for (int i = 0; i < SM; ++i)
+#pragma unroll
+          for (int j = 0; j < SN; ++j)
+            *(float4v*)(lds + ((i * SN + j) * THREADS + tid) * 16) = acc[i][j];
+      }
+      __syncthreads();
+      if (group > 0) return;
+#pragma unroll
+      for (int o = 1; o < KG; ++o)
+#pragma unroll
+        for (int i = 0; i < SM; ++i)
+#pragma unroll
+          for (int j = 0; j < SN; ++j)
+            acc[i][j] += *(const float4v*)(lds + o * 2 * SLOT + ((i * SN + j) * THREADS + tid) * 16);
     }
   }
+  if (KG > 1 && group > 0) return;
 
   constexpr int OUT = !F8T ? T::CODE : exact(HOW) ? -1 : GEMM_LP_BF16;
   store_tile<OB, OUT>(p, w, wn, g, acc,

@@ -6,12 +6,12 @@
 
 namespace gemmlp {
 
-// Tiles of the pipelined kernel.
-enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileCount = 3 };
+// Tiles of the pipelined kernels (K4: four groups of waves share the K steps).
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64K4 = 3, kTileCount = 4 };
 struct TileSize {
   int bm, bn, threads;
 };
-constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}, {64, 64, 256}};
+constexpr TileSize kTiles[] = {{256, 256, 512}, {128, 128, 256}, {64, 64, 256}, {64, 64, 1024}};
 
 template <class T, bool A, bool B, bool W, int H>
 struct Unit {
