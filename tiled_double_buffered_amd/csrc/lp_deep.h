@@ -8,9 +8,9 @@
 // lower half A2.  A step has two barriers:
 //   middle (before the products of the last A1 fragment): B, A1 of this step are read by all
 //     waves, A2 of this step has landed; the copies of B, A1 (and scales) two steps on start;
-//   end (before the products of the last A2 fragment): A2 of this step is read, B and A1 of
-//     the next have landed; the copies of A2 two steps on start, and the next step's first
-//     fragments are read while this step's last products run.
+//   end (before the products of the last two A2 fragments): A2 of this step is read, B and A1
+//     of the next have landed; the copies of A2 two steps on start.  The last two rows of
+//     products go column by column, so that B's fragments are replaced one by one.
 // A tile of 128 rows or fewer leaves A2 and its products out.
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
@@ -27,16 +27,24 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
   constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
   constexpr bool F8T = T::BYTES == 1;
-  static_assert(!F8T || !exact(HOW), "not enough registers");
+  static_assert(!F8T || HOW == kFast8Blocks || HOW == kScaled8, "not enough registers");
   constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
   using OA = PipeOperand<T, AKC, BM / 2, HALF, WAVES>;
   using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
   using OS = ScaleCopy<HOW, BM, BN>;
-  constexpr int SCALES = F8T ? OS::BYTES : 0;
+  // FP32 scales: 16 bytes, four steps' worth, of every row of A and column of B at once, into
+  // two tables in turn (64 rows' scales lie in 64 lines of the cache, and a copy takes a line a
+  // cycle).  So that a wave's count of copies is the same in every step, the three steps between
+  // copy nothing, zeros, to a place of their own.
+  constexpr bool QUADS = F8T && !OS::EXP;
+  constexpr int SCALES = F8T && !QUADS ? OS::BYTES : 0;
+  constexpr int TABLE = (BM + BN) * 16;
   constexpr int A1 = 0, A2 = OA::BYTES, B0 = 2 * OA::BYTES, S0 = B0 + OB::BYTES;
   constexpr int SLOT = S0 + SCALES;
+  constexpr int TABLES = 2 * SLOT, NOWHERE = TABLES + 2 * TABLE;
   constexpr int FIRST = OA::COPIES + OB::COPIES + (F8T ? 1 : 0), SECOND = OA::COPIES;
-  __shared__ __align__(1024) char lds[2 * SLOT];
+  __shared__ __align__(1024) char lds[2 * SLOT + (QUADS ? 2 * TABLE + WAVES * 1024 : 0)];
+  static_assert(sizeof(lds) <= 160 * 1024, "LDS of one CU");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -59,14 +67,36 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
     OS os;
     if constexpr (F8T) os.init(p, w, steps, wave, lane);
+    auto issue_scales = [&](int kt, int4v r) {
+      if constexpr (QUADS) {
+        const bool real = (kt & 3) == 0;
+        r[2] = real ? r[2] : 0;
+        copy16(lds0 + (uint32_t)((real ? TABLES + (kt >> 2 & 1) * TABLE : NOWHERE) + wave * 1024),
+               r, os.off);
+      } else if constexpr (F8T) {
+        os.copy(r, lds0 + (uint32_t)((kt & 1) * SLOT + S0));
+      }
+    };
+    // (each is called for one step after another)
+    Walk to_b, to_a1, to_a2, to_s;
+    ob.start(to_b);
+    oa1.start(to_a1);
+    oa2.start(to_a2);
+    if constexpr (F8T) os.start(to_s);
     auto issue_first = [&](int kt) {
       const uint32_t at = lds0 + (uint32_t)((kt & 1) * SLOT);
-      ob.issue(kt, at + B0, wave);
-      oa1.issue(kt, at + A1, wave);
-      if constexpr (F8T) os.issue(kt, at + S0);
+      const int4v rb = to_b.next(), ra = to_a1.next();
+#pragma unroll
+      for (int i = 0; i < OB::COPIES; ++i) ob.copy(i, rb, at + B0, wave);
+#pragma unroll
+      for (int i = 0; i < OA::COPIES; ++i) oa1.copy(i, ra, at + A1, wave);
+      if constexpr (F8T) issue_scales(kt, to_s.next());
     };
     auto issue_second = [&](int kt) {
-      oa2.issue(kt, lds0 + (uint32_t)((kt & 1) * SLOT + A2), wave);
+      const uint32_t at = lds0 + (uint32_t)((kt & 1) * SLOT);
+      const int4v ra = to_a2.next();
+#pragma unroll
+      for (int i = 0; i < OA::COPIES; ++i) oa2.copy(i, ra, at + A2, wave);
     };
     // Where k is contiguous, a row's last K step ends inside it and the rest came from beyond
     // the row: the last step's fragments are masked (a lane's 16-byte groups g and g + 4).
@@ -80,36 +110,30 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       }
     }
 
-    int8v b[SN], a[2 * OA::READ];
-    float s_a[SM];              // kFast8
-    float4v s_b[SN];
-    int x_a[SM], x_b[SN];       // kScaled8
-    // fragments of A, READ of them at a time, into the two sets in turn
+    int8v b[SN], a[OA::READ == 1 ? 4 : 2 * OA::READ];
+    float s_a[SM];         // kFast8Blocks: of the row, times the block's of B
+    int x_a[SM], x_b[SN];  // kScaled8
+    // Fragment i of A is held in a[set_of(i)] from before its products to their end; the first
+    // of a step is read while the last two of the step before are still in use.
+    auto set_of = [](int i) { return OA::READ > 1 ? i : i == 0 ? 2 : i == SM - 1 ? 3 : 1 - (i & 1); };
+    static_assert(OA::READ == 1 || 2 * OA::READ == SM, "two groups of fragments");
     auto read_a = [&](const char* slot, int i, bool masked) {
-      const int at = (i / OA::READ & 1) * OA::READ;
-      (i < SH ? oa1 : oa2).read(slot + (i < SH ? A1 : A2), i % SH, a + at);
-      if (AKC && masked) a[at] &= last_mask;
+      (i < SH ? oa1 : oa2).read(slot + (i < SH ? A1 : A2), i % SH, a + set_of(i));
+      if (AKC && masked) a[set_of(i)] &= last_mask;
     };
-    auto set_of = [](int i) { return (i / OA::READ & 1) * OA::READ + i % OA::READ; };
-    auto read_scales = [&](const char* slot) {
-      if constexpr (F8T) {
-        const char* table = slot + S0;
+    auto read_scales = [&](int kt) {
+      if constexpr (QUADS) {
+        const char* table = lds + TABLES + (kt >> 2 & 1) * TABLE + (kt & 3) * 4;
+        const float block = *(const float*)(table + (BM + wn) * 16);
+#pragma unroll
+        for (int i = 0; i < SM; ++i) s_a[i] = *(const float*)(table + row_of(i) * 16) * block;
+      } else if constexpr (F8T) {
+        const char* table = lds + (kt & 1) * SLOT + S0;
         if constexpr (HOW == kScaled8) {
 #pragma unroll
           for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, row_of(i));
 #pragma unroll
           for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
-        } else {
-#pragma unroll
-          for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, row_of(i));
-          if constexpr (HOW == kFast8Blocks) {
-            const float block = OS::b(table, wn);
-#pragma unroll
-            for (int i = 0; i < SM; ++i) s_a[i] *= block;
-          } else {
-#pragma unroll
-            for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
-          }
         }
       }
     };
@@ -117,8 +141,11 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     // matrix cores work on the next ones.
     constexpr int kLag = 2, kRing = 3;
     float4v d[kRing];
-    auto product_of = [&](int s, const int8v& fa) {  // product s = i * SN + j of the step
-      const int i = s / SN, j = s % SN;
+    // Product number s of a step: row by row, the last two rows column by column.
+    constexpr int ROWS = SM - 2;
+    auto row_at = [](int s) { return s < ROWS * SN ? s / SN : ROWS + (s & 1); };
+    auto col_at = [](int s) { return s < ROWS * SN ? s % SN : (s - ROWS * SN) / 2; };
+    auto product_of = [&](int s, int i, int j, const int8v& fa) {
       if constexpr (HOW == kScaled8) {
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], fa, acc[i][j], 0, 0, 0,
                                                                      x_b[j], 0, x_a[i]);
@@ -132,19 +159,18 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         acc[i][j] = mma_half<T>(half_of(b[j], 1), half_of(fa, 1), acc[i][j]);
       }
     };
-    auto product = [&](int s) { product_of(s, a[set_of(s / SN)]); };
-    auto add = [&](int s) {
+    auto add_to = [&](int s, int i, int j) {
       if constexpr (F8T && HOW != kScaled8) {
-        if (s < 0) return;
-        const int i = s / SN, j = s % SN;
         const float4v v = d[s % kRing];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] += v[r] * (HOW == kFast8Blocks ? s_a[i] : s_a[i] * s_b[j][r]);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] += v[r] * s_a[i];
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-
+    auto product = [&](int s) { product_of(s, row_at(s), col_at(s), a[set_of(row_at(s))]); };
+    auto add = [&](int s) {
+      if (s >= 0) add_to(s, row_at(s), col_at(s));
+    };
     // Step kt, of which LEFT follow (2: two or more).  No branch inside: values that live across
     // branches cost registers that the wave does not have.
     auto step = [&](auto left, int kt) {
@@ -155,59 +181,59 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       int4v rb, ra, rs;  // sources of the copies for step kt + 2
       int done = 0;      // of them (a constant wherever it is used)
       if constexpr (LEFT == 0) {
-        if constexpr (AKC) a[0] &= last_mask;
+        if constexpr (AKC) a[set_of(0)] &= last_mask;
         if constexpr (BKC) {
 #pragma unroll
           for (int j = 0; j < SN; ++j) b[j] &= last_mask;
         }
       }
 #pragma unroll
-      for (int i = 0; i < SM; ++i) {
-        if (i == SH - 1) {
+      for (int s = 0; s < SM * SN; ++s) {
+        const int i = row_at(s), j = col_at(s);
+        if (s == (SH - 1) * SN) {
           part_barrier<LEFT == 0 ? 0 : FIRST + SECOND>();
           if constexpr (LEFT == 2) {
-            rb = ob.words(kt + 2);
-            ra = oa1.words(kt + 2);
-            if constexpr (F8T) rs = os.words(kt + 2);
+            rb = to_b.next();
+            ra = to_a1.next();
+            if constexpr (F8T) rs = to_s.next();
           }
         }
-        if (i == SM - 1 && LEFT > 0) {
+        if (s == ROWS * SN && LEFT > 0) {
           part_barrier<LEFT == 2 ? SECOND + FIRST : SECOND>();
-          if constexpr (LEFT == 2) ra = oa2.words(kt + 2);
+          if constexpr (LEFT == 2) ra = to_a2.next();
           read_a(next, 0, false);
         }
-        if (i + 1 < SM && (i + 1) % OA::READ == 0) read_a(slot, i + 1, LEFT == 0);
+        if (j == 0 && i < ROWS && (i + 1) % OA::READ == 0) read_a(slot, i + 1, LEFT == 0);
+        if (OA::READ == 1 && s == (ROWS - 1) * SN + 1)  // before the end barrier
+          read_a(slot, SM - 1, LEFT == 0);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < SN; ++j) {
-          product(i * SN + j);
-          add(i * SN + j - kLag);
-          // The copies go out between the products: a wave waits for each to be taken, 16
-          // cycles a copy for all waves of the CU together.
-          if constexpr (LEFT == 2) {
-            if (i >= SH - 1 && i < SM - 1) {
-              constexpr int SLOTS = SH * SN;
-              const int at = (i - (SH - 1)) * SN + j;
-              while (done * SLOTS < (at + 1) * FIRST) {
-                if (done < OB::COPIES) ob.copy(done, rb, to + B0, wave);
-                else if (done < OB::COPIES + OA::COPIES) oa1.copy(done - OB::COPIES, ra, to + A1, wave);
-                else if constexpr (F8T) os.copy(rs, to + S0);
-                ++done;
-              }
-            } else if (i == SM - 1 && j * OA::COPIES / SN != (j + 1) * OA::COPIES / SN) {
-              oa2.copy(j * OA::COPIES / SN, ra, to + A2, wave);
+        product(s);
+        add(s - kLag);
+        // The copies go out between the products: a wave waits for each to be taken, 16 cycles
+        // a copy for all waves of the CU together.
+        if constexpr (LEFT == 2) {
+          if (s >= (SH - 1) * SN && s < ROWS * SN) {
+            constexpr int SLOTS = (ROWS - SH + 1) * SN;
+            while (done * SLOTS < (s - (SH - 1) * SN + 1) * FIRST) {
+              if (done < OB::COPIES) ob.copy(done, rb, to + B0, wave);
+              else if (done < OB::COPIES + OA::COPIES) oa1.copy(done - OB::COPIES, ra, to + A1, wave);
+              else if constexpr (F8T) issue_scales(kt + 2, rs);
+              ++done;
             }
-            __builtin_amdgcn_sched_barrier(0);
+          } else if (s >= ROWS * SN) {
+            constexpr int SLOTS = 2 * SN;
+            const int n = s - ROWS * SN;
+            if (n * OA::COPIES / SLOTS != (n + 1) * OA::COPIES / SLOTS)
+              oa2.copy(n * OA::COPIES / SLOTS, ra, to + A2, wave);
           }
-          if (i == SM - 1 && LEFT > 0 && (j + 1) % OB::READ == 0)  // done with these columns
-            ob.read(next + B0, j + 1 - OB::READ, b + j + 1 - OB::READ);
-          if (i == SM - 1) __builtin_amdgcn_sched_barrier(0);
         }
+        if (LEFT > 0 && s >= ROWS * SN && row_at(s) == SM - 1 && (j + 1) % OB::READ == 0)
+          ob.read(next + B0, j + 1 - OB::READ, b + j + 1 - OB::READ);  // done with these columns
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int s = SM * SN - kLag; s < SM * SN; ++s) add(s);
-      if constexpr (LEFT > 0) read_scales(next);
+      if constexpr (LEFT > 0) read_scales(kt + 1);
     };
     using Two = std::integral_constant<int, 2>;
     using One = std::integral_constant<int, 1>;
@@ -226,7 +252,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         for (int j = 0; j < SN; j += OB::READ) ob.read(slot + B0, j, b + j);
 #pragma unroll
         for (int i = 0; i < SH; i += OA::READ) oa1.read(slot + A1, i, h + i);
-        read_scales(slot);
+        read_scales(kt);
         part_barrier<63>();  // (the copies stay open)
         if (kt + 2 < steps) issue_first(kt + 2);
         if (kt + 1 == steps) {
@@ -241,8 +267,8 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         }
 #pragma unroll
         for (int s = 0; s < SH * SN + kLag; ++s) {
-          if (s < SH * SN) product_of(s, h[s / SN]);
-          if (s >= kLag) add(s - kLag);
+          if (s < SH * SN) product_of(s, s / SN, s % SN, h[s / SN]);
+          if (s >= kLag) add_to(s - kLag, (s - kLag) / SN, (s - kLag) % SN);
         }
       }
       store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
@@ -261,7 +287,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     read_a(lds, 0, false);
 #pragma unroll
     for (int j = 0; j < SN; j += OB::READ) ob.read(lds + B0, j, b + j);
-    read_scales(lds);
+    read_scales(0);
     for (int kt = 0; kt + 2 < steps; ++kt) step(Two{}, kt);
     if (steps > 1) step(One{}, steps - 2);
     step(None{}, steps - 1);

@@ -45,6 +45,42 @@ __device__ __forceinline__ int4v buffer_words(const char* base, int64_t bytes) {
   return r;
 }
 
+// The descriptors of an operand's K steps, one after another, by scalar arithmetic alone (a wave
+// that computes them between its products holds the matrix cores up).
+struct Walk {
+  uint32_t lo, hi;   // base of the next step
+  uint32_t rem_lo;   // bytes from there on, rounded up to whole words
+  int rem_hi;
+  uint32_t step_lo, step_hi;
+  static __device__ __forceinline__ uint32_t scalar(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+  }
+  __device__ __forceinline__ void init(const char* base, int64_t left, int64_t step) {
+    const uint64_t b = (uint64_t)(uintptr_t)base, n = (uint64_t)((left + 3) & ~(int64_t)3);
+    lo = scalar((uint32_t)b), hi = scalar((uint32_t)(b >> 32));
+    rem_lo = scalar((uint32_t)n), rem_hi = (int)scalar((uint32_t)(n >> 32));
+    step_lo = scalar((uint32_t)step), step_hi = scalar((uint32_t)((uint64_t)step >> 32));
+    // a load may read a scalar that vector code wrote five wait states later, and the compiler
+    // does not see the loads
+    asm volatile("s_nop 4" : "+s"(lo), "+s"(hi), "+s"(rem_lo), "+s"(rem_hi));
+  }
+  __device__ __forceinline__ int4v next() {
+    int4v r;
+    r[0] = (int)lo;
+    r[1] = (int)hi;
+    uint32_t n = rem_lo;
+    n = rem_hi > 0 ? kMaxRange : n;
+    n = rem_hi < 0 ? 0u : n;
+    r[2] = (int)n;
+    r[3] = kBufferWord3;
+    const uint64_t b = ((uint64_t)hi << 32 | lo) + ((uint64_t)step_hi << 32 | step_lo);
+    lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+    const uint64_t m = ((uint64_t)(uint32_t)rem_hi << 32 | rem_lo) - ((uint64_t)step_hi << 32 | step_lo);
+    rem_lo = (uint32_t)m, rem_hi = (int)(uint32_t)(m >> 32);
+    return r;
+  }
+};
+
 // 16 (or 4) bytes of every lane into LDS at `lds` + lane * 16 (4); counted by vmcnt.  The
 // scalar write of M0 needs one wait state before the load.
 #pragma clang diagnostic push
@@ -149,6 +185,7 @@ struct PipeOperand {
   __device__ __forceinline__ int4v words(int kt) const {
     return buffer_words(base + kt * step, left - kt * step);
   }
+  __device__ __forceinline__ void start(Walk& walk) const { walk.init(base, left, step); }
   __device__ __forceinline__ void copy(int i, int4v r, uint32_t lds, int wave) const {
     copy16(__builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave + i * WAVES) * 1024u), r, off[i]);
   }
@@ -402,6 +439,7 @@ struct ScaleCopy {
   __device__ __forceinline__ int4v words(int kt) const {
     return buffer_words(base + kt * step, left - kt * step);
   }
+  __device__ __forceinline__ void start(Walk& walk) const { walk.init(base, left, step); }
   __device__ __forceinline__ void copy(int4v r, uint32_t table) const {
     copy4(__builtin_amdgcn_readfirstlane(table + to), r, off);
   }
