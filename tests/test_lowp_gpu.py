@@ -433,3 +433,45 @@ def test_graph_replays_follow_their_inputs():
         for got, ref in zip(held, step()):
             assert torch.equal(got, ref)
     del wq, ws
+
+
+# --------------------------------------------------------------------------- the layer of experts
+def test_expert_layer_trains_and_serves():
+    """The products together: the loss falls, and the layer served in 8 bits stays near.  Each
+    of the served form's two products in a row has inputs and weights off by at most half a step
+    of 2^-4 relative, four roundings that differ from the training form's: 4 * 2^-4."""
+    from tiled_double_buffered_amd import expert_layer as el
+    layer = el.ExpertLayer(256, 384, 6, DEV)
+    losses, x = el.train(layer, 500, 256, 12, DEV)
+    assert losses[-1] < 0.8 * losses[0] and all(b == b for b in losses)
+    serve = layer.served()
+    for n in (500, 33, 1):
+        with torch.no_grad():
+            ref = layer(x[:n]).float()
+        y = serve(x[:n]).float()
+        assert y.shape == ref.shape
+        assert (y - ref).norm() <= 4 * 2.0 ** -4 * ref.norm()
+
+
+def test_broadcast_weights_share_their_gradient():
+    """One matrix for all experts, as an expanded view: its gradient is the experts' sum."""
+    K, N, E = 40, 24, 3
+    x = torch.randint(-3, 4, (30, K), generator=_gen(91)).float().to(DEV)
+    w = torch.randint(-3, 4, (K, N), generator=_gen(92)).float().to(DEV).requires_grad_()
+    off = torch.tensor([0, 4, 4, 30], dtype=torch.int32, device=DEV)
+    y = tdb.linear_grouped(x, w.expand(E, K, N), off)
+    dy = torch.randint(-3, 4, (30, N), generator=_gen(93)).float().to(DEV)
+    (dw,) = torch.autograd.grad(y, w, dy)
+    assert torch.equal(y.detach(), x @ w.detach())  # whole numbers: exact
+    assert torch.equal(dw, x.t() @ dy)
+
+
+@pytest.mark.parametrize("op", ["fp8", "grouped"])
+def test_only_once_differentiable(op):
+    x = _randn(_gen(94), 8, 16).to(DEV).requires_grad_()
+    w = _randn(_gen(95), 1, 16, 8).to(DEV)
+    off = torch.tensor([0, 8], dtype=torch.int32, device=DEV)
+    y = tdb.linear_grouped(x, w, off) if op == "grouped" else tdb.linear_fp8(x, w[0].t().contiguous())
+    (dx,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()

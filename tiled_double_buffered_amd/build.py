@@ -53,12 +53,16 @@ def _run(cmd, **kw):
     return subprocess.run(cmd, check=True, **kw)
 
 
-def _units():
+def _units(poison: bool = False):
     """(name, source, extra flags) of every translation unit: the host code and reduction
     kernels, one unit per tile configuration, and the low-precision and expert-grouped
-    products, their pipelined kernels one unit per element type and operand order."""
-    units = [("gemm_f32", MAIN_SOURCE, []), ("gemm_lp", LP_SOURCE, [])]
+    products, their pipelined kernels one unit per element type and operand order (which the
+    LDS-poison build leaves out: the mode is the FP32 kernels')."""
+    units = [("gemm_f32", MAIN_SOURCE, [])]
     units += [(f"cfg{i}", CFG_SOURCE, [f"-DGEMMF32_CFG_ID={i}"]) for i in range(NUM_CONFIGS)]
+    if poison:
+        return units
+    units += [("gemm_lp", LP_SOURCE, [])]
     units += [(f"lp{i}", LP_UNIT_SOURCE, [f"-DLP_UNIT={i}"]) for i in range(NUM_LP_UNITS)]
     return units
 
@@ -77,7 +81,7 @@ def _library_jobs(poison: bool):
     flags = ["-DGEMMF32_LDS_POISON=1"] if poison else []
     out = LIB_POISON if poison else LIB
     objs, cmds = [], []
-    for name, src, extra in _units():
+    for name, src, extra in _units(poison):
         obj = os.path.join(obj_dir, name + ".o")
         objs.append(obj)
         cmds.append([HIPCC, *DEVICE_FLAGS, *flags, *extra, "-fPIC", "-c", src, "-o", obj])

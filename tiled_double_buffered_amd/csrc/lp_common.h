@@ -152,7 +152,7 @@ __device__ __forceinline__ void band_order(int id, int tiles_m, int tiles_n, int
 // Weight gradients: workgroup wg computes tile (tm, tn) of expert e.  The experts follow one
 // another and each expert's tiles are spread over all XCDs: their work goes by its rows, and
 // whole experts on one XCD left the others waiting (16384 rows of 32 experts, bf16, 4096 x
-// 2048: 483 us, against WGRAD_US).
+// 2048: 483 us, against 418).
 __device__ __forceinline__ void wgrad_tile(int wg, int per, int tiles_m, int tiles_n, int& e,
                                            int& tm, int& tn) {
   e = wg / per;

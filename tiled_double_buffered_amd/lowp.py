@@ -146,17 +146,23 @@ def _offsets(t, like, E=None):
 
 
 _nothing = contextlib.nullcontext()
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _here(t, stream):
+    """Whether a call can run as it is: on the current stream, its tensors on the current GPU
+    (or not on any, which the argument checks refuse)."""
+    if stream is not None or not isinstance(t, torch.Tensor):
+        return stream is None
+    index = t.get_device()
+    return index < 0 or index == _device()
 
 
 def _on(t, stream):
-    """The context a call runs in: the tensor's device, and `stream` where one is given."""
+    """The context another call runs in: the tensor's device, and `stream` where one is given."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return _nothing  # the argument checks refuse it
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return _nothing
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(t.device)
 
 
 # the current stream's handle without a torch.cuda.Stream around it (2 us less a call)
@@ -224,6 +230,8 @@ def quantize_fp8(x, block=(1, BLOCK), stream=None):
     and q the nearest 8-bit value of x / scale, ties to even.  Inf and NaN become NaN and
     leave the scale to the block's other values.  q's rows start at multiples of 16 bytes."""
     rows = _block_rows(block)
+    if _here(x, stream):
+        return _quantize(x, rows, True, False)[:2]
     with _on(x, stream):
         return _quantize(x, rows, True, False)[:2]
 
@@ -233,6 +241,8 @@ def quantize_fp8_pair(x, block=(1, BLOCK), stream=None):
     training step, which contracts over both.  With (128, 128) blocks qt and st are the
     transposes of q and s; with (1, 128) ones qt has blocks of 128 rows of x of its own."""
     rows = _block_rows(block)
+    if _here(x, stream):
+        return _quantize(x, rows, True, True)
     with _on(x, stream):
         return _quantize(x, rows, True, True)
 
@@ -289,6 +299,8 @@ def matmul_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, stream=None):
     ceil(K/128), one for each block of 128 x 128, or N x ceil(K/128), one for each row and
     block.  Sums are held in float32 and rounded once to out_dtype.  The product of two
     scales has to lie in float32's normal range."""
+    if _here(a, stream):
+        return _fp8(a, sa, b, sb, out_dtype)
     with _on(a, stream):
         return _fp8(a, sa, b, sb, out_dtype)
 
@@ -299,6 +311,8 @@ def matmul_fp8_grouped(a, sa, b, sb, offsets, out_dtype=torch.bfloat16, stream=N
     decrease; rows before the first and from the last on give zeros."""
     if offsets is None:
         raise TypeError("offsets must be a contiguous 1-D int32 tensor of E + 1 elements")
+    if _here(a, stream):
+        return _fp8(a, sa, b, sb, out_dtype, offsets)
     with _on(a, stream):
         return _fp8(a, sa, b, sb, out_dtype, offsets)
 
@@ -326,6 +340,8 @@ def matmul_grouped(x, w, offsets, transpose_w=False, stream=None):
     """y[t] = x[t] @ w[e] for the rows t of expert e, offsets[e] .. offsets[e+1] - 1: x is
     rows x K and w E x K x N (E x N x K with transpose_w), of one type, bfloat16, float16 or
     float32.  offsets as in `matmul_fp8_grouped`.  Sums are held in float32."""
+    if _here(x, stream):
+        return _grouped(x, w, offsets, transpose_w)
     with _on(x, stream):
         return _grouped(x, w, offsets, transpose_w)
 
@@ -350,6 +366,8 @@ def _grouped_wgrad(a, b, offsets):
 def matmul_grouped_wgrad(a, b, offsets, stream=None):
     """dw[e] = a_e^T @ b_e, E x M x N, over the rows of expert e: a is rows x M, b rows x N.
     An expert without rows gets zeros."""
+    if _here(a, stream):
+        return _grouped_wgrad(a, b, offsets)
     with _on(a, stream):
         return _grouped_wgrad(a, b, offsets)
 
@@ -432,13 +450,20 @@ def linear_fp8(x, w):
     along its rows; quantization itself counts as the identity."""
     if not isinstance(x, torch.Tensor) or x.dtype not in TYPES:
         raise TypeError(f"x must be a tensor of {_names(TYPES)}")
-    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise TypeError("w must be a 2-D tensor of x's type")
+    if x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"inner dimensions differ: {tuple(x.shape)} and {tuple(w.shape)}")
     if w.dtype != x.dtype:
         raise TypeError(f"x is {x.dtype}, w {w.dtype}")
-    with _on(x, None):
-        flat = _row_major(x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x)
-        y = _LinearFp8.apply(flat, _row_major(w))
+    _same_device(x, w)
+    flat = _row_major(x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x)
+    w = _row_major(w)
+    if _here(x, None):
+        y = _LinearFp8.apply(flat, w)
+    else:
+        with _on(x, None):
+            y = _LinearFp8.apply(flat, w)
     return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
 
 
@@ -469,6 +494,8 @@ def linear_grouped(x, w, offsets, transpose_w=False):
     experts without rows zeros in dw."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in TYPES:
         raise TypeError(f"x must be a 2-D tensor of {_names(TYPES)}")
+    x, transpose_w = _row_major(x), bool(transpose_w)
+    if _here(x, None):
+        return _LinearGrouped.apply(x, w, offsets, transpose_w)
     with _on(x, None):
-        return _LinearGrouped.apply(_row_major(x), w, offsets,
-                                    bool(transpose_w))
+        return _LinearGrouped.apply(x, w, offsets, transpose_w)
