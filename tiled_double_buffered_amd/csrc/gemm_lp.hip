@@ -76,7 +76,8 @@ static LpKernel pipe_kernel(int unit, int tile, bool staged) {
     case 10: return pipe_kernel_10(tile, staged);
     case 11: return pipe_kernel_11(tile, staged);
     case 12: return pipe_kernel_12(tile, staged);
-    default: return pipe_kernel_13(tile, staged);
+    case 13: return pipe_kernel_13(tile, staged);
+    default: return pipe_kernel_14(tile, staged);
   }
 }
 
@@ -136,7 +137,7 @@ static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) 
     for (int t = 0; t < kTileCount; ++t)
       if (kForced[t] == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
   }
-  const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 || unit == 13 ? kStep8Exact : kStep8;
+  const StepCost* cost = unit < 6 ? kStep16 : unit < 9 ? kStep32 : unit == 9 || unit >= 13 ? kStep8Exact : kStep8;
   int best = -1;
   double least = 0;
   for (int t = 0; t < kTileCount; ++t) {
@@ -280,7 +281,7 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
   // themselves; other results go through the 16-bit instruction, which cuts nothing.
   const bool fast = c_type == GEMM_LP_BF16 && K >= 1024;
-  const int unit = EXP ? (fast ? 12 : 13) : fast ? (b_block == 1 ? 11 : 10) : 9;
+  const int unit = EXP ? (fast ? 12 : 13) : b_block == 1 ? (fast ? 11 : 9) : fast ? 10 : 14;
   const bool staged = !(word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1));
   const int t = pick_tile(unit, staged, k_steps(K, 1), 1.0,
                           [&](int bm, int bn) { return expected_rows(a, bm, bn); });

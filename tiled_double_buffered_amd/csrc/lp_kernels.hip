@@ -29,8 +29,13 @@ static LpKernel pick(int tile, bool staged) {
     else if constexpr (U::HOW == kFast8Rows)
       return pipe<U, 256, 256, 2, 4, false>();
   }
-  if (tile == kTile128)
-    return staged ? pipe<U, 128, 128, 2, 2, true>() : pipe<U, 128, 128, 2, 2, false>();
+  if (tile == kTile128) {
+    // (these need a few registers more than two workgroups of a CU have)
+    if constexpr (T::BYTES == 1 && U::HOW == kExact8Rows)
+      if (staged) return nullptr;
+    return staged ? pipe<U, 128, 128, 2, 2, !(T::BYTES == 1 && U::HOW == kExact8Rows)>()
+                  : pipe<U, 128, 128, 2, 2, false>();
+  }
   if (tile == kTile64)
     return staged ? pipe<U, 64, 64, 2, 2, true>() : pipe<U, 64, 64, 2, 2, false>();
   if (tile == kTile64K4)

@@ -385,15 +385,25 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
 }
 
 // How 8-bit values are multiplied and scaled:
-//   kExact8: through the 16-bit instruction, FP32 scales (B's by blocks of 128 columns or column
-//     by column);
+//   kExact8Blocks, kExact8Rows: through the 16-bit instruction, FP32 scales, B's by blocks of
+//     128 columns or column by column;
 //   kFast8Blocks, kFast8Rows: through the 8-bit instruction, B's scales by blocks, by columns;
 //   kScaled8: through the 8-bit instruction, which applies the scales itself: they are powers of
 //     two, one exponent byte for each row and column;
 //   kExactScaled8: such scales, through the 16-bit instruction.
-enum { kExact8 = 0, kFast8Blocks = 1, kFast8Rows = 2, kScaled8 = 3, kExactScaled8 = 4 };
+enum {
+  kExact8Rows = 0,
+  kFast8Blocks = 1,
+  kFast8Rows = 2,
+  kScaled8 = 3,
+  kExactScaled8 = 4,
+  kExact8Blocks = 5
+};
 constexpr bool by_exponents(int how) { return how == kScaled8 || how == kExactScaled8; }
-constexpr bool exact(int how) { return how == kExact8 || how == kExactScaled8; }
+constexpr bool exact(int how) {
+  return how == kExact8Rows || how == kExact8Blocks || how == kExactScaled8;
+}
+constexpr bool by_blocks(int how) { return how == kFast8Blocks || how == kExact8Blocks; }
 
 // The copies of a K step's scales (8-bit values) into the slot's table, A's rows first: FP32
 // numbers, 64 a wave, or exponent bytes, which every wave copies for A or for B (the same bytes:
@@ -513,7 +523,7 @@ __device__ __forceinline__ void store_tile(const LpArgs& p, const TileOf& w, int
 // wait for memory most of the time.
 template <class T, bool AKC, bool BKC, bool WGRAD, int BM, int BN, int WM, int WN, int HOW,
           bool STAGED, int KG>
-__global__ __launch_bounds__(WM * WN * 64 * KG) void lp_pipe_kernel(LpArgs p) {
+__global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_kernel(LpArgs p) {
   constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
   constexpr bool F8T = T::BYTES == 1;
@@ -623,7 +633,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG) void lp_pipe_kernel(LpArgs p) {
         } else {
 #pragma unroll
           for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
-          if constexpr (HOW == kFast8Blocks) {
+          if constexpr (by_blocks(HOW)) {
             // the wave's columns lie in one block of 128: one factor a row
             static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
             const float block = OS::b(table, wn);
@@ -661,7 +671,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG) void lp_pipe_kernel(LpArgs p) {
             const float4v v = d[(s - kLag) % kRing];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              if constexpr (HOW == kFast8Blocks)
+              if constexpr (by_blocks(HOW))
                 acc[i][j][r] += v[r] * s_a[i];
               else
                 acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
