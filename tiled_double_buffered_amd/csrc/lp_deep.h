@@ -204,7 +204,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           read_a(next, 0, false);
         }
         if (j == 0 && i < ROWS && (i + 1) % OA::READ == 0) read_a(slot, i + 1, LEFT == 0);
-        if (OA::READ == 1 && s == (ROWS - 1) * SN + 1)  // before the end barrier
+        if (OA::READ == 1 && s == SH * SN + 1)  // well before the end barrier
           read_a(slot, SM - 1, LEFT == 0);
         __builtin_amdgcn_sched_barrier(0);
         product(s);
