@@ -475,3 +475,40 @@ def test_only_once_differentiable(op):
     (dx,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         dx.sum().backward()
+
+
+# ------------------------------------------------------------------------------- far offsets
+def test_rows_and_experts_past_32_bit_offsets():
+    """Operands of more than 2^32 bytes: rows and experts at the far end, whole numbers (exact)."""
+    if torch.cuda.get_device_properties(0).total_memory < 48 * 2 ** 30:
+        pytest.skip("needs 48 GiB")
+    rows, K, N = 140000, 32768, 32
+    x = torch.zeros(rows, K, dtype=torch.uint8, device=DEV).view(lo.F8)  # 4.6 GB
+    far = torch.randint(-3, 4, (5, K), generator=_gen(96)).float().to(DEV)
+    x[-5:] = far.to(lo.F8)
+    sx = torch.ones(rows, K // 128, device=DEV)
+    b = torch.randint(-3, 4, (N, K), generator=_gen(97)).float().to(DEV)
+    sb = torch.ones(1, K // 128, device=DEV)
+    ref = far.double() @ b.double().t()
+    c = tdb.matmul_fp8(x, sx, b.to(lo.F8), sb, out_dtype=torch.float32)
+    assert torch.equal(c[-5:].double(), ref) and not c[:-5].any()
+    del x, sx, c
+    y = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)  # 9.2 GB
+    y[-5:] = far.bfloat16()
+    q, s = tdb.quantize_fp8(y)
+    assert torch.equal(q[-5:].float() * s[-5:].repeat_interleave(128, 1), far)
+    off = torch.tensor([0, rows - 5, rows], dtype=torch.int32, device=DEV)
+    w = torch.stack([torch.zeros_like(b.t()), b.t()]).bfloat16()
+    z = tdb.matmul_grouped(y, w, off)
+    assert torch.equal(z[-5:], ref.bfloat16()) and not z[:-5].any()
+    dw = tdb.matmul_grouped_wgrad(z[:, :8], y, off)
+    assert torch.equal(dw[1].float(), (z[-5:, :8].double().t() @ far.double()).bfloat16().float())
+    assert not dw[0].any()
+    del y, q, s, z, dw
+    E = 70
+    w = torch.zeros(E, 1024, K, dtype=torch.bfloat16, device=DEV)  # 4.7 GB
+    w[-1] = 1.0
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 5
+    z = tdb.matmul_grouped(far.bfloat16(), w, off, transpose_w=True)
+    assert torch.equal(z.float(), far.sum(1, keepdim=True).bfloat16().float().expand(5, 1024))

@@ -14,6 +14,14 @@
 // A tile of 128 rows or fewer leaves A2 and its products out.
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
+//
+// Measured on MI355X at 8192^3: bf16 X W^T 912 us, X W 820, weight gradient 800 (1.2 to 1.37
+// PFLOP/s; torch.matmul 1.16 to 1.31 on the same box), the matrix cores busy 75 % of the time at
+// the 1.8 GHz that the power limit leaves; 8 bits 438 us (2.5 PFLOP/s) warm and 555 from rest,
+// busy 63 %; FP32 137 to 144 TFLOP/s.  A step's copies, reads and barriers take about as long as
+// its products: the spread copies (8 bits 630 -> 604 us), B replaced piece by piece and scalar
+// walks (596 -> 555) are what overlaps them.  Three half slots for half tiles, wave priorities and
+// scales fetched earlier made no difference.
 #pragma once
 
 #include <type_traits>
