@@ -42,15 +42,16 @@ __device__ __forceinline__ int scale_exponent(float top) {  // top: finite, not 
 __device__ __forceinline__ float power_of_two(int e) {
   return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
 }
-// Eight values as 8-bit numbers: the conversion rounds to nearest even, and turns Inf and NaN
-// into NaN.
-__device__ __forceinline__ uint2 to_fp8x8(const float* v, int step, float inv) {
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[step] * inv, lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2 * step] * inv, v[3 * step] * inv, lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * step] * inv, v[5 * step] * inv, hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6 * step] * inv, v[7 * step] * inv, hi, true);
-  return make_uint2((uint32_t)lo, (uint32_t)hi);
+// Eight values over 2^e as 8-bit numbers: the conversion divides by the power of two, rounds to
+// nearest even, and turns Inf and NaN into NaN.
+__device__ __forceinline__ uint2 to_fp8x8(const float* v, int step, float scale) {
+  typedef short short2v __attribute__((ext_vector_type(2)));
+  short2v lo = {0, 0}, hi = {0, 0};
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[0], v[step], scale, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[2 * step], v[3 * step], scale, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[4 * step], v[5 * step], scale, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[6 * step], v[7 * step], scale, true);
+  return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
 // Eight neighbouring values of a row, the first `n` of them inside it.
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(256) void lp_quantize_rows_kernel(QuantArgs p) {
   float top = max_over_16(top_of<8, true>(v, 1));
   if (top == __builtin_inff()) top = max_over_16(top_of<8, false>(v, 1));
   const int e = scale_exponent(top);
-  store_bytes8(p.Q + row * p.ldq + c, p.cols - c, to_fp8x8(v, 1, power_of_two(-e)));
+  store_bytes8(p.Q + row * p.ldq + c, p.cols - c, to_fp8x8(v, 1, power_of_two(e)));
   if ((threadIdx.x & 15) == 0) put_scale<EXP>(p.S, p.lds, row, b, e);
 }
 
@@ -148,7 +149,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
         const int r = r0 + ty * 8 + i;
         const int e = scale_exponent(max_over_16(top_of<8, NO_INF>(v[i], 1)));
         if (r < p.rows) {
-          store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, power_of_two(-e)));
+          store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, power_of_two(e)));
           if (tx == 0) put_scale<EXP>(p.S, p.lds, r, blockIdx.x, e);
         }
       }
@@ -167,7 +168,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
       const int k = tx * 8 + j;
       const int e =
           scale_exponent(fmaxf(fmaxf(part[0][k], part[1][k]), fmaxf(part[2][k], part[3][k])));
-      *(uint2*)(turn + k * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, power_of_two(-e));
+      *(uint2*)(turn + k * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, power_of_two(e));
       if (ty == 0 && c0 + k < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + k, blockIdx.y, e);
     }
   } else {
@@ -179,12 +180,12 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
     __syncthreads();
     const int e =
         scale_exponent(fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3])));
-    const float inv = power_of_two(-e);
+    const float scale = power_of_two(e);
     if (p.Q != nullptr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = r0 + ty * 8 + i;
-        if (r < p.rows) store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, inv));
+        if (r < p.rows) store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, scale));
       }
       if constexpr (EXP) {
         if (tid < kBlock && r0 + tid < p.rows) put_scale<EXP>(p.S, p.lds, r0 + tid, blockIdx.x, e);
@@ -200,7 +201,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      *(uint2*)(turn + (tx * 8 + j) * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, inv);
+      *(uint2*)(turn + (tx * 8 + j) * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, scale);
   }
   __syncthreads();
 #pragma unroll
