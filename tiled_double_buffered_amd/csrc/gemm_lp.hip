@@ -126,7 +126,7 @@ constexpr int kFit[kTileCount] = {1, 2, 4, 1};
 constexpr StepCost kStep16[kTileCount] = {{1.40, 1.75}, {0.80, 0.60}, {0.45, 0.24}, {0.25, 0.25}};
 constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.58}, {0.58, 0.58}};
 constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}, {0.24, 0.24}};
-constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.30, 1.10}, {0.60, 0.36}, {0.37, 0.37}};
+constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.20, 0.93}, {0.60, 0.36}, {0.37, 0.37}};
 
 // The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number,
 // and the longest of them has `skew` times the average's K steps.
@@ -361,7 +361,7 @@ static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_
   // (an expert with three times the average's rows is common)
   const int t = pick_tile(unit, staged, k_steps((rows + E - 1) / E, b), E > 1 ? 3.0 : 1.0,
                           [&](int64_t bm, int64_t bn) {
-                            return (double)((M + bm - 1) / bm * ((N + bn - 1) / bn) * E);
+                            return (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn) * (double)E;
                           });
   return launch_wgrad(unit, t, staged, a, stream);
 }

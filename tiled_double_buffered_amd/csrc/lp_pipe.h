@@ -596,11 +596,42 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
       issue(group, 0);
       settle(0);
     }
+    // 8-bit values through the 16-bit instruction: the next step's copies go out between this
+    // one's products, since a wave waits for each to be taken (8192^3: 1014 us, 1153 with the
+    // copies first); past the last step they have nothing to copy, zeros into a slot that is
+    // not read again.  The others, whose steps are shorter, lose by it (bf16 X W^T 1167 us, 1024
+    // with the copies first).
+    constexpr bool SPREAD = F8T && exact(HOW) && !STAGED && KG == 1 && BM >= 128;
+    constexpr int SENT = OA::COPIES + OB::COPIES + 1;
+    static_assert(!SPREAD || OS::EXP || OS::WAVES == WAVES, "every wave copies scales");
     const int rounds = (steps + KG - 1) / KG;
     for (int it = 0; it < rounds; ++it) {
       const int kt = it * KG + group;
       part_barrier<0>();
-      if (kt + KG < steps) issue(kt + KG, (it + 1) & 1);
+      int4v ra, rb, rs;
+      int sent = 0;  // (a constant wherever it is used)
+      const uint32_t to = lds0 + (uint32_t)(((it + 1) & 1) * SLOT);
+      if constexpr (SPREAD) {
+        ra = oa.words(kt + 1);
+        rb = ob.words(kt + 1);
+        rs = os.words(kt + 1);
+        const bool more = kt + 1 < steps;
+        ra[2] = more ? ra[2] : 0;
+        rb[2] = more ? rb[2] : 0;
+        rs[2] = more ? rs[2] : 0;
+      } else {
+        if (kt + KG < steps) issue(kt + KG, (it + 1) & 1);
+      }
+      auto send = [&](int product, int products) {  // behind this product of so many
+        if constexpr (SPREAD) {
+          while (sent * products < (product + 1) * SENT && sent < SENT) {
+            if (sent < OB::COPIES) ob.copy(sent, rb, to + OA::BYTES, wave);
+            else if (sent < OB::COPIES + OA::COPIES) oa.copy(sent - OB::COPIES, ra, to, wave);
+            else os.copy(rs, to + OA::BYTES + OB::BYTES);
+            ++sent;
+          }
+        }
+      };
       char* sa = lds + (it & 1) * SLOT;
       char* sb = sa + OA::BYTES;
       if (!STAGED && (AKC || BKC) && tail != 0 && it + 1 == rounds) {
@@ -622,7 +653,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
 #pragma unroll
           for (int i = 0; i < SM; ++i)
 #pragma unroll
-            for (int j = 0; j < SN; ++j) 
+            for (int j = 0; j < SN; ++j)
               acc[i][j] = mma_half<T>(half_of(b[j], h), half_of(a[i], h), acc[i][j]);
       } else {
         const char* table = sb + OB::BYTES;
@@ -672,6 +703,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
             else
               d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                   b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
+            send(s, SM * SN * 3 / 4);  // the last with a quarter of the step to land
           }
           if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
           if (s >= kLag && HOW != kScaled8) {
