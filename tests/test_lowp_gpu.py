@@ -364,6 +364,23 @@ def test_linear_fp8_leading_axes_and_missing_gradients():
 
 
 @pytest.mark.parametrize("op", ["fp8", "grouped"])
+def test_without_gradients(op):
+    """Parameters under no_grad: the same product, nothing to differentiate."""
+    x = _randn(_gen(64), 40, 256).bfloat16().to(DEV).requires_grad_()
+    w = _randn(_gen(65), 2, 72, 256).bfloat16().to(DEV).requires_grad_()
+    off = torch.tensor([0, 11, 40], dtype=torch.int32, device=DEV)
+
+    def f():
+        return tdb.linear_fp8(x, w[0]) if op == "fp8" else tdb.linear_grouped(x, w, off, True)
+
+    y = f()
+    with torch.no_grad():
+        z = f()
+    assert y.requires_grad and not z.requires_grad
+    assert torch.equal(y.detach(), z)
+
+
+@pytest.mark.parametrize("op", ["fp8", "grouped"])
 def test_gradients_against_differences(op):
     """Both layers are linear wherever the 8-bit values are exact (whole numbers up to 15 are),
     so that differences of the loss are exact too: along any direction of whole numbers,

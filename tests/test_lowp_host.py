@@ -185,3 +185,26 @@ def test_tensor_calls_refuse_what_they_cannot_take():
     ):
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------------- compiled structure
+def test_compiled_kernels():
+    """This library's own gfx950 assembly: no register spills, no packed FP32 arithmetic, and M0
+    written only for a direct-to-LDS copy, one wait state and the load right behind it (the
+    copies are inline assembly, whose M0 the compiler does not track)."""
+    asm = build.device_asm()
+    meta = build.kernel_metadata(asm)
+    names = [n for n in meta if "gemmlp" in n]
+    assert len(names) > 60
+    for n in names:
+        assert meta[n]["private_segment_fixed_size"] == 0, n
+        assert meta[n]["group_segment_fixed_size"] <= 160 * 1024, n
+        start = re.search(rf"^{re.escape(n)}:", asm, re.M).end()
+        lines = [t.strip() for t in asm[start:asm.index(".Lfunc_end", start)].split("\n")]
+        lines = [t for t in lines if t and not t.startswith((";", "."))]
+        for i, t in enumerate(lines):
+            assert not re.match(r"v_pk_(fma|mul|add)_f32\b", t), (n, t)
+            if re.search(r"\bm0\b", t):
+                assert t.startswith("s_mov_b32 m0,"), (n, t)
+                assert lines[i + 1] == "s_nop 0", (n, lines[i + 1])
+                assert re.match(r"buffer_load_dword(x4)? .*\blds$", lines[i + 2]), (n, lines[i + 2])

@@ -421,8 +421,8 @@ def _fp8_exp(a, sa, b, sb, M, N, K, dtype):
 
 class _LinearFp8(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w):
-        need_x, need_w = ctx.needs_input_grad
+    def forward(ctx, x, w, grads):
+        need_x, need_w = (n and grads for n in ctx.needs_input_grad[:2])
         q, s, qt, st = _quantize_exp(x, 1, True, need_w)
         wq, ws, wqt, wst = _quantize_exp(w, BLOCK, True, need_x)
         ctx.save_for_backward(qt, st, wqt, wst)
@@ -432,13 +432,13 @@ class _LinearFp8(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        need_x, need_w = ctx.needs_input_grad
+        need_x, need_w = ctx.needs_input_grad[:2]
         qt, st, wqt, wst = ctx.saved_tensors
         M, N, K = ctx.sizes
         g, sg, gt, sgt = _quantize_exp(_row_major(dy), 1, need_x, need_w)
         dx = _fp8_exp(g, sg, wqt, wst, M, K, N, dy.dtype) if need_x else None
         dw = _fp8_exp(gt, sgt, qt, st, N, K, M, dy.dtype) if need_w else None
-        return dx, dw
+        return dx, dw, None
 
 
 def linear_fp8(x, w):
@@ -459,11 +459,12 @@ def linear_fp8(x, w):
     _same_device(x, w)
     flat = _row_major(x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x)
     w = _row_major(w)
+    grads = torch.is_grad_enabled()  # without, no transpose is quantized for the backward pass
     if _here(x, None):
-        y = _LinearFp8.apply(flat, w)
+        y = _LinearFp8.apply(flat, w, grads)
     else:
         with _on(x, None):
-            y = _LinearFp8.apply(flat, w)
+            y = _LinearFp8.apply(flat, w, grads)
     return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
 
 
