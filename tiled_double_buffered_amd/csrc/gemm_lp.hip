@@ -81,9 +81,13 @@ static LpKernel pipe_kernel(int unit, int tile, bool staged) {
   }
 }
 
+// Whether a row product's tiles may be computed in halves (lp_deep.h).
+static bool halves(int unit, int tile) { return tile == kTile256 && unit != 11; }
+
 static int launch_rows(int unit, int tile, bool staged, LpArgs a, void* stream) {
   const TileSize& s = kTiles[tile];
-  const int64_t wgs = row_tiles(a, s.bm, s.bn);
+  // (half a round more where the last round's tiles may be halved)
+  const int64_t wgs = row_tiles(a, s.bm, s.bn) + (halves(unit, tile) ? kCus / 2 : 0);
   if (wgs * s.threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
   a.tiles_n = (a.N + s.bn - 1) / s.bn;
   return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
@@ -129,10 +133,11 @@ constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23
 constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.20, 0.93}, {0.60, 0.36}, {0.37, 0.37}};
 
 // The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number,
-// and the longest of them has `skew` times the average's K steps.
+// and the longest of them has `skew` times the average's K steps.  rows: of a row product, the
+// tiles of whose last round are halved where they fill half of it or less.
 constexpr int kForced[kTileCount] = {256, 128, 64, 644};
 template <class F>
-static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) {
+static int pick_tile(int unit, bool staged, bool rows, double steps, double skew, F tiles) {
   if (const int forced = env_tile()) {
     for (int t = 0; t < kTileCount; ++t)
       if (kForced[t] == forced && pipe_kernel(unit, t, staged) != nullptr) return t;
@@ -142,7 +147,9 @@ static int pick_tile(int unit, bool staged, double steps, double skew, F tiles) 
   double least = 0;
   for (int t = 0; t < kTileCount; ++t) {
     if (pipe_kernel(unit, t, staged) == nullptr) continue;
-    const double n = std::ceil(tiles(kTiles[t].bm, kTiles[t].bn) / 256.0);
+    const double all = tiles(kTiles[t].bm, kTiles[t].bn) / kCus, rest = all - std::floor(all);
+    const bool halved = rows && halves(unit, t) && rest > 0 && rest <= 0.5;
+    const double n = halved ? std::floor(all) + 0.72 : std::ceil(all);
     // every tile's own prologue and epilogue cost it about two steps
     const double us = std::max({(steps + 2) * n * cost[t].full,
                                 (steps + 2) * std::ceil(n / kFit[t]) * cost[t].alone,
@@ -283,7 +290,7 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   const bool fast = c_type == GEMM_LP_BF16 && K >= 1024;
   const int unit = EXP ? (fast ? 12 : 13) : b_block == 1 ? (fast ? 11 : 9) : fast ? 10 : 14;
   const bool staged = !(word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1));
-  const int t = pick_tile(unit, staged, k_steps(K, 1), 1.0,
+  const int t = pick_tile(unit, staged, true, k_steps(K, 1), 1.0,
                           [&](int bm, int bn) { return expected_rows(a, bm, bn); });
   return launch_rows(unit, t, staged, a, stream);
 }
@@ -320,7 +327,7 @@ static int run_grouped(int64_t rows, int64_t N, int64_t K, int64_t E, const int3
   a.c_type = type;
   const int unit = 3 * type + (transpose_w ? 0 : 1);
   const bool staged = !(word_rows(X, ldx, 0, b) && word_rows(W, ldw, stride_w, b));
-  const int t = pick_tile(unit, staged, k_steps(K, b), 1.0,
+  const int t = pick_tile(unit, staged, true, k_steps(K, b), 1.0,
                           [&](int bm, int bn) { return expected_rows(a, bm, bn); });
   return launch_rows(unit, t, staged, a, stream);
 }
@@ -359,7 +366,7 @@ static int run_wgrad(int64_t rows, int64_t M, int64_t N, int64_t E, const int32_
   const int unit = 3 * type + 2;
   const bool staged = !(word_rows(A, lda, 0, b) && word_rows(B, ldb, 0, b));
   // (an expert with three times the average's rows is common)
-  const int t = pick_tile(unit, staged, k_steps((rows + E - 1) / E, b), E > 1 ? 3.0 : 1.0,
+  const int t = pick_tile(unit, staged, false, k_steps((rows + E - 1) / E, b), E > 1 ? 3.0 : 1.0,
                           [&](int64_t bm, int64_t bn) {
                             return (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn) * (double)E;
                           });
