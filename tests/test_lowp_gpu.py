@@ -494,6 +494,39 @@ def test_only_once_differentiable(op):
         dx.sum().backward()
 
 
+@pytest.mark.parametrize("spare", [(0, 0), (1, 0), (64, 3), (128, 0), (129, 0), (100, 56), (100, 57)],
+                         ids=str)
+@pytest.mark.parametrize("kind", ["bf16-256", "f16-256", "f32-256", "f32-64", "f32-644"])
+def test_last_round_in_halves(kind, spare, monkeypatch):
+    """256 + R whole row tiles of one column, and P groups that end with half a tile or less,
+    around the counts at which the last round's tiles are computed in halves (2 R + P <= 256).
+    Whole numbers: exact, with one rounding at the end."""
+    dtype, tile = kind.split("-")
+    monkeypatch.setenv("GEMM_LP_TILE", tile)
+    bm = 256 if tile == "256" else 64
+    R, P = spare
+    E = max(P, 3)
+    sizes = [(256 + R) // E * bm] * E
+    sizes[-1] += (256 + R) % E * bm
+    for e in range(P):
+        sizes[e] += 1 + e * 7 % (bm // 2)  # 1 .. half a tile
+    if P == 0:
+        sizes[0] -= bm // 4  # a whole tile still: more than half of its rows are left
+    g = _gen(66)
+    rows, K, N = sum(sizes), 72, 40
+    off = torch.tensor([0] + sizes, dtype=torch.int64).cumsum(0).int().to(DEV)
+    x = torch.randint(-3, 4, (rows, K), generator=g).float().to(DEV)
+    w = torch.randint(-3, 4, (E, K, N), generator=g).float().to(DEV)
+    expected = torch.cat([a @ b for a, b in zip(x.split(sizes), w)]).to(TYPES[dtype])
+    _say("[halves]", kind, spare)
+    for tw in (False, True):
+        b = (w.transpose(1, 2).contiguous() if tw else w).to(TYPES[dtype])
+        y = tdb.matmul_grouped(x.to(TYPES[dtype]), b, off, transpose_w=tw)
+        assert torch.equal(y, expected), tw
+        one = tdb.matmul_grouped(x.to(TYPES[dtype]), b[:1], off[[0, -1]].contiguous(), transpose_w=tw)
+        assert torch.equal(one, (x @ w[0]).to(TYPES[dtype])), tw
+
+
 # ------------------------------------------------------------------------------- far offsets
 def test_rows_and_experts_past_32_bit_offsets():
     """Operands of more than 2^32 bytes: rows and experts at the far end, whole numbers (exact)."""

@@ -81,13 +81,17 @@ static LpKernel pipe_kernel(int unit, int tile, bool staged) {
   }
 }
 
-// Whether a row product's tiles may be computed in halves (lp_deep.h).
-static bool halves(int unit, int tile) { return tile == kTile256 && unit != 11; }
+// What half a tile of a row product costs, where it is computed in halves (lp_deep.h, and the
+// 64-row tiles of FP32); 1 where it is not.
+static double half_cost(int unit, int tile) {
+  if (tile == kTile256) return unit == 11 ? 1.0 : 0.72;
+  return tile != kTile128 && (unit == 6 || unit == 7) ? 0.55 : 1.0;
+}
 
 static int launch_rows(int unit, int tile, bool staged, LpArgs a, void* stream) {
   const TileSize& s = kTiles[tile];
   // (half a round more where the last round's tiles may be halved)
-  const int64_t wgs = row_tiles(a, s.bm, s.bn) + (halves(unit, tile) ? kCus / 2 : 0);
+  const int64_t wgs = row_tiles(a, s.bm, s.bn) + (half_cost(unit, tile) < 1 ? kCus / 2 : 0);
   if (wgs * s.threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
   a.tiles_n = (a.N + s.bn - 1) / s.bn;
   return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
@@ -120,17 +124,22 @@ static int env_tile() {
   return v == nullptr ? 0 : std::atoi(v);
 }
 // Time of one 128-byte K step of a tile, in us, measured on MI355X: `alone` with one workgroup
-// on the CU, `full` a CU's time for each with as many as fit (and the chip as warm as it gets).
-// A CU works through n = ceil(tiles / 256) tiles in n * full or, where that is more, in rounds
-// of `fit` tiles of `alone`; a launch, its first loads and last stores add about 4 us to all.
+// on the CU, `full` a CU's time for each with as many as fit (and the chip as warm as it gets);
+// a tile's own first loads and last stores cost it about `extra` steps, fewer where others fill
+// the gap.  A CU works through n = ceil(tiles / 256) tiles in n * full or, where that is more,
+// in rounds of `fit` tiles of `alone`; a launch adds about 4 us to all.
 struct StepCost {
-  double alone, full;
+  double alone, full, extra;
 };
 constexpr int kFit[kTileCount] = {1, 2, 4, 1};
-constexpr StepCost kStep16[kTileCount] = {{1.40, 1.75}, {0.80, 0.60}, {0.45, 0.24}, {0.25, 0.25}};
-constexpr StepCost kStep32[kTileCount] = {{7.60, 7.60}, {1.90, 1.92}, {0.58, 0.58}, {0.58, 0.58}};
-constexpr StepCost kStep8[kTileCount] = {{1.40, 1.95}, {0.80, 0.68}, {0.45, 0.23}, {0.24, 0.24}};
-constexpr StepCost kStep8Exact[kTileCount] = {{0, 0}, {1.20, 0.93}, {0.60, 0.36}, {0.37, 0.37}};
+constexpr StepCost kStep16[kTileCount] = {
+    {1.40, 1.75, 2}, {0.80, 0.60, 2}, {0.45, 0.24, 2}, {0.25, 0.25, 2}};
+constexpr StepCost kStep32[kTileCount] = {
+    {7.30, 7.30, 2}, {2.00, 1.87, 3.5}, {0.66, 0.51, 0.7}, {0.60, 0.60, 2}};
+constexpr StepCost kStep8[kTileCount] = {
+    {1.40, 1.95, 2}, {0.80, 0.68, 2}, {0.45, 0.23, 2}, {0.24, 0.24, 2}};
+constexpr StepCost kStep8Exact[kTileCount] = {
+    {0, 0, 0}, {1.20, 0.93, 2}, {0.60, 0.36, 2}, {0.37, 0.37, 2}};
 
 // The tile of the pipelined kernels with the least time; `tiles(bm, bn)` is the expected number,
 // and the longest of them has `skew` times the average's K steps.  rows: of a row product, the
@@ -148,22 +157,22 @@ static int pick_tile(int unit, bool staged, bool rows, double steps, double skew
   for (int t = 0; t < kTileCount; ++t) {
     if (pipe_kernel(unit, t, staged) == nullptr) continue;
     const double all = tiles(kTiles[t].bm, kTiles[t].bn) / kCus, rest = all - std::floor(all);
-    const bool halved = rows && halves(unit, t) && rest > 0 && rest <= 0.5;
-    const double n = halved ? std::floor(all) + 0.72 : std::ceil(all);
-    // every tile's own prologue and epilogue cost it about two steps
-    const double us = std::max({(steps + 2) * n * cost[t].full,
-                                (steps + 2) * std::ceil(n / kFit[t]) * cost[t].alone,
-                                (skew * steps + 2) * cost[t].alone});
+    const double n = std::floor(all) +
+                     (rest == 0 ? 0 : rows && rest <= 0.5 ? half_cost(unit, t) : 1);
+    const double us = std::max({(steps + cost[t].extra) * n * cost[t].full,
+                                (steps + cost[t].extra) * std::ceil(n / kFit[t]) * cost[t].alone,
+                                (skew * steps + cost[t].extra) * cost[t].alone});
     if (best < 0 || us < least) best = t, least = us;
   }
   return best;
 }
 
 // Tiles of a row product to expect: every group with rows leaves half a tile row unused (a
-// quarter where the tile is computed in halves).
+// quarter where the tile is computed in halves); one group alone has all rows.
 static double expected_rows(const LpArgs& a, double bm, double bn) {
-  const double waste = bm == 256 ? 0.25 : 0.5;
-  const double m = a.offsets == nullptr
+  const bool fp32 = a.SA == nullptr && a.c_type == GEMM_LP_F32;
+  const double waste = bm == 256 || (fp32 && bm == 64) ? 0.25 : 0.5;
+  const double m = a.offsets == nullptr || a.E == 1
                        ? std::ceil(a.rows / bm)
                        : std::max<double>(a.rows / bm + waste * std::min(a.E, a.rows), 1.0);
   return m * std::ceil(a.N / bn);

@@ -129,6 +129,7 @@ struct TileAt {
   int row0;      // first row of the tile
   int row_end;   // end of the group's rows
   int tn;        // tile column
+  bool half;     // HALF rows or fewer
 };
 
 // Consecutive ids for the workgroups of one XCD: workgroup w runs on XCD w mod 8, and
@@ -164,10 +165,10 @@ __device__ __forceinline__ void wgrad_tile(int wg, int per, int tiles_m, int til
 // number of tiles that any offsets can give; the count that these give is found here, by
 // every wave for itself, 64 groups at a time, and the workgroups past it return false.
 // Group 0 is the rows before offsets[0], group E + 1 the ones from offsets[E] on.
-// HALF > 0: half a tile (HALF rows or fewer) costs about 0.72 of a whole one, and they come
-// last, to fill the last round: a group's last tile where it has no more rows; and both halves
-// of each tile of the last round, where these and the others fit into one round (8 bits, 2304 x
-// 8192 x 4096, 288 tiles: 98 us, 105 with whole tiles).
+// HALF > 0: half a tile (HALF rows or fewer) costs less than a whole one (256 rows 0.72, 64 rows
+// of FP32 0.55), and they come last, to fill the last round: a group's last tile where it has no
+// more rows; and both halves of each tile of the last round, where these and the others fit into
+// one round (8 bits, 2304 x 8192 x 4096, 288 tiles: 98 us, 105 with whole tiles).
 template <int BM, int HALF>
 __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   int tm;
@@ -179,6 +180,7 @@ __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
     t.e = 0;
     t.row0 = tm * BM;
     t.row_end = p.rows;
+    t.half = false;
     return true;
   }
   const int lane = threadIdx.x & 63;
@@ -214,6 +216,7 @@ __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   nw -= cut;
   if (wg >= nw + np + 2 * cut) return false;
   const bool small = wg >= nw && wg < nw + np, halved = wg >= nw + np;
+  t.half = small || halved;
   int id = small ? xcd_order(wg - nw, np)
                  : halved ? nw + (wg - nw - np) / 2 : xcd_order(wg, nw);
   for (int base = 0; base < groups; base += 64) {

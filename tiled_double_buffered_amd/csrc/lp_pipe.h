@@ -27,6 +27,8 @@
 // by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles.
 #pragma once
 
+#include <type_traits>
+
 #include "lp_common.h"
 
 namespace gemmlp {
@@ -360,6 +362,7 @@ struct TileOf {
   const char* B;
   int64_t c_base;
   int m0, m_end, n0, e, k_end;
+  bool half;
 };
 template <class T, bool WGRAD, int BM, int BN, int HALF = 0>
 __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
@@ -383,6 +386,7 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
     TileAt t;
     if (!find_tile<BM, HALF>(p, blockIdx.x, gridDim.x, t)) return false;
     w.e = __builtin_amdgcn_readfirstlane(t.e);
+    w.half = __builtin_amdgcn_readfirstlane((int)t.half) != 0;
     w.k_end = w.e < 0 ? 0 : p.K;
     if (w.e > 0) w.B += w.e * p.stride_b * T::BYTES;
     w.m0 = __builtin_amdgcn_readfirstlane(t.row0);
@@ -549,8 +553,13 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
   const int l16 = lane & 15, g = lane >> 4;
 
   TileOf w;
-  if (!locate<T, WGRAD, BM, BN>(p, w)) return;
-  const int wm = (wave / WN) * WTM, wn = (wave % WN) * WTN;
+  // A tile of FP32 rows takes the matrix cores long enough for half of it to be worth leaving
+  // out: each wave then has the first half of its fragments, from half as far down (2048 rows of
+  // 8 experts, 2048 -> 1024: 89 us, 105 in whole tiles; 1024 -> 2048: 85, 92).
+  constexpr int HALF = T::BYTES == 4 && !WGRAD && BM == 64 && SM == 2 ? BM / 2 : 0;
+  if (!locate<T, WGRAD, BM, BN, HALF>(p, w)) return;
+  const bool half = HALF > 0 && w.half;
+  const int wm = (wave / WN) * (half ? WTM / 2 : WTM), wn = (wave % WN) * WTN;
 
   float4v acc[SM][SN] = {};
   const int steps = (w.k_end + OA::KS - 1) / OA::KS;
@@ -605,122 +614,131 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
     constexpr int SENT = OA::COPIES + OB::COPIES + 1;
     static_assert(!SPREAD || OS::EXP || OS::WAVES == WAVES, "every wave copies scales");
     const int rounds = (steps + KG - 1) / KG;
-    for (int it = 0; it < rounds; ++it) {
-      const int kt = it * KG + group;
-      part_barrier<0>();
-      int4v ra, rb, rs;
-      int sent = 0;  // (a constant wherever it is used)
-      const uint32_t to = lds0 + (uint32_t)(((it + 1) & 1) * SLOT);
-      if constexpr (SPREAD) {
-        ra = oa.words(kt + 1);
-        rb = ob.words(kt + 1);
-        rs = os.words(kt + 1);
-        const bool more = kt + 1 < steps;
-        ra[2] = more ? ra[2] : 0;
-        rb[2] = more ? rb[2] : 0;
-        rs[2] = more ? rs[2] : 0;
-      } else {
-        if (kt + KG < steps) issue(kt + KG, (it + 1) & 1);
-      }
-      auto send = [&](int product, int products) {  // behind this product of so many
+    auto loop = [&](auto fragments) {  // of A a wave
+      for (int it = 0; it < rounds; ++it) {
+        const int kt = it * KG + group;
+        part_barrier<0>();
+        int4v ra, rb, rs;
+        int sent = 0;  // (a constant wherever it is used)
+        const uint32_t to = lds0 + (uint32_t)(((it + 1) & 1) * SLOT);
         if constexpr (SPREAD) {
-          while (sent * products < (product + 1) * SENT && sent < SENT) {
-            if (sent < OB::COPIES) ob.copy(sent, rb, to + OA::BYTES, wave);
-            else if (sent < OB::COPIES + OA::COPIES) oa.copy(sent - OB::COPIES, ra, to, wave);
-            else os.copy(rs, to + OA::BYTES + OB::BYTES);
-            ++sent;
-          }
-        }
-      };
-      char* sa = lds + (it & 1) * SLOT;
-      char* sb = sa + OA::BYTES;
-      if (!STAGED && (AKC || BKC) && tail != 0 && it + 1 == rounds) {
-        if (KG == 1 || kt + 1 == steps) {
-          if constexpr (AKC) OA::clear_tail(sa, tail, tid, THREADS);
-          if constexpr (BKC) OB::clear_tail(sb, tail, tid, THREADS);
-        }
-        __syncthreads();
-      }
-      if (KG > 1 && kt >= steps) continue;
-      if constexpr (!F8T) {
-        int8v a[SM], b[SN];
-#pragma unroll
-        for (int j = 0; j < SN; j += OB::READ) ob.read(sb, j, b + j);
-#pragma unroll
-        for (int i = 0; i < SM; i += OA::READ) oa.read(sa, i, a + i);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < SM; ++i)
-#pragma unroll
-            for (int j = 0; j < SN; ++j)
-              acc[i][j] = mma_half<T>(half_of(b[j], h), half_of(a[i], h), acc[i][j]);
-      } else {
-        const char* table = sb + OB::BYTES;
-        int8v b[SN], a[2];
-#pragma unroll
-        for (int j = 0; j < SN; ++j) ob.read(sb, j, b + j);
-        oa.read(sa, 0, a);
-        float4v s_b[SN];
-        float s_a[SM];
-        int x_a[SM], x_b[SN];
-        if constexpr (HOW == kScaled8) {
-#pragma unroll
-          for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
-#pragma unroll
-          for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, wm + 16 * i + l16);
+          ra = oa.words(kt + 1);
+          rb = ob.words(kt + 1);
+          rs = os.words(kt + 1);
+          const bool more = kt + 1 < steps;
+          ra[2] = more ? ra[2] : 0;
+          rb[2] = more ? rb[2] : 0;
+          rs[2] = more ? rs[2] : 0;
         } else {
-#pragma unroll
-          for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
-          if constexpr (by_blocks(HOW)) {
-            // the wave's columns lie in one block of 128: one factor a row
-            static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
-            const float block = OS::b(table, wn);
-#pragma unroll
-            for (int i = 0; i < SM; ++i) s_a[i] *= block;
-          } else {
-#pragma unroll
-            for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
-          }
+          if (kt + KG < steps) issue(kt + KG, (it + 1) & 1);
         }
-        // The sums of a step are scaled and added kLag products behind, while the matrix
-        // cores work on the next ones; the order is pinned, since the compiler would put each
-        // addition right behind its product and wait.
-        constexpr int kLag = HOW == kScaled8 ? 0 : exact(HOW) ? 1 : 2, kRing = kLag + 1;
-        float4v d[kRing];
-#pragma unroll
-        for (int s = 0; s < SM * SN + kLag; ++s) {
-          if (s < SM * SN) {
-            const int i = s / SN, j = s % SN;
-            if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
-            const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (HOW == kScaled8)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  b[j], a[i & 1], acc[i][j], 0, 0, 0, x_b[j], 0, x_a[i]);
-            else if constexpr (exact(HOW))
-              d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
-                                         half_of(a[i & 1], 1), z);
-            else
-              d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
-            send(s, SM * SN * 3 / 4);  // the last with a quarter of the step to land
-          }
-          if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
-          if (s >= kLag && HOW != kScaled8) {
-            const int i = (s - kLag) / SN, j = (s - kLag) % SN;
-            const float4v v = d[(s - kLag) % kRing];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if constexpr (by_blocks(HOW))
-                acc[i][j][r] += v[r] * s_a[i];
-              else
-                acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
+        auto send = [&](int product, int products) {  // behind this product of so many
+          if constexpr (SPREAD) {
+            while (sent * products < (product + 1) * SENT && sent < SENT) {
+              if (sent < OB::COPIES) ob.copy(sent, rb, to + OA::BYTES, wave);
+              else if (sent < OB::COPIES + OA::COPIES) oa.copy(sent - OB::COPIES, ra, to, wave);
+              else os.copy(rs, to + OA::BYTES + OB::BYTES);
+              ++sent;
             }
           }
-          if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
+        };
+        char* sa = lds + (it & 1) * SLOT;
+        char* sb = sa + OA::BYTES;
+        if (!STAGED && (AKC || BKC) && tail != 0 && it + 1 == rounds) {
+          if (KG == 1 || kt + 1 == steps) {
+            if constexpr (AKC) OA::clear_tail(sa, tail, tid, THREADS);
+            if constexpr (BKC) OB::clear_tail(sb, tail, tid, THREADS);
+          }
+          __syncthreads();
         }
+        if (KG > 1 && kt >= steps) continue;
+        if constexpr (!F8T) {
+          constexpr int N = decltype(fragments)::value;
+          int8v a[SM], b[SN];
+#pragma unroll
+          for (int j = 0; j < SN; j += OB::READ) ob.read(sb, j, b + j);
+#pragma unroll
+          for (int i = 0; i < N; i += OA::READ) oa.read(sa, i, a + i);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+              for (int j = 0; j < SN; ++j)
+                acc[i][j] = mma_half<T>(half_of(b[j], h), half_of(a[i], h), acc[i][j]);
+        } else {
+          const char* table = sb + OB::BYTES;
+          int8v b[SN], a[2];
+#pragma unroll
+          for (int j = 0; j < SN; ++j) ob.read(sb, j, b + j);
+          oa.read(sa, 0, a);
+          float4v s_b[SN];
+          float s_a[SM];
+          int x_a[SM], x_b[SN];
+          if constexpr (HOW == kScaled8) {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
+#pragma unroll
+            for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, wm + 16 * i + l16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
+            if constexpr (by_blocks(HOW)) {
+              // the wave's columns lie in one block of 128: one factor a row
+              static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
+              const float block = OS::b(table, wn);
+#pragma unroll
+              for (int i = 0; i < SM; ++i) s_a[i] *= block;
+            } else {
+#pragma unroll
+              for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
+            }
+          }
+          // The sums of a step are scaled and added kLag products behind, while the matrix
+          // cores work on the next ones; the order is pinned, since the compiler would put each
+          // addition right behind its product and wait.
+          constexpr int kLag = HOW == kScaled8 ? 0 : exact(HOW) ? 1 : 2, kRing = kLag + 1;
+          float4v d[kRing];
+#pragma unroll
+          for (int s = 0; s < SM * SN + kLag; ++s) {
+            if (s < SM * SN) {
+              const int i = s / SN, j = s % SN;
+              if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
+              const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
+              if constexpr (HOW == kScaled8)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    b[j], a[i & 1], acc[i][j], 0, 0, 0, x_b[j], 0, x_a[i]);
+              else if constexpr (exact(HOW))
+                d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
+                                           half_of(a[i & 1], 1), z);
+              else
+                d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
+              send(s, SM * SN * 3 / 4);  // the last with a quarter of the step to land
+            }
+            if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
+            if (s >= kLag && HOW != kScaled8) {
+              const int i = (s - kLag) / SN, j = (s - kLag) % SN;
+              const float4v v = d[(s - kLag) % kRing];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                if constexpr (by_blocks(HOW))
+                  acc[i][j][r] += v[r] * s_a[i];
+                else
+                  acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
+              }
+            }
+            if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        if (kt + KG < steps) settle((it + 1) & 1);
       }
-      if (kt + KG < steps) settle((it + 1) & 1);
+    };
+    if constexpr (HALF > 0) {
+      if (half) loop(std::integral_constant<int, SM / 2>{});
+      else loop(std::integral_constant<int, SM>{});
+    } else {
+      loop(std::integral_constant<int, SM>{});
     }
     if constexpr (KG > 1) {
       // the groups' sums, in their order: lane by lane, 16 bytes at a time
@@ -748,7 +766,9 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
 
   constexpr int OUT = !F8T ? T::CODE : exact(HOW) ? -1 : GEMM_LP_BF16;
   store_tile<OB, OUT>(p, w, wn, g, acc,
-                     [&](int i) { return w.m0 + wm + OA::row_of(i, l16); });
+                     [&](int i) {
+                       return half && i >= SM / 2 ? w.m_end : w.m0 + wm + OA::row_of(i, l16);
+                     });
 }
 
 }  // namespace gemmlp
