@@ -1,5 +1,6 @@
-// The pipelined product kernel for large products: 256 x 256 tiles, eight waves of 128 x 64,
-// two LDS slots refilled in halves, so that a copy has one and a half K steps to land.
+// The pipelined product kernel for large products: 256 x 256 tiles, eight waves of 128 x 64 or
+// four of 128 x 128, two LDS slots refilled in halves, so that a copy has one and a half K steps
+// to land.
 //
 // The kernel of lp_pipe.h starts a step's copies when the slot's last reader is done and needs
 // them one step later, and waits for them (8 bits: 40 % of all wave cycles).  Here each slot has
@@ -15,13 +16,19 @@
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
 //
-// Measured on MI355X at 8192^3: bf16 X W^T 912 us, X W 820, weight gradient 800 (1.2 to 1.37
-// PFLOP/s; torch.matmul 1.16 to 1.31 on the same box), the matrix cores busy 75 % of the time at
-// the 1.8 GHz that the power limit leaves; 8 bits 438 us (2.5 PFLOP/s) warm and 555 from rest,
-// busy 63 %; FP32 137 to 144 TFLOP/s.  A step's copies, reads and barriers take about as long as
-// its products: the spread copies (8 bits 630 -> 604 us), B replaced piece by piece and scalar
-// walks (596 -> 555) are what overlaps them.  Three half slots for half tiles, wave priorities and
-// scales fetched earlier made no difference.
+// Four waves read a third less from LDS for a step, and with one wave on each SIMD the sums and
+// the fragments have 512 registers: 16 bits 750 us at 8192^3, 785 with eight; exponents for
+// scales 378, 389.  8-bit values with FP32 scales keep eight (their sums are added by vector
+// instructions, which cannot use half of the 512), and so do FP32 ones (weight gradient 4096^3:
+// 951 us, 1081 with four; X W the same).
+//
+// Measured on MI355X at 8192^3, warm: bf16 X W^T 750 us, X W 730, weight gradient 730 (1.5
+// PFLOP/s); 8 bits with FP32 scales 438 (2.5 PFLOP/s) and 555 from rest, the matrix cores busy
+// 63 % of the time at the 1.8 GHz that the power limit leaves; FP32 137 to 148 TFLOP/s.  A
+// step's copies, reads and barriers take about as long as its products: the spread copies (8 bits
+// 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555) are what overlaps them.
+// Three half slots for half tiles, wave priorities, scales fetched earlier, and workgroups that
+// stay and fetch their next tile's first steps before they store made no difference.
 #pragma once
 
 #include <type_traits>
@@ -30,10 +37,10 @@
 
 namespace gemmlp {
 
-template <class T, bool AKC, bool BKC, bool WGRAD, int HOW>
-__global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
-  constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
-  constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
+template <class T, bool AKC, bool BKC, bool WGRAD, int HOW, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void lp_deep_kernel(LpArgs p) {
+  constexpr int BM = 256, BN = 256, WN = WAVES / 2;
+  constexpr int WTM = 128, WTN = BN / WN, HALF = WTM / 2, SM = 8, SN = WTN / 16, SH = SM / 2;
   constexpr bool F8T = T::BYTES == 1;
   static_assert(!F8T || HOW == kFast8Blocks || HOW == kScaled8, "not enough registers");
   constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
@@ -252,18 +259,18 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       issue_first(0);
       if (steps > 1) issue_first(1);
       int8v h[SH];
-      for (int kt = 0; kt < steps; ++kt) {
+      auto half_step = [&](auto left, int kt) {  // of which LEFT follow
+        constexpr int LEFT = decltype(left)::value;
         const char* slot = lds + (kt & 1) * SLOT;
-        if (kt + 1 < steps) part_barrier<FIRST>();
-        else part_barrier<0>();
+        part_barrier<LEFT == 0 ? 0 : FIRST>();
 #pragma unroll
         for (int j = 0; j < SN; j += OB::READ) ob.read(slot + B0, j, b + j);
 #pragma unroll
         for (int i = 0; i < SH; i += OA::READ) oa1.read(slot + A1, i, h + i);
         read_scales(kt);
         part_barrier<63>();  // (the copies stay open)
-        if (kt + 2 < steps) issue_first(kt + 2);
-        if (kt + 1 == steps) {
+        if constexpr (LEFT == 2) issue_first(kt + 2);
+        if constexpr (LEFT == 0) {
           if constexpr (AKC) {
 #pragma unroll
             for (int i = 0; i < SH; ++i) h[i] &= last_mask;
@@ -278,7 +285,10 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           if (s < SH * SN) product_of(s, s / SN, s % SN, h[s / SN]);
           if (s >= kLag) add_to(s - kLag, (s - kLag) / SN, (s - kLag) % SN);
         }
-      }
+      };
+      for (int kt = 0; kt + 2 < steps; ++kt) half_step(Two{}, kt);
+      if (steps > 1) half_step(One{}, steps - 2);
+      half_step(None{}, steps - 1);
       store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
       return;
     }
