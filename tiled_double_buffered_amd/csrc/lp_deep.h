@@ -17,18 +17,20 @@
 // part it needs.
 //
 // Four waves read a third less from LDS for a step, and with one wave on each SIMD the sums and
-// the fragments have 512 registers: 16 bits 750 us at 8192^3, 785 with eight; exponents for
-// scales 378, 389.  8-bit values with FP32 scales keep eight (their sums are added by vector
-// instructions, which cannot use half of the 512), and so do FP32 ones (weight gradient 4096^3:
-// 951 us, 1081 with four; X W the same).
+// the fragments have 512 registers: 16 bits 751 us at 8192^3, 788 with eight; exponents for
+// scales 380, 387.  8-bit values with FP32 scales keep eight (their sums are added by vector
+// instructions, which cannot use half of the 512), and so do FP32 values (weight gradient 4096^3:
+// 951 us, 1081 with four; X W the same) and weight gradients, which store more for each step
+// (16384 rows of 32 experts, 4096 x 2048: 351 us, 364 with four; one of 4096^3 99, 97).
 //
-// Measured on MI355X at 8192^3, warm: bf16 X W^T 750 us, X W 730, weight gradient 730 (1.5
-// PFLOP/s); 8 bits with FP32 scales 438 (2.5 PFLOP/s) and 555 from rest, the matrix cores busy
-// 63 % of the time at the 1.8 GHz that the power limit leaves; FP32 137 to 148 TFLOP/s.  A
-// step's copies, reads and barriers take about as long as its products: the spread copies (8 bits
-// 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555) are what overlaps them.
-// Three half slots for half tiles, wave priorities, scales fetched earlier, and workgroups that
-// stay and fetch their next tile's first steps before they store made no difference.
+// Measured on MI355X at 8192^3, warm: bf16 X W^T 751 us, X W 728, weight gradient 745 (1.5
+// PFLOP/s, the matrix cores busy 72 to 74 % of the time); 8 bits with FP32 scales 438 (2.5
+// PFLOP/s, busy 62 % at the 1.8 GHz that the power limit leaves) and 555 from rest; FP32 137 to
+// 148 TFLOP/s.  A step's copies, reads and barriers take about as long as its products: the
+// spread copies (8 bits 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555)
+// are what overlaps them.  Three half slots for half tiles, wave priorities, scales fetched
+// earlier, and workgroups that stay and fetch their next tile's first steps before they store
+// made no difference.
 #pragma once
 
 #include <type_traits>

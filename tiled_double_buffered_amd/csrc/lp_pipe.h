@@ -23,8 +23,9 @@
 // bf16 at 8192^3), with few rows the reading of B (16 rows of 14 of 64 experts, 4096 x 2048 in
 // bf16: 58 us, 4.05 TB/s; torch.sum reads as much memory at 3.5), with little work the latency of
 // a step, which four wave groups on one tile share (1 x 11008 x 4096 in 8 bits: 12 us, 18 with one
-// group).  8-bit values through the 16-bit instruction: 1040 TFLOP/s at 8192 x 4096 x 4096, bound
-// by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles.
+// group).  8-bit values through the 16-bit instruction: 1120 TFLOP/s at 8192 x 4096 x 4096, bound
+// by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles, 132 on
+// 64 x 64.
 #pragma once
 
 #include <type_traits>
