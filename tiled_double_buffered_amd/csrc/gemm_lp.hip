@@ -92,10 +92,10 @@ static int launch_rows(int unit, int tile, bool staged, LpArgs a, void* stream) 
   const TileSize& s = kTiles[tile];
   // (half a round more where the last round's tiles may be halved)
   const int64_t wgs = row_tiles(a, s.bm, s.bn) + (half_cost(unit, tile) < 1 ? kCus / 2 : 0);
-  if (wgs * threads_of(unit, tile) > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (wgs * s.threads > 0xFFFFFFFFLL || wgs > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
   a.tiles_n = (a.N + s.bn - 1) / s.bn;
-  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs),
-                threads_of(unit, tile), &a, stream);
+  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
+                stream);
 }
 
 static int launch_wgrad(int unit, int tile, bool staged, LpArgs a, void* stream) {
@@ -103,11 +103,11 @@ static int launch_wgrad(int unit, int tile, bool staged, LpArgs a, void* stream)
   const int64_t tm = (a.M + s.bm - 1) / s.bm, tn = (a.N + s.bn - 1) / s.bn;
   int64_t wgs;
   if (__builtin_mul_overflow(tm * tn, (int64_t)a.E, &wgs) || wgs > kMaxDim ||
-      wgs * threads_of(unit, tile) > 0xFFFFFFFFLL)
+      wgs * s.threads > 0xFFFFFFFFLL)
     return GEMMF32_ERR_TOO_LARGE;
   a.tiles_n = (int)tn;
-  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs),
-                threads_of(unit, tile), &a, stream);
+  return launch((const void*)pipe_kernel(unit, tile, staged), dim3((unsigned)wgs), s.threads, &a,
+                stream);
 }
 
 // Whether an operand can be copied in words: rows and experts that start at multiples of four

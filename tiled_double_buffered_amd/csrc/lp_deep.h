@@ -1,6 +1,5 @@
-// The pipelined product kernel for large products: 256 x 256 tiles, eight waves of 128 x 64 or
-// four of 128 x 128, two LDS slots refilled in halves, so that a copy has one and a half K steps
-// to land.
+// The pipelined product kernel for large products: 256 x 256 tiles, eight waves of 128 x 64,
+// two LDS slots refilled in halves, so that a copy has one and a half K steps to land.
 //
 // The kernel of lp_pipe.h starts a step's copies when the slot's last reader is done and needs
 // them one step later, and waits for them (8 bits: 40 % of all wave cycles).  Here each slot has
@@ -16,21 +15,16 @@
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
 //
-// Four waves read a third less from LDS for a step, and with one wave on each SIMD the sums and
-// the fragments have 512 registers: 16 bits 751 us at 8192^3, 788 with eight; exponents for
-// scales 380, 387.  8-bit values with FP32 scales keep eight (their sums are added by vector
-// instructions, which cannot use half of the 512), and so do FP32 values (weight gradient 4096^3:
-// 951 us, 1081 with four; X W the same) and weight gradients, which store more for each step
-// (16384 rows of 32 experts, 4096 x 2048: 351 us, 364 with four; one of 4096^3 99, 97).
-//
-// Measured on MI355X at 8192^3, warm: bf16 X W^T 751 us, X W 728, weight gradient 745 (1.5
-// PFLOP/s, the matrix cores busy 72 to 74 % of the time); 8 bits with FP32 scales 438 (2.5
-// PFLOP/s, busy 62 % at the 1.8 GHz that the power limit leaves) and 555 from rest; FP32 137 to
-// 148 TFLOP/s.  A step's copies, reads and barriers take about as long as its products: the
-// spread copies (8 bits 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555)
-// are what overlaps them.  Three half slots for half tiles, wave priorities, scales fetched
-// earlier, and workgroups that stay and fetch their next tile's first steps before they store
-// made no difference.
+// Measured on MI355X at 8192^3, warm: bf16 X W^T 788 us, X W 766, weight gradient 745 (1.4 to
+// 1.5 PFLOP/s, the matrix cores busy 72 to 75 % of the time at the 1.8 GHz that the power limit
+// leaves); 8 bits 438 us (2.5 PFLOP/s, busy 62 %) and 555 from rest; FP32 137 to 148 TFLOP/s.  A
+// step's copies, reads and barriers take about as long as its products: the spread copies (8 bits
+// 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555) are what overlaps them.
+// Three half slots for half tiles, wave priorities, scales fetched earlier, and workgroups that
+// stay and fetch their next tile's first steps before they store made no difference.  Four waves
+// of 128 x 128 read a third less from LDS, which is faster while the power limit holds (bf16
+// 8192^3: 751 us) but slower for ragged groups (16384 rows of 32 experts, X W 318 us against
+// 311, X W^T 336 against 323), whose half tiles then lack waves to hide their waits.
 #pragma once
 
 #include <type_traits>
@@ -39,10 +33,10 @@
 
 namespace gemmlp {
 
-template <class T, bool AKC, bool BKC, bool WGRAD, int HOW, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void lp_deep_kernel(LpArgs p) {
-  constexpr int BM = 256, BN = 256, WN = WAVES / 2;
-  constexpr int WTM = 128, WTN = BN / WN, HALF = WTM / 2, SM = 8, SN = WTN / 16, SH = SM / 2;
+template <class T, bool AKC, bool BKC, bool WGRAD, int HOW>
+__global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
+  constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
+  constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
   constexpr bool F8T = T::BYTES == 1;
   static_assert(!F8T || HOW == kFast8Blocks || HOW == kScaled8, "not enough registers");
   constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
@@ -261,18 +255,18 @@ __global__ __launch_bounds__(64 * WAVES) void lp_deep_kernel(LpArgs p) {
       issue_first(0);
       if (steps > 1) issue_first(1);
       int8v h[SH];
-      auto half_step = [&](auto left, int kt) {  // of which LEFT follow
-        constexpr int LEFT = decltype(left)::value;
+      for (int kt = 0; kt < steps; ++kt) {
         const char* slot = lds + (kt & 1) * SLOT;
-        part_barrier<LEFT == 0 ? 0 : FIRST>();
+        if (kt + 1 < steps) part_barrier<FIRST>();
+        else part_barrier<0>();
 #pragma unroll
         for (int j = 0; j < SN; j += OB::READ) ob.read(slot + B0, j, b + j);
 #pragma unroll
         for (int i = 0; i < SH; i += OA::READ) oa1.read(slot + A1, i, h + i);
         read_scales(kt);
         part_barrier<63>();  // (the copies stay open)
-        if constexpr (LEFT == 2) issue_first(kt + 2);
-        if constexpr (LEFT == 0) {
+        if (kt + 2 < steps) issue_first(kt + 2);
+        if (kt + 1 == steps) {
           if constexpr (AKC) {
 #pragma unroll
             for (int i = 0; i < SH; ++i) h[i] &= last_mask;
@@ -287,10 +281,7 @@ __global__ __launch_bounds__(64 * WAVES) void lp_deep_kernel(LpArgs p) {
           if (s < SH * SN) product_of(s, s / SN, s % SN, h[s / SN]);
           if (s >= kLag) add_to(s - kLag, (s - kLag) / SN, (s - kLag) % SN);
         }
-      };
-      for (int kt = 0; kt + 2 < steps; ++kt) half_step(Two{}, kt);
-      if (steps > 1) half_step(One{}, steps - 2);
-      half_step(None{}, steps - 1);
+      }
       store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
       return;
     }

@@ -25,7 +25,7 @@ static LpKernel pick(int tile, bool staged) {
     // 8-bit values through the 16-bit instruction, or with a scale for each column, need more
     // registers than a wave of the deep kernel has
     if constexpr (T::BYTES != 1 || U::HOW == kFast8Blocks || U::HOW == kScaled8)
-      return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD, U::HOW, deep_waves(LP_UNIT)>;
+      return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD, U::HOW>;
     else if constexpr (U::HOW == kFast8Rows)
       return pipe<U, 256, 256, 2, 4, false>();
   }

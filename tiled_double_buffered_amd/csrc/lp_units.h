@@ -43,12 +43,6 @@ template <> struct UnitOf<13> : Unit<F8, true, true, false, 4> {};
 template <> struct UnitOf<14> : Unit<F8, true, true, false, 5> {};
 constexpr int kUnits = 15;
 
-// Waves of the 256 x 256 tile (lp_deep.h): four for 16-bit rows and exponent scales.
-constexpr int deep_waves(int unit) { return (unit < 6 && unit % 3 != 2) || unit == 12 ? 4 : 8; }
-constexpr int threads_of(int unit, int tile) {
-  return tile == kTile256 ? 64 * deep_waves(unit) : kTiles[tile].threads;
-}
-
 // The kernel of a tile, or NULL where the unit has none; staged: for operands of any alignment.
 LpKernel pipe_kernel_0(int tile, bool staged);
 LpKernel pipe_kernel_1(int tile, bool staged);
