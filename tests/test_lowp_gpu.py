@@ -562,3 +562,92 @@ def test_rows_and_experts_past_32_bit_offsets():
     off[-1] = 5
     z = tdb.matmul_grouped(far.bfloat16(), w, off, transpose_w=True)
     assert torch.equal(z.float(), far.sum(1, keepdim=True).bfloat16().float().expand(5, 1024))
+
+
+# -------------------------------------------------------------------- sums of 8-bit values
+def _cancelling(M, N, K, seed):
+    """(a, b), M x K and N x K whole numbers that 8 bits hold: products of 2^16 and -2^16 cancel,
+    anywhere along K, and ones of -1, 0, 1 are what is left of them.  Every partial sum, in any
+    order, is a whole number below 2^24, so that FP32 sums are exact."""
+    g = _gen(seed)
+    a = torch.randint(0, 2, (M, K), generator=g).float()
+    b = torch.randint(-1, 2, (N, K), generator=g).float()
+    at = torch.randperm(K, generator=g)[:K // 32 * 2]
+    plus, minus = at[0::2], at[1::2]
+    big = 256.0 * (1 - 2 * torch.randint(0, 2, (M, 1), generator=g).float())
+    a[:, plus], a[:, minus] = big, -big
+    b[:, at] = 256.0 * (1 - 2 * torch.randint(0, 2, (N, 1), generator=g).float())
+    ref, mag = lo.product(a.double(), b.double().t())
+    assert mag.max() < 2 ** 24 and ref.abs().max() <= 256  # which every type holds
+    assert ref.abs().max() > 0
+    return a, b, ref
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("b_block", [1, 128])
+@pytest.mark.parametrize("shape", [(40, 70, 128), (300, 130, 1024), (1, 260, 2053), (130, 300, 3000)],
+                         ids=str)
+def test_8_bit_sums_hold_32_bits(shape, b_block, out, tile):
+    """Small products next to large ones that cancel: what is left of the sum is exact."""
+    M, N, K = shape
+    a, b, ref = _cancelling(M, N, K, 101 + K)
+    g = _gen(102)
+    sa = torch.exp2(torch.randint(-2, 3, (M, 1), generator=g).float()).expand(M, lo.blocks(K))
+    sb = torch.exp2(torch.randint(-2, 3, (-(-N // b_block), 1), generator=g).float())
+    ref = ref * sa[:, :1].double() * sb.double().repeat_interleave(b_block, 0)[:N].t()
+    sa, sb = sa.contiguous().to(DEV), sb.expand(-1, lo.blocks(K)).contiguous().to(DEV)
+    ad, bd = a.to(lo.F8).to(DEV), b.to(lo.F8).to(DEV)
+    for p, r in ((ad, bd), (_aligned(ad), _aligned(bd))):
+        _say("[sums]", shape, b_block, out)
+        c = tdb.matmul_fp8(p, sa, r, sb, out_dtype=TYPES[out])
+        assert torch.equal(c.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("out", TYPES)
+def test_8_bit_sums_of_experts_hold_32_bits(out, tile):
+    M, N, K = 70, 130, 1280
+    a, b, _ = _cancelling(M, 2 * N, K, 103)
+    off, one = [0, 30, 30, M], torch.ones(M, lo.blocks(K), device=DEV)
+    w = torch.stack([b[:N], b[:N], b[N:]])
+    ref = torch.cat([a[:30].double() @ b[:N].double().t(), a[30:].double() @ b[N:].double().t()])
+    c = tdb.matmul_fp8_grouped(a.to(lo.F8).to(DEV), one, w.to(lo.F8).to(DEV),
+                               torch.ones(3, lo.blocks(N), lo.blocks(K), device=DEV),
+                               torch.tensor(off, dtype=torch.int32, device=DEV), TYPES[out])
+    assert torch.equal(c.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_8_bit_training_sums_hold_32_bits(dtype, tile):
+    """The same along each of the three contractions of a step (256 and 1 are exact in 8 bits
+    with any scale that a block of them gets)."""
+    for which, (M, N, K) in enumerate(((50, 90, 2048), (50, 2048, 90), (2048, 50, 90))):
+        x, w, dy = (torch.zeros(s) for s in ((M, K), (N, K), (M, N)))
+        if which == 0:
+            x, w, ref = _cancelling(M, N, K, 104)
+        elif which == 1:
+            dy, wt, ref = _cancelling(M, K, N, 105)
+            w = wt.t().contiguous()
+        else:
+            dyt, xt, ref = _cancelling(N, K, M, 106)
+            dy, x = dyt.t().contiguous(), xt.t().contiguous()
+        xd, wd = (t.to(TYPES[dtype]).to(DEV).requires_grad_() for t in (x, w))
+        _say("[training sums]", dtype, which)
+        y = tdb.linear_fp8(xd, wd)
+        got = (y.detach(), *torch.autograd.grad(y, (xd, wd), dy.to(TYPES[dtype]).to(DEV)))
+        assert torch.equal(got[which].cpu().double(), ref), which
+
+
+@pytest.mark.parametrize("K", [1024, 8192])
+@pytest.mark.parametrize("b_block", [1, 128])
+def test_8_bit_sums_are_off_by_little_in_the_mean(K, b_block, tile):
+    """n roundings of at most 2^-23 of partial sums that stay under 4 sqrt(n) p (p the products'
+    root mean square), with no common sign: together 4 n p 2^-23 in the mean square, and the sum
+    of magnitudes is n p / 2 at least for normal values, so 8 * 2^-23 of it."""
+    a, sa = _scaled(64, K, 1, 107)
+    b, sb = _scaled(96, K, b_block, 108)
+    sa = torch.exp2(torch.round(torch.log2(sa[:, :1]))).expand(sa.shape).contiguous()
+    sb = torch.ones_like(sb)
+    ref, mag = lo.product(lo.values(a, sa, 1), lo.values(b, sb, b_block).t())
+    c = tdb.matmul_fp8(*(t.to(DEV) for t in (a, sa, b, sb)), out_dtype=torch.float32)
+    off = (c.cpu().double() - ref).square().mean().sqrt()
+    assert off <= 8 * 2.0 ** -23 * mag.square().mean().sqrt()

@@ -28,7 +28,7 @@ CFG_SOURCE = os.path.join(CSRC, "cfg_kernels.hip")
 NUM_CONFIGS = 20  # configs.h: kNumConfigs
 LP_SOURCE = os.path.join(CSRC, "gemm_lp.hip")  # low-precision and expert-grouped products
 LP_UNIT_SOURCE = os.path.join(CSRC, "lp_kernels.hip")
-NUM_LP_UNITS = 15  # lp_units.h: kUnits
+NUM_LP_UNITS = 12  # lp_units.h: kUnits
 SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",

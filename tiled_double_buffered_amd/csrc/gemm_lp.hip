@@ -74,17 +74,14 @@ static LpKernel pipe_kernel(int unit, int tile, bool staged) {
     case 8: return pipe_kernel_8(tile, staged);
     case 9: return pipe_kernel_9(tile, staged);
     case 10: return pipe_kernel_10(tile, staged);
-    case 11: return pipe_kernel_11(tile, staged);
-    case 12: return pipe_kernel_12(tile, staged);
-    case 13: return pipe_kernel_13(tile, staged);
-    default: return pipe_kernel_14(tile, staged);
+    default: return pipe_kernel_11(tile, staged);
   }
 }
 
 // What half a tile of a row product costs, where it is computed in halves (lp_deep.h, and the
 // 64-row tiles of FP32); 1 where it is not.
 static double half_cost(int unit, int tile) {
-  if (tile == kTile256) return unit == 11 ? 1.0 : 0.72;
+  if (tile == kTile256) return 0.72;
   return tile != kTile128 && (unit == 6 || unit == 7) ? 0.55 : 1.0;
 }
 
@@ -139,8 +136,6 @@ constexpr StepCost kStep16Grad[kTileCount] = {
 constexpr StepCost kStep32[kTileCount] = {
     {7.30, 7.30, 2}, {2.00, 1.87, 3.5}, {0.66, 0.51, 0.7}, {0.60, 0.60, 2}};
 constexpr StepCost kStep8[kTileCount] = {
-    {1.40, 1.95, 2}, {0.80, 0.68, 2}, {0.45, 0.29, 2}, {0.25, 0.34, 4}};
-constexpr StepCost kStep8Exact[kTileCount] = {
     {0, 0, 0}, {1.20, 0.93, 2}, {0.60, 0.36, 2}, {0.37, 0.37, 2}};
 
 // The tile of the pipelined kernels with the least time; `rounds(tile)` is the number of rounds
@@ -156,8 +151,7 @@ static int pick_tile(int unit, bool staged, bool rows, double steps, double skew
   }
   const StepCost* cost = unit < 6 ? (rows ? kStep16 : kStep16Grad)
                          : unit < 9 ? kStep32
-                         : unit == 9 || unit >= 13 ? kStep8Exact
-                                                   : kStep8;
+                                    : kStep8;
   int best = -1;
   double least = 0;
   for (int t = 0; t < kTileCount; ++t) {
@@ -301,12 +295,7 @@ static int run_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t* of
   a.ldsa = ldsa, a.ldsb = ldsb, a.stride_sb = stride_sb;
   a.rows = a.M = (int)M, a.N = (int)N, a.K = (int)K, a.E = (int)E;
   a.sb_shift = b_block == 1 ? 0 : 7, a.c_type = c_type;
-  // The 8-bit instruction cuts up to 2^-12.2 of its 128 products' magnitudes S (2^-16 on
-  // average, lp_common.h).  It is taken for bf16 results, which keep 8 bits, of contractions
-  // from 1024 on, where n products added in FP32 in any order may be off by n 2^-23 S = 2^-13 S
-  // themselves; other results go through the 16-bit instruction, which cuts nothing.
-  const bool fast = c_type == GEMM_LP_BF16 && K >= 1024;
-  const int unit = EXP ? (fast ? 12 : 13) : b_block == 1 ? (fast ? 11 : 9) : fast ? 10 : 14;
+  const int unit = EXP ? 11 : b_block == 1 ? 9 : 10;
   const bool staged = !(word_rows(A, lda, 0, 1) && word_rows(B, ldb, stride_b, 1));
   const int t = pick_tile(unit, staged, true, k_steps(K, 1), 1.0,
                           [&](int tile) { return row_rounds(a, unit, tile); });

@@ -49,10 +49,11 @@ static inline __host__ __device__ int type_bytes(int code) { return code == GEMM
 // its lane group l / 16 stands for; both operands use the same groups, so that the order of
 // k inside the step does not matter.  D's row index comes from `a`, its column from `b`:
 // lane l, register r hold row 4 (l / 16) + r, column l % 16.
-// 8-bit values go through the 16-bit instruction here, which every e4m3 number and product
-// fits exactly: the 8-bit instruction aligns its 128 products to the largest and cuts what
-// falls below (measured: up to 2^-12.2 of the sum of magnitudes, 2^-16 on average), so its
-// sums hold fewer than 32 bits.
+// 8-bit values go through the 16-bit instruction, which every e4m3 number fits exactly and
+// whose sums hold FP32's 24 bits below their largest product.  The 8-bit instructions (16x16x128
+// and 16x16x32 alike) hold 13 bits below the largest of each eight neighbouring products:
+// 256 * 256 - 256 * 256 + 2 * 2 comes out as 0, and sums over all of e4m3's exponents are off by
+// up to 2^-12.5 of their magnitudes (2^-15.4 in the mean square; FP32 2^-21.3 and 2^-24).
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ half8v fp8x8_to_half(int w0, int w1) {
   const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
@@ -140,8 +141,7 @@ __device__ __forceinline__ int xcd_order(int w, int n) {
 }
 
 // Tiles of one group are walked in bands of kBand tile rows, column by column, so that the
-// workgroups of one XCD that run together share rows of A and of B in its L2 (8192^3 in 8 bits:
-// 438 us in bands of 4, 443 of 6, 454 of 8, 459 of 16).
+// workgroups of one XCD that run together share rows of A and of B in its L2.
 constexpr int kBand = 4;
 __device__ __forceinline__ void band_order(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = id / (kBand * tiles_n);
@@ -168,7 +168,7 @@ __device__ __forceinline__ void wgrad_tile(int wg, int per, int tiles_m, int til
 // HALF > 0: half a tile (HALF rows or fewer) costs less than a whole one (256 rows 0.72, 64 rows
 // of FP32 0.55), and they come last, to fill the last round: a group's last tile where it has no
 // more rows; and both halves of each tile of the last round, where these and the others fit into
-// one round (8 bits, 2304 x 8192 x 4096, 288 tiles: 98 us, 105 with whole tiles).
+// one round.
 template <int BM, int HALF>
 __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   int tm;

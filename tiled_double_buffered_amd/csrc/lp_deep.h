@@ -1,13 +1,12 @@
-// The pipelined product kernel for large products: 256 x 256 tiles, eight waves of 128 x 64,
+// The pipelined product kernel for large products of 16- and 32-bit values: 256 x 256 tiles, eight waves of 128 x 64,
 // two LDS slots refilled in halves, so that a copy has one and a half K steps to land.
 //
 // The kernel of lp_pipe.h starts a step's copies when the slot's last reader is done and needs
-// them one step later, and waits for them (8 bits: 40 % of all wave cycles).  Here each slot has
-// three parts that are freed at different times: B, which a wave holds in registers for the
+// them one step later, and waits for them.  Here each slot has three parts that are freed at different times: B, which a wave holds in registers for the
 // whole step, the upper half A1 of A's rows, which the step's first products read, and the
 // lower half A2.  A step has two barriers:
 //   middle (before the products of the last A1 fragment): B, A1 of this step are read by all
-//     waves, A2 of this step has landed; the copies of B, A1 (and scales) two steps on start;
+//     waves, A2 of this step has landed; the copies of B, A1 two steps on start;
 //   end (before the products of the last two A2 fragments): A2 of this step is read, B and A1
 //     of the next have landed; the copies of A2 two steps on start.  The last two rows of
 //     products go column by column, so that B's fragments are replaced one by one.
@@ -17,11 +16,10 @@
 //
 // Measured on MI355X at 8192^3, warm: bf16 X W^T 788 us, X W 766, weight gradient 745 (1.4 to
 // 1.5 PFLOP/s, the matrix cores busy 72 to 75 % of the time at the 1.8 GHz that the power limit
-// leaves); 8 bits 438 us (2.5 PFLOP/s, busy 62 %) and 555 from rest; FP32 137 to 148 TFLOP/s.  A
-// step's copies, reads and barriers take about as long as its products: the spread copies (8 bits
-// 630 -> 604 us), B replaced piece by piece and scalar walks (596 -> 555) are what overlaps them.
-// Three half slots for half tiles, wave priorities, scales fetched earlier, and workgroups that
-// stay and fetch their next tile's first steps before they store made no difference.  Four waves
+// leaves); FP32 137 to 148 TFLOP/s.  A step's copies, reads and barriers take about as long as its
+// products: the spread copies, B replaced piece by piece and scalar walks are what overlaps them.
+// Three half slots for half tiles, wave priorities, and workgroups that stay and fetch their next
+// tile's first steps before they store made no difference.  Four waves
 // of 128 x 128 read a third less from LDS, which is faster while the power limit holds (bf16
 // 8192^3: 751 us) but slower for ragged groups (16384 rows of 32 experts, X W 318 us against
 // 311, X W^T 336 against 323), whose half tiles then lack waves to hide their waits.
@@ -33,28 +31,17 @@
 
 namespace gemmlp {
 
-template <class T, bool AKC, bool BKC, bool WGRAD, int HOW>
+template <class T, bool AKC, bool BKC, bool WGRAD>
 __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
   constexpr int BM = 256, BN = 256, WN = 4, WAVES = 8;
   constexpr int WTM = 128, WTN = 64, HALF = WTM / 2, SM = 8, SN = 4, SH = SM / 2;
-  constexpr bool F8T = T::BYTES == 1;
-  static_assert(!F8T || HOW == kFast8Blocks || HOW == kScaled8, "not enough registers");
-  constexpr bool PACK = T::BYTES <= 2;  // C has 16 bits
+  static_assert(T::BYTES != 1, "not enough registers");
+  constexpr bool PACK = T::BYTES == 2;
   using OA = PipeOperand<T, AKC, BM / 2, HALF, WAVES>;
   using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
-  using OS = ScaleCopy<HOW, BM, BN>;
-  // FP32 scales: 16 bytes, four steps' worth, of every row of A and column of B at once, into
-  // two tables in turn (64 rows' scales lie in 64 lines of the cache, and a copy takes a line a
-  // cycle).  So that a wave's count of copies is the same in every step, the three steps between
-  // copy nothing, zeros, to a place of their own.
-  constexpr bool QUADS = F8T && !OS::EXP;
-  constexpr int SCALES = F8T && !QUADS ? OS::BYTES : 0;
-  constexpr int TABLE = (BM + BN) * 16;
-  constexpr int A1 = 0, A2 = OA::BYTES, B0 = 2 * OA::BYTES, S0 = B0 + OB::BYTES;
-  constexpr int SLOT = S0 + SCALES;
-  constexpr int TABLES = 2 * SLOT, NOWHERE = TABLES + 2 * TABLE;
-  constexpr int FIRST = OA::COPIES + OB::COPIES + (F8T ? 1 : 0), SECOND = OA::COPIES;
-  __shared__ __align__(1024) char lds[2 * SLOT + (QUADS ? 2 * TABLE + WAVES * 1024 : 0)];
+  constexpr int A1 = 0, A2 = OA::BYTES, B0 = 2 * OA::BYTES, SLOT = B0 + OB::BYTES;
+  constexpr int FIRST = OA::COPIES + OB::COPIES, SECOND = OA::COPIES;
+  __shared__ __align__(1024) char lds[2 * SLOT];
   static_assert(sizeof(lds) <= 160 * 1024, "LDS of one CU");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -76,24 +63,11 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     ob.init(w.B, p.ldb, w.n0, p.N, w.k_end, wave, lane, wn);
     const uint32_t lds0 =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_char*)lds);
-    OS os;
-    if constexpr (F8T) os.init(p, w, steps, wave, lane);
-    auto issue_scales = [&](int kt, int4v r) {
-      if constexpr (QUADS) {
-        const bool real = (kt & 3) == 0;
-        r[2] = real ? r[2] : 0;
-        copy16(lds0 + (uint32_t)((real ? TABLES + (kt >> 2 & 1) * TABLE : NOWHERE) + wave * 1024),
-               r, os.off);
-      } else if constexpr (F8T) {
-        os.copy(r, lds0 + (uint32_t)((kt & 1) * SLOT + S0));
-      }
-    };
     // (each is called for one step after another)
-    Walk to_b, to_a1, to_a2, to_s;
+    Walk to_b, to_a1, to_a2;
     ob.start(to_b);
     oa1.start(to_a1);
     oa2.start(to_a2);
-    if constexpr (F8T) os.start(to_s);
     auto issue_first = [&](int kt) {
       const uint32_t at = lds0 + (uint32_t)((kt & 1) * SLOT);
       const int4v rb = to_b.next(), ra = to_a1.next();
@@ -101,7 +75,6 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       for (int i = 0; i < OB::COPIES; ++i) ob.copy(i, rb, at + B0, wave);
 #pragma unroll
       for (int i = 0; i < OA::COPIES; ++i) oa1.copy(i, ra, at + A1, wave);
-      if constexpr (F8T) issue_scales(kt, to_s.next());
     };
     auto issue_second = [&](int kt) {
       const uint32_t at = lds0 + (uint32_t)((kt & 1) * SLOT);
@@ -122,8 +95,6 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     }
 
     int8v b[SN], a[OA::READ == 1 ? 4 : 2 * OA::READ];
-    float s_a[SM];         // kFast8Blocks: of the row, times the block's of B
-    int x_a[SM], x_b[SN];  // kScaled8
     // Fragment i of A is held in a[set_of(i)] from before its products to their end; the first
     // of a step is read while the last two of the step before are still in use.
     auto set_of = [](int i) { return OA::READ > 1 ? i : i == 0 ? 2 : i == SM - 1 ? 3 : 1 - (i & 1); };
@@ -132,55 +103,13 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       (i < SH ? oa1 : oa2).read(slot + (i < SH ? A1 : A2), i % SH, a + set_of(i));
       if (AKC && masked) a[set_of(i)] &= last_mask;
     };
-    auto read_scales = [&](int kt) {
-      if constexpr (QUADS) {
-        const char* table = lds + TABLES + (kt >> 2 & 1) * TABLE + (kt & 3) * 4;
-        const float block = *(const float*)(table + (BM + wn) * 16);
-#pragma unroll
-        for (int i = 0; i < SM; ++i) s_a[i] = *(const float*)(table + row_of(i) * 16) * block;
-      } else if constexpr (F8T) {
-        const char* table = lds + (kt & 1) * SLOT + S0;
-        if constexpr (HOW == kScaled8) {
-#pragma unroll
-          for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, row_of(i));
-#pragma unroll
-          for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
-        }
-      }
-    };
-    // The sums of a step of 8-bit values are scaled and added kLag products behind, while the
-    // matrix cores work on the next ones.
-    constexpr int kLag = 2, kRing = 3;
-    float4v d[kRing];
     // Product number s of a step: row by row, the last two rows column by column.
     constexpr int ROWS = SM - 2;
     auto row_at = [](int s) { return s < ROWS * SN ? s / SN : ROWS + (s & 1); };
     auto col_at = [](int s) { return s < ROWS * SN ? s % SN : (s - ROWS * SN) / 2; };
-    auto product_of = [&](int s, int i, int j, const int8v& fa) {
-      if constexpr (HOW == kScaled8) {
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], fa, acc[i][j], 0, 0, 0,
-                                                                     x_b[j], 0, x_a[i]);
-      } else if constexpr (F8T) {
-        const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-        d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            b[j], fa, z, 0, 0, 0, 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      } else {
-        acc[i][j] = mma_half<T>(half_of(b[j], 0), half_of(fa, 0), acc[i][j]);
-        acc[i][j] = mma_half<T>(half_of(b[j], 1), half_of(fa, 1), acc[i][j]);
-      }
-    };
-    auto add_to = [&](int s, int i, int j) {
-      if constexpr (F8T && HOW != kScaled8) {
-        const float4v v = d[s % kRing];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] += v[r] * s_a[i];
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    auto product = [&](int s) { product_of(s, row_at(s), col_at(s), a[set_of(row_at(s))]); };
-    auto add = [&](int s) {
-      if (s >= 0) add_to(s, row_at(s), col_at(s));
+    auto product_of = [&](int i, int j, const int8v& fa) {
+      acc[i][j] = mma_half<T>(half_of(b[j], 0), half_of(fa, 0), acc[i][j]);
+      acc[i][j] = mma_half<T>(half_of(b[j], 1), half_of(fa, 1), acc[i][j]);
     };
     // Step kt, of which LEFT follow (2: two or more).  No branch inside: values that live across
     // branches cost registers that the wave does not have.
@@ -189,8 +118,8 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
       const char* slot = lds + (kt & 1) * SLOT;
       const char* next = lds + ((kt + 1) & 1) * SLOT;
       const uint32_t to = lds0 + (uint32_t)((kt & 1) * SLOT);
-      int4v rb, ra, rs;  // sources of the copies for step kt + 2
-      int done = 0;      // of them (a constant wherever it is used)
+      int4v rb, ra;  // sources of the copies for step kt + 2
+      int done = 0;  // of them (a constant wherever it is used)
       if constexpr (LEFT == 0) {
         if constexpr (AKC) a[set_of(0)] &= last_mask;
         if constexpr (BKC) {
@@ -206,7 +135,6 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           if constexpr (LEFT == 2) {
             rb = to_b.next();
             ra = to_a1.next();
-            if constexpr (F8T) rs = to_s.next();
           }
         }
         if (s == ROWS * SN && LEFT > 0) {
@@ -218,8 +146,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         if (OA::READ == 1 && s == SH * SN + 1)  // well before the end barrier
           read_a(slot, SM - 1, LEFT == 0);
         __builtin_amdgcn_sched_barrier(0);
-        product(s);
-        add(s - kLag);
+        product_of(i, j, a[set_of(i)]);
         // The copies go out between the products: a wave waits for each to be taken, 16 cycles
         // a copy for all waves of the CU together.
         if constexpr (LEFT == 2) {
@@ -227,8 +154,7 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
             constexpr int SLOTS = (ROWS - SH + 1) * SN;
             while (done * SLOTS < (s - (SH - 1) * SN + 1) * FIRST) {
               if (done < OB::COPIES) ob.copy(done, rb, to + B0, wave);
-              else if (done < OB::COPIES + OA::COPIES) oa1.copy(done - OB::COPIES, ra, to + A1, wave);
-              else if constexpr (F8T) issue_scales(kt + 2, rs);
+              else oa1.copy(done - OB::COPIES, ra, to + A1, wave);
               ++done;
             }
           } else if (s >= ROWS * SN) {
@@ -242,9 +168,6 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           ob.read(next + B0, j + 1 - OB::READ, b + j + 1 - OB::READ);  // done with these columns
         __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int s = SM * SN - kLag; s < SM * SN; ++s) add(s);
-      if constexpr (LEFT > 0) read_scales(kt + 1);
     };
     using Two = std::integral_constant<int, 2>;
     using One = std::integral_constant<int, 1>;
@@ -263,7 +186,6 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
         for (int j = 0; j < SN; j += OB::READ) ob.read(slot + B0, j, b + j);
 #pragma unroll
         for (int i = 0; i < SH; i += OA::READ) oa1.read(slot + A1, i, h + i);
-        read_scales(kt);
         part_barrier<63>();  // (the copies stay open)
         if (kt + 2 < steps) issue_first(kt + 2);
         if (kt + 1 == steps) {
@@ -277,12 +199,9 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
           }
         }
 #pragma unroll
-        for (int s = 0; s < SH * SN + kLag; ++s) {
-          if (s < SH * SN) product_of(s, s / SN, s % SN, h[s / SN]);
-          if (s >= kLag) add_to(s - kLag, (s - kLag) / SN, (s - kLag) % SN);
-        }
+        for (int s = 0; s < SH * SN; ++s) product_of(s / SN, s % SN, h[s / SN]);
       }
-      store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
+      store_tile<OB, T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
       return;
     }
 
@@ -298,12 +217,11 @@ __global__ __launch_bounds__(512) void lp_deep_kernel(LpArgs p) {
     read_a(lds, 0, false);
 #pragma unroll
     for (int j = 0; j < SN; j += OB::READ) ob.read(lds + B0, j, b + j);
-    read_scales(0);
     for (int kt = 0; kt + 2 < steps; ++kt) step(Two{}, kt);
     if (steps > 1) step(One{}, steps - 2);
     step(None{}, steps - 1);
   }
-  store_tile<OB, F8T ? GEMM_LP_BF16 : T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
+  store_tile<OB, T::CODE>(p, w, wn, g, acc, [&](int i) { return w.m0 + row_of(i); });
 }
 
 }  // namespace gemmlp

@@ -22,18 +22,14 @@ template <class U>
 static LpKernel pick(int tile, bool staged) {
   using T = typename U::type;
   if (tile == kTile256 && !staged) {
-    // 8-bit values through the 16-bit instruction, or with a scale for each column, need more
-    // registers than a wave of the deep kernel has
-    if constexpr (T::BYTES != 1 || U::HOW == kFast8Blocks || U::HOW == kScaled8)
-      return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD, U::HOW>;
-    else if constexpr (U::HOW == kFast8Rows)
-      return pipe<U, 256, 256, 2, 4, false>();
+    // 8-bit values, converted on the way, need more registers than a wave of this kernel has
+    if constexpr (T::BYTES != 1) return &lp_deep_kernel<T, U::AKC, U::BKC, U::WGRAD>;
   }
   if (tile == kTile128) {
     // (these need a few registers more than two workgroups of a CU have)
-    if constexpr (T::BYTES == 1 && U::HOW == kExact8Rows)
+    if constexpr (T::BYTES == 1 && U::HOW == kScaleRows)
       if (staged) return nullptr;
-    return staged ? pipe<U, 128, 128, 2, 2, !(T::BYTES == 1 && U::HOW == kExact8Rows)>()
+    return staged ? pipe<U, 128, 128, 2, 2, !(T::BYTES == 1 && U::HOW == kScaleRows)>()
                   : pipe<U, 128, 128, 2, 2, false>();
   }
   if (tile == kTile64)

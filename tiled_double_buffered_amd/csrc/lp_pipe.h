@@ -22,9 +22,8 @@
 // 128 x 128 tiles need as many cycles for them as for their products in 16 bits, 1090 TFLOP/s in
 // bf16 at 8192^3), with few rows the reading of B (16 rows of 14 of 64 experts, 4096 x 2048 in
 // bf16: 58 us, 4.05 TB/s; torch.sum reads as much memory at 3.5), with little work the latency of
-// a step, which four wave groups on one tile share (1 x 11008 x 4096 in 8 bits: 12 us, 18 with one
-// group).  8-bit values through the 16-bit instruction: 1120 TFLOP/s at 8192 x 4096 x 4096, bound
-// by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles, 132 on
+// a step, which four wave groups on one tile share.  8-bit values: 1120 TFLOP/s at 8192 x 4096 x
+// 4096, bound by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles, 132 on
 // 64 x 64.
 #pragma once
 
@@ -397,33 +396,16 @@ __device__ __forceinline__ bool locate(const LpArgs& p, TileOf& w) {
   return true;
 }
 
-// How 8-bit values are multiplied and scaled:
-//   kExact8Blocks, kExact8Rows: through the 16-bit instruction, FP32 scales, B's by blocks of
-//     128 columns or column by column;
-//   kFast8Blocks, kFast8Rows: through the 8-bit instruction, B's scales by blocks, by columns;
-//   kScaled8: through the 8-bit instruction, which applies the scales itself: they are powers of
-//     two, one exponent byte for each row and column;
-//   kExactScaled8: such scales, through the 16-bit instruction.
-enum {
-  kExact8Rows = 0,
-  kFast8Blocks = 1,
-  kFast8Rows = 2,
-  kScaled8 = 3,
-  kExactScaled8 = 4,
-  kExact8Blocks = 5
-};
-constexpr bool by_exponents(int how) { return how == kScaled8 || how == kExactScaled8; }
-constexpr bool exact(int how) {
-  return how == kExact8Rows || how == kExact8Blocks || how == kExactScaled8;
-}
-constexpr bool by_blocks(int how) { return how == kFast8Blocks || how == kExact8Blocks; }
+// How 8-bit values are scaled: FP32 scales, B's column by column or by blocks of 128 columns; or
+// powers of two, one exponent byte for each row and column.
+enum { kScaleRows = 0, kScaleBlocks = 1, kScaleExponents = 2 };
 
 // The copies of a K step's scales (8-bit values) into the slot's table, A's rows first: FP32
 // numbers, 64 a wave, or exponent bytes, which every wave copies for A or for B (the same bytes:
 // a wave's copies of a step then have one count).
 template <int HOW, int BM, int BN>
 struct ScaleCopy {
-  static constexpr bool EXP = by_exponents(HOW);
+  static constexpr bool EXP = HOW == kScaleExponents;
   static constexpr int B_AT = EXP ? 256 : BM * 4;       // B's part
   static constexpr int BYTES = EXP ? 512 : (BM + BN) * 4;
   static constexpr int WAVES = EXP ? 64 : (BM + BN) / 64;  // waves that copy
@@ -471,12 +453,6 @@ struct ScaleCopy {
   // Scales from the table: of row r of A, of column c of B, of columns c .. c + 3.
   static __device__ __forceinline__ float number(uint32_t byte) {
     return __builtin_bit_cast(float, byte << 23);  // 2^(byte - 127)
-  }
-  static __device__ __forceinline__ int a_byte(const char* table, int r) {
-    return (uint8_t)table[r];
-  }
-  static __device__ __forceinline__ int b_byte(const char* table, int c) {
-    return (uint8_t)table[B_AT + c];
   }
   static __device__ __forceinline__ float a(const char* table, int r) {
     if constexpr (EXP) return number((uint8_t)table[r]);
@@ -541,7 +517,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 16, SN = WTN / 16;
   constexpr bool F8T = T::BYTES == 1;
   using OA = PipeOperand<T, AKC, BM, WTM, WAVES>;
-  constexpr bool PACK = T::BYTES == 2 || (F8T && !exact(HOW));  // C has 16 bits
+  constexpr bool PACK = T::BYTES == 2;  // (C has 16 bits)
   using OB = PipeOperand<T, BKC, BN, WTN, WAVES, PACK>;
   using OS = ScaleCopy<HOW, BM, BN>;
   constexpr int SCALES = F8T ? OS::BYTES : 0;
@@ -606,12 +582,12 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
       issue(group, 0);
       settle(0);
     }
-    // 8-bit values through the 16-bit instruction: the next step's copies go out between this
+    // 8-bit values: the next step's copies go out between this
     // one's products, since a wave waits for each to be taken (8192^3: 1014 us, 1153 with the
     // copies first); past the last step they have nothing to copy, zeros into a slot that is
     // not read again.  The others, whose steps are shorter, lose by it (bf16 X W^T 1167 us, 1024
     // with the copies first).
-    constexpr bool SPREAD = F8T && exact(HOW) && !STAGED && KG == 1 && BM >= 128;
+    constexpr bool SPREAD = F8T && !STAGED && KG == 1 && BM >= 128;
     constexpr int SENT = OA::COPIES + OB::COPIES + 1;
     static_assert(!SPREAD || OS::EXP || OS::WAVES == WAVES, "every wave copies scales");
     const int rounds = (steps + KG - 1) / KG;
@@ -675,30 +651,21 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
           oa.read(sa, 0, a);
           float4v s_b[SN];
           float s_a[SM];
-          int x_a[SM], x_b[SN];
-          if constexpr (HOW == kScaled8) {
 #pragma unroll
-            for (int j = 0; j < SN; ++j) x_b[j] = OS::b_byte(table, wn + OB::row_of(j, l16));
+          for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
+          if constexpr (HOW == kScaleBlocks) {
+            // the wave's columns lie in one block of 128: one factor a row
+            static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
+            const float block = OS::b(table, wn);
 #pragma unroll
-            for (int i = 0; i < SM; ++i) x_a[i] = OS::a_byte(table, wm + 16 * i + l16);
+            for (int i = 0; i < SM; ++i) s_a[i] *= block;
           } else {
 #pragma unroll
-            for (int i = 0; i < SM; ++i) s_a[i] = OS::a(table, wm + 16 * i + l16);
-            if constexpr (by_blocks(HOW)) {
-              // the wave's columns lie in one block of 128: one factor a row
-              static_assert(kBlock % WTN == 0, "a wave's columns cross a block of scales");
-              const float block = OS::b(table, wn);
-#pragma unroll
-              for (int i = 0; i < SM; ++i) s_a[i] *= block;
-            } else {
-#pragma unroll
-              for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
-            }
+            for (int j = 0; j < SN; ++j) s_b[j] = OS::b4(table, wn + OB::row_of(j, 4 * g));
           }
           // The sums of a step are scaled and added kLag products behind, while the matrix
-          // cores work on the next ones; the order is pinned, since the compiler would put each
-          // addition right behind its product and wait.
-          constexpr int kLag = HOW == kScaled8 ? 0 : exact(HOW) ? 1 : 2, kRing = kLag + 1;
+          // cores work on the next ones.
+          constexpr int kLag = 1, kRing = kLag + 1;
           float4v d[kRing];
 #pragma unroll
           for (int s = 0; s < SM * SN + kLag; ++s) {
@@ -706,30 +673,21 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
               const int i = s / SN, j = s % SN;
               if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
               const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-              if constexpr (HOW == kScaled8)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    b[j], a[i & 1], acc[i][j], 0, 0, 0, x_b[j], 0, x_a[i]);
-              else if constexpr (exact(HOW))
-                d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
-                                           half_of(a[i & 1], 1), z);
-              else
-                d[s % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    b[j], a[i & 1], z, 0, 0, 0, 0, 0, 0);
+              d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
+                                         half_of(a[i & 1], 1), z);
               send(s, SM * SN * 3 / 4);  // the last with a quarter of the step to land
             }
-            if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
-            if (s >= kLag && HOW != kScaled8) {
+            if (s >= kLag) {
               const int i = (s - kLag) / SN, j = (s - kLag) % SN;
               const float4v v = d[(s - kLag) % kRing];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                if constexpr (by_blocks(HOW))
+                if constexpr (HOW == kScaleBlocks)
                   acc[i][j][r] += v[r] * s_a[i];
                 else
                   acc[i][j][r] += v[r] * (s_a[i] * s_b[j][r]);
               }
             }
-            if constexpr (!exact(HOW)) __builtin_amdgcn_sched_barrier(0);
           }
         }
         if (kt + KG < steps) settle((it + 1) & 1);
@@ -765,7 +723,7 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
   }
   if (KG > 1 && group > 0) return;
 
-  constexpr int OUT = !F8T ? T::CODE : exact(HOW) ? -1 : GEMM_LP_BF16;
+  constexpr int OUT = F8T ? -1 : T::CODE;
   store_tile<OB, OUT>(p, w, wn, g, acc,
                      [&](int i) {
                        return half && i >= SM / 2 ? w.m_end : w.m0 + wm + OA::row_of(i, l16);

@@ -31,17 +31,12 @@ template <> struct UnitOf<5> : Unit<F16, false, false, true, 0> {};
 template <> struct UnitOf<6> : Unit<F32, true, true, false, 0> {};
 template <> struct UnitOf<7> : Unit<F32, true, false, false, 0> {};
 template <> struct UnitOf<8> : Unit<F32, false, false, true, 0> {};
-// 8-bit (the last number is lp_pipe.h's HOW): B's scales by columns through the 16-bit
-// instruction; by blocks and by columns through the 8-bit one
+// 8-bit (the last number is lp_pipe.h's HOW): B's scales by columns, by blocks, and exponents for
+// scales
 template <> struct UnitOf<9> : Unit<F8, true, true, false, 0> {};
 template <> struct UnitOf<10> : Unit<F8, true, true, false, 1> {};
 template <> struct UnitOf<11> : Unit<F8, true, true, false, 2> {};
-// 8-bit with exponents for scales: through the 8-bit instruction, and through the 16-bit one
-template <> struct UnitOf<12> : Unit<F8, true, true, false, 3> {};
-template <> struct UnitOf<13> : Unit<F8, true, true, false, 4> {};
-// 8-bit, B's scales by blocks, through the 16-bit instruction
-template <> struct UnitOf<14> : Unit<F8, true, true, false, 5> {};
-constexpr int kUnits = 15;
+constexpr int kUnits = 12;
 
 // The kernel of a tile, or NULL where the unit has none; staged: for operands of any alignment.
 LpKernel pipe_kernel_0(int tile, bool staged);
@@ -56,8 +51,5 @@ LpKernel pipe_kernel_8(int tile, bool staged);
 LpKernel pipe_kernel_9(int tile, bool staged);
 LpKernel pipe_kernel_10(int tile, bool staged);
 LpKernel pipe_kernel_11(int tile, bool staged);
-LpKernel pipe_kernel_12(int tile, bool staged);
-LpKernel pipe_kernel_13(int tile, bool staged);
-LpKernel pipe_kernel_14(int tile, bool staged);
 
 }  // namespace gemmlp
