@@ -651,3 +651,15 @@ def test_8_bit_sums_are_off_by_little_in_the_mean(K, b_block, tile):
     c = tdb.matmul_fp8(*(t.to(DEV) for t in (a, sa, b, sb)), out_dtype=torch.float32)
     off = (c.cpu().double() - ref).square().mean().sqrt()
     assert off <= 8 * 2.0 ** -23 * mag.square().mean().sqrt()
+
+
+@pytest.mark.parametrize("shape", [(3, 5, 0), (0, 5, 64), (4, 0, 64), (64,), (0,)], ids=str)
+def test_linear_fp8_empty_and_leading_axes(shape):
+    """No rows, no depth and a single row: the axes that a linear layer gives, and zeros."""
+    K = shape[-1]
+    x = torch.zeros(shape, device=DEV).requires_grad_()
+    w = _randn(_gen(109), 7, K).to(DEV).requires_grad_()
+    y = tdb.linear_fp8(x, w)
+    assert y.shape == (*shape[:-1], 7) and not y.any()
+    dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y))
+    assert dx.shape == x.shape and dw.shape == w.shape and not dw.any()

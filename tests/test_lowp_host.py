@@ -218,3 +218,11 @@ def test_8_bit_values_are_multiplied_in_16():
         start = re.search(rf"^{re.escape(n)}:", asm, re.M).end()
         body = asm[start:asm.index(".Lfunc_end", start)]
         assert not re.search(r"v_mfma\w*(f8f6f4|fp8|bf8)", body), n
+
+
+def test_linear_fp8_of_no_depth_and_leading_axes_reaches_the_checks():
+    """(3, 5, 0): the leading axes are 15 rows, which no -1 can stand for; refused on the CPU for
+    living there alone."""
+    for shape in ((3, 5, 0), (0,), (2, 0, 0)):
+        with pytest.raises(ValueError, match="must live on the GPU"):
+            tdb.linear_fp8(torch.zeros(shape), torch.zeros(4, 0))

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -457,7 +458,8 @@ def linear_fp8(x, w):
     if w.dtype != x.dtype:
         raise TypeError(f"x is {x.dtype}, w {w.dtype}")
     _same_device(x, w)
-    flat = _row_major(x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x)
+    # (rows counted: -1 is ambiguous where K is 0)
+    flat = _row_major(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]) if x.dim() != 2 else x)
     w = _row_major(w)
     grads = torch.is_grad_enabled()  # without, no transpose is quantized for the backward pass
     if _here(x, None):
