@@ -49,7 +49,9 @@ enum {
  * is ceil(rows / block_rows) x ceil(cols / 128) with row stride lds.
  * QT, ST (both or neither): the same for the transpose of X, cols x rows bytes with row
  * stride ldqt and ceil(cols / block_rows) x ceil(rows / 128) scales with row stride ldst.
- * Q, S may be NULL (both) where only the transpose is wanted. */
+ * Q, S may be NULL (both) where only the transpose is wanted.
+ * GEMMF32_ERR_TOO_LARGE past 2^24 - 1 workgroups, of which each takes a block of 128 x 128, or
+ * sixteen of 1 x 128 where only Q and S of such blocks are wanted. */
 int gemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int64_t ldx, int type,
                       int block_rows, void *Q, int64_t ldq, float *S, int64_t lds,
                       void *QT, int64_t ldqt, float *ST, int64_t ldst, void *stream);

@@ -663,3 +663,34 @@ def test_linear_fp8_empty_and_leading_axes(shape):
     assert y.shape == (*shape[:-1], 7) and not y.any()
     dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y))
     assert dx.shape == x.shape and dw.shape == w.shape and not dw.any()
+
+
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_more_rows_than_an_axis_of_workgroups(block):
+    """Past 65535 blocks of rows; a short last one.  Whole numbers up to 15: exact."""
+    rows, cols = 65536 * 128 + 40, 8
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    some = torch.randint(-15, 16, (300, cols), generator=_gen(110)).bfloat16().to(DEV)
+    x[-300:], x[:300] = some, some.flip(0)
+    _say("[tall]", block)
+    q, s, qt, st = tdb.quantize_fp8_pair(x, block=(block, 128))
+    assert qt.shape == (cols, rows) and st.shape == ((cols, 1)[block == 128], rows // 128 + 1)
+    for at in (slice(0, 300), slice(rows - 300, rows)):
+        r = torch.arange(rows, device=DEV)[at]
+        assert torch.equal(q[at].float() * s[r // block], x[at].float())
+        scale = st[:, r // 128] if block == 1 else st[0, r // 128]
+        assert torch.equal(qt[:, at].float() * scale, x[at].float().t())
+    assert not q[300:-300].view(torch.uint8).any() and not qt[:, 300:-300].float().any()
+
+
+def test_tall_training_step():
+    """linear_fp8 of more rows than that: the weight gradient sums over all of them, exactly."""
+    rows = 65536 * 128 + 3
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV)
+    x[-5:] = torch.randint(-3, 4, (5, 8), generator=_gen(111)).bfloat16().to(DEV)
+    x[0] = 1.0
+    w = torch.randint(-3, 4, (16, 8), generator=_gen(112)).bfloat16().to(DEV).requires_grad_()
+    y = tdb.linear_fp8(x, w)
+    assert torch.equal(y[-5:].float(), x[-5:].float() @ w.detach().float().t())
+    (dw,) = torch.autograd.grad(y, w, torch.ones_like(y))
+    assert torch.equal(dw.float(), x.float().sum(0).expand(16, 8))

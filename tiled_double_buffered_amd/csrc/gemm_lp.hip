@@ -243,8 +243,9 @@ static int run_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, 
     if (wgs > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
     return launch(fn, dim3((unsigned)wgs), 256, &a, stream);
   }
-  if (mb > 65535 || kb > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
-  return launch(fn, dim3((unsigned)kb, (unsigned)mb), 256, &a, stream);
+  const int64_t wgs = mb * kb;  // (each at most 2^24)
+  if (wgs > 0xFFFFFFFFLL / 256) return GEMMF32_ERR_TOO_LARGE;
+  return launch(fn, dim3((unsigned)wgs), 256, &a, stream);
 }
 
 // EXP: the scales are exponent bytes, [block][row], as run_quantize writes them.

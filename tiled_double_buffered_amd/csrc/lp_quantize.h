@@ -138,9 +138,10 @@ __global__ __launch_bounds__(256) void lp_quantize_rows_kernel(QuantArgs p) {
 constexpr int kTurnStride = kBlock + 16;
 template <int ROWS, bool EXP, bool NO_INF>
 __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&v)[8][8],
-                                              float (&part)[4][kBlock], uint8_t* turn) {
+                                              float (&part)[4][kBlock], uint8_t* turn, int bm,
+                                              int bk) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, wave = tid >> 6;
-  const int r0 = blockIdx.y * kBlock, c0 = blockIdx.x * kBlock;
+  const int r0 = bm * kBlock, c0 = bk * kBlock;
   const int c = c0 + tx * 8;
   if constexpr (ROWS == 1) {
     if (p.Q != nullptr) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
         const int e = scale_exponent(max_over_16(top_of<8, NO_INF>(v[i], 1)));
         if (r < p.rows) {
           store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, power_of_two(e)));
-          if (tx == 0) put_scale<EXP>(p.S, p.lds, r, blockIdx.x, e);
+          if (tx == 0) put_scale<EXP>(p.S, p.lds, r, bk, e);
         }
       }
     }
@@ -169,7 +170,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
       const int e =
           scale_exponent(fmaxf(fmaxf(part[0][k], part[1][k]), fmaxf(part[2][k], part[3][k])));
       *(uint2*)(turn + k * kTurnStride + ty * 8) = to_fp8x8(&v[0][j], 8, power_of_two(e));
-      if (ty == 0 && c0 + k < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + k, blockIdx.y, e);
+      if (ty == 0 && c0 + k < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + k, bm, e);
     }
   } else {
     float m = 0.0f;
@@ -188,16 +189,16 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const float (&
         if (r < p.rows) store_bytes8(p.Q + r * p.ldq + c, p.cols - c, to_fp8x8(v[i], 1, scale));
       }
       if constexpr (EXP) {
-        if (tid < kBlock && r0 + tid < p.rows) put_scale<EXP>(p.S, p.lds, r0 + tid, blockIdx.x, e);
+        if (tid < kBlock && r0 + tid < p.rows) put_scale<EXP>(p.S, p.lds, r0 + tid, bk, e);
       } else {
-        if (tid == 0) put_scale<EXP>(p.S, p.lds, blockIdx.y, blockIdx.x, e);
+        if (tid == 0) put_scale<EXP>(p.S, p.lds, bm, bk, e);
       }
     }
     if (p.QT == nullptr) return;
     if constexpr (EXP) {
-      if (tid < kBlock && c0 + tid < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + tid, blockIdx.y, e);
+      if (tid < kBlock && c0 + tid < p.cols) put_scale<EXP>(p.ST, p.ldst, c0 + tid, bm, e);
     } else {
-      if (tid == 0) put_scale<EXP>(p.ST, p.ldst, blockIdx.x, blockIdx.y, e);
+      if (tid == 0) put_scale<EXP>(p.ST, p.ldst, bk, bm, e);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -226,8 +227,10 @@ template <class T, int ROWS, bool EXP>
 __global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
   __shared__ float part[4][kBlock];
   __shared__ __align__(16) uint8_t turn[kBlock * kTurnStride];
-  const int tid = threadIdx.x;
-  const int r0 = blockIdx.y * kBlock + (tid >> 4) * 8, c = blockIdx.x * kBlock + (tid & 15) * 8;
+  // (one axis of workgroups: the others end at 65535 of them)
+  const int tid = threadIdx.x, kb = (p.cols + kBlock - 1) / kBlock;
+  const int bm = blockIdx.x / kb, bk = blockIdx.x - bm * kb;
+  const int r0 = bm * kBlock + (tid >> 4) * 8, c = bk * kBlock + (tid & 15) * 8;
   float v[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -238,9 +241,9 @@ __global__ __launch_bounds__(256) void lp_quantize_tile_kernel(QuantArgs p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) any = fmaxf(any, top_of<8, true>(v[i], 1));
   if (__syncthreads_or(any == __builtin_inff()))
-    quantize_tile<ROWS, EXP, false>(p, v, part, turn);
+    quantize_tile<ROWS, EXP, false>(p, v, part, turn, bm, bk);
   else
-    quantize_tile<ROWS, EXP, true>(p, v, part, turn);
+    quantize_tile<ROWS, EXP, true>(p, v, part, turn, bm, bk);
 }
 
 }  // namespace gemmlp
