@@ -694,3 +694,17 @@ def test_tall_training_step():
     assert torch.equal(y[-5:].float(), x[-5:].float() @ w.detach().float().t())
     (dw,) = torch.autograd.grad(y, w, torch.ones_like(y))
     assert torch.equal(dw.float(), x.float().sum(0).expand(16, 8))
+
+
+@pytest.mark.parametrize("width, hidden", [(200, 300), (129, 40), (384, 256)])
+def test_expert_layer_serves_any_width(width, hidden):
+    """Widths that blocks of 128 do not divide; within the same 4 * 2^-4 of the training form."""
+    from tiled_double_buffered_amd import expert_layer as el
+    layer = el.ExpertLayer(width, hidden, 5, DEV)
+    x = _randn(_gen(113), 77, width).bfloat16().to(DEV)
+    serve = layer.served()
+    for n in (77, 1):
+        with torch.no_grad():
+            ref = layer(x[:n]).float()
+        y = serve(x[:n]).float()
+        assert (y - ref).norm() <= 4 * 2.0 ** -4 * ref.norm()

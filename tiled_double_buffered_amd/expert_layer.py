@@ -59,10 +59,10 @@ class ExpertLayer:
 
     def served(self):
         """The layer with all weights in 8 bits, one scale for each block of 128 x 128."""
-        def stack(w):  # E x K x N -> E x N x K, quantized: N is a multiple of 128
-            e, k, n = w.shape
-            q, s = tdb.quantize_fp8(w.detach().transpose(1, 2).reshape(e * n, k), (BLOCK, BLOCK))
-            return q.view(e, n, k), s.view(e, n // BLOCK, -1)
+        def stack(w):  # E x K x N -> E x N x K, quantized: no block spans two experts
+            each = [tdb.quantize_fp8(m.t().contiguous(), (BLOCK, BLOCK)) for m in w.detach()]
+            q = torch.stack([q.view(torch.uint8) for q, _ in each])
+            return q.view(each[0][0].dtype), torch.stack([s for _, s in each])
 
         w_in, w_out = stack(self.w_in), stack(self.w_out)
         shared = tdb.quantize_fp8(self.shared.detach(), (BLOCK, BLOCK))
