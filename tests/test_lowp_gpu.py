@@ -708,3 +708,50 @@ def test_expert_layer_serves_any_width(width, hidden):
             ref = layer(x[:n]).float()
         y = serve(x[:n]).float()
         assert (y - ref).norm() <= 4 * 2.0 ** -4 * ref.norm()
+
+
+def _stream_calls():
+    """Every call that takes a stream, as (name, call of tensors, fresh tensors)."""
+    x = _randn(_gen(114), 64, 256).bfloat16().to(DEV)
+    w = _randn(_gen(115), 2, 256, 128).bfloat16().to(DEV)
+    off = torch.tensor([0, 20, 64], dtype=torch.int32, device=DEV)
+    a, sa = tdb.quantize_fp8(x)
+    b, sb = tdb.quantize_fp8(w[0].t().contiguous(), block=(128, 128))
+    bb, sbb = torch.stack([b.view(torch.uint8)] * 2).view(b.dtype), torch.stack([sb] * 2)
+    return [("quantize", tdb.quantize_fp8, (x,)), ("pair", tdb.quantize_fp8_pair, (x,)),
+            ("fp8", tdb.matmul_fp8, (a, sa, b, sb)),
+            ("fp8_grouped", tdb.matmul_fp8_grouped, (a, sa, bb, sbb, off)),
+            ("grouped", tdb.matmul_grouped, (x, w, off)),
+            ("wgrad", tdb.matmul_grouped_wgrad, (x, x.clone(), off))]
+
+
+def test_operands_dropped_after_a_call_on_another_stream():
+    """While the stream is busy with other work, the memory of operands that the caller dropped
+    is not handed out again; and the results are the operands'."""
+    side = torch.cuda.Stream(DEV)
+    for name, call, tensors in _stream_calls():
+        ref = call(*tensors)
+        own = [t.clone() for t in tensors]
+        torch.cuda.synchronize()
+        held = {t.data_ptr() for t in own}
+        _say("[dropped]", name)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        got = call(*own, stream=side)
+        sizes = [t.numel() * t.element_size() for t in own]
+        del own
+        again = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes]
+        assert not side.query(), "the other work was over too soon to tell"
+        assert not held & {t.data_ptr() for t in again}, name
+        side.synchronize()
+        for g, r in zip(*((v if isinstance(v, tuple) else (v,)) for v in (got, ref))):
+            assert torch.equal(g.float(), r.float()), name
+
+
+def test_stream_of_another_device_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda:1")
+
+    for name, call, tensors in _stream_calls():
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call(*tensors, stream=Elsewhere())

@@ -6,8 +6,9 @@ As in `matmul`, this module only checks arguments, allocates outputs and passes 
 strides and the stream; every value is computed in the library's HIP kernels, and there is no
 other path: without the library, or on tensors that are not on the GPU, every call raises.
 
-Calls are asynchronous.  `stream` (a torch.cuda.Stream) is where they run, the current stream
-by default; what a call allocates belongs to that stream.
+Calls are asynchronous.  `stream` (a torch.cuda.Stream of the operands' GPU) is where they run,
+the current stream by default; what a call allocates belongs to that stream.  It does not wait for
+work on other streams: what made the operands has to be done or waited for.
 """
 from __future__ import annotations
 
@@ -159,11 +160,21 @@ def _here(t, stream):
     return index < 0 or index == _device()
 
 
-def _on(t, stream):
-    """The context another call runs in: the tensor's device, and `stream` where one is given."""
+def _on(stream, *tensors):
+    """The context another call runs in: the first tensor's device, and `stream` where one is
+    given.  The tensors' memory then waits for what runs on `stream` before it is used again, so
+    that the caller may drop them at once."""
+    t = tensors[0]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return _nothing  # the argument checks refuse it
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(t.device)
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {t.device}")
+    for u in tensors:
+        if isinstance(u, torch.Tensor) and u.is_cuda:
+            u.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
 # the current stream's handle without a torch.cuda.Stream around it (2 us less a call)
@@ -233,7 +244,7 @@ def quantize_fp8(x, block=(1, BLOCK), stream=None):
     rows = _block_rows(block)
     if _here(x, stream):
         return _quantize(x, rows, True, False)[:2]
-    with _on(x, stream):
+    with _on(stream, x):
         return _quantize(x, rows, True, False)[:2]
 
 
@@ -244,7 +255,7 @@ def quantize_fp8_pair(x, block=(1, BLOCK), stream=None):
     rows = _block_rows(block)
     if _here(x, stream):
         return _quantize(x, rows, True, True)
-    with _on(x, stream):
+    with _on(stream, x):
         return _quantize(x, rows, True, True)
 
 
@@ -302,7 +313,7 @@ def matmul_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, stream=None):
     scales has to lie in float32's normal range."""
     if _here(a, stream):
         return _fp8(a, sa, b, sb, out_dtype)
-    with _on(a, stream):
+    with _on(stream, a, sa, b, sb):
         return _fp8(a, sa, b, sb, out_dtype)
 
 
@@ -314,7 +325,7 @@ def matmul_fp8_grouped(a, sa, b, sb, offsets, out_dtype=torch.bfloat16, stream=N
         raise TypeError("offsets must be a contiguous 1-D int32 tensor of E + 1 elements")
     if _here(a, stream):
         return _fp8(a, sa, b, sb, out_dtype, offsets)
-    with _on(a, stream):
+    with _on(stream, a, sa, b, sb, offsets):
         return _fp8(a, sa, b, sb, out_dtype, offsets)
 
 
@@ -343,7 +354,7 @@ def matmul_grouped(x, w, offsets, transpose_w=False, stream=None):
     float32.  offsets as in `matmul_fp8_grouped`.  Sums are held in float32."""
     if _here(x, stream):
         return _grouped(x, w, offsets, transpose_w)
-    with _on(x, stream):
+    with _on(stream, x, w, offsets):
         return _grouped(x, w, offsets, transpose_w)
 
 
@@ -369,7 +380,7 @@ def matmul_grouped_wgrad(a, b, offsets, stream=None):
     An expert without rows gets zeros."""
     if _here(a, stream):
         return _grouped_wgrad(a, b, offsets)
-    with _on(a, stream):
+    with _on(stream, a, b, offsets):
         return _grouped_wgrad(a, b, offsets)
 
 
@@ -465,7 +476,7 @@ def linear_fp8(x, w):
     if _here(x, None):
         y = _LinearFp8.apply(flat, w, grads)
     else:
-        with _on(x, None):
+        with _on(None, x):
             y = _LinearFp8.apply(flat, w, grads)
     return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
 
@@ -500,5 +511,5 @@ def linear_grouped(x, w, offsets, transpose_w=False):
     x, transpose_w = _row_major(x), bool(transpose_w)
     if _here(x, None):
         return _LinearGrouped.apply(x, w, offsets, transpose_w)
-    with _on(x, None):
+    with _on(None, x):
         return _LinearGrouped.apply(x, w, offsets, transpose_w)
