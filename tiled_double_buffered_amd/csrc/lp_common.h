@@ -44,16 +44,7 @@ struct F8 {
 
 static inline __host__ __device__ int type_bytes(int code) { return code == GEMM_LP_F32 ? 4 : 2; }
 
-// The product of two 16-row operands over one K step of 128 bytes a row (128 8-bit values,
-// 64 16-bit, 32 32-bit).  Lane l holds of row l % 16 the two 16-byte groups lo and hi that
-// its lane group l / 16 stands for; both operands use the same groups, so that the order of
-// k inside the step does not matter.  D's row index comes from `a`, its column from `b`:
-// lane l, register r hold row 4 (l / 16) + r, column l % 16.
-// 8-bit values go through the 16-bit instruction, which every e4m3 number fits exactly and
-// whose sums hold FP32's 24 bits below their largest product.  The 8-bit instructions (16x16x128
-// and 16x16x32 alike) hold 13 bits below the largest of each eight neighbouring products:
-// 256 * 256 - 256 * 256 + 2 * 2 comes out as 0, and sums over all of e4m3's exponents are off by
-// up to 2^-12.5 of their magnitudes (2^-15.4 in the mean square; FP32 2^-21.3 and 2^-24).
+// Eight 8-bit values as halves.
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ half8v fp8x8_to_half(int w0, int w1) {
   const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
@@ -63,40 +54,26 @@ __device__ __forceinline__ half8v fp8x8_to_half(int w0, int w1) {
   return half8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-template <class T>
-__device__ __forceinline__ float4v mma_step(int4v alo, int4v ahi, int4v blo, int4v bhi,
-                                            float4v c) {
-  if constexpr (T::BYTES == 1) {
+// The product of two 16-row operands of 8-bit values over one K step of 128.  Lane l holds of row
+// l % 16 the two 16-byte groups lo and hi that its lane group l / 16 stands for; both operands
+// use the same groups, so that the order of k inside the step does not matter.  D's row index
+// comes from `a`, its column from `b`: lane l, register r hold row 4 (l / 16) + r, column l % 16.
+// The values go through the 16-bit instruction, which every e4m3 number fits exactly and whose
+// sums hold FP32's 24 bits below their largest product.  The 8-bit instructions (16x16x128 and
+// 16x16x32 alike) hold 13 bits below the largest of each eight neighbouring products:
+// 256 * 256 - 256 * 256 + 2 * 2 comes out as 0, and sums over all of e4m3's exponents are off by
+// up to 2^-12.5 of their magnitudes (2^-15.4 in the mean square; FP32 2^-21.3 and 2^-24).
+__device__ __forceinline__ float4v mma_fp8_step(int4v alo, int4v ahi, int4v blo, int4v bhi,
+                                                float4v c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int4v a = i ? ahi : alo, b = i ? bhi : blo;
-      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[0], a[1]),
-                                                 fp8x8_to_half(b[0], b[1]), c, 0, 0, 0);
-      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[2], a[3]),
-                                                 fp8x8_to_half(b[2], b[3]), c, 0, 0, 0);
-    }
-    return c;
-  } else if constexpr (T::CODE == GEMM_LP_BF16) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf168v, alo),
-                                                __builtin_bit_cast(bf168v, blo), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf168v, ahi),
-                                                   __builtin_bit_cast(bf168v, bhi), c, 0, 0, 0);
-  } else if constexpr (T::CODE == GEMM_LP_F16) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, alo),
-                                               __builtin_bit_cast(half8v, blo), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, ahi),
-                                                  __builtin_bit_cast(half8v, bhi), c, 0, 0, 0);
-  } else {
-    const float4v a0 = __builtin_bit_cast(float4v, alo), a1 = __builtin_bit_cast(float4v, ahi);
-    const float4v b0 = __builtin_bit_cast(float4v, blo), b1 = __builtin_bit_cast(float4v, bhi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a0[i], b0[i], c, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[i], b1[i], c, 0, 0, 0);
-    return c;
+  for (int i = 0; i < 2; ++i) {
+    const int4v a = i ? ahi : alo, b = i ? bhi : blo;
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[0], a[1]),
+                                               fp8x8_to_half(b[0], b[1]), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp8x8_to_half(a[2], a[3]),
+                                               fp8x8_to_half(b[2], b[3]), c, 0, 0, 0);
   }
+  return c;
 }
 
 // Arguments of every product kernel.  Row products: C rows m0.. of group e from A's rows and

@@ -444,7 +444,6 @@ struct ScaleCopy {
   __device__ __forceinline__ int4v words(int kt) const {
     return buffer_words(base + kt * step, left - kt * step);
   }
-  __device__ __forceinline__ void start(Walk& walk) const { walk.init(base, left, step); }
   __device__ __forceinline__ void copy(int4v r, uint32_t table) const {
     copy4(__builtin_amdgcn_readfirstlane(table + to), r, off);
   }
@@ -673,8 +672,8 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
               const int i = s / SN, j = s % SN;
               if (j == 0 && i + 1 < SM) oa.read(sa, i + 1, a + ((i + 1) & 1));
               const float4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-              d[s % kRing] = mma_step<T>(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
-                                         half_of(a[i & 1], 1), z);
+              d[s % kRing] = mma_fp8_step(half_of(b[j], 0), half_of(b[j], 1), half_of(a[i & 1], 0),
+                                          half_of(a[i & 1], 1), z);
               send(s, SM * SN * 3 / 4);  // the last with a quarter of the step to land
             }
             if (s >= kLag) {
