@@ -755,3 +755,73 @@ def test_stream_of_another_device_is_refused():
     for name, call, tensors in _stream_calls():
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call(*tensors, stream=Elsewhere())
+
+
+# ------------------------------------------------------------- whole 256x256 tiles, step by step
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tiles", [(16, 16), (11, 35)], ids=["256", "385"])
+@pytest.mark.parametrize("steps, short", [(1, 0), (1, 3), (2, 0), (2, 5), (3, 1), (4, 0), (9, 7)])
+def test_whole_tiles_of_any_depth(steps, short, tiles, dtype, monkeypatch):
+    """As many 256x256 tiles as are never computed in halves (256, or more than 128 past that), of
+    one group and of ragged ones, from a single K step to the loop's steady state.  Whole numbers:
+    exact, with one rounding at the end."""
+    monkeypatch.setenv("GEMM_LP_TILE", "256")
+    tm, tn = tiles
+    K = steps * (32 if dtype == "f32" else 64) - short
+    sizes = [(tm - 9) * 256, 4 * 256 - 50, 0, 5 * 256]  # (the second ends with more than half a tile)
+    rows, N = sum(sizes), tn * 256 - 6
+    g = _gen(116)
+    x = torch.randint(-3, 4, (rows, K), generator=g).float().to(DEV)
+    w = torch.randint(-3, 4, (4, K, N), generator=g).float().to(DEV)
+    off = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    each = torch.cat([a @ b for a, b in zip(x.split(sizes), w)]).to(TYPES[dtype])
+    one = (x @ w[0]).to(TYPES[dtype])
+    _say("[whole tiles]", steps, short, tiles, dtype)
+    for tw in (False, True):
+        b = (w.transpose(1, 2).contiguous() if tw else w).to(TYPES[dtype])
+        xd = x.to(TYPES[dtype])
+        if K % 4:  # rows that start at multiples of four bytes, NaN between them
+            xd = torch.nn.functional.pad(xd, (0, 4 - K % 4), value=NAN)[:, :K]
+            if tw:
+                b = torch.nn.functional.pad(b, (0, 4 - K % 4), value=NAN)[..., :K]
+        assert torch.equal(tdb.matmul_grouped(xd, b, off, transpose_w=tw), each), tw
+        ends = off[[0, -1]].contiguous()
+        assert torch.equal(tdb.matmul_grouped(xd, b[:1], ends, transpose_w=tw), one), tw
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_whole_weight_gradient_tiles_of_any_depth(dtype, monkeypatch):
+    """Experts of no row, one row, and one to nine K steps, whole and not."""
+    monkeypatch.setenv("GEMM_LP_TILE", "256")
+    ks = 32 if dtype == "f32" else 64
+    sizes = [0, 1, ks, ks + 1, 2 * ks, 3 * ks - 5, 4 * ks, 9 * ks - 1]
+    g = _gen(117)
+    x = torch.randint(-3, 4, (sum(sizes), 512), generator=g).float().to(DEV)
+    dy = torch.randint(-3, 4, (sum(sizes), 768), generator=g).float().to(DEV)
+    off = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    dw = tdb.matmul_grouped_wgrad(x.to(TYPES[dtype]), dy.to(TYPES[dtype]), off)
+    for e, (a, b) in enumerate(zip(x.split(sizes), dy.split(sizes))):
+        assert torch.equal(dw[e], (a.t() @ b).to(TYPES[dtype])), e
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{len(g[0])}e-{sum(g[0])}")
+@pytest.mark.parametrize("NK", [(64, 128), (130, 400), (257, 261), (132, 1300)], ids=str)
+def test_matmul_fp8_grouped_with_a_scale_for_each_row(groups, NK, out, tile):
+    N, K = NK
+    off, rows = _split(*groups)
+    E = len(groups[0])
+    a, sa = _scaled(rows, K, 1, 118)
+    b, sb = _scaled(N, K, 1, 119, (E,))
+    sa *= 2.0 ** -12
+    ref = torch.zeros(rows, N, dtype=torch.float64)
+    mag = torch.zeros_like(ref)
+    av = lo.values(a, sa, 1)
+    for e, (i, j) in enumerate(lo.ranges(off)):
+        ref[i:j], mag[i:j] = lo.product(av[i:j], lo.values(b[e], sb[e], 1).t())
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    ad, sad, bd, sbd = (t.to(DEV) for t in (a, sa, b, sb))
+    for how, (p, r) in dict(plain=(ad, bd), aligned=(_aligned(ad), _aligned(bd))).items():
+        _say("[fp8_grouped rows]", E, rows, NK, out, how)
+        lo.check(tdb.matmul_fp8_grouped(p, sad, r, sbd, offd, out_dtype=TYPES[out]), ref, mag, K,
+                 how)
