@@ -67,8 +67,9 @@ int gemm_fp8_quantize_exp(int64_t rows, int64_t cols, const void *X, int64_t ldx
  * A: M x K e4m3fn, row stride lda; SA: M x ceil(K/128), row stride ldsa.
  * B: N x K e4m3fn, row stride ldb; SB: ceil(N/b_block) x ceil(K/128), row stride ldsb;
  * b_block is 1 or 128.  C: M x N of c_type, row stride ldc.  Any alignment of A and B.
- * The product sa * sb of two scales has to lie in FP32's normal range; ldsa and ldsb are below
- * 2^22.
+ * sa and sb are any FP32 numbers, and their product is formed in FP32: where it overflows, so
+ * does the block's part of C; where it falls below 2^-149 that part is lost.  ldsa and ldsb are
+ * below 2^22.
  * offsets == NULL: one product (E must be 1).  Otherwise E experts: expert e's B and SB
  * start e * stride_b bytes and e * stride_sb floats after the first's, and rows of no
  * expert are zeroed in C. */
@@ -79,8 +80,7 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, int64_t E, const int32_t *offsets,
              void *C, int64_t ldc, int c_type, void *stream);
 
 /* gemm_fp8 of one product whose scales are gemm_fp8_quantize_exp's bytes: SA is ceil(K/128) x M,
- * SB ceil(K/128) x N, both 4-byte aligned with row strides that are multiples of 4.  The matrix
- * cores apply such scales themselves. */
+ * SB ceil(K/128) x N, both 4-byte aligned with row strides that are multiples of 4. */
 int gemm_fp8_exp(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const uint8_t *SA,
                  int64_t ldsa, const void *B, int64_t ldb, const uint8_t *SB, int64_t ldsb,
                  void *C, int64_t ldc, int c_type, void *stream);

@@ -825,3 +825,44 @@ def test_matmul_fp8_grouped_with_a_scale_for_each_row(groups, NK, out, tile):
         _say("[fp8_grouped rows]", E, rows, NK, out, how)
         lo.check(tdb.matmul_fp8_grouped(p, sad, r, sbd, offd, out_dtype=TYPES[out]), ref, mag, K,
                  how)
+
+
+# ------------------------------------------------------------------------------ ends of ranges
+@pytest.mark.parametrize("b_block", [1, 128])
+def test_scales_at_the_ends_of_their_range(b_block, tile):
+    """Scales whose product is 0, subnormal, or near the largest number: whole numbers, so that
+    each result is exact wherever float32 holds it (down to 2^-149)."""
+    K, N = 256, 3 * b_block
+    g = _gen(120)
+    a = torch.randint(-3, 4, (5, K), generator=g).float()
+    b = torch.randint(-3, 4, (N, K), generator=g).float()
+    sa = torch.tensor([2.0 ** -126, 2.0 ** -100, 0.0, 1.0, 2.0 ** 100])[:, None].expand(5, 2)
+    sb = torch.tensor([2.0 ** -23, 1.0, 2.0 ** 15])[:, None].expand(3, 2)
+    ref = lo.values(a.to(lo.F8), sa, 1) @ lo.values(b.to(lo.F8), sb, b_block).t()
+    assert (ref == 0).sum() < ref.numel() / 2 and ref.abs().max() < 2.0 ** 127
+    c = tdb.matmul_fp8(*(t.contiguous().to(DEV) for t in (a.to(lo.F8), sa, b.to(lo.F8), sb)),
+                       out_dtype=torch.float32)
+    assert torch.equal(c.cpu().double(), ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_experts_and_no_rows(dtype, tile):
+    """Without experts every row is no expert's; without rows every expert's gradient is zeros."""
+    dt = TYPES[dtype]
+    x = torch.full((70, 96), NAN, dtype=dt, device=DEV)
+    for at in (0, 30, 70):
+        none = torch.tensor([at], dtype=torch.int32, device=DEV)
+        y = tdb.matmul_grouped(x, torch.empty(0, 96, 40, dtype=dt, device=DEV), none)
+        assert y.shape == (70, 40) and not y.any()
+        assert tdb.matmul_grouped_wgrad(x, x, none).shape == (0, 96, 96)
+    q, s = x.to(lo.F8), torch.full((70, 1), NAN, device=DEV)
+    b, sb = torch.empty(0, 40, 96, device=DEV).to(lo.F8), torch.empty(0, 1, 1, device=DEV)
+    c = tdb.matmul_fp8_grouped(q, s, b, sb, none, out_dtype=dt)
+    assert c.shape == (70, 40) and not c.any()
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    w = torch.full((3, 96, 40), NAN, dtype=dt, device=DEV).requires_grad_()
+    e = x[:0].clone().requires_grad_()
+    y = tdb.linear_grouped(e, w, off)
+    assert y.shape == (0, 40)
+    dx, dw = torch.autograd.grad(y, (e, w), torch.ones_like(y))
+    assert dx.shape == (0, 96) and dw.shape == w.shape and not dw.any()

@@ -309,8 +309,9 @@ def matmul_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, stream=None):
     """(a * sa) @ (b * sb)^T: a is M x K and b N x K, both float8_e4m3fn; sa is M x
     ceil(K/128), one float32 scale for each row and block of 128 columns; sb is ceil(N/128) x
     ceil(K/128), one for each block of 128 x 128, or N x ceil(K/128), one for each row and
-    block.  Sums are held in float32 and rounded once to out_dtype.  The product of two
-    scales has to lie in float32's normal range."""
+    block.  Sums are held in float32 and rounded once to out_dtype.  Scales are any float32
+    numbers, and the product of two is formed in float32: where it overflows, so does the block's
+    part of the result; where it falls below 2^-149 that part is lost."""
     if _here(a, stream):
         return _fp8(a, sa, b, sb, out_dtype)
     with _on(stream, a, sa, b, sb):
@@ -459,7 +460,9 @@ def linear_fp8(x, w):
 
     Differentiable in both: the gradient of y is quantized by blocks of 1 x 128 along N for
     dx = dy w, with w's 8-bit values, and along the rows for dw = dy^T x, with x quantized
-    along its rows; quantization itself counts as the identity."""
+    along its rows; quantization itself counts as the identity.  Sums are held in float32 and
+    rounded once.  As in `matmul_fp8`, blocks whose scales' product leaves float32's range are
+    lost or overflow: magnitudes whose product is below about 2^-131 or above 2^143."""
     if not isinstance(x, torch.Tensor) or x.dtype not in TYPES:
         raise TypeError(f"x must be a tensor of {_names(TYPES)}")
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
