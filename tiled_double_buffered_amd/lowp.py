@@ -394,11 +394,8 @@ def _row_major(t):
 
 def _exp_half(rows, cols, device):
     """Empty 8-bit rows x cols and their exponents, one plane of rows for each block of 128
-    columns, with their row strides.  Rows that are a multiple of 8 KiB apart meet in one
-    channel of the cache (8192^3: 1.12 times the time), so such ones are moved apart."""
+    columns, with their row strides."""
     ld, lds = (cols + 15) // 16 * 16, (rows + 15) // 16 * 16
-    if ld % 8192 == 0:
-        ld += 256
     q = torch.empty((rows, ld), dtype=_F8, device=device)
     return q, ld, torch.empty((_blocks(cols), lds), dtype=torch.uint8, device=device), lds
 
