@@ -140,8 +140,10 @@ constexpr StepCost kStep8[kTileCount] = {
 
 // The tile of the pipelined kernels with the least time; `rounds(tile)` is the number of rounds
 // of tiles on all CUs to expect, and the longest tile has `skew` times the average's K steps.
-// rows: a row product.  Over 94 random sizes of every product and type the choice took 0 to 3 %
-// longer on average than the best of all tiles.
+// rows: a row product.  Over 48 random sizes of every product and type the choice took 0 to 2 %
+// longer on average than the best of all tiles, and at worst 1.35 times as long (a weight gradient
+// of 8 rows in all; of those above 20 us 1.2 times).  Weight gradients of few experts are its weak
+// spot: their longest expert decides, whose rows the host does not know, only `skew`.
 constexpr int kForced[kTileCount] = {256, 128, 64, 644};
 template <class F>
 static int pick_tile(int unit, bool staged, bool rows, double steps, double skew, F rounds) {

@@ -118,7 +118,8 @@ __device__ __forceinline__ int xcd_order(int w, int n) {
 }
 
 // Tiles of one group are walked in bands of kBand tile rows, column by column, so that the
-// workgroups of one XCD that run together share rows of A and of B in its L2.
+// workgroups of one XCD that run together share rows of A and of B in its L2 (8192^3 in
+// bf16: 763 us in bands of 4, 763 of 6, 760 of 8, 784 of 16; in 8 bits 933, 930, 918, 950).
 constexpr int kBand = 4;
 __device__ __forceinline__ void band_order(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = id / (kBand * tiles_n);
@@ -145,7 +146,7 @@ __device__ __forceinline__ void wgrad_tile(int wg, int per, int tiles_m, int til
 // HALF > 0: half a tile (HALF rows or fewer) costs less than a whole one (256 rows 0.72, 64 rows
 // of FP32 0.55), and they come last, to fill the last round: a group's last tile where it has no
 // more rows; and both halves of each tile of the last round, where these and the others fit into
-// one round.
+// one round (bf16, 2304 x 8192 x 4096, 288 tiles: 157 us, 169 with whole tiles).
 template <int BM, int HALF>
 __device__ inline bool find_tile(const LpArgs& p, int wg, int nwg, TileAt& t) {
   int tm;

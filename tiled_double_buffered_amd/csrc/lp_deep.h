@@ -1,10 +1,12 @@
-// The pipelined product kernel for large products of 16- and 32-bit values: 256 x 256 tiles, eight waves of 128 x 64,
-// two LDS slots refilled in halves, so that a copy has one and a half K steps to land.
+// The pipelined product kernel for large products of 16- and 32-bit values: 256 x 256 tiles, eight
+// waves of 128 x 64, two LDS slots refilled in halves, so that a copy has one and a half K steps
+// to land.
 //
 // The kernel of lp_pipe.h starts a step's copies when the slot's last reader is done and needs
-// them one step later, and waits for them.  Here each slot has three parts that are freed at different times: B, which a wave holds in registers for the
-// whole step, the upper half A1 of A's rows, which the step's first products read, and the
-// lower half A2.  A step has two barriers:
+// them one step later, and waits for them.  Here each slot has three parts that are freed at
+// different times: B, which a wave holds in registers for the whole step, the upper half A1 of
+// A's rows, which the step's first products read, and the lower half A2.  A step has two
+// barriers:
 //   middle (before the products of the last A1 fragment): B, A1 of this step are read by all
 //     waves, A2 of this step has landed; the copies of B, A1 two steps on start;
 //   end (before the products of the last two A2 fragments): A2 of this step is read, B and A1
@@ -14,15 +16,15 @@
 // Copies complete in order, so a wave waits until no more are open than were started after the
 // part it needs.
 //
-// Measured on MI355X at 8192^3, warm: bf16 X W^T 788 us, X W 766, weight gradient 745 (1.4 to
-// 1.5 PFLOP/s, the matrix cores busy 72 to 75 % of the time at the 1.8 GHz that the power limit
+// Measured on MI355X at 8192^3, warm: bf16 X W^T 763 us, X W 766, weight gradient 745 (1.4 to
+// 1.5 PFLOP/s, the matrix cores busy 74 to 75 % of the time at the 1.8 GHz that the power limit
 // leaves); FP32 137 to 148 TFLOP/s.  A step's copies, reads and barriers take about as long as its
 // products: the spread copies, B replaced piece by piece and scalar walks are what overlaps them.
 // Three half slots for half tiles, wave priorities, and workgroups that stay and fetch their next
-// tile's first steps before they store made no difference.  Four waves
-// of 128 x 128 read a third less from LDS, which is faster while the power limit holds (bf16
-// 8192^3: 751 us) but slower for ragged groups (16384 rows of 32 experts, X W 318 us against
-// 311, X W^T 336 against 323), whose half tiles then lack waves to hide their waits.
+// tile's first steps before they store made no difference.  Four waves of 128 x 128 read a third
+// less from LDS, which is faster while the power limit holds (bf16 8192^3: 751 us, where eight
+// took 788) but slower for ragged groups (16384 rows of 32 experts, X W 318 us against 311,
+// X W^T 336 against 323), whose half tiles then lack waves to hide their waits.
 #pragma once
 
 #include <type_traits>

@@ -22,9 +22,10 @@
 // 128 x 128 tiles need as many cycles for them as for their products in 16 bits, 1090 TFLOP/s in
 // bf16 at 8192^3), with few rows the reading of B (16 rows of 14 of 64 experts, 4096 x 2048 in
 // bf16: 58 us, 4.05 TB/s; torch.sum reads as much memory at 3.5), with little work the latency of
-// a step, which four wave groups on one tile share.  8-bit values: 1120 TFLOP/s at 8192 x 4096 x
-// 4096, bound by the conversions beside the products.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles, 132 on
-// 64 x 64.
+// a step, which four wave groups on one tile share (1 x 11008 x 4096 in 8 bits: 15 us, 21 with one
+// group).  8-bit values: 1.16 PFLOP/s at 8192 x 4096 x 4096 (237 us; with a scale for each column
+// 263, with exponents 258), bound by the conversions beside the products, the matrix cores busy
+// 56 %.  FP32: 139 TFLOP/s of 157 on 128 x 128 tiles, 132 on 64 x 64.
 #pragma once
 
 #include <type_traits>
@@ -531,7 +532,8 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
   TileOf w;
   // A tile of FP32 rows takes the matrix cores long enough for half of it to be worth leaving
   // out: each wave then has the first half of its fragments, from half as far down (2048 rows of
-  // 8 experts, 2048 -> 1024: 89 us, 105 in whole tiles; 1024 -> 2048: 85, 92).
+  // 8 experts, warm: X W 2048 -> 1024 97 us, 108 in whole tiles; 1024 -> 2048 85, 92; X W^T 91,
+  // 104; 84, 91).
   constexpr int HALF = T::BYTES == 4 && !WGRAD && BM == 64 && SM == 2 ? BM / 2 : 0;
   if (!locate<T, WGRAD, BM, BN, HALF>(p, w)) return;
   const bool half = HALF > 0 && w.half;
@@ -581,11 +583,11 @@ __global__ __launch_bounds__(WM * WN * 64 * KG, BM == 64 ? 4 : 2) void lp_pipe_k
       issue(group, 0);
       settle(0);
     }
-    // 8-bit values: the next step's copies go out between this
-    // one's products, since a wave waits for each to be taken (8192^3: 1014 us, 1153 with the
-    // copies first); past the last step they have nothing to copy, zeros into a slot that is
-    // not read again.  The others, whose steps are shorter, lose by it (bf16 X W^T 1167 us, 1024
-    // with the copies first).
+    // 8-bit values: the next step's copies go out between this one's products, since a wave waits
+    // for each to be taken (8192 x 4096 x 4096: 237 us, 260 with the copies first; 263 and 265
+    // with a scale for each column, 258 and 264 with exponents); past the last step they have
+    // nothing to copy, zeros into a slot that is not read again.  The others, whose steps are
+    // shorter, lose by it (bf16 X W^T 1167 us, 1024 with the copies first).
     constexpr bool SPREAD = F8T && !STAGED && KG == 1 && BM >= 128;
     constexpr int SENT = OA::COPIES + OB::COPIES + 1;
     static_assert(!SPREAD || OS::EXP || OS::WAVES == WAVES, "every wave copies scales");

@@ -8,8 +8,9 @@
 // conversion instruction's, to nearest with ties to even.
 //
 // Bound by memory: every value is read once, whatever is asked for, and 8 bits of it written once
-// or twice.  8192 x 8192 in bf16 with its transpose takes 64 us for 273 MB, 4.3 of the 5.1 TB/s
-// that a large copy reaches; 16 x 4096 takes 2.8 us, a launch and one reading's latency.  A
+// or twice.  8192 x 8192 in bf16 with its transpose takes 64 to 66 us for 273 MB, 4.1 to 4.3 of
+// the 5.1 TB/s that a large copy reaches; 4096 x 4096 in 128 x 128 blocks with its transpose
+// 16.5 to 19; 16 x 4096 takes 2.5 us, a launch and one reading's latency.  A
 // thread holds 8 x 8 values, so that the scales by rows and by columns and both orders of the
 // result come from one reading (92 us with a check of every value for Inf, which the maxima now
 // make unnecessary but for one test a workgroup).
