@@ -866,3 +866,51 @@ def test_no_experts_and_no_rows(dtype, tile):
     assert y.shape == (0, 40)
     dx, dw = torch.autograd.grad(y, (e, w), torch.ones_like(y))
     assert dx.shape == (0, 96) and dw.shape == w.shape and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tw", [False, True])
+def test_expert_sums_hold_32_bits(dtype, tw, tile):
+    """What large products leave when they cancel, along each contraction of a grouped step (an
+    expert without rows in between); exact in every type."""
+    dt, off = TYPES[dtype], [0, 300, 300, 340]
+    a, b, ref = _cancelling(340, 130, 1100, 121)   # rows, one side, the contraction
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    for side, call in (("y", tw), ("dx", not tw)):  # dx is the product with the other transposition
+        w = (b if call else b.t().contiguous()).expand(3, *(b.shape if call else b.t().shape))
+        w = w.to(dt).to(DEV).contiguous()
+        if side == "y":
+            got = tdb.matmul_grouped(a.to(dt).to(DEV), w, offd, transpose_w=call)
+        else:
+            x = torch.zeros(340, 130, dtype=dt, device=DEV).requires_grad_()
+            y = tdb.linear_grouped(x, w, offd, transpose_w=not call)
+            (got,) = torch.autograd.grad(y, x, a.to(dt).to(DEV))
+        _say("[expert sums]", dtype, tw, side)
+        assert torch.equal(got.cpu().double(), ref), side
+    p, q, ref = _cancelling(260, 90, 1500, 122)    # dw: the rows are the contraction
+    rows = torch.cat([p.t(), p.t()[:7]]).contiguous(), torch.cat([q.t(), q.t()[:7]]).contiguous()
+    offd = torch.tensor([0, 0, 1500, 1507], dtype=torch.int32, device=DEV)
+    dw = tdb.matmul_grouped_wgrad(*(t.to(dt).to(DEV) for t in rows), offd).cpu().double()
+    assert not dw[0].any() and torch.equal(dw[1], ref)
+    if not tw:
+        return
+    lin = rows[1].to(dt).to(DEV), torch.zeros(3, 260, 90, dtype=dt, device=DEV).requires_grad_()
+    y = tdb.linear_grouped(*lin, offd, transpose_w=True)
+    (dw,) = torch.autograd.grad(y, lin[1], rows[0].to(dt).to(DEV))
+    assert torch.equal(dw[1].cpu().double(), ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_expert_sums_are_off_by_little_in_the_mean(dtype, tile):
+    """As for 8-bit values: 8 * 2^-23 of the sum of magnitudes in the mean square, and the result's
+    rounding, half a step at most of each."""
+    K, N, off = 4096, 96, [0, 50, 64]
+    g = _gen(123)
+    x, w = _randn(g, 64, K).to(TYPES[dtype]), _randn(g, 2, K, N).to(TYPES[dtype])
+    got = tdb.matmul_grouped(x.to(DEV), w.to(DEV), torch.tensor(off, dtype=torch.int32, device=DEV))
+    ref, mag = zip(*(lo.product(x[i:j].double(), w[e].double())
+                     for e, (i, j) in enumerate(lo.ranges(off))))
+    ref, mag = torch.cat(ref), torch.cat(mag)
+    half = torch.finfo(got.dtype).eps / 2
+    err = ((got.cpu().double() - ref).abs() - half * ref.abs()).clamp_min(0)
+    assert err.square().mean().sqrt() <= 8 * 2.0 ** -23 * mag.square().mean().sqrt()
