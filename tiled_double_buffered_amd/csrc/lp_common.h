@@ -61,8 +61,8 @@ __device__ __forceinline__ half8v fp8x8_to_half(int w0, int w1) {
 // The values go through the 16-bit instruction, which every e4m3 number fits exactly and whose
 // sums hold FP32's 24 bits below their largest product.  The 8-bit instructions (16x16x128 and
 // 16x16x32 alike) hold 13 bits below the largest of each eight neighbouring products:
-// 256 * 256 - 256 * 256 + 2 * 2 comes out as 0, and sums over all of e4m3's exponents are off by
-// up to 2^-12.5 of their magnitudes (2^-15.4 in the mean square; FP32 2^-21.3 and 2^-24).
+// 256 * 256 - 256 * 256 + 2 * 2 comes out as 0, and sums of values of all sizes are off by up to
+// 2^-12.5 of their magnitudes (2^-15.4 in the mean square; the 16-bit one 2^-21.3 and 2^-24).
 __device__ __forceinline__ float4v mma_fp8_step(int4v alo, int4v ahi, int4v blo, int4v bhi,
                                                 float4v c) {
 #pragma unroll
