@@ -29,13 +29,18 @@ NUM_CONFIGS = 20  # configs.h: kNumConfigs
 LP_SOURCE = os.path.join(CSRC, "gemm_lp.hip")  # low-precision and expert-grouped products
 LP_UNIT_SOURCE = os.path.join(CSRC, "lp_kernels.hip")
 NUM_LP_UNITS = 12  # lp_units.h: kUnits
-SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE]
+EX_SOURCES = [os.path.join(CSRC, f)  # the operators around the experts' products
+              for f in ("gemm_experts.hip", "ex_adapters.hip")]
+SOURCES = [MAIN_SOURCE, CFG_SOURCE, LP_SOURCE, LP_UNIT_SOURCE, *EX_SOURCES]
 HEADERS = [os.path.join(CSRC, f) for f in ("configs.h", "gemm_common.h", "kernels_sb_db.h",
                                             "kernels_ms.h", "kernels_ks.h", "kernels_ks16.h", "splitk_reduce.h",
                                             "dispatch_table.h", "mfma_peak.h",
-                                            "lp_common.h", "lp_quantize.h",
-                                            "lp_pipe.h", "lp_deep.h", "lp_units.h")]
-DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h")]
+                                            "lp_common.h", "lp_host.h", "lp_quantize.h",
+                                            "lp_pipe.h", "lp_deep.h", "lp_units.h",
+                                            "ex_common.h", "ex_route.h", "ex_group.h",
+                                            "ex_gated.h", "ex_adapters.h")]
+DEPS = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("gemmf32.h", "gemm_lp.h",
+                                                               "gemm_experts.h")]
 LIB = os.path.join(PKG, "libgemmf32.so")
 LIB_POISON = os.path.join(PKG, "libgemmf32_lds_poison.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
@@ -56,14 +61,16 @@ def _run(cmd, **kw):
 def _units(poison: bool = False):
     """(name, source, extra flags) of every translation unit: the host code and reduction
     kernels, one unit per tile configuration, and the low-precision and expert-grouped
-    products, their pipelined kernels one unit per element type and operand order (which the
-    LDS-poison build leaves out: the mode is the FP32 kernels')."""
+    products, their pipelined kernels one unit per element type and operand order, and the
+    operators around the experts' products (which the LDS-poison build leaves out: the mode is
+    the FP32 kernels')."""
     units = [("gemm_f32", MAIN_SOURCE, [])]
     units += [(f"cfg{i}", CFG_SOURCE, [f"-DGEMMF32_CFG_ID={i}"]) for i in range(NUM_CONFIGS)]
     if poison:
         return units
     units += [("gemm_lp", LP_SOURCE, [])]
     units += [(f"lp{i}", LP_UNIT_SOURCE, [f"-DLP_UNIT={i}"]) for i in range(NUM_LP_UNITS)]
+    units += [(os.path.splitext(os.path.basename(s))[0], s, []) for s in EX_SOURCES]
     return units
 
 

@@ -1,0 +1,70 @@
+// Shared parts of the kernels around the experts' products.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "gemm_experts.h"
+#include "lp_common.h"
+
+namespace gemmlp {
+
+// Reductions over groups of 16 neighbouring lanes, by rotations on the vector unit, and from there
+// over the wave.  Every lane gets the result, and the same one: sums of FP32 are the same tree
+// from every lane, as a + b = b + a.
+template <class X, class F>
+__device__ __forceinline__ X over_16(X v, F f) {
+  auto turn = [&](auto ctrl) {
+    const int i = __builtin_bit_cast(int, v);
+    v = f(v, __builtin_bit_cast(
+                 X, __builtin_amdgcn_update_dpp(i, i, decltype(ctrl)::value, 0xf, 0xf, false)));
+  };
+  turn(std::integral_constant<int, 0x128>{});  // row_ror:8
+  turn(std::integral_constant<int, 0x124>{});
+  turn(std::integral_constant<int, 0x122>{});
+  turn(std::integral_constant<int, 0x121>{});
+  return v;
+}
+// L: lanes of a group, 16 or 64.
+template <int L, class X, class F>
+__device__ __forceinline__ X over_lanes(X v, F f) {
+  v = over_16(v, f);
+  if constexpr (L == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+struct Add {
+  template <class X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return a + b; }
+};
+struct Least {
+  template <class X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return min(a, b); }
+};
+struct Most {
+  template <class X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return max(a, b); }
+};
+
+// COUNT neighbouring values of a row of any alignment, the first `n` of them inside it; `fill`
+// in the place of the others.
+template <class T, int COUNT>
+__device__ __forceinline__ void load_row(const typename T::type* p, int n, float fill, float* v) {
+  typedef typename T::type E;
+  typedef E group __attribute__((ext_vector_type(COUNT), aligned(sizeof(E))));
+  if (n >= COUNT) {
+    const group e = *(const group*)p;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) v[i] = (float)e[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) v[i] = i < n ? (float)p[i] : fill;
+  }
+}
+
+}  // namespace gemmlp

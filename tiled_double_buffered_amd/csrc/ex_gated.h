@@ -1,0 +1,173 @@
+// The gated unit h = silu(g) u, silu(g) = g s(g), s(g) = 1 / (1 + exp(-g)), with g and u kept for
+// its backward pass in 8 bits (or not kept: the backward pass then reads the input), and 8-bit
+// values turned back into numbers.
+//   dg = dh u s (1 + g (1 - s)),  du = dh g s
+// s and 1 - s both come from exp(-|g|), so that neither is a difference of near numbers and the
+// exponential never overflows.
+//
+// Bound by memory: everything is read once and written once.  16 lanes hold a block of 128 columns,
+// eight each, so that a block's scale needs four rotations.
+#pragma once
+
+#include "ex_common.h"
+#include "lp_quantize.h"
+
+namespace gemmlp {
+
+struct GatedArgs {
+  const void* X;
+  void* H;
+  uint8_t* Q;        // the values kept: gate's N columns, then up's
+  float* S;          // their scales: gate's blocks, then up's
+  const void* DH;
+  void* DX;
+  int64_t ldx, ldh, ldq, lds, lddh, lddx;
+  int rows, N;
+};
+
+// s(g) and 1 - s(g).  FP32 results keep the exponential's and the quotient's full precision; 16-bit
+// ones, rounded at 2^-9 or 2^-12, take the instructions' (2^-22) for a third of the time.
+template <class T>
+__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
+  float t, r;
+  if constexpr (T::BYTES == 4) {
+    t = expf(-fabsf(g));
+    r = 1.0f / (1.0f + t);
+  } else {
+    t = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
+    r = __builtin_amdgcn_rcpf(1.0f + t);
+  }
+  s = g >= 0 ? r : t * r;
+  rest = g >= 0 ? t * r : r;
+  if (g != g) s = rest = g;
+}
+
+__device__ __forceinline__ void from_fp8x8(uint2 q, float scale, float* v) {
+  typedef float float2v __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = (int)(i ? q.y : q.x);
+    const float2v a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+    const float2v b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    v[4 * i] = a[0] * scale;
+    v[4 * i + 1] = a[1] * scale;
+    v[4 * i + 2] = b[0] * scale;
+    v[4 * i + 3] = b[1] * scale;
+  }
+}
+__device__ __forceinline__ uint2 load_bytes8(const uint8_t* p, int n) {
+  typedef uint32_t group __attribute__((ext_vector_type(2), aligned(1)));
+  if (n >= 8) {
+    const group g = *(const group*)p;
+    return make_uint2(g[0], g[1]);
+  }
+  uint2 q = make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) (i < 4 ? q.x : q.y) |= (uint32_t)p[i] << (8 * (i & 3));
+  return q;
+}
+
+// Which row, block and first column a thread has; false past the end (for whole 16 lanes).
+__device__ __forceinline__ bool block_at(int rows, int cols, int& row, int& block, int& c) {
+  const int kb = (cols + kBlock - 1) / kBlock;
+  const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (unit >= (int64_t)rows * kb) return false;
+  row = (int)(unit / kb);
+  block = (int)(unit - (int64_t)row * kb);
+  c = block * kBlock + (threadIdx.x & 15) * 8;
+  return true;
+}
+
+__device__ __forceinline__ int block_exponent(const float* v) {
+  float top = max_over_16(top_of<8, true>(v, 1));
+  if (top == __builtin_inff()) top = max_over_16(top_of<8, false>(v, 1));
+  return scale_exponent(top);
+}
+
+template <class T, bool KEEP>
+__global__ __launch_bounds__(256) void ex_gated_kernel(GatedArgs p) {
+  int row, block, c;
+  if (!block_at(p.rows, p.N, row, block, c)) return;
+  const int n = p.N - c;
+  const typename T::type* x = (const typename T::type*)p.X + row * p.ldx + c;
+  float g[8], u[8], h[8];
+  load8<T>(x, n, g);
+  load8<T>(x + p.N, n, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float s, rest;
+    sigmoid<T>(g[i], s, rest);
+    h[i] = g[i] * s * u[i];
+  }
+  store_row<8, T::CODE>(p.H, row * p.ldh + c, n, T::CODE, h);
+  if constexpr (KEEP) {
+    const int eg = block_exponent(g), eu = block_exponent(u);
+    uint8_t* q = p.Q + row * p.ldq + c;
+    store_bytes8(q, n, to_fp8x8(g, 1, power_of_two(eg)));
+    store_bytes8(q + p.N, n, to_fp8x8(u, 1, power_of_two(eu)));
+    if ((threadIdx.x & 15) == 0) {
+      float* s = p.S + row * p.lds + block;
+      s[0] = power_of_two(eg);
+      s[(p.N + kBlock - 1) / kBlock] = power_of_two(eu);
+    }
+  }
+}
+
+template <class T, bool KEEP>
+__global__ __launch_bounds__(256) void ex_gated_grad_kernel(GatedArgs p) {
+  int row, block, c;
+  if (!block_at(p.rows, p.N, row, block, c)) return;
+  const int n = p.N - c;
+  float g[8], u[8], dh[8];
+  if constexpr (KEEP) {
+    const uint8_t* q = p.Q + row * p.ldq + c;
+    const float* s = p.S + row * p.lds + block;
+    from_fp8x8(load_bytes8(q, n), s[0], g);
+    from_fp8x8(load_bytes8(q + p.N, n), s[(p.N + kBlock - 1) / kBlock], u);
+  } else {
+    const typename T::type* x = (const typename T::type*)p.X + row * p.ldx + c;
+    load8<T>(x, n, g);
+    load8<T>(x + p.N, n, u);
+  }
+  load8<T>((const typename T::type*)p.DH + row * p.lddh + c, n, dh);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float s, rest;
+    sigmoid<T>(g[i], s, rest);
+    const float gs = g[i] * s;
+    g[i] = dh[i] * u[i] * (s + gs * rest);
+    u[i] = dh[i] * gs;
+  }
+  store_row<8, T::CODE>(p.DX, row * p.lddx + c, n, T::CODE, g);
+  store_row<8, T::CODE>(p.DX, row * p.lddx + p.N + c, n, T::CODE, u);
+}
+
+struct DequantArgs {
+  const uint8_t* Q;
+  const float* S;
+  void* Y;
+  int64_t ldq, lds, ldy;
+  int rows, cols, shift;  // shift: log2 of the rows of a block
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void ex_dequantize_kernel(DequantArgs p) {
+  int row, block, c;
+  if (!block_at(p.rows, p.cols, row, block, c)) return;
+  const int n = p.cols - c;
+  const float scale = p.S[(int64_t)(row >> p.shift) * p.lds + block];
+  const float most = T::CODE == GEMM_LP_F16   ? 65504.0f
+                     : T::CODE == GEMM_LP_BF16 ? 3.3895313892515355e38f
+                                               : 3.4028234663852886e38f;
+  float q[8], v[8];
+  from_fp8x8(load_bytes8(p.Q + row * p.ldq + c, n), 1.0f, q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = q[i] * scale;
+    if (fabsf(v[i]) > most && fabsf(scale) < __builtin_inff()) v[i] = copysignf(most, v[i]);
+  }
+  store_row<8, T::CODE>(p.Y, row * p.ldy + c, n, T::CODE, v);
+}
+
+}  // namespace gemmlp

@@ -1,0 +1,119 @@
+// Rows in the order of their experts: a stable counting sort.  Rows of no expert are one more
+// expert, the last.  Every workgroup takes a run of neighbouring rows and every wave of it a part
+// of that run, so that places go by row number: the first place of (expert, workgroup, wave) is
+// the number of rows of lower experts, of the expert's rows in earlier workgroups, and in earlier
+// waves.  64 rows at a time, a wave finds the rows of the same expert by one ballot for each bit
+// of its number.  Where one workgroup does not hold all rows, a launch before counts every
+// workgroup's.  Integers throughout: nothing depends on the order of the counting.
+#pragma once
+
+#include "ex_common.h"
+
+namespace gemmlp {
+
+struct GroupArgs {
+  const void* ids;
+  int64_t* order;
+  int64_t* place;
+  int32_t* offsets;
+  int32_t* hist;  // [workgroup][E + 1], where there are several workgroups
+  int n, E, id_bytes;
+  int run;        // rows of a workgroup, a multiple of 64 for each wave
+  int bits;       // of an expert's number, E included
+};
+
+constexpr int kGroupThreads = 512, kGroupWaves = kGroupThreads / 64;
+
+__device__ __forceinline__ int expert_of(const GroupArgs& a, int64_t i) {
+  const int64_t e = a.id_bytes == 8 ? ((const int64_t*)a.ids)[i] : ((const int32_t*)a.ids)[i];
+  return e < 0 || e >= a.E ? a.E : (int)e;
+}
+
+template <int MAX>
+__global__ __launch_bounds__(kGroupThreads) void ex_group_count_kernel(GroupArgs a) {
+  __shared__ int32_t count[MAX + 1];
+  for (int e = threadIdx.x; e <= a.E; e += kGroupThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * a.run, end = min(first + a.run, (int64_t)a.n);
+  for (int64_t i = first + threadIdx.x; i < end; i += kGroupThreads)
+    atomicAdd(&count[expert_of(a, i)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.E; e += kGroupThreads)
+    a.hist[(int64_t)blockIdx.x * (a.E + 1) + e] = count[e];
+}
+
+template <int MAX>
+__global__ __launch_bounds__(kGroupThreads) void ex_group_place_kernel(GroupArgs a) {
+  __shared__ int32_t count[kGroupWaves][MAX + 1];  // of a wave; then its next place
+  __shared__ int32_t total[MAX + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e <= a.E; e += kGroupThreads)
+    for (int w = 0; w < kGroupWaves; ++w) count[w][e] = 0;
+  __syncthreads();
+  const int part = a.run / kGroupWaves;
+  const int64_t first = (int64_t)blockIdx.x * a.run + (int64_t)wave * part;
+  const int64_t end = min(first + part, (int64_t)a.n);
+  for (int64_t i = first + lane; i < end; i += 64) atomicAdd(&count[wave][expert_of(a, i)], 1);
+  __syncthreads();
+  for (int e = tid; e <= a.E; e += kGroupThreads) {
+    int all = 0, before = 0;
+    if (gridDim.x == 1) {
+      for (int w = 0; w < kGroupWaves; ++w) all += count[w][e];
+    } else {
+#pragma unroll 4
+      for (int g = 0; g < (int)gridDim.x; ++g) {
+        const int c = a.hist[(int64_t)g * (a.E + 1) + e];
+        all += c;
+        before += g < (int)blockIdx.x ? c : 0;
+      }
+    }
+    total[e] = all;
+    int at = before;  // the waves' first places, from the expert's first on
+    for (int w = 0; w < kGroupWaves; ++w) {
+      const int c = count[w][e];
+      count[w][e] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {  // total becomes each expert's first place
+    int carry = 0;
+    for (int base = 0; base <= a.E; base += 64) {
+      const int e = base + lane, c = e <= a.E ? total[e] : 0;
+      int sum = c;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (e <= a.E) {
+        total[e] = carry + sum - c;
+        if (blockIdx.x == 0) a.offsets[e] = carry + sum - c;
+      }
+      carry += __shfl(sum, 63);
+    }
+  }
+  __syncthreads();
+  for (int64_t base = first; base < end; base += 64) {  // (the same for all lanes of a wave)
+    const int64_t i = base + lane;
+    const bool in = i < end;
+    const int e = in ? expert_of(a, i) : 0;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < a.bits; ++b) {
+      const bool one = (e >> b) & 1;
+      const uint64_t with = __ballot(one);
+      same &= one ? with : ~with;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    if (in) {
+      const int at = count[wave][e], to = total[e] + at + rank;
+      __builtin_amdgcn_wave_barrier();  // all lanes have read before one counts on
+      if (rank == 0) count[wave][e] = at + __popcll(same);
+      a.place[i] = to;
+      a.order[to] = i;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+}  // namespace gemmlp

@@ -9,47 +9,13 @@
 
 #include "gemm_lp.h"
 #include "lp_common.h"
+#include "lp_host.h"
 #include "lp_quantize.h"
 #include "lp_units.h"
 
 namespace gemmlp {
 
-constexpr int64_t kMaxDim = 2147483647LL - 1024;  // keeps tile-end arithmetic in int32
-constexpr int64_t kMaxExtent = (int64_t)1 << 61;   // bytes one operand may span
 constexpr int64_t kMaxScaleLd = (int64_t)1 << 22;  // 256 rows of scales in 32-bit offsets
-
-// Byte range [lo, hi) of `count` blocks of rows x cols values of `bytes` bytes, row stride ld
-// and block stride `stride` (elements).  False where it passes kMaxExtent or wraps.
-struct Range {
-  uintptr_t lo = 0, hi = 0;
-};
-static bool byte_range(const void* p, int64_t count, int64_t stride, int64_t rows, int64_t cols,
-                       int64_t ld, int64_t bytes, Range* r) {
-  int64_t e, s;
-  if (__builtin_mul_overflow(rows - 1, ld, &e) || __builtin_add_overflow(e, cols, &e) ||
-      __builtin_mul_overflow(count - 1, stride, &s) || __builtin_add_overflow(e, s, &e) ||
-      __builtin_mul_overflow(e, bytes, &e) || e > kMaxExtent)
-    return false;
-  r->lo = (uintptr_t)p;
-  return !__builtin_add_overflow(r->lo, (uintptr_t)e, &r->hi);
-}
-static bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-static bool known_type(int t) { return t == GEMM_LP_BF16 || t == GEMM_LP_F16 || t == GEMM_LP_F32; }
-static bool misaligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) != 0; }
-static int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
-static int64_t at_least_1(int64_t n) { return n > 1 ? n : 1; }
-
-static int launch(const void* fn, dim3 grid, int threads, void* args, void* stream) {
-  void* list[] = {args};
-  const hipError_t err =
-      hipLaunchKernel(fn, grid, dim3((unsigned)threads), list, 0, (hipStream_t)stream);
-  if (err != hipSuccess) {
-    gemmf32::set_last_hip_error((int)err);
-    return GEMMF32_ERR_HIP;
-  }
-  return GEMMF32_OK;
-}
 
 // Workgroups of a row product with BM x BN tiles: the most tiles that any offsets give.  A
 // group adds at most one partly filled tile to its rows' whole ones, and a group without

@@ -1,0 +1,515 @@
+"""What a layer of experts needs around its products, on GPU tensors, through the C ABI of
+include/gemm_experts.h: a router with its balance loss, rows by expert, adapters of low rank for
+many requests at once, gated units whose input is kept in 8 bits, and 8-bit values as numbers.
+
+As in `lowp`, this module only checks arguments, allocates outputs and workspaces and passes
+pointers, strides and the stream; every value is computed in the library's HIP kernels, and there is
+no other path.  Calls are asynchronous and run on the current stream, or on `stream` where there is
+one, under `lowp`'s rules.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _binding
+from .lowp import (BLOCK, TYPES, _F8, _blocks, _check, _current, _here, _matrix, _names, _offsets,
+                   _on, _out_type, _row_major, _rows16, _same_device, _stack)
+
+MAX_EXPERTS = 1024         # of a router; GEMM_ROUTE_MAX_EXPERTS
+MAX_CHOSEN = 16            # GEMM_ROUTE_MAX_CHOSEN
+MAX_GROUPS = 4096          # of group_rows; GEMM_GROUP_MAX_EXPERTS
+MAX_RANK = 128             # GEMM_ADAPTERS_MAX_RANK
+
+_i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+# Every exported symbol and its C signature (kept in step with include/gemm_experts.h).
+SIGNATURES = {
+    "gemm_route": (_int, [_i64, _i64, _i64, _vp, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp, _vp,
+                          _vp, _i64, _vp]),
+    "gemm_route_workspace": (_i64, [_i64, _i64]),
+    "gemm_route_grad": (_int, [_i64, _i64, _i64, _vp, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp,
+                               _vp, _vp, _vp, _i64, _vp]),
+    "gemm_group_rows": (_int, [_i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "gemm_group_rows_workspace": (_i64, [_i64, _i64]),
+    "gemm_adapters_down": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64,
+                                  _vp, _vp, _int, _int, _vp]),
+    "gemm_adapters_up": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp,
+                                _i64, _vp, _i64, _int, _vp]),
+    "gemm_adapters_grad": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _vp,
+                                  _i64, _i64, _vp, _i64, _int, _vp]),
+    "gemm_adapters_splits": (_int, [_i64, _i64, _i64, _i64]),
+    "gemm_adapters_grad_workspace": (_i64, [_i64, _i64, _i64, _i64]),
+    "gemm_gated": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "gemm_gated_grad": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                               _int, _vp]),
+    "gemm_fp8_dequantize": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _int, _vp]),
+}
+_lib = None
+
+
+def load():
+    """The library with this module's entry points typed.  Raises if it is not built."""
+    global _lib
+    if _lib is None:
+        lib = _binding.load()
+        for name, (res, args) in SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = res, args
+        _lib = lib
+    return _lib
+
+
+# ----------------------------------------------------------------------------- raw C ABI
+def gemm_route(*args) -> int:
+    return load().gemm_route(*args)
+
+
+def gemm_route_workspace(rows, E) -> int:
+    return load().gemm_route_workspace(rows, E)
+
+
+def gemm_route_grad(*args) -> int:
+    return load().gemm_route_grad(*args)
+
+
+def gemm_group_rows(*args) -> int:
+    return load().gemm_group_rows(*args)
+
+
+def gemm_group_rows_workspace(n, E) -> int:
+    return load().gemm_group_rows_workspace(n, E)
+
+
+def gemm_adapters_down(*args) -> int:
+    return load().gemm_adapters_down(*args)
+
+
+def gemm_adapters_up(*args) -> int:
+    return load().gemm_adapters_up(*args)
+
+
+def gemm_adapters_grad(*args) -> int:
+    return load().gemm_adapters_grad(*args)
+
+
+def gemm_adapters_splits(rows, K, rank, E) -> int:
+    return load().gemm_adapters_splits(rows, K, rank, E)
+
+
+def gemm_adapters_grad_workspace(rows, N, rank, E) -> int:
+    return load().gemm_adapters_grad_workspace(rows, N, rank, E)
+
+
+def gemm_gated(*args) -> int:
+    return load().gemm_gated(*args)
+
+
+def gemm_gated_grad(*args) -> int:
+    return load().gemm_gated_grad(*args)
+
+
+def gemm_fp8_dequantize(*args) -> int:
+    return load().gemm_fp8_dequantize(*args)
+
+
+# ------------------------------------------------------------------------------- arguments
+def _size(n, what):
+    """A workspace query's answer, or its error raised."""
+    if n < 0:
+        _check(n, what)
+    return n
+
+
+def _workspace(n, device):
+    """(tensor that holds it, pointer): n bytes, none for 0."""
+    if n == 0:
+        return None, None
+    w = torch.empty((n + 7) // 8, dtype=torch.int64, device=device)
+    return w, w.data_ptr()
+
+
+def _flat(x):
+    """x as rows of its last axis (rows counted: -1 is ambiguous where the last axis is empty)."""
+    return x if x.dim() == 2 else x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+# ---------------------------------------------------------------------------------- router
+def _route(logits, k, valid, renormalize):
+    """(gates, experts, counts, sums, loss)."""
+    px, ldx = _matrix(logits, "logits", TYPES)
+    rows, E = logits.shape
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"logits must have 1 to {MAX_EXPERTS} columns, one for each expert")
+    if not 1 <= k <= min(E, MAX_CHOSEN):
+        raise ValueError(f"k must be 1 to {min(E, MAX_CHOSEN)} for {E} experts")
+    if valid is not None:
+        if valid.device != logits.device:
+            raise ValueError("valid must live on the logits' GPU")
+    dev = logits.device
+    gates = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    experts = torch.empty((rows, k), dtype=torch.int32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    sums = torch.empty(2, dtype=torch.int32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    need = _size(load().gemm_route_workspace(rows, E), "gemm_route_workspace")
+    hold, pw = _workspace(need, dev)
+    _check(load().gemm_route(rows, E, k, px, max(ldx, E), TYPES[logits.dtype], _pointer(valid),
+                             1 if renormalize else 0, gates.data_ptr(), experts.data_ptr(),
+                             counts.data_ptr(), sums.data_ptr(), loss.data_ptr(), pw, need,
+                             _current(logits)), "gemm_route")
+    return gates, experts, counts, sums, loss
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, valid, renormalize):
+        gates, experts, counts, sums, loss = _route(logits, k, valid, renormalize)
+        ctx.save_for_backward(logits, valid, gates, experts, counts, sums)
+        ctx.k, ctx.renormalize = k, renormalize
+        ctx.mark_non_differentiable(experts, counts)
+        ctx.set_materialize_grads(False)
+        return gates, experts, counts, loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dgates, dexperts, dcounts, dloss):
+        logits, valid, gates, experts, counts, sums = ctx.saved_tensors
+        rows, E = logits.shape
+        px, ldx = _matrix(logits, "logits", TYPES)
+        dgates = None if dgates is None else dgates.contiguous()
+        dx = torch.empty((rows, E), dtype=logits.dtype, device=logits.device)
+        _check(load().gemm_route_grad(rows, E, ctx.k, px, max(ldx, E), TYPES[logits.dtype],
+                                      _pointer(valid), 1 if ctx.renormalize else 0,
+                                      gates.data_ptr(), experts.data_ptr(), counts.data_ptr(),
+                                      sums.data_ptr(), _pointer(dgates), _pointer(dloss),
+                                      dx.data_ptr(), E, _current(logits)), "gemm_route_grad")
+        return dx, None, None, None
+
+
+def route_experts(logits, k, valid=None, renormalize=False):
+    """(gates, experts, counts, loss): the k experts of every row, and how evenly they are used.
+
+    logits is T x E (bfloat16, float16 or float32; E up to 1024, k up to 16), valid T truth values,
+    False for rows to be left out (padding), or None.  With p the softmax of a row,
+      experts  T x k int32, the largest logits first, of equal ones the lowest index
+      gates    T x k float32, their p, with renormalize over the sum of the row's
+      counts   E int32, how often each expert was taken
+      loss     float32: E sum_e f_e P_e, f_e the share of counts that is e's, P_e the mean of p_e
+               over the rows that count; 1 where all experts are used alike, E where one is
+    An expert whose logit is -Inf is never taken.  Where a row has none left, its place holds -1
+    with a gate of 0 (`group_rows` puts such places last); rows that are not valid, or have no
+    logit above -Inf, hold nothing else and do not count.  NaN is taken before every number; it, or
+    +Inf, makes the row's gates and the loss NaN.
+
+    Differentiable in logits through gates and loss; counts are constants in it, as usual."""
+    if valid is not None:
+        if not isinstance(valid, torch.Tensor) or valid.dtype != torch.bool or valid.dim() != 1:
+            raise TypeError("valid must be a 1-D bool tensor")
+        if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or \
+                valid.shape[0] != logits.shape[0]:
+            raise ValueError("valid must have one value for each row of logits")
+        valid = valid.contiguous()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in TYPES:
+        raise TypeError(f"logits must be a 2-D tensor of {_names(TYPES)}")
+    logits, k = _row_major(logits), int(k)
+    if not (logits.requires_grad and torch.is_grad_enabled()):
+        if _here(logits, None):
+            gates, experts, counts, _, loss = _route(logits, k, valid, renormalize)
+        else:
+            with _on(None, logits):
+                gates, experts, counts, _, loss = _route(logits, k, valid, renormalize)
+        return gates, experts, counts, loss
+    if _here(logits, None):
+        return _Route.apply(logits, k, valid, renormalize)
+    with _on(None, logits):
+        return _Route.apply(logits, k, valid, renormalize)
+
+
+# --------------------------------------------------------------------------------- grouping
+def _group(experts, count):
+    ids = experts.contiguous()
+    n, dev = ids.numel(), ids.device
+    order = torch.empty(n, dtype=torch.int64, device=dev)
+    place = torch.empty(experts.shape, dtype=torch.int64, device=dev)
+    offsets = torch.empty(count + 1, dtype=torch.int32, device=dev)
+    need = _size(load().gemm_group_rows_workspace(n, count), "gemm_group_rows_workspace")
+    hold, pw = _workspace(need, dev)
+    _check(load().gemm_group_rows(n, count, ids.data_ptr(), ids.element_size(), order.data_ptr(),
+                                  place.data_ptr(), offsets.data_ptr(), pw, need, _current(ids)),
+           "gemm_group_rows")
+    return order, place, offsets
+
+
+def group_rows(experts, count, stream=None):
+    """(order, place, offsets): rows sorted by expert, as the grouped products and `add_adapters`
+    take them.  experts is an int32 or int64 GPU tensor of any shape, its n elements counted in
+    row-major order; those outside 0 .. count - 1 belong to no expert and come last.
+
+    order (n int64) holds the element at each place, equal experts in the order of the elements;
+    place (int64, experts' shape) the place of each element; offsets (count + 1 int32) each
+    expert's first place, and that of the elements of none.  For k experts a row, as `route_experts`
+    gives them, order // k is the row at a place.  count is 4096 at most."""
+    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError("experts must be an int32 or int64 tensor")
+    count = int(count)
+    if not 0 <= count <= MAX_GROUPS:
+        raise ValueError(f"count must be 0 to {MAX_GROUPS}")
+    if not experts.is_cuda:
+        raise ValueError("experts must live on the GPU (the library takes device pointers)")
+    if _here(experts, stream):
+        return _group(experts, count)
+    with _on(stream, experts):
+        return _group(experts, count)
+
+
+# --------------------------------------------------------------------------------- adapters
+def _plan(order, offsets, rows, E, like):
+    """(order's pointer, offsets' pointer)."""
+    if not isinstance(order, torch.Tensor) or order.dim() != 1 or order.dtype != torch.int64 or \
+            (order.numel() > 1 and order.stride(0) != 1):
+        raise TypeError("order must be a contiguous 1-D int64 tensor")
+    if order.numel() != rows:
+        raise ValueError(f"order has {order.numel()} elements for {rows} rows")
+    if order.device != like.device:
+        raise ValueError("order must live on the operands' GPU")
+    return order.data_ptr(), _offsets(offsets, like, E)[0]
+
+
+def _down(x, a, order, offsets, scale):
+    """u: splits x rows x rank, the contraction of x's rows with their adapter's."""
+    px, ldx = _matrix(x, "x", TYPES)
+    pa, lda, step = _stack(a, "a", (x.dtype,))
+    rows, K = x.shape
+    E, rank = a.shape[:2]
+    po, pf = _plan(order, offsets, rows, E, x)
+    splits = _size(load().gemm_adapters_splits(rows, K, rank, E), "gemm_adapters_splits")
+    u = torch.empty((splits, rows, rank), dtype=torch.float32, device=x.device)
+    _check(load().gemm_adapters_down(rows, K, rank, E, po, pf, px, max(ldx, K), pa, max(lda, K),
+                                     step, _pointer(scale), u.data_ptr(), splits, TYPES[x.dtype],
+                                     _current(x)), "gemm_adapters_down")
+    return u
+
+
+def _up(u, b, y, order, offsets):
+    """y + u b of each row's adapter; y None for 0."""
+    splits, rows, rank = u.shape
+    pb, ldb, step = _stack(b, "b", TYPES)
+    E, _, N = b.shape
+    po, pf = _plan(order, offsets, rows, E, b)
+    py, ldy = (None, 0) if y is None else _matrix(y, "y", (b.dtype,))
+    out = torch.empty((rows, N), dtype=b.dtype, device=b.device)
+    _check(load().gemm_adapters_up(rows, N, rank, E, po, pf, u.data_ptr(), splits, pb,
+                                   max(ldb, N), step, py, max(ldy, N), out.data_ptr(), max(N, 1),
+                                   TYPES[b.dtype], _current(b)), "gemm_adapters_up")
+    return out
+
+
+def _adapter_grad(u, x, E, order, offsets):
+    """E x rank x N: u^T x over each adapter's rows."""
+    splits, rows, rank = u.shape
+    px, ldx = _matrix(x, "x", TYPES)
+    N = x.shape[1]
+    po, pf = _plan(order, offsets, rows, E, x)
+    d = torch.empty((E, rank, N), dtype=x.dtype, device=x.device)
+    need = _size(load().gemm_adapters_grad_workspace(rows, N, rank, E),
+                 "gemm_adapters_grad_workspace")
+    hold, pw = _workspace(need, x.device)
+    _check(load().gemm_adapters_grad(rows, N, rank, E, po, pf, u.data_ptr(), splits, px,
+                                     max(ldx, N), d.data_ptr(), max(N, 1), rank * N, pw, need,
+                                     TYPES[x.dtype], _current(x)), "gemm_adapters_grad")
+    return d
+
+
+class _Adapters(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, x, a, b, order, offsets, scale):
+        u = _down(x, a, order, offsets, scale)
+        need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
+        ctx.save_for_backward(x if need_a else None, a if need_x else None,
+                              b if need_x or need_a else None, u if need_b else None, order,
+                              offsets, scale)
+        ctx.experts = a.shape[0]
+        return _up(u, b, y, order, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
+        x, a, b, u, order, offsets, scale = ctx.saved_tensors
+        dx = da = db = None
+        if need_x or need_a or need_b:
+            rows = _row_major(dout)
+            if need_x or need_a:
+                v = _down(rows, b, order, offsets, scale)
+                dx = _up(v, a, None, order, offsets) if need_x else None
+                da = _adapter_grad(v, x, ctx.experts, order, offsets) if need_a else None
+            db = _adapter_grad(u, rows, ctx.experts, order, offsets) if need_b else None
+        return dout if need_y else None, dx, da, db, None, None, None
+
+
+def add_adapters(y, x, a, b, order, offsets, scale=None):
+    """y + scale[e] (x a[e]^T) b[e] for the rows of each adapter e: adapters of low rank beside a
+    projection that all rows share, whose result y is and which x went into.
+
+    x is (..., K) and y (..., N), with T rows each; a is E x rank x K and b E x rank x N (both with
+    the wide axis contiguous, so that the forward and the backward pass read whole lines), rank up
+    to 128; all of one type, bfloat16, float16 or float32.  order (T int64) and offsets (E + 1
+    int32) are `group_rows` of the rows' adapters, made once for all projections of a batch: order
+    holds every row once.  scale is E float32 on the GPU, or None for 1.  Rows of no adapter keep y.
+    The contraction over K is kept in float32; all sums are, and are rounded once.
+
+    Differentiable in y, x, a and b; adapters without rows get zeros."""
+    for name, t in (("y", y), ("x", x)):
+        if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.dtype not in TYPES:
+            raise TypeError(f"{name} must be a tensor of {_names(TYPES)}")
+    for name, t in (("a", a), ("b", b)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != x.dtype:
+            raise TypeError(f"{name} must be a 3-D tensor of x's type")
+    if y.dtype != x.dtype:
+        raise TypeError(f"x is {x.dtype}, y {y.dtype}")
+    E, rank, K = a.shape
+    N = b.shape[2]
+    if tuple(b.shape[:2]) != (E, rank):
+        raise ValueError(f"a is {tuple(a.shape)}, b {tuple(b.shape)}: experts or ranks differ")
+    if not 1 <= rank <= MAX_RANK:
+        raise ValueError(f"the rank must be 1 to {MAX_RANK}")
+    if x.shape[-1] != K or y.shape[-1] != N or x.shape[:-1] != y.shape[:-1]:
+        raise ValueError(f"x is {tuple(x.shape)}, y {tuple(y.shape)}: the adapters take (..., {K}) "
+                         f"to (..., {N})")
+    _same_device(x, y, a, b)
+    if scale is not None:
+        if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or \
+                scale.dim() != 1 or (E > 1 and scale.stride(0) != 1):
+            raise TypeError("scale must be a contiguous 1-D float32 tensor")
+        if scale.shape[0] != E:
+            raise ValueError(f"scale has {scale.shape[0]} elements for {E} adapters")
+        _same_device(x, scale)
+        if scale.requires_grad and torch.is_grad_enabled():
+            raise ValueError("scale has no gradient here: detach it")
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU (the library takes device pointers)")
+    rows, base = _row_major(_flat(x)), _row_major(_flat(y))
+    a, b = _unit_columns(a), _unit_columns(b)
+    args = (base, rows, a, b, order, offsets, scale)
+    if _here(x, None):
+        out = _adapted(*args)
+    else:
+        with _on(None, x):
+            out = _adapted(*args)
+    return out if y.dim() == 2 else out.view(y.shape)
+
+
+def _adapted(y, x, a, b, order, offsets, scale):
+    if torch.is_grad_enabled() and (y.requires_grad or x.requires_grad or a.requires_grad or
+                                    b.requires_grad):
+        return _Adapters.apply(y, x, a, b, order, offsets, scale)
+    return _up(_down(x, a, order, offsets, scale), b, y, order, offsets)
+
+
+def _unit_columns(w):
+    """w with unit column stride and rows that do not overlap (a copy where it is neither)."""
+    ok = (w.shape[2] <= 1 or w.stride(2) == 1) and (w.shape[1] <= 1 or w.stride(1) >= w.shape[2])
+    return w if ok else w.contiguous()
+
+
+# ------------------------------------------------------------------------------- gated unit
+def _gated(x, keep):
+    """(h, q, s): q and s None where nothing is kept."""
+    px, ldx = _matrix(x, "x", TYPES)
+    rows, N = x.shape[0], x.shape[1] // 2
+    h = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+    q = s = pq = ps = None
+    ldq = lds = 0
+    if keep:
+        q = _rows16(rows, 2 * N, x.device)
+        s = torch.empty((rows, 2 * _blocks(N)), dtype=torch.float32, device=x.device)
+        pq, ldq, ps, lds = q.data_ptr(), max(q.stride(0), 1), s.data_ptr(), max(s.shape[1], 1)
+    if rows and N:
+        _check(load().gemm_gated(rows, N, px, max(ldx, 2 * N), TYPES[x.dtype], h.data_ptr(), N,
+                                 pq, ldq, ps, lds, _current(x)), "gemm_gated")
+    return h, q, s
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, keep):
+        h, q, s = _gated(x, keep)
+        ctx.save_for_backward(None if keep else x, q, s)
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, q, s = ctx.saved_tensors
+        dh = _row_major(dh)
+        pd, ldd = _matrix(dh, "dh", TYPES)
+        rows, N = dh.shape
+        dx = torch.empty((rows, 2 * N), dtype=dh.dtype, device=dh.device)
+        if rows and N:
+            px, ldx = (None, 0) if x is None else _matrix(x, "x", TYPES)
+            _check(load().gemm_gated_grad(
+                rows, N, px, max(ldx, 2 * N), _pointer(q), 0 if q is None else max(q.stride(0), 1),
+                _pointer(s), 0 if s is None else max(s.shape[1], 1), pd, max(ldd, N),
+                dx.data_ptr(), 2 * N, TYPES[dh.dtype], _current(dh)), "gemm_gated_grad")
+        return dx, None
+
+
+def gated_silu(x, checkpoint=False):
+    """silu(gate) * up, silu(g) = g / (1 + exp(-g)): gate is the first half of x's last axis, up the
+    second (the two results of one product with twice the columns), of bfloat16, float16 or
+    float32; sums and functions in float32, rounded once.
+
+    Differentiable.  With checkpoint the backward pass works on the 8-bit values that `quantize_fp8`
+    has of gate and of up, by blocks of 1 x 128 each, and x itself need not be kept: 8 bits a value
+    and a scale for every 128, and a gradient of these values; the forward result is x's own."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in TYPES:
+        raise TypeError(f"x must be a tensor of {_names(TYPES)}")
+    if x.shape[-1] % 2:
+        raise ValueError(f"x has {x.shape[-1]} columns: gate and up need as many each")
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU (the library takes device pointers)")
+    flat, keep = _row_major(_flat(x)), bool(checkpoint)
+    grads = x.requires_grad and torch.is_grad_enabled()
+    if _here(x, None):
+        h = _Gated.apply(flat, keep) if grads else _gated(flat, False)[0]
+    else:
+        with _on(None, x):
+            h = _Gated.apply(flat, keep) if grads else _gated(flat, False)[0]
+    return h if x.dim() == 2 else h.view(*x.shape[:-1], x.shape[-1] // 2)
+
+
+# --------------------------------------------------------------------------- 8-bit values
+def _dequantize(q, s, out_dtype):
+    code = _out_type(out_dtype)
+    pq, ldq = _matrix(q, "q", (_F8,))
+    ps, lds = _matrix(s, "s", (torch.float32,))
+    rows, cols = q.shape
+    _same_device(q, s)
+    if tuple(s.shape) == (rows, _blocks(cols)):
+        block = 1
+    elif tuple(s.shape) == (_blocks(rows), _blocks(cols)):
+        block = BLOCK
+    else:
+        raise ValueError(f"s must be {(rows, _blocks(cols))} (blocks of 1 x {BLOCK}) or "
+                         f"{(_blocks(rows), _blocks(cols))} (blocks of {BLOCK} x {BLOCK})")
+    y = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
+    if rows and cols:
+        _check(load().gemm_fp8_dequantize(rows, cols, pq, ldq, ps, lds, block, y.data_ptr(), cols,
+                                          code, _current(q)), "gemm_fp8_dequantize")
+    return y
+
+
+def dequantize_fp8(q, s, out_dtype=torch.bfloat16, stream=None):
+    """The numbers q * s that `quantize_fp8`'s results stand for, rounded once to out_dtype: q is
+    2-D float8_e4m3fn, s float32 with one scale for each block of 1 x 128 or of 128 x 128, any
+    numbers.  Finite products past out_dtype's range become its largest number."""
+    if _here(q, stream):
+        return _dequantize(q, s, out_dtype)
+    with _on(stream, q, s):
+        return _dequantize(q, s, out_dtype)

@@ -483,33 +483,46 @@ def linear_fp8(x, w):
 
 class _LinearGrouped(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, transpose_w):
+    def forward(ctx, x, w, offsets, transpose_w, keep):
         need_x, need_w = ctx.needs_input_grad[:2]
-        ctx.save_for_backward(x if need_w else None, w if need_x else None, offsets)
+        y = _grouped(x, w, offsets, transpose_w)
+        q = s = None
+        if keep and need_w:
+            q, s = _quantize(x, 1, True, False)[:2]
+        ctx.save_for_backward(x if need_w and not keep else None, q, s, w if need_x else None,
+                              offsets)
         ctx.transpose_w = transpose_w
-        return _grouped(x, w, offsets, transpose_w)
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
-        x, w, offsets = ctx.saved_tensors
+        x, q, s, w, offsets = ctx.saved_tensors
         dy = _row_major(dy)
         dx = _grouped(dy, w, offsets, not ctx.transpose_w) if need_x else None
         dw = None
         if need_w:
+            if x is None:
+                from .experts import _dequantize
+                x = _dequantize(q, s, dy.dtype)
             dw = _grouped_wgrad(dy, x, offsets) if ctx.transpose_w else \
                 _grouped_wgrad(x, dy, offsets)
-        return dx, dw, None, None
+        return dx, dw, None, None, None
 
 
-def linear_grouped(x, w, offsets, transpose_w=False):
+def linear_grouped(x, w, offsets, transpose_w=False, checkpoint=False):
     """`matmul_grouped`, differentiable in x and w.  Rows of no expert get zeros in dx, and
-    experts without rows zeros in dw."""
+    experts without rows zeros in dw.
+
+    With checkpoint, w's gradient is that of the 8-bit values that `quantize_fp8` has of x's rows,
+    by blocks of 1 x 128, and x itself need not be kept for it: 8 bits a value and a scale for every
+    128.  y and dx do not change; Inf in x, which has no 8-bit value, gives NaN in dw."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in TYPES:
         raise TypeError(f"x must be a 2-D tensor of {_names(TYPES)}")
-    x, transpose_w = _row_major(x), bool(transpose_w)
+    x, transpose_w, keep = _row_major(x), bool(transpose_w), bool(checkpoint)
+    keep = keep and torch.is_grad_enabled()  # without, nothing is kept
     if _here(x, None):
-        return _LinearGrouped.apply(x, w, offsets, transpose_w)
+        return _LinearGrouped.apply(x, w, offsets, transpose_w, keep)
     with _on(None, x):
-        return _LinearGrouped.apply(x, w, offsets, transpose_w)
+        return _LinearGrouped.apply(x, w, offsets, transpose_w, keep)
