@@ -81,7 +81,8 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  * GEMMF32_ERR_BAD_CONFIG.
  *
  * down: U[p] = scale[e] X[order[p]] A_e^T for the places p of e, in FP32, as `splits` partial sums
- *   over K, each rows x rank (places of no expert are left as they were).  scale may be NULL (1).
+ *   over K, each rows x 16 ceil(rank / 16) with zeros past the rank, one after another and 16-byte
+ *   aligned (places of no expert are left as they were).  scale may be NULL (1).
  * up: OUT[order[p]] = Y[order[p]] + (sum of U's splits)[p] B_e; places of no expert: Y alone.
  *   Y may be NULL (0).
  * grad: D_e (rank x N, row stride ldd, stride_d elements apart) = sum over the places p of e of
@@ -101,7 +102,7 @@ int gemm_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E, const i
                        int64_t ldx, void *D, int64_t ldd, int64_t stride_d, void *workspace,
                        int64_t workspace_bytes, int type, void *stream);
 int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E);
-int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E);
+int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int type);
 
 /* H = silu(G) * U, silu(g) = g / (1 + exp(-g)): X is rows x 2N, G its first N columns and U the
  * others; H rows x N.  Q, S (both or neither): G and U in 8 bits as gemm_fp8_quantize gives them,

@@ -295,7 +295,7 @@ def test_adapters_sizes(size, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_adapters_rows_split_for_the_gradient(dtype):
     """One adapter with many rows: its gradients' rows are split over workgroups."""
-    assert tdb.gemm_adapters_grad_workspace(3001, 136, 24, 1) > 0
+    assert tdb.gemm_adapters_grad_workspace(3001, 136, 24, 1, 0) > 0
     y, x, a, b, d, s = _adapter_inputs(3001, 1, 24, 136, 200, dtype, 1)
     _check_adapters(y, x, a, b, *_groups((2900,), 3001, 3), s, d)
 
@@ -384,10 +384,11 @@ def test_adapters_rows_behind_are_left():
     y, x, a, b, d, s = _adapter_inputs(T, E, r, K, N, torch.bfloat16, 2)
     order, offsets = _groups((7, 6), T, 1)
     stream = torch.cuda.current_stream().cuda_stream
-    u = torch.full((2, T, r), 7.0, device=DEV)
+    u = torch.full((2, T, 16), 7.0, device=DEV)
     rc = tdb.gemm_adapters_down(T, K, r, E, order.data_ptr(), offsets.data_ptr(), x.data_ptr(), K,
                                 a.data_ptr(), K, r * K, s.data_ptr(), u.data_ptr(), 2, 0, stream)
     assert rc == tdb.OK and (u[:, 13:] == 7).all() and (u[:, :13] != 7).all()
+    assert (u[:, :13, r:] == 0).all()
     out = torch.full((T + 1, N + 3), 7.0, dtype=torch.bfloat16, device=DEV)
     rc = tdb.gemm_adapters_up(T, N, r, E, order.data_ptr(), offsets.data_ptr(), u.data_ptr(), 2,
                               b.data_ptr(), N, r * N, y.data_ptr(), N, out.data_ptr(), N + 3, 0, stream)

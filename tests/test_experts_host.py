@@ -108,7 +108,8 @@ def _down(rows=4, K=64, r=8, E=2, order=P[0], off=P[1], X=P[2], ldx=64, A=P[3], 
     (dict(order=None), tdb.ERR_NULL_PTR), (dict(U=None), tdb.ERR_NULL_PTR),
     (dict(X=None), tdb.ERR_NULL_PTR), (dict(order=P[0] + 4), tdb.ERR_MISALIGNED),
     (dict(A=P[3] + 1), tdb.ERR_MISALIGNED), (dict(scale=P[4] + 2), tdb.ERR_MISALIGNED),
-    (dict(U=P[2]), tdb.ERR_ALIAS), (dict(U=P[4]), tdb.ERR_ALIAS), (dict(U=P[0] + 8), tdb.ERR_ALIAS),
+    (dict(U=P[2]), tdb.ERR_ALIAS), (dict(U=P[4]), tdb.ERR_ALIAS), (dict(U=P[0] + 16), tdb.ERR_ALIAS),
+    (dict(U=P[5] + 8), tdb.ERR_MISALIGNED),
     (dict(rows=1 << 31), tdb.ERR_TOO_LARGE), (dict(sA=1 << 61), tdb.ERR_TOO_LARGE),
 ])
 def test_down_refusals(change, code):
@@ -235,9 +236,10 @@ def test_workspace_and_split_queries():
     assert tdb.gemm_adapters_splits(100000, 4096, 16, 4) == 1
     assert tdb.gemm_adapters_splits(0, 0, 1, 0) == 1
     assert tdb.gemm_adapters_splits(1, 4096, 129, 4) == tdb.ERR_BAD_CONFIG
-    assert tdb.gemm_adapters_grad_workspace(4, 4096, 16, 4) == 0
-    assert tdb.gemm_adapters_grad_workspace(100000, 128, 16, 1) > 0
-    assert tdb.gemm_adapters_grad_workspace(-4, 128, 16, 1) == tdb.ERR_NEGATIVE_DIM
+    assert tdb.gemm_adapters_grad_workspace(4, 4096, 16, 4, BF16) == 0
+    assert tdb.gemm_adapters_grad_workspace(100000, 128, 16, 1, F32) > 0
+    assert tdb.gemm_adapters_grad_workspace(-4, 128, 16, 1, F16) == tdb.ERR_NEGATIVE_DIM
+    assert tdb.gemm_adapters_grad_workspace(4, 128, 16, 1, 3) == tdb.ERR_BAD_TYPE
 
 
 def test_tensor_calls_refuse_what_they_cannot_take():

@@ -11,42 +11,78 @@
 
 namespace gemmlp {
 
-// Tiles of 16 places: the most that any offsets give.
-static int64_t place_tiles(int64_t rows, int64_t E) {
-  return rows / 16 + std::min<int64_t>(E + 2, rows);
+// Tiles of bm places: the most that any offsets give.
+static int64_t place_tiles(int64_t rows, int64_t E, int bm) {
+  return rows / bm + std::min<int64_t>(E + 2, rows);
 }
 
-// Splits of K: enough workgroups for two a CU, but 256 columns a split.
+// Waves of a workgroup of `down` with places of their own (the others share K): more than one only
+// where that leaves a workgroup for every CU, and the adapters have several tiles on average.
+static int down_waves(int64_t rows, int64_t E) {
+  for (int w = 4; w > 1; w /= 2)
+    if (rows >= 16 * w * kCus && rows >= 64 * w * E) return w;
+  return 1;
+}
+// Splits of K: enough workgroups for two a CU where there is not one for each, but 256 columns a
+// split.
 static int adapter_splits(int64_t rows, int64_t K, int64_t E) {
-  const int64_t tiles = std::max<int64_t>(place_tiles(rows, E), 1);
+  const int64_t tiles = std::max<int64_t>(place_tiles(rows, E, 16 * down_waves(rows, E)), 1);
+  if (tiles >= kCus) return 1;
   return (int)std::max<int64_t>(
       std::min<int64_t>({(2 * kCus + tiles - 1) / tiles, K / 256, 8}), 1);
 }
-// Splits of a group's rows in `grad`: enough workgroups for two a CU where the groups are as long
-// as the average, but 128 rows a split.
-static int64_t grad_blocks(int64_t N, int64_t rank, int64_t E) {
-  const int64_t rb = rank <= 64 ? 1 : 2;
-  return (N + kWaveCols - 1) / kWaveCols * rb * E;
-}
-static int grad_splits(int64_t rows, int64_t N, int64_t rank, int64_t E) {
-  const int64_t wgs = std::max<int64_t>(grad_blocks(N, rank, E), 1);
-  const int64_t each = rows / std::max<int64_t>(E, 1);
-  return (int)std::max<int64_t>(
-      std::min<int64_t>({(2 * kCus + wgs - 1) / wgs, each / 128, 16}), 1);
+// Places of a workgroup of `up`.
+static int up_places(int64_t rows, int64_t E, int splits) {
+  return rows >= 32 * E && splits == 1 ? 64 : 16;
 }
 
-template <class T>
+// Fragments of the rank of a workgroup of `grad`.
+static int grad_fragments(int64_t rank, int bytes) {
+  return rank <= 16 ? 1 : rank <= 32 || bytes == 4 ? 2 : 4;
+}
+static int64_t grad_blocks(int64_t N, int64_t rank, int64_t E, int bytes) {
+  const int64_t per = 16 * grad_fragments(rank, bytes);
+  return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per) * E;
+}
+// Splits of a group's rows in `grad`: enough workgroups for one a CU where the groups are as long
+// as the average, but 256 rows a split.
+static int grad_splits(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
+  const int64_t wgs = std::max<int64_t>(grad_blocks(N, rank, E, bytes), 1);
+  const int64_t each = rows / std::max<int64_t>(E, 1);
+  return (int)std::max<int64_t>(
+      std::min<int64_t>({(kCus + wgs - 1) / wgs, each / 256, 16}), 1);
+}
+
+template <class T, int RW>
 static const void* down_kernel(int64_t rank) {
-  return rank <= 16   ? (const void*)&ex_adapters_down_kernel<T, 1>
-         : rank <= 32 ? (const void*)&ex_adapters_down_kernel<T, 2>
-         : rank <= 64 ? (const void*)&ex_adapters_down_kernel<T, 4>
-                      : (const void*)&ex_adapters_down_kernel<T, 8>;
+  return rank <= 16   ? (const void*)&ex_adapters_down_kernel<T, 1, RW>
+         : rank <= 32 ? (const void*)&ex_adapters_down_kernel<T, 2, RW>
+         : rank <= 64 ? (const void*)&ex_adapters_down_kernel<T, 4, RW>
+                      : (const void*)&ex_adapters_down_kernel<T, 8, RW>;
 }
 template <class T>
-static const void* grad_kernel(int64_t rank) {
-  return rank <= 16   ? (const void*)&ex_adapters_grad_kernel<T, 1>
-         : rank <= 32 ? (const void*)&ex_adapters_grad_kernel<T, 2>
-                      : (const void*)&ex_adapters_grad_kernel<T, 4>;
+static const void* down_kernel(int64_t rank, int waves) {
+  return waves == 4   ? down_kernel<T, 4>(rank)
+         : waves == 2 ? down_kernel<T, 2>(rank)
+                      : down_kernel<T, 1>(rank);
+}
+template <class T, int BM>
+static const void* up_kernel(int64_t rank) {
+  return rank <= 32   ? (const void*)&ex_adapters_up_kernel<T, 1, BM>
+         : rank <= 64 ? (const void*)&ex_adapters_up_kernel<T, 2, BM>
+                      : (const void*)&ex_adapters_up_kernel<T, 4, BM>;
+}
+template <class T>
+static const void* up_kernel(int64_t rank, int places) {
+  return places == 64 ? up_kernel<T, 64>(rank) : up_kernel<T, 16>(rank);
+}
+template <class T>
+static const void* grad_kernel(int fragments) {
+  if constexpr (T::BYTES == 2) {
+    if (fragments == 4) return (const void*)&ex_adapters_grad_kernel<T, 4>;
+  }
+  return fragments == 1 ? (const void*)&ex_adapters_grad_kernel<T, 1>
+                        : (const void*)&ex_adapters_grad_kernel<T, 2>;
 }
 #define BY_TYPE(type, f)                                     \
   ((type) == GEMM_LP_BF16  ? (const void*)f(Bf16)            \
@@ -78,11 +114,12 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
       (K && (X == nullptr || A == nullptr)))
     return GEMMF32_ERR_NULL_PTR;
   const int b = type_bytes(type);
-  if (misaligned(order, 8) || misaligned(offsets, 4) || misaligned(scale, 4) || misaligned(U, 4) ||
+  if (misaligned(order, 8) || misaligned(offsets, 4) || misaligned(scale, 4) || misaligned(U, 16) ||
       misaligned(X, b) || misaligned(A, b))
     return GEMMF32_ERR_MISALIGNED;
+  const int64_t ldu = u_columns((int)rank);
   Range u, in[5];
-  if (!byte_range(U, splits, rows * rank, rows, rank, rank, 4, &u) ||
+  if (!byte_range(U, splits, rows * ldu, rows, ldu, ldu, 4, &u) ||
       !byte_range(order, 1, 0, 1, rows, rows, 8, &in[0]) ||
       !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[1]) ||
       (scale && !byte_range(scale, 1, 0, 1, E, E, 4, &in[2])) ||
@@ -92,16 +129,17 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
   for (const Range& r : in)
     if (overlap(u, r)) return GEMMF32_ERR_ALIAS;
   AdapterArgs a{};
-  a.p.A = X, a.p.B = A, a.p.offsets = offsets, a.p.lda = ldx, a.p.ldb = lda;
-  a.p.stride_b = stride_a, a.p.rows = (int)rows, a.p.M = (int)rank, a.p.K = (int)K;
-  a.p.E = (int)E, a.p.tiles_n = splits;
-  a.order = order, a.scale = scale, a.U = U, a.splits = splits;
+  a.X = X, a.W = A, a.offsets = offsets, a.order = order, a.scale = scale, a.U = U;
+  a.ldx = ldx, a.ldw = lda, a.stride_w = stride_a;
+  a.rows = (int)rows, a.K = (int)K, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
+  a.splits = splits;
   // (a multiple of the steps that four waves take at once)
   const int64_t unit = 4 * 128 / b;
   a.k_chunk = (int)((K + splits * unit - 1) / (splits * unit) * unit);
-  const int64_t wgs = place_tiles(rows, E) * splits;
+  const int waves = down_waves(rows, E);
+  const int64_t wgs = place_tiles(rows, E, 16 * waves) * splits;
   if (!fits_grid(wgs, kDownThreads)) return GEMMF32_ERR_TOO_LARGE;
-#define DOWN(T) down_kernel<T>(rank)
+#define DOWN(T) down_kernel<T>(rank, waves)
   return launch(BY_TYPE(type, DOWN), dim3((unsigned)wgs), kDownThreads, &a, stream);
 #undef DOWN
 }
@@ -122,35 +160,39 @@ static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_
       (reads && (U == nullptr || B == nullptr)))
     return GEMMF32_ERR_NULL_PTR;
   const int b = type_bytes(type);
-  if (misaligned(order, 8) || misaligned(offsets, 4) || misaligned(U, 4) || misaligned(B, b) ||
+  if (misaligned(order, 8) || misaligned(offsets, 4) || misaligned(U, 16) || misaligned(B, b) ||
       misaligned(Y, b) || misaligned(OUT, b))
     return GEMMF32_ERR_MISALIGNED;
+  const int64_t ldu = u_columns((int)rank);
   Range o, in[5];
   if (!byte_range(OUT, 1, 0, rows, N, ldo, b, &o) ||
       !byte_range(order, 1, 0, 1, rows, rows, 8, &in[0]) ||
       !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[1]) ||
-      (reads && (!byte_range(U, splits, rows * rank, rows, rank, rank, 4, &in[2]) ||
+      (reads && (!byte_range(U, splits, rows * ldu, rows, ldu, ldu, 4, &in[2]) ||
                  !byte_range(B, E, stride_b, rank, N, ldb, b, &in[3]))) ||
       (Y && !byte_range(Y, 1, 0, rows, N, ldy, b, &in[4])))
     return GEMMF32_ERR_TOO_LARGE;
   for (const Range& r : in)
     if (overlap(o, r)) return GEMMF32_ERR_ALIAS;
   AdapterArgs a{};
-  a.p.B = B, a.p.C = OUT, a.p.offsets = offsets, a.p.ldb = ldb, a.p.ldc = ldo;
-  a.p.stride_b = stride_b, a.p.rows = (int)rows, a.p.M = reads ? (int)rank : 0, a.p.N = (int)N;
-  a.p.E = (int)E, a.p.tiles_n = (int)((N + kUpCols - 1) / kUpCols);
-  a.order = order, a.U = (float*)U, a.splits = splits, a.Y = Y, a.ldy = ldy;
+  a.W = B, a.C = OUT, a.offsets = offsets, a.order = order, a.U = (float*)U, a.Y = Y;
+  a.ldw = ldb, a.stride_w = stride_b, a.ldc = ldo, a.ldy = ldy;
+  a.rows = (int)rows, a.N = (int)N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
+  a.splits = splits, a.tiles_n = (int)((N + kUpCols - 1) / kUpCols);
+  // (rank 0: no place has an adapter)
+  if (!reads) a.E = 0;
+  const int places = up_places(rows, E, splits);
   int64_t wgs;
-  if (__builtin_mul_overflow(place_tiles(rows, E), (int64_t)a.p.tiles_n, &wgs) ||
+  if (__builtin_mul_overflow(place_tiles(rows, E, places), (int64_t)a.tiles_n, &wgs) ||
       !fits_grid(wgs, kUpThreads))
     return GEMMF32_ERR_TOO_LARGE;
-#define UP(T) &ex_adapters_up_kernel<T>
+#define UP(T) up_kernel<T>(rank, places)
   return launch(BY_TYPE(type, UP), dim3((unsigned)wgs), kUpThreads, &a, stream);
 #undef UP
 }
 
-static int64_t grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E) {
-  const int s = grad_splits(rows, N, rank, E);
+static int64_t grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
+  const int s = grad_splits(rows, N, rank, E, bytes);
   return s > 1 ? (int64_t)s * E * rank * N * 4 : 0;
 }
 
@@ -167,24 +209,25 @@ static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
   if (N == 0 || rank == 0 || E == 0) return GEMMF32_OK;
   const int b = type_bytes(type);
   const bool reads = rows > 0;
+  const int64_t ldu = u_columns((int)rank);
   Range out[2], one, in[4];
   if (D == nullptr || offsets == nullptr ||
       (reads && (order == nullptr || U == nullptr || X == nullptr)))
     return GEMMF32_ERR_NULL_PTR;
-  if (misaligned(D, b) || misaligned(X, b) || misaligned(U, 4) || misaligned(order, 8) ||
+  if (misaligned(D, b) || misaligned(X, b) || misaligned(U, 16) || misaligned(order, 8) ||
       misaligned(offsets, 4) || misaligned(workspace, 8))
     return GEMMF32_ERR_MISALIGNED;
   if (!byte_range(D, E, stride_d, rank, N, ldd, b, &out[0]) ||
       !byte_range(D, 1, 0, rank, N, ldd, b, &one) ||
       !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[0]) ||
       (reads && (!byte_range(order, 1, 0, 1, rows, rows, 8, &in[1]) ||
-                 !byte_range(U, splits, rows * rank, rows, rank, rank, 4, &in[2]) ||
+                 !byte_range(U, splits, rows * ldu, rows, ldu, ldu, 4, &in[2]) ||
                  !byte_range(X, 1, 0, rows, N, ldx, b, &in[3]))))
     return GEMMF32_ERR_TOO_LARGE;
   // each expert's D has to end where the next begins, or it would be written twice
   if (E > 1 && (stride_d < 0 || (uint64_t)stride_d * b < (uint64_t)(one.hi - one.lo)))
     return GEMMF32_ERR_BAD_LD;
-  const int64_t need = grad_workspace(rows, N, rank, E);  // (fits: D's extent does)
+  const int64_t need = grad_workspace(rows, N, rank, E, b);  // (fits: D's extent does)
   if (workspace_bytes < need) return GEMMF32_ERR_BAD_LD;
   if (need && workspace == nullptr) return GEMMF32_ERR_NULL_PTR;
   if (need && !byte_range(workspace, 1, 0, 1, need, need, 1, &out[1])) return GEMMF32_ERR_TOO_LARGE;
@@ -192,17 +235,18 @@ static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
   for (const Range& r : in)
     if (overlap(out[0], r) || overlap(out[1], r)) return GEMMF32_ERR_ALIAS;
   AdapterArgs a{};
-  a.p.A = X, a.p.C = D, a.p.offsets = offsets, a.p.lda = ldx, a.p.ldc = ldd;
-  a.p.stride_c = stride_d, a.p.rows = (int)rows, a.p.M = (int)rank, a.p.N = (int)N;
-  a.p.E = (int)E, a.p.tiles_n = (int)((N + kWaveCols - 1) / kWaveCols);
-  a.order = order, a.U = (float*)U, a.splits = splits, a.part = (float*)workspace;
-  a.row_splits = grad_splits(rows, N, rank, E);
-  const int threads = 64 * (rank <= 32 ? GradShape<1>::WAVES : GradShape<4>::WAVES);
+  a.X = X, a.C = D, a.offsets = offsets, a.order = order, a.U = (float*)U;
+  a.part = (float*)workspace, a.ldx = ldx, a.ldc = ldd, a.stride_c = stride_d;
+  a.rows = (int)rows, a.N = (int)N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
+  a.splits = splits, a.tiles_n = (int)((N + kWaveCols - 1) / kWaveCols);
+  a.row_splits = grad_splits(rows, N, rank, E, b);
+  const int fragments = grad_fragments(rank, b);
+  const int threads = 64 * (fragments <= 2 ? GradShape<1>::WAVES : GradShape<4>::WAVES);
   int64_t wgs;
-  if (__builtin_mul_overflow(grad_blocks(N, rank, E), (int64_t)a.row_splits, &wgs) ||
+  if (__builtin_mul_overflow(grad_blocks(N, rank, E, b), (int64_t)a.row_splits, &wgs) ||
       !fits_grid(wgs, threads))
     return GEMMF32_ERR_TOO_LARGE;
-#define GRAD(T) grad_kernel<T>(rank)
+#define GRAD(T) grad_kernel<T>(fragments)
   if (const int rc = launch(BY_TYPE(type, GRAD), dim3((unsigned)wgs), threads, &a, stream)) return rc;
 #undef GRAD
   if (a.row_splits == 1) return GEMMF32_OK;
@@ -248,11 +292,12 @@ int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
   return gemmlp::adapter_splits(rows, K, E);
 }
 
-int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E) {
+int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int type) {
   if (gemmlp::bad_dims(rows, N, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
   if (gemmlp::too_large(rows, N, E)) return GEMMF32_ERR_TOO_LARGE;
-  return gemmlp::grad_workspace(rows, N, rank, E);
+  if (!gemmlp::known_type(type)) return GEMMF32_ERR_BAD_TYPE;
+  return gemmlp::grad_workspace(rows, N, rank, E, gemmlp::type_bytes(type));
 }
 
 }  // extern "C"

@@ -51,20 +51,24 @@ struct Most {
   __device__ __forceinline__ X operator()(X a, X b) const { return max(a, b); }
 };
 
-// COUNT neighbouring values of a row of any alignment, the first `n` of them inside it; `fill`
-// in the place of the others.
+// COUNT neighbouring values as they are, from p on, of any alignment.
 template <class T, int COUNT>
-__device__ __forceinline__ void load_row(const typename T::type* p, int n, float fill, float* v) {
-  typedef typename T::type E;
-  typedef E group __attribute__((ext_vector_type(COUNT), aligned(sizeof(E))));
-  if (n >= COUNT) {
-    const group e = *(const group*)p;
+using Raw = typename T::type __attribute__((ext_vector_type(COUNT)));
+template <class T, int COUNT>
+__device__ __forceinline__ Raw<T, COUNT> load_raw(const typename T::type* p) {
+  typedef typename T::type any __attribute__((ext_vector_type(COUNT), aligned(sizeof(typename T::type))));
+  return *(const any*)p;
+}
+// The same for columns c .. of a row of n > 0: INSIDE where all are known to be, and otherwise one by
+// one, the row's last value in the place of those past it.  Either way without a branch, at which
+// the loads before it would have to arrive.
+template <class T, int COUNT, bool INSIDE>
+__device__ __forceinline__ Raw<T, COUNT> load_columns(const typename T::type* row, int c, int n) {
+  if constexpr (INSIDE) return load_raw<T, COUNT>(row + c);
+  Raw<T, COUNT> v;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] = (float)e[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] = i < n ? (float)p[i] : fill;
-  }
+  for (int i = 0; i < COUNT; ++i) v[i] = row[min(c + i, n - 1)];
+  return v;
 }
 
 }  // namespace gemmlp

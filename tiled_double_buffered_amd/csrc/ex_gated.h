@@ -68,6 +68,23 @@ __device__ __forceinline__ uint2 load_bytes8(const uint8_t* p, int n) {
   return q;
 }
 
+// load8 of several rows, all of them under way together: one branch for all, as the loads before a
+// branch have to arrive at it.
+template <class T, class P, class V>
+__device__ __forceinline__ void load8_each(int n, P p, V v) {
+  load8<T>(p, n, v);
+}
+template <class T, class P, class V, class... More>
+__device__ __forceinline__ void load8_each(int n, P p, V v, More... more) {
+  load8<T>(p, n, v);
+  load8_each<T>(n, more...);
+}
+template <class T, class... PV>
+__device__ __forceinline__ void load8s(int n, PV... pv) {
+  if (n >= 8) load8_each<T>(8, pv...);
+  else load8_each<T>(n, pv...);
+}
+
 // Which row, block and first column a thread has; false past the end (for whole 16 lanes).
 __device__ __forceinline__ bool block_at(int rows, int cols, int& row, int& block, int& c) {
   const int kb = (cols + kBlock - 1) / kBlock;
@@ -92,8 +109,7 @@ __global__ __launch_bounds__(256) void ex_gated_kernel(GatedArgs p) {
   const int n = p.N - c;
   const typename T::type* x = (const typename T::type*)p.X + row * p.ldx + c;
   float g[8], u[8], h[8];
-  load8<T>(x, n, g);
-  load8<T>(x + p.N, n, u);
+  load8s<T>(n, x, g, x + p.N, u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float s, rest;
@@ -120,17 +136,25 @@ __global__ __launch_bounds__(256) void ex_gated_grad_kernel(GatedArgs p) {
   if (!block_at(p.rows, p.N, row, block, c)) return;
   const int n = p.N - c;
   float g[8], u[8], dh[8];
+  const typename T::type* d = (const typename T::type*)p.DH + row * p.lddh + c;
   if constexpr (KEEP) {
     const uint8_t* q = p.Q + row * p.ldq + c;
     const float* s = p.S + row * p.lds + block;
-    from_fp8x8(load_bytes8(q, n), s[0], g);
-    from_fp8x8(load_bytes8(q + p.N, n), s[(p.N + kBlock - 1) / kBlock], u);
+    const float sg = s[0], su = s[(p.N + kBlock - 1) / kBlock];
+    uint2 qg, qu;
+    if (n >= 8) {
+      qg = load_bytes8(q, 8), qu = load_bytes8(q + p.N, 8);
+      load8<T>(d, 8, dh);
+    } else {
+      qg = load_bytes8(q, n), qu = load_bytes8(q + p.N, n);
+      load8<T>(d, n, dh);
+    }
+    from_fp8x8(qg, sg, g);
+    from_fp8x8(qu, su, u);
   } else {
     const typename T::type* x = (const typename T::type*)p.X + row * p.ldx + c;
-    load8<T>(x, n, g);
-    load8<T>(x + p.N, n, u);
+    load8s<T>(n, x, g, x + p.N, u, d, dh);
   }
-  load8<T>((const typename T::type*)p.DH + row * p.lddh + c, n, dh);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float s, rest;

@@ -52,18 +52,23 @@ __device__ __forceinline__ int column(int lane, int v) {
   if constexpr (V == 1) return lane;
   return ((v / 4) * L + lane) * 4 + v % 4;
 }
+// A lane's logits of a row, -Inf past the last: wide loads where groups of four end with the row.
 template <class T, int L, int V>
 __device__ __forceinline__ void load_logits(const void* X, int64_t at, int E, int lane, float* x) {
   const typename T::type* row = (const typename T::type*)X + at;
-  if constexpr (V == 1) {
-    x[0] = lane < E ? (float)row[lane] : -__builtin_inff();
+  if (V > 1 && E % 4 == 0) {
+    Raw<T, 4> r[(V + 3) / 4];
+#pragma unroll
+    for (int q = 0; q < V; q += 4)
+      r[q / 4] = load_raw<T, 4>(row + min(column<L, V>(lane, q), E - 4));
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = (float)r[v / 4][v % 4];
   } else {
 #pragma unroll
-    for (int q = 0; q < V; q += 4) {
-      const int c = column<L, V>(lane, q);
-      load_row<T, 4>(row + c, E - c, -__builtin_inff(), x + q);
-    }
+    for (int v = 0; v < V; ++v) x[v] = (float)row[min(column<L, V>(lane, v), E - 1)];
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = column<L, V>(lane, v) < E ? x[v] : -__builtin_inff();
 }
 
 // x becomes its softmax's numerators, over the largest; returns one over their sum.

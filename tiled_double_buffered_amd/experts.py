@@ -40,7 +40,7 @@ SIGNATURES = {
     "gemm_adapters_grad": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _vp,
                                   _i64, _i64, _vp, _i64, _int, _vp]),
     "gemm_adapters_splits": (_int, [_i64, _i64, _i64, _i64]),
-    "gemm_adapters_grad_workspace": (_i64, [_i64, _i64, _i64, _i64]),
+    "gemm_adapters_grad_workspace": (_i64, [_i64, _i64, _i64, _i64, _int]),
     "gemm_gated": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
     "gemm_gated_grad": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                                _int, _vp]),
@@ -98,8 +98,8 @@ def gemm_adapters_splits(rows, K, rank, E) -> int:
     return load().gemm_adapters_splits(rows, K, rank, E)
 
 
-def gemm_adapters_grad_workspace(rows, N, rank, E) -> int:
-    return load().gemm_adapters_grad_workspace(rows, N, rank, E)
+def gemm_adapters_grad_workspace(rows, N, rank, E, type_code) -> int:
+    return load().gemm_adapters_grad_workspace(rows, N, rank, E, type_code)
 
 
 def gemm_gated(*args) -> int:
@@ -282,14 +282,15 @@ def _plan(order, offsets, rows, E, like):
 
 
 def _down(x, a, order, offsets, scale):
-    """u: splits x rows x rank, the contraction of x's rows with their adapter's."""
+    """u: the contraction of x's rows with their adapter's, as partial sums by place."""
     px, ldx = _matrix(x, "x", TYPES)
     pa, lda, step = _stack(a, "a", (x.dtype,))
     rows, K = x.shape
     E, rank = a.shape[:2]
     po, pf = _plan(order, offsets, rows, E, x)
     splits = _size(load().gemm_adapters_splits(rows, K, rank, E), "gemm_adapters_splits")
-    u = torch.empty((splits, rows, rank), dtype=torch.float32, device=x.device)
+    # (whole fragments of 16, the columns past the rank zeros)
+    u = torch.empty((splits, rows, (rank + 15) // 16 * 16), dtype=torch.float32, device=x.device)
     _check(load().gemm_adapters_down(rows, K, rank, E, po, pf, px, max(ldx, K), pa, max(lda, K),
                                      step, _pointer(scale), u.data_ptr(), splits, TYPES[x.dtype],
                                      _current(x)), "gemm_adapters_down")
@@ -298,9 +299,9 @@ def _down(x, a, order, offsets, scale):
 
 def _up(u, b, y, order, offsets):
     """y + u b of each row's adapter; y None for 0."""
-    splits, rows, rank = u.shape
+    splits, rows, _ = u.shape
     pb, ldb, step = _stack(b, "b", TYPES)
-    E, _, N = b.shape
+    E, rank, N = b.shape
     po, pf = _plan(order, offsets, rows, E, b)
     py, ldy = (None, 0) if y is None else _matrix(y, "y", (b.dtype,))
     out = torch.empty((rows, N), dtype=b.dtype, device=b.device)
@@ -310,14 +311,14 @@ def _up(u, b, y, order, offsets):
     return out
 
 
-def _adapter_grad(u, x, E, order, offsets):
+def _adapter_grad(u, rank, x, E, order, offsets):
     """E x rank x N: u^T x over each adapter's rows."""
-    splits, rows, rank = u.shape
+    splits, rows, _ = u.shape
     px, ldx = _matrix(x, "x", TYPES)
     N = x.shape[1]
     po, pf = _plan(order, offsets, rows, E, x)
     d = torch.empty((E, rank, N), dtype=x.dtype, device=x.device)
-    need = _size(load().gemm_adapters_grad_workspace(rows, N, rank, E),
+    need = _size(load().gemm_adapters_grad_workspace(rows, N, rank, E, TYPES[x.dtype]),
                  "gemm_adapters_grad_workspace")
     hold, pw = _workspace(need, x.device)
     _check(load().gemm_adapters_grad(rows, N, rank, E, po, pf, u.data_ptr(), splits, px,
@@ -334,7 +335,7 @@ class _Adapters(torch.autograd.Function):
         ctx.save_for_backward(x if need_a else None, a if need_x else None,
                               b if need_x or need_a else None, u if need_b else None, order,
                               offsets, scale)
-        ctx.experts = a.shape[0]
+        ctx.size = a.shape[:2]
         return _up(u, b, y, order, offsets)
 
     @staticmethod
@@ -342,14 +343,15 @@ class _Adapters(torch.autograd.Function):
     def backward(ctx, dout):
         need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
         x, a, b, u, order, offsets, scale = ctx.saved_tensors
+        E, rank = ctx.size
         dx = da = db = None
         if need_x or need_a or need_b:
             rows = _row_major(dout)
             if need_x or need_a:
                 v = _down(rows, b, order, offsets, scale)
                 dx = _up(v, a, None, order, offsets) if need_x else None
-                da = _adapter_grad(v, x, ctx.experts, order, offsets) if need_a else None
-            db = _adapter_grad(u, rows, ctx.experts, order, offsets) if need_b else None
+                da = _adapter_grad(v, rank, x, E, order, offsets) if need_a else None
+            db = _adapter_grad(u, rank, rows, E, order, offsets) if need_b else None
         return dout if need_y else None, dx, da, db, None, None, None
 
 
