@@ -16,7 +16,7 @@ import torch
 
 from . import _binding
 from .lowp import (BLOCK, TYPES, _F8, _blocks, _check, _current, _here, _matrix, _names, _offsets,
-                   _on, _out_type, _row_major, _rows16, _same_device, _stack)
+                   _on, _once, _out_type, _row_major, _rows16, _same_device)
 
 MAX_EXPERTS = 1024         # of a router; GEMM_ROUTE_MAX_EXPERTS
 MAX_CHOSEN = 16            # GEMM_ROUTE_MAX_CHOSEN
@@ -171,24 +171,23 @@ class _Route(torch.autograd.Function):
     def forward(ctx, logits, k, valid, renormalize):
         gates, experts, counts, sums, loss = _route(logits, k, valid, renormalize)
         ctx.save_for_backward(logits, valid, gates, experts, counts, sums)
-        ctx.k, ctx.renormalize = k, renormalize
+        ctx.k, ctx.renormalize = k, 1 if renormalize else 0
         ctx.mark_non_differentiable(experts, counts)
         ctx.set_materialize_grads(False)
         return gates, experts, counts, loss
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dgates, dexperts, dcounts, dloss):
         logits, valid, gates, experts, counts, sums = ctx.saved_tensors
         rows, E = logits.shape
-        px, ldx = _matrix(logits, "logits", TYPES)
         dgates = None if dgates is None else dgates.contiguous()
-        dx = torch.empty((rows, E), dtype=logits.dtype, device=logits.device)
-        _check(load().gemm_route_grad(rows, E, ctx.k, px, max(ldx, E), TYPES[logits.dtype],
-                                      _pointer(valid), 1 if ctx.renormalize else 0,
-                                      gates.data_ptr(), experts.data_ptr(), counts.data_ptr(),
-                                      sums.data_ptr(), _pointer(dgates), _pointer(dloss),
-                                      dx.data_ptr(), E, _current(logits)), "gemm_route_grad")
+        dx = logits.new_empty((rows, E))
+        _check(load().gemm_route_grad(
+            rows, E, ctx.k, logits.data_ptr(), max(logits.stride(0), E), TYPES[logits.dtype],
+            _pointer(valid), ctx.renormalize, gates.data_ptr(), experts.data_ptr(),
+            counts.data_ptr(), sums.data_ptr(), _pointer(dgates), _pointer(dloss), dx.data_ptr(), E,
+            _current(logits)), "gemm_route_grad")
         return dx, None, None, None
 
 
@@ -269,61 +268,54 @@ def group_rows(experts, count, stream=None):
 
 
 # --------------------------------------------------------------------------------- adapters
-def _plan(order, offsets, rows, E, like):
-    """(order's pointer, offsets' pointer)."""
-    if not isinstance(order, torch.Tensor) or order.dim() != 1 or order.dtype != torch.int64 or \
-            (order.numel() > 1 and order.stride(0) != 1):
-        raise TypeError("order must be a contiguous 1-D int64 tensor")
-    if order.numel() != rows:
-        raise ValueError(f"order has {order.numel()} elements for {rows} rows")
-    if order.device != like.device:
-        raise ValueError("order must live on the operands' GPU")
-    return order.data_ptr(), _offsets(offsets, like, E)[0]
+# (operands that `add_adapters` has checked: row-major with unit column stride)
+def _ld(t):
+    """The row stride of a 2-D tensor (of a stack: of its matrices); of one row, any will do."""
+    return max(t.stride(-2), t.shape[-1], 1)
 
 
 def _down(x, a, order, offsets, scale):
     """u: the contraction of x's rows with their adapter's, as partial sums by place."""
-    px, ldx = _matrix(x, "x", TYPES)
-    pa, lda, step = _stack(a, "a", (x.dtype,))
     rows, K = x.shape
     E, rank = a.shape[:2]
-    po, pf = _plan(order, offsets, rows, E, x)
-    splits = _size(load().gemm_adapters_splits(rows, K, rank, E), "gemm_adapters_splits")
+    lib = load()
+    splits = lib.gemm_adapters_splits(rows, K, rank, E)
+    if splits < 0:
+        _check(splits, "gemm_adapters_splits")
     # (whole fragments of 16, the columns past the rank zeros)
     u = torch.empty((splits, rows, (rank + 15) // 16 * 16), dtype=torch.float32, device=x.device)
-    _check(load().gemm_adapters_down(rows, K, rank, E, po, pf, px, max(ldx, K), pa, max(lda, K),
-                                     step, _pointer(scale), u.data_ptr(), splits, TYPES[x.dtype],
-                                     _current(x)), "gemm_adapters_down")
+    _check(lib.gemm_adapters_down(rows, K, rank, E, order.data_ptr(), offsets.data_ptr(),
+                                  x.data_ptr(), _ld(x), a.data_ptr(), _ld(a), a.stride(0),
+                                  _pointer(scale), u.data_ptr(), splits, TYPES[x.dtype],
+                                  _current(x)), "gemm_adapters_down")
     return u
 
 
 def _up(u, b, y, order, offsets):
     """y + u b of each row's adapter; y None for 0."""
-    splits, rows, _ = u.shape
-    pb, ldb, step = _stack(b, "b", TYPES)
     E, rank, N = b.shape
-    po, pf = _plan(order, offsets, rows, E, b)
-    py, ldy = (None, 0) if y is None else _matrix(y, "y", (b.dtype,))
-    out = torch.empty((rows, N), dtype=b.dtype, device=b.device)
-    _check(load().gemm_adapters_up(rows, N, rank, E, po, pf, u.data_ptr(), splits, pb,
-                                   max(ldb, N), step, py, max(ldy, N), out.data_ptr(), max(N, 1),
-                                   TYPES[b.dtype], _current(b)), "gemm_adapters_up")
+    rows = u.shape[1]
+    out = b.new_empty((rows, N))
+    py, ldy = (None, 0) if y is None else (y.data_ptr(), _ld(y))
+    _check(load().gemm_adapters_up(rows, N, rank, E, order.data_ptr(), offsets.data_ptr(),
+                                   u.data_ptr(), u.shape[0], b.data_ptr(), _ld(b), b.stride(0), py,
+                                   ldy, out.data_ptr(), max(N, 1), TYPES[b.dtype], _current(b)),
+           "gemm_adapters_up")
     return out
 
 
 def _adapter_grad(u, rank, x, E, order, offsets):
     """E x rank x N: u^T x over each adapter's rows."""
-    splits, rows, _ = u.shape
-    px, ldx = _matrix(x, "x", TYPES)
-    N = x.shape[1]
-    po, pf = _plan(order, offsets, rows, E, x)
-    d = torch.empty((E, rank, N), dtype=x.dtype, device=x.device)
-    need = _size(load().gemm_adapters_grad_workspace(rows, N, rank, E, TYPES[x.dtype]),
+    rows, N = x.shape
+    lib, code = load(), TYPES[x.dtype]
+    d = x.new_empty((E, rank, N))
+    need = _size(lib.gemm_adapters_grad_workspace(rows, N, rank, E, code),
                  "gemm_adapters_grad_workspace")
     hold, pw = _workspace(need, x.device)
-    _check(load().gemm_adapters_grad(rows, N, rank, E, po, pf, u.data_ptr(), splits, px,
-                                     max(ldx, N), d.data_ptr(), max(N, 1), rank * N, pw, need,
-                                     TYPES[x.dtype], _current(x)), "gemm_adapters_grad")
+    _check(lib.gemm_adapters_grad(rows, N, rank, E, order.data_ptr(), offsets.data_ptr(),
+                                  u.data_ptr(), u.shape[0], x.data_ptr(), _ld(x), d.data_ptr(),
+                                  max(N, 1), rank * N, pw, need, code, _current(x)),
+           "gemm_adapters_grad")
     return d
 
 
@@ -339,7 +331,7 @@ class _Adapters(torch.autograd.Function):
         return _up(u, b, y, order, offsets)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dout):
         need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
         x, a, b, u, order, offsets, scale = ctx.saved_tensors
@@ -367,14 +359,13 @@ def add_adapters(y, x, a, b, order, offsets, scale=None):
     The contraction over K is kept in float32; all sums are, and are rounded once.
 
     Differentiable in y, x, a and b; adapters without rows get zeros."""
-    for name, t in (("y", y), ("x", x)):
-        if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.dtype not in TYPES:
-            raise TypeError(f"{name} must be a tensor of {_names(TYPES)}")
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in TYPES:
+        raise TypeError(f"x must be a tensor of {_names(TYPES)}")
+    if not isinstance(y, torch.Tensor) or y.dim() < 1 or y.dtype != x.dtype:
+        raise TypeError("y must be a tensor of x's type")
     for name, t in (("a", a), ("b", b)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != x.dtype:
             raise TypeError(f"{name} must be a 3-D tensor of x's type")
-    if y.dtype != x.dtype:
-        raise TypeError(f"x is {x.dtype}, y {y.dtype}")
     E, rank, K = a.shape
     N = b.shape[2]
     if tuple(b.shape[:2]) != (E, rank):
@@ -397,8 +388,14 @@ def add_adapters(y, x, a, b, order, offsets, scale=None):
     if not x.is_cuda:
         raise ValueError("x must live on the GPU (the library takes device pointers)")
     rows, base = _row_major(_flat(x)), _row_major(_flat(y))
-    a, b = _unit_columns(a), _unit_columns(b)
-    args = (base, rows, a, b, order, offsets, scale)
+    if not isinstance(order, torch.Tensor) or order.dim() != 1 or order.dtype != torch.int64 or \
+            (order.numel() > 1 and order.stride(0) != 1):
+        raise TypeError("order must be a contiguous 1-D int64 tensor")
+    if order.shape[0] != rows.shape[0]:
+        raise ValueError(f"order has {order.shape[0]} elements for {rows.shape[0]} rows")
+    _same_device(x, order)
+    _offsets(offsets, x, E)
+    args = base, rows, _unit_columns(a), _unit_columns(b), order, offsets, scale
     if _here(x, None):
         out = _adapted(*args)
     else:
@@ -425,7 +422,7 @@ def _gated(x, keep):
     """(h, q, s): q and s None where nothing is kept."""
     px, ldx = _matrix(x, "x", TYPES)
     rows, N = x.shape[0], x.shape[1] // 2
-    h = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+    h = x.new_empty((rows, N))
     q = s = pq = ps = None
     ldq = lds = 0
     if keep:
@@ -446,19 +443,20 @@ class _Gated(torch.autograd.Function):
         return h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dh):
         x, q, s = ctx.saved_tensors
         dh = _row_major(dh)
-        pd, ldd = _matrix(dh, "dh", TYPES)
         rows, N = dh.shape
-        dx = torch.empty((rows, 2 * N), dtype=dh.dtype, device=dh.device)
+        dx = dh.new_empty((rows, 2 * N))
         if rows and N:
-            px, ldx = (None, 0) if x is None else _matrix(x, "x", TYPES)
-            _check(load().gemm_gated_grad(
-                rows, N, px, max(ldx, 2 * N), _pointer(q), 0 if q is None else max(q.stride(0), 1),
-                _pointer(s), 0 if s is None else max(s.shape[1], 1), pd, max(ldd, N),
-                dx.data_ptr(), 2 * N, TYPES[dh.dtype], _current(dh)), "gemm_gated_grad")
+            ldd = max(dh.stride(0), N)  # (of one row, any)
+            if x is None:
+                kept = None, 0, q.data_ptr(), q.stride(0), s.data_ptr(), s.shape[1]
+            else:
+                kept = x.data_ptr(), max(x.stride(0), 2 * N), None, 0, None, 0
+            _check(load().gemm_gated_grad(rows, N, *kept, dh.data_ptr(), ldd, dx.data_ptr(), 2 * N,
+                                          TYPES[dh.dtype], _current(dh)), "gemm_gated_grad")
         return dx, None
 
 

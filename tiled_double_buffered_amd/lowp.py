@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -429,6 +430,17 @@ def _fp8_exp(a, sa, b, sb, M, N, K, dtype):
     return c
 
 
+def _once(backward):
+    """torch's once_differentiable, which refuses a second derivative, without its cost (7 us) where
+    no graph of the backward pass is asked for."""
+    checked = torch.autograd.function.once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        return (checked if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return call
+
+
 class _LinearFp8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, grads):
@@ -440,7 +452,7 @@ class _LinearFp8(torch.autograd.Function):
         return _fp8_exp(q, s, wq, ws, *ctx.sizes, x.dtype)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
         qt, st, wqt, wst = ctx.saved_tensors
@@ -495,7 +507,7 @@ class _LinearGrouped(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
         x, q, s, w, offsets = ctx.saved_tensors
