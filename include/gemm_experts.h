@@ -82,7 +82,9 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  *
  * down: U[p] = scale[e] X[order[p]] A_e^T for the places p of e, in FP32, as `splits` partial sums
  *   over K, each rows x 16 ceil(rank / 16) with zeros past the rank, one after another and 16-byte
- *   aligned (places of no expert are left as they were).  scale may be NULL (1).
+ *   aligned (places of no expert are left as they were).  scale may be NULL (1).  With `join` the
+ *   first holds their sum in the end (of places of no expert what it may), so that `up` and `grad`
+ *   take it as one split: for many rows, as they read U several times.
  * up: OUT[order[p]] = Y[order[p]] + (sum of U's splits)[p] B_e; places of no expert: Y alone.
  *   Y may be NULL (0).
  * grad: D_e (rank x N, row stride ldd, stride_d elements apart) = sum over the places p of e of
@@ -92,7 +94,7 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
 int gemm_adapters_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t *order,
                        const int32_t *offsets, const void *X, int64_t ldx, const void *A,
                        int64_t lda, int64_t stride_a, const float *scale, float *U, int splits,
-                       int type, void *stream);
+                       int join, int type, void *stream);
 int gemm_adapters_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_t *order,
                      const int32_t *offsets, const float *U, int splits, const void *B,
                      int64_t ldb, int64_t stride_b, const void *Y, int64_t ldy, void *OUT,

@@ -386,7 +386,7 @@ def test_adapters_rows_behind_are_left():
     stream = torch.cuda.current_stream().cuda_stream
     u = torch.full((2, T, 16), 7.0, device=DEV)
     rc = tdb.gemm_adapters_down(T, K, r, E, order.data_ptr(), offsets.data_ptr(), x.data_ptr(), K,
-                                a.data_ptr(), K, r * K, s.data_ptr(), u.data_ptr(), 2, 0, stream)
+                                a.data_ptr(), K, r * K, s.data_ptr(), u.data_ptr(), 2, 0, 0, stream)
     assert rc == tdb.OK and (u[:, 13:] == 7).all() and (u[:, :13] != 7).all()
     assert (u[:, :13, r:] == 0).all()
     out = torch.full((T + 1, N + 3), 7.0, dtype=torch.bfloat16, device=DEV)

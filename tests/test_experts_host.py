@@ -95,9 +95,9 @@ def test_group_refusals(change, code):
 
 
 def _down(rows=4, K=64, r=8, E=2, order=P[0], off=P[1], X=P[2], ldx=64, A=P[3], lda=64, sA=512,
-          scale=P[4], U=P[5], splits=1, t=BF16):
+          scale=P[4], U=P[5], splits=1, join=0, t=BF16):
     return tdb.gemm_adapters_down(rows, K, r, E, order, off, X, ldx, A, lda, sA, scale, U, splits,
-                                  t, None)
+                                  join, t, None)
 
 
 @pytest.mark.parametrize("change, code", [

@@ -27,14 +27,14 @@ struct AdapterArgs {
   const float* scale;
   const void* Y;
   float* U;              // [split][place][ldu], zeros past the rank
-  float* part;           // grad: [split of rows][E][rank][N], where there are several
+  float* part;           // grad: [tile][rank][N] of the adapters with several tiles
   int64_t ldx, ldw, stride_w, ldc, stride_c, ldy;
   int rows, N, K, E;
   int rank, ldu;
   int splits;            // of U
   int tiles_n;           // up, grad: blocks of columns
   int k_chunk;           // down: columns of a split
-  int row_splits;        // grad
+  int run, runs;         // grad: places of a run, and how many runs `part` has room for
 };
 
 // The columns of U: whole fragments of 16, so that its loads need no bounds.
@@ -60,32 +60,36 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// The places of tile `id` of BM: adapter e's are offsets[e] .. offsets[e+1] - 1, and -1 has those
-// before the first and from the last on.  Every wave looks for itself, 64 groups at a time (E of
-// them and the two of none); false past the last tile.
+// The places of tile `id` of bm: adapter e's are offsets[e] .. offsets[e+1] - 1, and -1 has those
+// before the first and from the last on.  Every wave looks for itself, 64 groups at a time; false
+// past the last tile.  NONE: with the places of no adapter; otherwise of the adapters alone, one
+// tile at least of each.
 struct Places {
   int e, first, end;
+  int tile, tiles;  // which of its adapter's, and how many that has
 };
-template <int BM>
-__device__ inline bool find_places(const AdapterArgs& a, int id, Places& t) {
-  const int lane = threadIdx.x & 63, groups = a.E + 2;
+template <bool NONE>
+__device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places& t) {
+  const int lane = threadIdx.x & 63, groups = NONE ? a.E + 2 : a.E;
   for (int base = 0; base < groups; base += 64) {
-    const int g = base + lane;
-    int lo = 0, hi = 0;
-    if (g < groups) {
-      lo = g == 0 ? 0 : clamped_offset(a.offsets, g - 1, a.rows);
-      hi = g == groups - 1 ? a.rows : clamped_offset(a.offsets, g, a.rows);
-    }
-    const int tiles = (max(hi - lo, 0) + BM - 1) / BM;
+    // group g: from edge g to edge g + 1, of which the adapters have 0 .. E
+    const int g = min(base + lane, groups - 1) - (NONE ? 1 : 0);
+    int lo = clamped_offset(a.offsets, max(g, 0), a.rows);
+    int hi = clamped_offset(a.offsets, min(g + 1, a.E), a.rows);
+    if (NONE && g < 0) lo = 0;
+    if (NONE && g >= a.E) hi = a.rows;
+    hi = max(hi, lo);
+    const int tiles = base + lane < groups ? max((hi - lo + bm - 1) / bm, NONE ? 0 : 1) : 0;
     const int upto = wave_scan(tiles);
     const uint64_t past = __ballot(upto > id);
     if (past) {
       const int l = __builtin_ctzll(past);
-      const int found = base + l;
-      t.e = found == 0 || found == groups - 1 ? -1 : found - 1;
-      t.first = __builtin_amdgcn_readlane(lo, l) +
-                (id - __builtin_amdgcn_readlane(upto - tiles, l)) * BM;
-      t.end = min(__builtin_amdgcn_readlane(hi, l), t.first + BM);
+      t.e = __builtin_amdgcn_readlane(g, l);
+      if (NONE && t.e >= a.E) t.e = -1;
+      t.tiles = __builtin_amdgcn_readlane(tiles, l);
+      t.tile = id - (__builtin_amdgcn_readlane(upto, l) - t.tiles);
+      t.first = __builtin_amdgcn_readlane(lo, l) + t.tile * bm;
+      t.end = min(__builtin_amdgcn_readlane(hi, l), t.first + bm);
       return true;
     }
     id -= __builtin_amdgcn_readlane(upto, 63);
@@ -103,10 +107,29 @@ __device__ __forceinline__ float4v mma32(float a, float b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// The operands' wide axis has kLeastWide columns at least (the kernels of fewer are at the end), so
+// that a load of as many can always be moved back into the row.
+constexpr int kLeastWide = 8;
+
 // ------------------------------------------------------------------------------------ down
-// u of 16 RW places and one split of K: RW waves have 16 places each, and 4 / RW share each wave's
-// steps of K and add up through LDS.  The instruction's rows are the rank, its columns the places.
-// RF: fragments of 16 of the rank.
+// Columns c .. of a row, zeros from `end` on.
+template <class T, int COUNT>
+__device__ __forceinline__ Raw<T, COUNT> load_end(const typename T::type* row, int c, int end) {
+  const int at = min(c, end - COUNT), back = c - at;
+  const Raw<T, COUNT> v = load_raw<T, COUNT>(row + at);
+  Raw<T, COUNT> o;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) {
+    o[i] = (typename T::type)0.0f;
+#pragma unroll
+    for (int j = i; j < COUNT; ++j)
+      if (j - i == back) o[i] = v[j];
+  }
+  return o;
+}
+
+// u of 16 places and one split of K, whose steps four waves share; they add up through LDS.  The
+// instruction's rows are the rank, its columns the places.  RF: fragments of 16 of the rank.
 //
 // A step is 128 bytes of every row, loaded by eight neighbouring lanes, and turned into fragments by
 // a tile of LDS of the wave's own, so that no barrier is needed: one wave's LDS instructions run in
@@ -120,95 +143,89 @@ constexpr int kDownDeep = RF == 1 ? 6 : RF == 2 ? 4 : RF == 4 ? 3 : 2;
 __device__ __forceinline__ int group_at(int row, int c) {  // of 16 bytes, in the wave's tile
   return row * 8 + (c ^ ((row >> 1) & 7));
 }
-template <class T, int RF, int RW>
+template <class T, int RF>
 __global__ __launch_bounds__(kDownThreads) void ex_adapters_down_kernel(AdapterArgs a) {
   constexpr int PER = 16 / T::BYTES, STEP = kRowBytes / T::BYTES;
-  constexpr int LD = RF * 16 + 4, KW = 4 / RW, DEEP = kDownDeep<RF>, ROWS = 2 * (1 + RF);
+  constexpr int LD = RF * 16 + 4, KW = 4, DEEP = kDownDeep<RF>, ROWS = 2 * (1 + RF);
   __shared__ int4v tile[4][ROWS * 8 * 8];
   using Vec = Raw<T, PER>;
   Places t;
   const int split = blockIdx.x % a.splits;
-  if (!find_places<16 * RW>(a, blockIdx.x / a.splits, t) || t.e < 0) return;
+  if (!find_places<true>(a, 16, blockIdx.x / a.splits, t) || t.e < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
-  const int place0 = t.first + 16 * (wave % RW), part = wave / RW;
+  const int part = wave;
   int4v* const mine = tile[wave];
   float4v acc[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) acc[f] = float4v{0, 0, 0, 0};
-  if (place0 < t.end) {
-    // the rows that this lane loads of: two of the places', then two of each fragment's
-    const int r8 = lane >> 3, c8 = lane & 7;
-    const typename T::type* from[ROWS];
+  // the rows that this lane loads of: two of the places', then two of each fragment's
+  const int r8 = lane >> 3, c8 = lane & 7;
+  const typename T::type* from[ROWS];
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j)
+    from[j] = (j < 2 ? (const typename T::type*)a.X +
+                           row_at(a, min(t.first + 8 * j + r8, t.end - 1)) * a.ldx
+                     : (const typename T::type*)a.W + t.e * a.stride_w +
+                           min(8 * (j - 2) + r8, a.rank - 1) * a.ldw) + c8 * PER;
+  const int first = (int)min((int64_t)split * a.k_chunk, (int64_t)a.K);
+  const int end = first + min(a.k_chunk, a.K - first);
+  Vec v[DEEP][ROWS];
+  const int whole = (end - first) / STEP;  // steps of all waves; this one has every KW-th
+  const int n = (whole - part + KW - 1) / KW;
+  auto load = [&](int d, int i) {
+    const int k = first + (part + i * KW) * STEP;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) v[d][j] = load_raw<T, PER>(from[j] + k);
+  };
+  auto multiply = [&](int d) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j)
-      from[j] = (j < 2 ? (const typename T::type*)a.X +
-                             row_at(a, min(place0 + 8 * j + r8, t.end - 1)) * a.ldx
-                       : (const typename T::type*)a.W + t.e * a.stride_w +
-                             min(8 * (j - 2) + r8, a.rank - 1) * a.ldw) + c8 * PER;
-    const int first = (int)min((int64_t)split * a.k_chunk, (int64_t)a.K);
-    const int end = first + min(a.k_chunk, a.K - first);
-    Vec v[DEEP][ROWS];
-    const int whole = (end - first) / STEP;  // steps of all waves; this one has every KW-th
-    const int n = (whole - part + KW - 1) / KW;
-    auto load = [&](int d, int i) {
-      const int k = first + (part + i * KW) * STEP;
+      mine[group_at(8 * j + r8, c8)] = __builtin_bit_cast(int4v, v[d][j]);
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j) v[d][j] = load_raw<T, PER>(from[j] + k);
-    };
-    auto multiply = [&](int d) {
+    for (int h = 0; h < 2; ++h) {
+      const Vec x = __builtin_bit_cast(Vec, mine[group_at(l16, g + 4 * h)]);
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j)
-        mine[group_at(8 * j + r8, c8)] = __builtin_bit_cast(int4v, v[d][j]);
-      __builtin_amdgcn_wave_barrier();
+      for (int f = 0; f < RF; ++f) {
+        const Vec w = __builtin_bit_cast(Vec, mine[group_at(16 * (f + 1) + l16, g + 4 * h)]);
+        if constexpr (T::BYTES == 4) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Vec x = __builtin_bit_cast(Vec, mine[group_at(l16, g + 4 * h)]);
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-          const Vec w = __builtin_bit_cast(Vec, mine[group_at(16 * (f + 1) + l16, g + 4 * h)]);
-          if constexpr (T::BYTES == 4) {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) acc[f] = mma32(w[j], x[j], acc[f]);
-          } else {
-            acc[f] = mma16(w, x, acc[f]);
-          }
+          for (int j = 0; j < PER; ++j) acc[f] = mma32(w[j], x[j], acc[f]);
+        } else {
+          acc[f] = mma16(w, x, acc[f]);
         }
       }
-      __builtin_amdgcn_wave_barrier();
-    };
-    int i = 0;
-    if (n >= DEEP) {
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  int i = 0;
+  if (n >= DEEP) {
 #pragma unroll
-      for (int d = 0; d < DEEP; ++d) load(d, d);
-      for (; i + 2 * DEEP <= n; i += DEEP) {
+    for (int d = 0; d < DEEP; ++d) load(d, d);
+    for (; i + 2 * DEEP <= n; i += DEEP) {
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d) {
-          multiply(d);
-          load(d, i + DEEP + d);
-        }
+      for (int d = 0; d < DEEP; ++d) {
+        multiply(d);
+        load(d, i + DEEP + d);
       }
-#pragma unroll
-      for (int d = 0; d < DEEP; ++d) multiply(d);
-      i += DEEP;
     }
 #pragma unroll
-    for (int d = 0; d < DEEP - 1; ++d)
-      if (i + d < n) load(d, i + d);
+    for (int d = 0; d < DEEP; ++d) multiply(d);
+    i += DEEP;
+  }
 #pragma unroll
-    for (int d = 0; d < DEEP - 1; ++d)
-      if (i + d < n) multiply(d);
-    // the columns past the last whole step, by the wave whose turn it is
-    const int rest = first + whole * STEP;
-    if (rest < end && whole % KW == part) {
+  for (int d = 0; d < DEEP - 1; ++d)
+    if (i + d < n) load(d, i + d);
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-        v[0][j] = load_columns<T, PER, false>(from[j] - c8 * PER, rest + c8 * PER, end);
+  for (int d = 0; d < DEEP - 1; ++d)
+    if (i + d < n) multiply(d);
+  // the columns past the last whole step, by the wave whose turn it is
+  const int rest = first + whole * STEP;
+  if (rest < end && whole % KW == part) {
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-          v[0][j][k] = rest + c8 * PER + k < end ? v[0][j][k] : (typename T::type)0.0f;
-      }
-      multiply(0);
-    }
+    for (int j = 0; j < ROWS; ++j)
+      v[0][j] = load_end<T, PER>(from[j] - c8 * PER, rest + c8 * PER, end);
+    multiply(0);
   }
   // (a wave's sums lie where its tile was)
   static_assert(16 * LD * 4 <= ROWS * 8 * kRowBytes, "the sums fit into the tile");
@@ -217,17 +234,150 @@ __global__ __launch_bounds__(kDownThreads) void ex_adapters_down_kernel(AdapterA
   __syncthreads();
   const float s = a.scale != nullptr ? a.scale[t.e] : 1.0f;
   float* u = a.U + (int64_t)split * a.rows * a.ldu;
-  for (int i = tid; i < RW * 16 * RF * 4; i += kDownThreads) {
+  for (int i = tid; i < 16 * RF * 4; i += kDownThreads) {
     const int row = i / (RF * 4), r = i % (RF * 4) * 4;
-    float4v v = *(const float4v*)((const float*)tile[row / 16] + row % 16 * LD + r);
+    float4v v = *(const float4v*)((const float*)tile[0] + row * LD + r);
 #pragma unroll
-    for (int q = 1; q < KW; ++q)
-      v += *(const float4v*)((const float*)tile[q * RW + row / 16] + row % 16 * LD + r);
+    for (int q = 1; q < KW; ++q) v += *(const float4v*)((const float*)tile[q] + row * LD + r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = r + j < a.rank ? v[j] * s : 0.0f;
     if (t.first + row < t.end && r < a.ldu)
       *(float4v*)(u + (int64_t)(t.first + row) * a.ldu + r) = v;
   }
+}
+
+// The same for 16 RW places, by eight waves: RW of them, a group, have 16 places each and share the
+// adapter's part of a step, of which each loads its share, in two slots of LDS in turn with one
+// barrier a step; their own rows' part they turn by themselves.  The 8 / RW groups share the steps of
+// K.  (With a copy for each wave the adapter's bytes, from the L2, take longer than the rows' from
+// memory: rank 32 has two of them for each of the rows', and a CU gets 16 a cycle.)
+constexpr int kWideThreads = 512;
+template <int RF>
+constexpr int kWideDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;
+template <class T, int RF, int RW>
+__global__ __launch_bounds__(kWideThreads) void ex_adapters_down_wide_kernel(AdapterArgs a) {
+  constexpr int PER = 16 / T::BYTES, STEP = kRowBytes / T::BYTES, DEEP = kWideDeep<RF>;
+  constexpr int KG = 8 / RW, WROWS = RF * 16, LD = RF * 16 + 4;
+  constexpr int OWN = (WROWS / 8 + RW - 1) / RW;  // loads of eight adapter rows a wave makes
+  __shared__ int4v rows_tile[8][16 * 8];
+  __shared__ int4v rank_tile[KG][2][WROWS * 8];
+  using Vec = Raw<T, PER>;
+  Places t;
+  const int split = blockIdx.x % a.splits;
+  if (!find_places<true>(a, 16 * RW, blockIdx.x / a.splits, t) || t.e < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
+  const int rw = wave % RW, kg = wave / RW;
+  const int r8 = lane >> 3, c8 = lane & 7, place0 = t.first + 16 * rw;
+  int4v* const mine = rows_tile[wave];
+  float4v acc[RF];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) acc[f] = float4v{0, 0, 0, 0};
+  const typename T::type* from[2 + OWN];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    from[j] = (const typename T::type*)a.X +
+              row_at(a, min(place0 + 8 * j + r8, t.end - 1)) * a.ldx + c8 * PER;
+#pragma unroll
+  for (int j = 0; j < OWN; ++j)
+    from[2 + j] = (const typename T::type*)a.W + t.e * a.stride_w +
+                  min(8 * (rw + RW * j) + r8, a.rank - 1) * a.ldw + c8 * PER;
+  const bool owns = 8 * rw < WROWS;  // (16 ranks are two waves' loads)
+  const int first = (int)min((int64_t)split * a.k_chunk, (int64_t)a.K);
+  const int end = first + min(a.k_chunk, a.K - first);
+  const int n = (end - first) / (STEP * KG);  // whole steps of every group
+  Vec v[DEEP][2 + OWN];
+  auto load = [&](int d, int i) {
+#pragma unroll
+    for (int j = 0; j < 2 + OWN; ++j)
+      v[d][j] = load_raw<T, PER>(from[j] + first + (i * KG + kg) * STEP);
+  };
+  auto multiply = [&](int d, int i) {
+    int4v* const shared = rank_tile[kg][i & 1];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) mine[group_at(8 * j + r8, c8)] = __builtin_bit_cast(int4v, v[d][j]);
+    if (owns) {
+#pragma unroll
+      for (int j = 0; j < OWN; ++j)
+        shared[group_at(8 * (rw + RW * j) + r8, c8)] = __builtin_bit_cast(int4v, v[d][2 + j]);
+    }
+    // LDS alone: the loads of later steps stay under way
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Vec x = __builtin_bit_cast(Vec, mine[group_at(l16, g + 4 * h)]);
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        const Vec w = __builtin_bit_cast(Vec, shared[group_at(16 * f + l16, g + 4 * h)]);
+        if constexpr (T::BYTES == 4) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) acc[f] = mma32(w[j], x[j], acc[f]);
+        } else {
+          acc[f] = mma16(w, x, acc[f]);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  int i = 0;
+  if (n >= DEEP) {
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) load(d, d);
+    for (; i + 2 * DEEP <= n; i += DEEP) {
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d) {
+        multiply(d, i + d);
+        load(d, i + DEEP + d);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) multiply(d, i + d);
+    i += DEEP;
+  }
+#pragma unroll
+  for (int d = 0; d < DEEP - 1; ++d)
+    if (i + d < n) load(d, i + d);
+#pragma unroll
+  for (int d = 0; d < DEEP - 1; ++d)
+    if (i + d < n) multiply(d, i + d);
+  if (first + n * KG * STEP < end) {  // the columns past the last whole step of all groups
+    const int k0 = first + (n * KG + kg) * STEP + c8 * PER;
+#pragma unroll
+    for (int j = 0; j < 2 + OWN; ++j) v[0][j] = load_end<T, PER>(from[j] - c8 * PER, k0, end);
+    multiply(0, n);
+  }
+  // the groups' sums meet where the adapter's slots were
+  static_assert((KG - 1) * RW * 16 * LD * 4 <= (int)sizeof(rank_tile), "they fit");
+  __syncthreads();
+  float* const sums = (float*)rank_tile;  // [group - 1][place][LD]
+  if (kg > 0) {
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      *(float4v*)(sums + ((kg - 1) * RW * 16 + rw * 16 + l16) * LD + 16 * f + 4 * g) = acc[f];
+  }
+  __syncthreads();
+  if (kg > 0) return;
+  const float s = a.scale != nullptr ? a.scale[t.e] : 1.0f;
+  float* u = a.U + (int64_t)split * a.rows * a.ldu + (int64_t)(place0 + l16) * a.ldu;
+#pragma unroll
+  for (int f = 0; f < RF; ++f) {
+    const int r = 16 * f + 4 * g;
+#pragma unroll
+    for (int q = 1; q < KG; ++q)
+      acc[f] += *(const float4v*)(sums + ((q - 1) * RW * 16 + rw * 16 + l16) * LD + r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[f][j] = r + j < a.rank ? acc[f][j] * s : 0.0f;
+    if (place0 + l16 < t.end && r < a.ldu) *(float4v*)(u + r) = acc[f];
+  }
+}
+
+// The splits' sum, in the first one's place; a thread has four numbers.
+__global__ __launch_bounds__(256) void ex_adapters_join_kernel(AdapterArgs a) {
+  const int64_t n = (int64_t)a.rows * a.ldu, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4v v = *(const float4v*)(a.U + i);
+#pragma unroll 8
+  for (int s = 1; s < a.splits; ++s) v += *(const float4v*)(a.U + s * n + i);
+  *(float4v*)(a.U + i) = v;
 }
 
 // ------------------------------------------------------------- contractions across both operands
@@ -286,207 +436,242 @@ __device__ __forceinline__ void multiply_across(const Block8<T>& w, const float 
   }
 }
 
-// Four neighbours of U, the splits' sum: their loads are in flight together.
-template <bool SPLIT>
-__device__ __forceinline__ float4v u_at(const AdapterArgs& a, int64_t at) {
-  const float* u = a.U + at;
-  float4v v = *(const float4v*)u;
-  if constexpr (!SPLIT) return v;
-  const int64_t step = (int64_t)a.rows * a.ldu;
-  for (int s = 1; s < a.splits; s += 4) {
-    float4v w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = *(const float4v*)(u + min(s + q, a.splits - 1) * step);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (s + q < a.splits) v += w[q];
-  }
-  return v;
-}
-
 // -------------------------------------------------------------------------------------- up
-// BM places x 512 columns, a wave 128 of them and 16 places at a time, B's part in registers (where
-// that takes 128 of them or fewer).  NB: blocks of 32 of the rank.  BM is 16, or 64 where U has one
-// split.
-constexpr int kUpThreads = 256, kWaveCols = 128, kUpCols = 4 * kWaveCols;
-template <class T, int NB, int BM, bool INSIDE>
-__device__ __forceinline__ void up_columns(const AdapterArgs& a, const Places& t, int n0) {
-  constexpr bool HOLD = NB * 32 * (T::BYTES / 2) <= 128 && BM > 16;
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int c = n0 + 8 * l16;
-  int64_t rows[BM / 16][4];  // of the results that this lane holds
+// A wave has 128 columns, and 16 places at a time: it reads their u and their rows of y, and B's part
+// is there already.  Up to rank 32 that part is in the wave's registers, a workgroup is a wave, and
+// it goes through BM places; past it four waves have 16 places each, and share B's part in LDS.
+constexpr int kWaveCols = 128;
+
+template <class T>
+struct UpColumns {
+  const AdapterArgs& a;
+  const Places& t;
+  int l16, g, c;
+
+  __device__ __forceinline__ UpColumns(const AdapterArgs& args, const Places& places, int n0)
+      : a(args), t(places), l16(threadIdx.x & 15), g(threadIdx.x >> 4 & 3),
+        // (columns past the last are computed once more as the last ones)
+        c(min(n0 + 8 * (int)(threadIdx.x & 15), args.N - 8)) {}
+
+  // Ranks 32 b .. of the columns, zeros past the last.
+  __device__ __forceinline__ void load(int b, Block8<T>& o) const {
+    const typename T::type* w = (const typename T::type*)a.W + max(t.e, 0) * a.stride_w + c;
 #pragma unroll
-  for (int i = 0; i < BM / 16; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      rows[i][q] = row_at(a, min(t.first + 16 * i + 4 * g + q, t.end - 1));
-  const typename T::type* w = (const typename T::type*)a.W + max(t.e, 0) * a.stride_w;
-  auto load_w = [&](int b, Block8<T>& o) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 32 * b + 8 * g + i;
-      o.v[i] = load_columns<T, 8, INSIDE>(w + min(r, a.rank - 1) * a.ldw, c, a.N);
-    }
-  };
-  auto finish_w = [&](int b, Block8<T>& o) {
+    for (int i = 0; i < 8; ++i) o.v[i] = load_raw<T, 8>(w + min(32 * b + 8 * g + i, a.rank - 1) * a.ldw);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (32 * b + 8 * g + i >= a.rank) o.v[i] = Raw<T, 8>{};
     if constexpr (std::is_same_v<T, Bf16>) o.turn();
-  };
-  auto load_u = [&](int b, int place, float4v (&u)[2]) {
+  }
+  // Eight of u for place l16 of those from p0 on; zeros past the rank.
+  __device__ __forceinline__ void load_u(int p0, int b, float (&v)[8]) const {
     const int r = 32 * b + 8 * g;
-    const int64_t at = (int64_t)place * a.ldu + (r < a.ldu ? r : 0);
-    u[0] = u_at<BM == 16>(a, at), u[1] = u_at<BM == 16>(a, at + 4);
-    if (r >= a.ldu) u[0] = u[1] = float4v{0, 0, 0, 0};
-  };
-  Raw<T, 8> y[2][4];
-  auto load_y = [&](int i) {
+    const float* at = a.U + (int64_t)min(p0 + l16, t.end - 1) * a.ldu + (r < a.ldu ? r : 0);
+    const int64_t step = (int64_t)a.rows * a.ldu;
+    float4v u[2] = {*(const float4v*)at, *(const float4v*)(at + 4)};
+    for (int s = 1; s < a.splits; s += 4) {  // (their loads together, four splits at a time)
+      float4v more[4][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      y[i & 1][q] = load_columns<T, 8, INSIDE>((const typename T::type*)a.Y + rows[i][q] * a.ldy,
-                                               c, a.N);
-  };
-  Block8<T> held[HOLD ? NB : 1];
-  if (HOLD && t.e >= 0) {
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) load_w(b, held[b]);
+        for (int h = 0; h < 2; ++h)
+          more[k][h] = *(const float4v*)(at + min(s + k, a.splits - 1) * step + 4 * h);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s + k < a.splits) u[0] += more[k][0], u[1] += more[k][1];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = r < a.ldu ? u[k / 4][k % 4] : 0.0f;
   }
-  if (a.Y != nullptr) load_y(0);
-  if (HOLD && t.e >= 0) {
+  // 16 places from p0 on; row_of: the number of row lane + first; sum(acc) adds u B.
+  template <class F>
+  __device__ __forceinline__ void places(int p0, int first, int row_of, F sum) const {
+    int64_t row[4];  // of the results that this lane holds
+    Raw<T, 8> y[4];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) finish_w(b, held[b]);
-  }
+    for (int q = 0; q < 4; ++q) row[q] = __shfl(row_of, min(p0 + 4 * g + q, t.end - 1) - first);
+    if (a.Y != nullptr) {
 #pragma unroll
-  for (int i = 0; i < BM / 16; ++i) {
-    const int p0 = t.first + 16 * i;
-    if (p0 >= t.end) break;
+      for (int q = 0; q < 4; ++q)
+        y[q] = load_raw<T, 8>((const typename T::type*)a.Y + row[q] * a.ldy + c);
+    }
     float4v acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = float4v{0, 0, 0, 0};
-    if (t.e >= 0) {
-      float4v u[NB][2];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) load_u(b, min(p0 + l16, t.end - 1), u[b]);
-      // the next places' y is on its way while these are multiplied
-      if (i + 1 < BM / 16 && a.Y != nullptr) load_y(i + 1 < BM / 16 ? i + 1 : i);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = u[b][k / 4][k % 4];
-        if constexpr (HOLD) {
-          multiply_across<T>(held[b], v, acc);
-        } else {
-          Block8<T> o;
-          load_w(b, o);
-          finish_w(b, o);
-          multiply_across<T>(o, v, acc);
-        }
-      }
-    } else if (i + 1 < BM / 16 && a.Y != nullptr) {
-      load_y(i + 1 < BM / 16 ? i + 1 : i);
-    }
+    if (t.e >= 0) sum(acc);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = a.Y != nullptr ? (float)y[i & 1][q][j] + acc[j][q] : acc[j][q];
+      for (int j = 0; j < 8; ++j) v[j] = a.Y != nullptr ? (float)y[q][j] + acc[j][q] : acc[j][q];
       if (p0 + 4 * g + q < t.end)
-        store_row<8, T::CODE>(a.C, rows[i][q] * a.ldc + c, INSIDE ? 8 : a.N - c, T::CODE, v);
+        store_row<8, T::CODE>(a.C, row[q] * a.ldc + c, 8, T::CODE, v);
     }
   }
-}
-template <class T, int NB, int BM>
-__global__ __launch_bounds__(kUpThreads) void ex_adapters_up_kernel(AdapterArgs a) {
+};
+
+// Rank 32 or less.  BM: 16, 32 or 64.
+template <class T, int BM>
+__global__ __launch_bounds__(64, (std::is_same_v<T, Bf16> ? 4 : T::BYTES == 2 ? 3 : 2)) void
+ex_adapters_up_kernel(AdapterArgs a) {
   Places t;
-  if (!find_places<BM>(a, blockIdx.x / a.tiles_n, t)) return;
-  const int n0 = __builtin_amdgcn_readfirstlane(blockIdx.x % a.tiles_n * kUpCols +
-                                                (threadIdx.x >> 6) * kWaveCols);
-  if (n0 + kWaveCols <= a.N) up_columns<T, NB, BM, true>(a, t, n0);
-  else if (n0 < a.N) up_columns<T, NB, BM, false>(a, t, n0);
+  if (!find_places<true>(a, BM, blockIdx.x / a.tiles_n, t)) return;
+  const UpColumns<T> w(a, t, blockIdx.x % a.tiles_n * kWaveCols);
+  const int row_of = (int)row_at(a, min(t.first + ((int)threadIdx.x & (BM - 1)), t.end - 1));
+  Block8<T> held;
+  if (t.e >= 0) w.load(0, held);
+  for (int p0 = t.first; p0 < t.end; p0 += 16)
+    w.places(p0, t.first, row_of, [&](float4v (&acc)[8]) {
+      float u[8];
+      w.load_u(p0, 0, u);
+      multiply_across<T>(held, u, acc);
+    });
+}
+
+// Rank 128 or less: 64 places a workgroup.
+template <class T>
+__global__ __launch_bounds__(256) void ex_adapters_up_deep_kernel(AdapterArgs a) {
+  __shared__ Raw<T, 8> shared[4][8][64];
+  Places t;
+  if (!find_places<true>(a, 64, blockIdx.x / a.tiles_n, t)) return;
+  const UpColumns<T> w(a, t, blockIdx.x % a.tiles_n * kWaveCols);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row_of = (int)row_at(a, min(t.first + lane, t.end - 1));
+  if (t.e >= 0 && 32 * wave < a.rank) {
+    Block8<T> o;
+    w.load(wave, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) shared[wave][i][lane] = o.v[i];
+  }
+  __syncthreads();
+  const int p0 = t.first + 16 * wave;
+  if (p0 >= t.end) return;
+  w.places(p0, t.first, row_of, [&](float4v (&acc)[8]) {
+    for (int b = 0; 32 * b < a.rank; ++b) {
+      float u[8];
+      w.load_u(p0, b, u);
+      Block8<T> o;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.v[i] = shared[b][i][lane];
+      multiply_across<T>(o, u, acc);
+    }
+  });
 }
 
 // ------------------------------------------------------------------------------------ grad
-// 128 columns of RF * 16 rows of one adapter's gradient.  The waves take turns at 32 of the group's
-// places and add up through LDS; row_splits workgroups share a group's places.
+// 128 columns of RF * 16 rows of one adapter's gradient, from a run of its places.  The waves take
+// turns at 32 of these and add up through LDS.  An adapter with one run has its result; those of one
+// with several are added by another launch.  (Runs of one length, however the places are shared out:
+// with as many for each adapter the largest one decides.)
 template <int RF>
 struct GradShape {
   static constexpr int WAVES = RF <= 2 ? 8 : 4;
+  static constexpr int LD = RF * 16 + 4;  // numbers of a place in LDS
+  static constexpr int PER_SIMD = RF == 4 ? 1 : 2;  // waves
 };
-// What one wave adds of the places first + 32 wave, + 32 WAVES and so on.
-template <class T, int RF, bool INSIDE>
-__device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int end, int n0, int r0,
-                                            float4v (&acc)[RF][8]) {
-  constexpr int WAVES = GradShape<RF>::WAVES;
+// What one wave adds of the places first + 32 wave, + 32 WAVES and so on.  u and the rows' numbers
+// come by whole lines, through LDS of the wave's own (lds: 32 LD numbers).
+template <class T, int RF>
+__device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int end, int c, int r0,
+                                            float* lds, float4v (&acc)[RF][8]) {
+  constexpr int WAVES = GradShape<RF>::WAVES, LD = GradShape<RF>::LD;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int64_t u_step = (int64_t)a.rows * a.ldu;
   for (int i0 = first + (threadIdx.x >> 6) * 32; i0 < end; i0 += WAVES * 32) {
-    int64_t rows[8];
+    const int row_of = (int)row_at(a, min(i0 + (lane & 31), end - 1));
+    // u: 4 RF lanes load a place's 16 RF numbers
+    constexpr int LANES = 4 * RF, PLACES = 64 / LANES;
+    float4v part[32 / PLACES];
+    const int ur = min(r0 + lane % LANES * 4, a.ldu - 4);
+    auto load_u = [&](int s, float4v (&to)[32 / PLACES]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rows[i] = row_at(a, min(i0 + 8 * g + i, end - 1));
+      for (int j = 0; j < 32 / PLACES; ++j)
+        to[j] = *(const float4v*)(a.U + s * u_step +
+                                  (int64_t)min(i0 + j * PLACES + lane / LANES, end - 1) * a.ldu + ur);
+    };
+    load_u(0, part);
     Block8<T> o;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      o.v[i] = load_columns<T, 8, INSIDE>((const typename T::type*)a.X + rows[i] * a.ldx,
-                                          n0 + 8 * l16, a.N);
-    float u[RF][8];
+      o.v[i] = load_raw<T, 8>((const typename T::type*)a.X +
+                              (int64_t)__shfl(row_of, 8 * g + i) * a.ldx + c);
+    for (int s = 1; s < a.splits; ++s) {
+      float4v more[32 / PLACES];
+      load_u(s, more);
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
+      for (int j = 0; j < 32 / PLACES; ++j) part[j] += more[j];
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[f][i] = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-      float part[RF][8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* at = a.U + s * u_step + (int64_t)min(i0 + 8 * g + i, end - 1) * a.ldu + l16;
-#pragma unroll
-        for (int f = 0; f < RF; ++f) part[f][i] = at[min(r0 + 16 * f, a.ldu - 16)];
-      }
-#pragma unroll
-      for (int f = 0; f < RF; ++f)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[f][i] += part[f][i];
+    for (int j = 0; j < 32 / PLACES; ++j) {
+      const int place = j * PLACES + lane / LANES;
+      // (the places past the last, and the numbers past u's columns, add nothing)
+      if (i0 + place >= end || r0 + lane % LANES * 4 >= a.ldu) part[j] = float4v{0, 0, 0, 0};
+      *(float4v*)(lds + place * LD + lane % LANES * 4) = part[j];
     }
     if (i0 + 32 > end) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i0 + 8 * g + i >= end) {
-          o.v[i] = Raw<T, 8>{};
-#pragma unroll
-          for (int f = 0; f < RF; ++f) u[f][i] = 0.0f;
-        }
+        if (i0 + 8 * g + i >= end) o.v[i] = Raw<T, 8>{};
     }
-    if constexpr (std::is_same_v<T, Bf16>) o.turn();
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (std::is_same_v<T, Bf16>) {
+      bf168v parts[RF][3];
 #pragma unroll
-    for (int f = 0; f < RF; ++f) multiply_across<T>(o, u[f], acc[f]);
+      for (int f = 0; f < RF; ++f) {
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = lds[(8 * g + i) * LD + 16 * f + l16];
+        three_parts(u, parts[f]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // (one fragment turned at a time: 32 registers fewer)
+        bf168v w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = o.v[i][j];
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int f = 0; f < RF; ++f) acc[f][j] = mma16(parts[f][p], w, acc[f][j]);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = lds[(8 * g + i) * LD + 16 * f + l16];
+        multiply_across<T>(o, u, acc[f]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 template <class T, int RF>
-__global__ __launch_bounds__(GradShape<RF>::WAVES * 64) void ex_adapters_grad_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD) void ex_adapters_grad_kernel(AdapterArgs a) {
   constexpr int WAVES = GradShape<RF>::WAVES, N = RF * 8 * 4;
   __shared__ float red[WAVES / 2][N][64];
+  constexpr int LD = GradShape<RF>::LD;
+  static_assert(WAVES * 32 * LD <= WAVES / 2 * N * 64, "the waves' u lies where their sums meet");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
-  // workgroups: columns, then row splits, then blocks of the rank, then adapters
+  // workgroups: columns, then blocks of the rank, then runs
   const int rb = (a.rank + RF * 16 - 1) / (RF * 16);
   int id = blockIdx.x;
   const int n0 = id % a.tiles_n * kWaveCols;
   id /= a.tiles_n;
-  const int split = id % a.row_splits;
-  id /= a.row_splits;
-  const int r0 = id % rb * (RF * 16), e = id / rb;
-  const int lo = clamped_offset(a.offsets, e, a.rows);
-  const int len = max(clamped_offset(a.offsets, e + 1, a.rows) - lo, 0);
-  const int first = lo + (int)((int64_t)len * split / a.row_splits);
-  const int end = lo + (int)((int64_t)len * (split + 1) / a.row_splits);
+  const int r0 = id % rb * (RF * 16);
+  id /= rb;
+  Places t;
+  if (!find_places<false>(a, a.run, id, t)) return;
+  const int first = t.first, end = t.end;
   float4v acc[RF][8];
 #pragma unroll
   for (int f = 0; f < RF; ++f)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[f][j] = float4v{0, 0, 0, 0};
-  if (n0 + kWaveCols <= a.N) grad_places<T, RF, true>(a, first, end, n0, r0, acc);
-  else grad_places<T, RF, false>(a, first, end, n0, r0, acc);
+  float* const lds = (float*)red + wave * 32 * LD;
+  // (columns past the last are computed once more as the last ones)
+  const int c = min(n0 + 8 * l16, a.N - 8);
+  grad_places<T, RF>(a, first, end, c, r0, lds, acc);
+  __syncthreads();
   for (int d = WAVES / 2; d > 0; d /= 2) {
     if (wave >= d && wave < 2 * d) {
 #pragma unroll
@@ -500,7 +685,6 @@ __global__ __launch_bounds__(GradShape<RF>::WAVES * 64) void ex_adapters_grad_ke
     __syncthreads();
   }
   if (wave != 0) return;
-  const int c = n0 + 8 * l16;
 #pragma unroll
   for (int f = 0; f < RF; ++f) {
 #pragma unroll
@@ -510,32 +694,111 @@ __global__ __launch_bounds__(GradShape<RF>::WAVES * 64) void ex_adapters_grad_ke
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = acc[f][j][q];
-      if (a.row_splits > 1) {
-        const int64_t at = (((int64_t)split * a.E + e) * a.rank + r) * a.N + c;
-        store_row<8, GEMM_LP_F32>(a.part, at, a.N - c, GEMM_LP_F32, v);
+      if (t.tiles > 1) {
+        store_row<8, GEMM_LP_F32>(a.part, ((int64_t)id * a.rank + r) * a.N + c, 8, GEMM_LP_F32, v);
       } else {
-        store_row<8, T::CODE>(a.C, e * a.stride_c + r * a.ldc + c, a.N - c, T::CODE, v);
+        store_row<8, T::CODE>(a.C, t.e * a.stride_c + r * a.ldc + c, 8, T::CODE, v);
       }
     }
   }
 }
 
-// The sum of the row splits' parts; a thread has eight columns.
+// The sums of the adapters that have several runs.  A workgroup has 2048 neighbouring values of one
+// adapter's gradient, a thread eight of one row.
 template <class T>
 __global__ __launch_bounds__(256) void ex_adapters_sum_kernel(AdapterArgs a) {
   const int per = (a.N + 7) / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.E * a.rank * per) return;
-  const int64_t row = i / per;  // e * rank + r
-  const int c = (int)(i - row * per) * 8, n = a.N - c;
-  float v[8] = {};
-  for (int s = 0; s < a.row_splits; ++s) {
-    const float* part = a.part + ((int64_t)s * a.E * a.rank + row) * a.N;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += part[min(c + j, a.N - 1)];
+  const int64_t blocks = ((int64_t)a.rank * per + 255) / 256;
+  const int e = (int)(blockIdx.x / blocks);
+  const int64_t i = (blockIdx.x - e * blocks) * 256 + threadIdx.x;
+  // its first run: the runs of the adapters before it
+  int before = 0, runs = 0;
+  for (int base = 0; base <= e; base += 64) {
+    const int g = base + (threadIdx.x & 63);
+    const int lo = clamped_offset(a.offsets, min(g, e), a.rows);
+    const int len = max(clamped_offset(a.offsets, min(g, e) + 1, a.rows) - lo, 0);
+    const int n = max((len + a.run - 1) / a.run, 1);
+    before += __builtin_amdgcn_readlane(wave_scan(g < e ? n : 0), 63);
+    runs = __builtin_amdgcn_readfirstlane(__shfl(n, e - base));  // (of the last turn)
   }
-  const int e = (int)(row / a.rank), r = (int)(row - (int64_t)e * a.rank);
-  store_row<8, T::CODE>(a.C, e * a.stride_c + r * a.ldc + c, n, T::CODE, v);
+  if (runs == 1 || i >= (int64_t)a.rank * per) return;
+  const int r = (int)(i / per), c = min((int)(i - (int64_t)r * per) * 8, a.N - 8);
+  float v[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < runs; ++s) {
+    // (offsets that overlap would count more runs than there are)
+    const int at = min(before + s, a.runs - 1);
+    const float* part = a.part + ((int64_t)at * a.rank + r) * a.N;
+    const Raw<F32, 8> w = load_raw<F32, 8>(part + c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
+  }
+  store_row<8, T::CODE>(a.C, e * a.stride_c + r * a.ldc + c, 8, T::CODE, v);
+}
+
+// ----------------------------------------------------------------- fewer than kLeastWide columns
+// u, 16 places and one split, a thread a number.  (The other splits are zeros.)
+template <class T>
+__global__ __launch_bounds__(256) void ex_adapters_down_few_kernel(AdapterArgs a) {
+  Places t;
+  const int split = blockIdx.x % a.splits;
+  if (!find_places<true>(a, 16, blockIdx.x / a.splits, t) || t.e < 0) return;
+  for (int i = threadIdx.x; i < (t.end - t.first) * a.ldu; i += 256) {
+    const int place = t.first + i / a.ldu, r = i % a.ldu;
+    float v = 0.0f;
+    if (r < a.rank && split == 0) {
+      const typename T::type* x = (const typename T::type*)a.X + row_at(a, place) * a.ldx;
+      const typename T::type* w = (const typename T::type*)a.W + t.e * a.stride_w + r * a.ldw;
+      for (int k = 0; k < a.K; ++k) v = fmaf((float)x[k], (float)w[k], v);
+      if (a.scale != nullptr) v *= a.scale[t.e];
+    }
+    a.U[((int64_t)split * a.rows + place) * a.ldu + r] = v;
+  }
+}
+// The result, 16 places, a thread a number.
+template <class T>
+__global__ __launch_bounds__(256) void ex_adapters_up_few_kernel(AdapterArgs a) {
+  Places t;
+  if (!find_places<true>(a, 16, blockIdx.x, t)) return;
+  for (int i = threadIdx.x; i < (t.end - t.first) * a.N; i += 256) {
+    const int place = t.first + i / a.N, n = i % a.N;
+    const int64_t row = row_at(a, place);
+    float v = 0.0f;
+    if (t.e >= 0) {
+      for (int r = 0; r < a.rank; ++r) {
+        float u = 0.0f;
+        for (int s = 0; s < a.splits; ++s) u += a.U[((int64_t)s * a.rows + place) * a.ldu + r];
+        v = fmaf(u, (float)((const typename T::type*)a.W)[t.e * a.stride_w + r * a.ldw + n], v);
+      }
+    }
+    if (a.Y != nullptr) v += (float)((const typename T::type*)a.Y)[row * a.ldy + n];
+    ((typename T::type*)a.C)[row * a.ldc + n] = (typename T::type)v;
+  }
+}
+// One row of one adapter's gradient, its places shared by the threads.
+template <class T>
+__global__ __launch_bounds__(256) void ex_adapters_grad_few_kernel(AdapterArgs a) {
+  __shared__ float part[4][kLeastWide];
+  const int e = blockIdx.x / a.rank, r = blockIdx.x % a.rank, tid = threadIdx.x;
+  const int lo = clamped_offset(a.offsets, e, a.rows), hi = clamped_offset(a.offsets, e + 1, a.rows);
+  float v[kLeastWide] = {};
+  for (int place = lo + tid; place < hi; place += 256) {
+    const typename T::type* x = (const typename T::type*)a.X + row_at(a, place) * a.ldx;
+    float u = 0.0f;
+    for (int s = 0; s < a.splits; ++s) u += a.U[((int64_t)s * a.rows + place) * a.ldu + r];
+#pragma unroll
+    for (int n = 0; n < kLeastWide; ++n)
+      if (n < a.N) v[n] = fmaf(u, (float)x[n], v[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < kLeastWide; ++n) {
+    v[n] = over_lanes<64>(v[n], Add{});
+    if ((tid & 63) == 0) part[tid >> 6][n] = v[n];
+  }
+  __syncthreads();
+  if (tid < a.N)
+    ((typename T::type*)a.C)[e * a.stride_c + r * a.ldc + tid] =
+        (typename T::type)((part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]));
 }
 
 }  // namespace gemmlp

@@ -16,65 +16,75 @@ static int64_t place_tiles(int64_t rows, int64_t E, int bm) {
   return rows / bm + std::min<int64_t>(E + 2, rows);
 }
 
-// Waves of a workgroup of `down` with places of their own (the others share K): more than one only
-// where that leaves a workgroup for every CU, and the adapters have several tiles on average.
-static int down_waves(int64_t rows, int64_t E) {
+// Waves of a workgroup of `down` with places of their own: four or two where that leaves a workgroup
+// for most CUs and the adapters have several such tiles; otherwise one, with a kernel of its own.
+// Past rank 64 four as soon as splits of K can make up for the workgroups (and never two, which would
+// need more registers than a wave has): there the adapter's bytes decide.
+static int down_waves(int64_t rows, int64_t rank, int64_t E) {
+  if (rank > 64) return rows >= 2048 && rows >= 128 * E ? 4 : 1;
   for (int w = 4; w > 1; w /= 2)
-    if (rows >= 16 * w * kCus && rows >= 64 * w * E) return w;
+    if (rows >= 16 * w * (kCus * 3 / 4) && rows >= 32 * w * E) return w;
   return 1;
 }
-// Splits of K: enough workgroups for two a CU where there is not one for each, but 256 columns a
-// split.
-static int adapter_splits(int64_t rows, int64_t K, int64_t E) {
-  const int64_t tiles = std::max<int64_t>(place_tiles(rows, E, 16 * down_waves(rows, E)), 1);
-  if (tiles >= kCus) return 1;
-  return (int)std::max<int64_t>(
-      std::min<int64_t>({(2 * kCus + tiles - 1) / tiles, K / 256, 8}), 1);
+// Splits of K: enough workgroups for two a CU where there are none for each, but 256 columns a split.
+static int adapter_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
+  const int64_t tiles =
+      std::max<int64_t>(place_tiles(rows, E, 16 * down_waves(rows, rank, E)), 1);
+  if (tiles >= kCus * 3 / 4) return 1;
+  return (int)std::max<int64_t>(std::min<int64_t>({2 * kCus / tiles, K / 256, 8}), 1);
 }
-// Places of a workgroup of `up`.
-static int up_places(int64_t rows, int64_t E, int splits) {
-  return rows >= 32 * E && splits == 1 ? 64 : 16;
+// Places of a workgroup of `up`, a wave, up to rank 32: those that take the least time, as the rounds
+// of waves (four of a SIMD) and a round's places, of which its start is worth about 24.  (bf16, rank
+// 16 to 32, in us with 16, 32 and 64: 4096 x 4096 23, 18 and 25; 8192 x 4096 43, 39 and 36;
+// 4096 x 11008 58, 47 and 53; 1024 x 4096 10, 12 and 19.)
+static int up_places(int64_t rows, int64_t N, int64_t E) {
+  int best = 16;
+  int64_t least = 0;
+  for (int bm = 16; bm <= 64; bm *= 2) {
+    const int64_t tiles = (rows + bm - 1) / bm + std::min(E, rows) / 2;
+    const int64_t rounds = (tiles * ((N + kWaveCols - 1) / kWaveCols) + 16 * kCus - 1) / (16 * kCus);
+    if (bm == 16 || rounds * (bm + 24) < least) best = bm, least = rounds * (bm + 24);
+  }
+  return best;
 }
 
 // Fragments of the rank of a workgroup of `grad`.
 static int grad_fragments(int64_t rank, int bytes) {
   return rank <= 16 ? 1 : rank <= 32 || bytes == 4 ? 2 : 4;
 }
-static int64_t grad_blocks(int64_t N, int64_t rank, int64_t E, int bytes) {
+static int64_t grad_blocks(int64_t N, int64_t rank, int bytes) {
   const int64_t per = 16 * grad_fragments(rank, bytes);
-  return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per) * E;
+  return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per);
 }
-// Splits of a group's rows in `grad`: enough workgroups for one a CU where the groups are as long
-// as the average, but 256 rows a split.
-static int grad_splits(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
-  const int64_t wgs = std::max<int64_t>(grad_blocks(N, rank, E, bytes), 1);
-  const int64_t each = rows / std::max<int64_t>(E, 1);
-  return (int)std::max<int64_t>(
-      std::min<int64_t>({(kCus + wgs - 1) / wgs, each / 256, 16}), 1);
+// Places of a run in `grad`: so many that there are two workgroups a CU, but 256 at least (a turn of
+// eight waves); and the most runs that there can be.
+static int64_t grad_run(int64_t rows, int64_t N, int64_t rank, int bytes) {
+  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(grad_blocks(N, rank, bytes), 1), 1);
+  return std::max<int64_t>(((rows + per - 1) / per + 255) / 256 * 256, 256);
 }
+static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
 
 template <class T, int RW>
-static const void* down_kernel(int64_t rank) {
-  return rank <= 16   ? (const void*)&ex_adapters_down_kernel<T, 1, RW>
-         : rank <= 32 ? (const void*)&ex_adapters_down_kernel<T, 2, RW>
-         : rank <= 64 ? (const void*)&ex_adapters_down_kernel<T, 4, RW>
-                      : (const void*)&ex_adapters_down_kernel<T, 8, RW>;
+static const void* down_wide_kernel(int64_t rank) {
+  return rank <= 16   ? (const void*)&ex_adapters_down_wide_kernel<T, 1, RW>
+         : rank <= 32 ? (const void*)&ex_adapters_down_wide_kernel<T, 2, RW>
+         : rank <= 64 ? (const void*)&ex_adapters_down_wide_kernel<T, 4, RW>
+                      : (const void*)&ex_adapters_down_wide_kernel<T, 8, 4>;
 }
 template <class T>
 static const void* down_kernel(int64_t rank, int waves) {
-  return waves == 4   ? down_kernel<T, 4>(rank)
-         : waves == 2 ? down_kernel<T, 2>(rank)
-                      : down_kernel<T, 1>(rank);
-}
-template <class T, int BM>
-static const void* up_kernel(int64_t rank) {
-  return rank <= 32   ? (const void*)&ex_adapters_up_kernel<T, 1, BM>
-         : rank <= 64 ? (const void*)&ex_adapters_up_kernel<T, 2, BM>
-                      : (const void*)&ex_adapters_up_kernel<T, 4, BM>;
+  if (waves > 1) return waves == 4 ? down_wide_kernel<T, 4>(rank) : down_wide_kernel<T, 2>(rank);
+  return rank <= 16   ? (const void*)&ex_adapters_down_kernel<T, 1>
+         : rank <= 32 ? (const void*)&ex_adapters_down_kernel<T, 2>
+         : rank <= 64 ? (const void*)&ex_adapters_down_kernel<T, 4>
+                      : (const void*)&ex_adapters_down_kernel<T, 8>;
 }
 template <class T>
 static const void* up_kernel(int64_t rank, int places) {
-  return places == 64 ? up_kernel<T, 64>(rank) : up_kernel<T, 16>(rank);
+  return rank > 32       ? (const void*)&ex_adapters_up_deep_kernel<T>
+         : places == 64 ? (const void*)&ex_adapters_up_kernel<T, 64>
+         : places == 32 ? (const void*)&ex_adapters_up_kernel<T, 32>
+                        : (const void*)&ex_adapters_up_kernel<T, 16>;
 }
 template <class T>
 static const void* grad_kernel(int fragments) {
@@ -102,8 +112,8 @@ static bool fits_grid(int64_t wgs, int threads) {
 
 static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t* order,
                     const int32_t* offsets, const void* X, int64_t ldx, const void* A, int64_t lda,
-                    int64_t stride_a, const float* scale, float* U, int splits, int type,
-                    void* stream) {
+                    int64_t stride_a, const float* scale, float* U, int splits, int join,
+                    int type, void* stream) {
   if (bad_dims(rows, K, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
   if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS) return GEMMF32_ERR_BAD_CONFIG;
@@ -136,12 +146,23 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
   // (a multiple of the steps that four waves take at once)
   const int64_t unit = 4 * 128 / b;
   a.k_chunk = (int)((K + splits * unit - 1) / (splits * unit) * unit);
-  const int waves = down_waves(rows, E);
+  const int waves = down_waves(rows, rank, E), threads = waves > 1 ? kWideThreads : kDownThreads;
   const int64_t wgs = place_tiles(rows, E, 16 * waves) * splits;
-  if (!fits_grid(wgs, kDownThreads)) return GEMMF32_ERR_TOO_LARGE;
+  if (K < kLeastWide) {
+    const int64_t few = place_tiles(rows, E, 16) * splits;
+    if (!fits_grid(few, 256)) return GEMMF32_ERR_TOO_LARGE;
+#define FEW(T) &ex_adapters_down_few_kernel<T>
+    return launch(BY_TYPE(type, FEW), dim3((unsigned)few), 256, &a, stream);
+#undef FEW
+  }
+  if (!fits_grid(wgs, threads)) return GEMMF32_ERR_TOO_LARGE;
 #define DOWN(T) down_kernel<T>(rank, waves)
-  return launch(BY_TYPE(type, DOWN), dim3((unsigned)wgs), kDownThreads, &a, stream);
+  if (const int rc = launch(BY_TYPE(type, DOWN), dim3((unsigned)wgs), threads, &a, stream)) return rc;
 #undef DOWN
+  if (!join || splits == 1) return GEMMF32_OK;
+  const int64_t sums = (rows * ldu / 4 + 255) / 256;
+  if (!fits_grid(sums, 256)) return GEMMF32_ERR_TOO_LARGE;
+  return launch((const void*)&ex_adapters_join_kernel, dim3((unsigned)sums), 256, &a, stream);
 }
 
 static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_t* order,
@@ -178,22 +199,29 @@ static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_
   a.W = B, a.C = OUT, a.offsets = offsets, a.order = order, a.U = (float*)U, a.Y = Y;
   a.ldw = ldb, a.stride_w = stride_b, a.ldc = ldo, a.ldy = ldy;
   a.rows = (int)rows, a.N = (int)N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
-  a.splits = splits, a.tiles_n = (int)((N + kUpCols - 1) / kUpCols);
+  a.splits = splits, a.tiles_n = (int)((N + kWaveCols - 1) / kWaveCols);
   // (rank 0: no place has an adapter)
   if (!reads) a.E = 0;
-  const int places = up_places(rows, E, splits);
+  if (N < kLeastWide) {
+    const int64_t few = place_tiles(rows, a.E, 16);
+    if (!fits_grid(few, 256)) return GEMMF32_ERR_TOO_LARGE;
+#define FEW(T) &ex_adapters_up_few_kernel<T>
+    return launch(BY_TYPE(type, FEW), dim3((unsigned)few), 256, &a, stream);
+#undef FEW
+  }
+  const int places = rank > 32 ? 64 : up_places(rows, N, E), threads = rank > 32 ? 256 : 64;
   int64_t wgs;
   if (__builtin_mul_overflow(place_tiles(rows, E, places), (int64_t)a.tiles_n, &wgs) ||
-      !fits_grid(wgs, kUpThreads))
+      !fits_grid(wgs, threads))
     return GEMMF32_ERR_TOO_LARGE;
 #define UP(T) up_kernel<T>(rank, places)
-  return launch(BY_TYPE(type, UP), dim3((unsigned)wgs), kUpThreads, &a, stream);
+  return launch(BY_TYPE(type, UP), dim3((unsigned)wgs), threads, &a, stream);
 #undef UP
 }
 
 static int64_t grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
-  const int s = grad_splits(rows, N, rank, E, bytes);
-  return s > 1 ? (int64_t)s * E * rank * N * 4 : 0;
+  const int64_t run = grad_run(rows, N, rank, bytes);
+  return rows > run && N >= kLeastWide ? grad_runs(rows, E, run) * rank * N * 4 : 0;
 }
 
 static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
@@ -239,19 +267,27 @@ static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
   a.part = (float*)workspace, a.ldx = ldx, a.ldc = ldd, a.stride_c = stride_d;
   a.rows = (int)rows, a.N = (int)N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
   a.splits = splits, a.tiles_n = (int)((N + kWaveCols - 1) / kWaveCols);
-  a.row_splits = grad_splits(rows, N, rank, E, b);
+  a.run = (int)grad_run(rows, N, rank, b);
+  a.runs = (int)std::min<int64_t>(grad_runs(rows, E, a.run), kMaxDim);
+  if (N < kLeastWide) {
+    if (!fits_grid(E * rank, 256)) return GEMMF32_ERR_TOO_LARGE;
+#define FEW(T) &ex_adapters_grad_few_kernel<T>
+    return launch(BY_TYPE(type, FEW), dim3((unsigned)(E * rank)), 256, &a, stream);
+#undef FEW
+  }
   const int fragments = grad_fragments(rank, b);
   const int threads = 64 * (fragments <= 2 ? GradShape<1>::WAVES : GradShape<4>::WAVES);
   int64_t wgs;
-  if (__builtin_mul_overflow(grad_blocks(N, rank, E, b), (int64_t)a.row_splits, &wgs) ||
+  if (__builtin_mul_overflow(grad_blocks(N, rank, b), grad_runs(rows, E, a.run), &wgs) ||
       !fits_grid(wgs, threads))
     return GEMMF32_ERR_TOO_LARGE;
+  const int64_t sums = E * ((rank * ((N + 7) / 8) + 255) / 256);
+  if (!fits_grid(sums, 256)) return GEMMF32_ERR_TOO_LARGE;
 #define GRAD(T) grad_kernel<T>(fragments)
   if (const int rc = launch(BY_TYPE(type, GRAD), dim3((unsigned)wgs), threads, &a, stream)) return rc;
 #undef GRAD
-  if (a.row_splits == 1) return GEMMF32_OK;
-  const int64_t sums = (E * rank * ((N + 7) / 8) + 255) / 256;
-  if (!fits_grid(sums, 256)) return GEMMF32_ERR_TOO_LARGE;
+  if (rows <= a.run) return GEMMF32_OK;  // (one run each)
+
 #define SUM(T) &ex_adapters_sum_kernel<T>
   return launch(BY_TYPE(type, SUM), dim3((unsigned)sums), 256, &a, stream);
 #undef SUM
@@ -264,9 +300,9 @@ extern "C" {
 int gemm_adapters_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t* order,
                        const int32_t* offsets, const void* X, int64_t ldx, const void* A,
                        int64_t lda, int64_t stride_a, const float* scale, float* U, int splits,
-                       int type, void* stream) {
+                       int join, int type, void* stream) {
   return gemmlp::run_down(rows, K, rank, E, order, offsets, X, ldx, A, lda, stride_a, scale, U,
-                          splits, type, stream);
+                          splits, join, type, stream);
 }
 
 int gemm_adapters_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_t* order,
@@ -289,7 +325,7 @@ int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
   if (gemmlp::bad_dims(rows, K, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
   if (gemmlp::too_large(rows, K, E)) return GEMMF32_ERR_TOO_LARGE;
-  return gemmlp::adapter_splits(rows, K, E);
+  return gemmlp::adapter_splits(rows, K, rank, E);
 }
 
 int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int type) {

@@ -59,16 +59,5 @@ __device__ __forceinline__ Raw<T, COUNT> load_raw(const typename T::type* p) {
   typedef typename T::type any __attribute__((ext_vector_type(COUNT), aligned(sizeof(typename T::type))));
   return *(const any*)p;
 }
-// The same for columns c .. of a row of n > 0: INSIDE where all are known to be, and otherwise one by
-// one, the row's last value in the place of those past it.  Either way without a branch, at which
-// the loads before it would have to arrive.
-template <class T, int COUNT, bool INSIDE>
-__device__ __forceinline__ Raw<T, COUNT> load_columns(const typename T::type* row, int c, int n) {
-  if constexpr (INSIDE) return load_raw<T, COUNT>(row + c);
-  Raw<T, COUNT> v;
-#pragma unroll
-  for (int i = 0; i < COUNT; ++i) v[i] = row[min(c + i, n - 1)];
-  return v;
-}
 
 }  // namespace gemmlp

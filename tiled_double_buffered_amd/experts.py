@@ -22,6 +22,9 @@ MAX_EXPERTS = 1024         # of a router; GEMM_ROUTE_MAX_EXPERTS
 MAX_CHOSEN = 16            # GEMM_ROUTE_MAX_CHOSEN
 MAX_GROUPS = 4096          # of group_rows; GEMM_GROUP_MAX_EXPERTS
 MAX_RANK = 128             # GEMM_ADAPTERS_MAX_RANK
+# Rows from which on u's partial sums are joined by a launch of their own (3 us) rather than by each
+# of its readers.
+JOINED_ROWS = 1024
 
 _i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 # Every exported symbol and its C signature (kept in step with include/gemm_experts.h).
@@ -34,7 +37,7 @@ SIGNATURES = {
     "gemm_group_rows": (_int, [_i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _i64, _vp]),
     "gemm_group_rows_workspace": (_i64, [_i64, _i64]),
     "gemm_adapters_down": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64,
-                                  _vp, _vp, _int, _int, _vp]),
+                                  _vp, _vp, _int, _int, _int, _vp]),
     "gemm_adapters_up": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp,
                                 _i64, _vp, _i64, _int, _vp]),
     "gemm_adapters_grad": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _vp,
@@ -275,7 +278,8 @@ def _ld(t):
 
 
 def _down(x, a, order, offsets, scale):
-    """u: the contraction of x's rows with their adapter's, as partial sums by place."""
+    """(u, splits): the contraction of x's rows with their adapter's, by place, as so many partial
+    sums."""
     rows, K = x.shape
     E, rank = a.shape[:2]
     lib = load()
@@ -284,27 +288,28 @@ def _down(x, a, order, offsets, scale):
         _check(splits, "gemm_adapters_splits")
     # (whole fragments of 16, the columns past the rank zeros)
     u = torch.empty((splits, rows, (rank + 15) // 16 * 16), dtype=torch.float32, device=x.device)
+    join = rows >= JOINED_ROWS
     _check(lib.gemm_adapters_down(rows, K, rank, E, order.data_ptr(), offsets.data_ptr(),
                                   x.data_ptr(), _ld(x), a.data_ptr(), _ld(a), a.stride(0),
-                                  _pointer(scale), u.data_ptr(), splits, TYPES[x.dtype],
-                                  _current(x)), "gemm_adapters_down")
-    return u
+                                  _pointer(scale), u.data_ptr(), splits, 1 if join else 0,
+                                  TYPES[x.dtype], _current(x)), "gemm_adapters_down")
+    return u, 1 if join else splits
 
 
-def _up(u, b, y, order, offsets):
+def _up(u, splits, b, y, order, offsets):
     """y + u b of each row's adapter; y None for 0."""
     E, rank, N = b.shape
     rows = u.shape[1]
     out = b.new_empty((rows, N))
     py, ldy = (None, 0) if y is None else (y.data_ptr(), _ld(y))
     _check(load().gemm_adapters_up(rows, N, rank, E, order.data_ptr(), offsets.data_ptr(),
-                                   u.data_ptr(), u.shape[0], b.data_ptr(), _ld(b), b.stride(0), py,
+                                   u.data_ptr(), splits, b.data_ptr(), _ld(b), b.stride(0), py,
                                    ldy, out.data_ptr(), max(N, 1), TYPES[b.dtype], _current(b)),
            "gemm_adapters_up")
     return out
 
 
-def _adapter_grad(u, rank, x, E, order, offsets):
+def _adapter_grad(u, splits, rank, x, E, order, offsets):
     """E x rank x N: u^T x over each adapter's rows."""
     rows, N = x.shape
     lib, code = load(), TYPES[x.dtype]
@@ -313,7 +318,7 @@ def _adapter_grad(u, rank, x, E, order, offsets):
                  "gemm_adapters_grad_workspace")
     hold, pw = _workspace(need, x.device)
     _check(lib.gemm_adapters_grad(rows, N, rank, E, order.data_ptr(), offsets.data_ptr(),
-                                  u.data_ptr(), u.shape[0], x.data_ptr(), _ld(x), d.data_ptr(),
+                                  u.data_ptr(), splits, x.data_ptr(), _ld(x), d.data_ptr(),
                                   max(N, 1), rank * N, pw, need, code, _current(x)),
            "gemm_adapters_grad")
     return d
@@ -322,13 +327,13 @@ def _adapter_grad(u, rank, x, E, order, offsets):
 class _Adapters(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, x, a, b, order, offsets, scale):
-        u = _down(x, a, order, offsets, scale)
+        u, ctx.splits = _down(x, a, order, offsets, scale)
         need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
         ctx.save_for_backward(x if need_a else None, a if need_x else None,
                               b if need_x or need_a else None, u if need_b else None, order,
                               offsets, scale)
         ctx.size = a.shape[:2]
-        return _up(u, b, y, order, offsets)
+        return _up(u, ctx.splits, b, y, order, offsets)
 
     @staticmethod
     @_once
@@ -340,10 +345,10 @@ class _Adapters(torch.autograd.Function):
         if need_x or need_a or need_b:
             rows = _row_major(dout)
             if need_x or need_a:
-                v = _down(rows, b, order, offsets, scale)
-                dx = _up(v, a, None, order, offsets) if need_x else None
-                da = _adapter_grad(v, rank, x, E, order, offsets) if need_a else None
-            db = _adapter_grad(u, rank, rows, E, order, offsets) if need_b else None
+                v, splits = _down(rows, b, order, offsets, scale)
+                dx = _up(v, splits, a, None, order, offsets) if need_x else None
+                da = _adapter_grad(v, splits, rank, x, E, order, offsets) if need_a else None
+            db = _adapter_grad(u, ctx.splits, rank, rows, E, order, offsets) if need_b else None
         return dout if need_y else None, dx, da, db, None, None, None
 
 
@@ -408,7 +413,7 @@ def _adapted(y, x, a, b, order, offsets, scale):
     if torch.is_grad_enabled() and (y.requires_grad or x.requires_grad or a.requires_grad or
                                     b.requires_grad):
         return _Adapters.apply(y, x, a, b, order, offsets, scale)
-    return _up(_down(x, a, order, offsets, scale), b, y, order, offsets)
+    return _up(*_down(x, a, order, offsets, scale), b, y, order, offsets)
 
 
 def _unit_columns(w):
