@@ -112,20 +112,15 @@ __device__ __forceinline__ float4v mma32(float a, float b, float4v c) {
 constexpr int kLeastWide = 8;
 
 // ------------------------------------------------------------------------------------ down
-// Columns c .. of a row, zeros from `end` on.
+// Columns c .. c + COUNT - 1 of a row that lie before `end`, at places that depend on c and `end`
+// alone (which is all that a contraction needs), zeros at the others.
 template <class T, int COUNT>
 __device__ __forceinline__ Raw<T, COUNT> load_end(const typename T::type* row, int c, int end) {
-  const int at = min(c, end - COUNT), back = c - at;
-  const Raw<T, COUNT> v = load_raw<T, COUNT>(row + at);
-  Raw<T, COUNT> o;
+  const int at = min(c, end - COUNT);
+  Raw<T, COUNT> v = load_raw<T, COUNT>(row + at);
 #pragma unroll
-  for (int i = 0; i < COUNT; ++i) {
-    o[i] = (typename T::type)0.0f;
-#pragma unroll
-    for (int j = i; j < COUNT; ++j)
-      if (j - i == back) o[i] = v[j];
-  }
-  return o;
+  for (int i = 0; i < COUNT; ++i) v[i] = at + i < c ? (typename T::type)0.0f : v[i];
+  return v;
 }
 
 // u of 16 places and one split of K, whose steps four waves share; they add up through LDS.  The
@@ -139,7 +134,7 @@ __device__ __forceinline__ Raw<T, COUNT> load_end(const typename T::type* row, i
 // steps are always under way.
 constexpr int kDownThreads = 256;
 template <int RF>
-constexpr int kDownDeep = RF == 1 ? 6 : RF == 2 ? 4 : RF == 4 ? 3 : 2;
+constexpr int kDownDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;
 __device__ __forceinline__ int group_at(int row, int c) {  // of 16 bytes, in the wave's tile
   return row * 8 + (c ^ ((row >> 1) & 7));
 }
@@ -198,27 +193,19 @@ __global__ __launch_bounds__(kDownThreads) void ex_adapters_down_kernel(AdapterA
     }
     __builtin_amdgcn_wave_barrier();
   };
-  int i = 0;
-  if (n >= DEEP) {
+  if (n > 0) {
+    // (past the last step its loads are made once more: without a branch, at which all loads would
+    // have to arrive, and without a second set of registers for what is left over)
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d) load(d, d);
-    for (; i + 2 * DEEP <= n; i += DEEP) {
+    for (int d = 0; d < DEEP; ++d) load(d, min(d, n - 1));
+    for (int i = 0; i < n; i += DEEP) {
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
-        multiply(d);
-        load(d, i + DEEP + d);
+        if (i + d < n) multiply(d);
+        load(d, min(i + d + DEEP, n - 1));
       }
     }
-#pragma unroll
-    for (int d = 0; d < DEEP; ++d) multiply(d);
-    i += DEEP;
   }
-#pragma unroll
-  for (int d = 0; d < DEEP - 1; ++d)
-    if (i + d < n) load(d, i + d);
-#pragma unroll
-  for (int d = 0; d < DEEP - 1; ++d)
-    if (i + d < n) multiply(d);
   // the columns past the last whole step, by the wave whose turn it is
   const int rest = first + whole * STEP;
   if (rest < end && whole % KW == part) {
@@ -255,7 +242,7 @@ constexpr int kWideThreads = 512;
 template <int RF>
 constexpr int kWideDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;
 template <class T, int RF, int RW>
-__global__ __launch_bounds__(kWideThreads) void ex_adapters_down_wide_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(kWideThreads, (RF <= 2 ? 4 : 2)) void ex_adapters_down_wide_kernel(AdapterArgs a) {
   constexpr int PER = 16 / T::BYTES, STEP = kRowBytes / T::BYTES, DEEP = kWideDeep<RF>;
   constexpr int KG = 8 / RW, WROWS = RF * 16, LD = RF * 16 + 4;
   constexpr int OWN = (WROWS / 8 + RW - 1) / RW;  // loads of eight adapter rows a wave makes
@@ -318,27 +305,18 @@ __global__ __launch_bounds__(kWideThreads) void ex_adapters_down_wide_kernel(Ada
     }
     __builtin_amdgcn_wave_barrier();
   };
-  int i = 0;
-  if (n >= DEEP) {
+  if (n > 0) {
+    // (as above)
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d) load(d, d);
-    for (; i + 2 * DEEP <= n; i += DEEP) {
+    for (int d = 0; d < DEEP; ++d) load(d, min(d, n - 1));
+    for (int i = 0; i < n; i += DEEP) {
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
-        multiply(d, i + d);
-        load(d, i + DEEP + d);
+        if (i + d < n) multiply(d, i + d);
+        load(d, min(i + d + DEEP, n - 1));
       }
     }
-#pragma unroll
-    for (int d = 0; d < DEEP; ++d) multiply(d, i + d);
-    i += DEEP;
   }
-#pragma unroll
-  for (int d = 0; d < DEEP - 1; ++d)
-    if (i + d < n) load(d, i + d);
-#pragma unroll
-  for (int d = 0; d < DEEP - 1; ++d)
-    if (i + d < n) multiply(d, i + d);
   if (first + n * KG * STEP < end) {  // the columns past the last whole step of all groups
     const int k0 = first + (n * KG + kg) * STEP + c8 * PER;
 #pragma unroll
