@@ -45,21 +45,6 @@ __device__ __forceinline__ int64_t row_at(const AdapterArgs& a, int place) {
   return min(max(r, (int64_t)0), (int64_t)a.rows - 1);
 }
 
-// Inclusive sums over the lanes of a wave, on the vector unit.
-__device__ __forceinline__ int wave_scan(int v) {
-  auto step = [&](auto ctrl, auto rows) {
-    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
-  };
-  using std::integral_constant;
-  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
-  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
-  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
-  return v;
-}
-
 // The places of tile `id` of bm: adapter e's are offsets[e] .. offsets[e+1] - 1, and -1 has those
 // before the first and from the last on.  Every wave looks for itself, 64 groups at a time; false
 // past the last tile.  NONE: with the places of no adapter; otherwise of the adapters alone, one

@@ -51,6 +51,21 @@ struct Most {
   __device__ __forceinline__ X operator()(X a, X b) const { return max(a, b); }
 };
 
+// Inclusive sums over the lanes of a wave, on the vector unit.
+__device__ __forceinline__ int wave_scan(int v) {
+  auto step = [&](auto ctrl, auto rows) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+  return v;
+}
+
 // COUNT neighbouring values as they are, from p on, of any alignment.
 template <class T, int COUNT>
 using Raw = typename T::type __attribute__((ext_vector_type(COUNT)));

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kGroupThreads) void ex_group_place_kernel(GroupArgs
     if (gridDim.x == 1) {
       for (int w = 0; w < kGroupWaves; ++w) all += count[w][e];
     } else {
-#pragma unroll 4
+#pragma unroll 16
       for (int g = 0; g < (int)gridDim.x; ++g) {
         const int c = a.hist[(int64_t)g * (a.E + 1) + e];
         all += c;
@@ -80,24 +80,21 @@ __global__ __launch_bounds__(kGroupThreads) void ex_group_place_kernel(GroupArgs
     int carry = 0;
     for (int base = 0; base <= a.E; base += 64) {
       const int e = base + lane, c = e <= a.E ? total[e] : 0;
-      int sum = c;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int up = __shfl_up(sum, d);
-        if (lane >= d) sum += up;
-      }
+      const int sum = wave_scan(c);
       if (e <= a.E) {
         total[e] = carry + sum - c;
         if (blockIdx.x == 0) a.offsets[e] = carry + sum - c;
       }
-      carry += __shfl(sum, 63);
+      carry += __builtin_amdgcn_readlane(sum, 63);
     }
   }
   __syncthreads();
+  int next = first < end ? expert_of(a, min(first + lane, end - 1)) : 0;
   for (int64_t base = first; base < end; base += 64) {  // (the same for all lanes of a wave)
     const int64_t i = base + lane;
     const bool in = i < end;
-    const int e = in ? expert_of(a, i) : 0;
+    const int e = next;
+    next = expert_of(a, min(i + 64, end - 1));  // (on its way while this one is placed)
     uint64_t same = __ballot(in);
     for (int b = 0; b < a.bits; ++b) {
       const bool one = (e >> b) & 1;

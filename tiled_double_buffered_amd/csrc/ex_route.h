@@ -71,6 +71,16 @@ __device__ __forceinline__ void load_logits(const void* X, int64_t at, int E, in
   for (int v = 0; v < V; ++v) x[v] = column<L, V>(lane, v) < E ? x[v] : -__builtin_inff();
 }
 
+// exp(x) for x <= 0 (and NaN), to 2^-22 of it: 2^(x log2 e), the product to 48 bits, as its rounding
+// would count |x| times.  Below the smallest normal number it may be 0.
+__device__ __forceinline__ float exp_below(float x) {
+  constexpr float hi = 1.44269502e+00f, lo = 1.92596303e-08f;  // log2 e = hi + lo
+  const float y = fmaxf(x, -1000.0f) * hi;
+  const float rest = fmaf(fmaxf(x, -1000.0f), lo, fmaf(fmaxf(x, -1000.0f), hi, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return x == x ? fmaf(e * rest, 0.693147181f, e) : x;
+}
+
 // x becomes its softmax's numerators, over the largest; returns one over their sum.
 template <int L, int V>
 __device__ __forceinline__ float exponentials(float* x) {
@@ -81,7 +91,7 @@ __device__ __forceinline__ float exponentials(float* x) {
   float z = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    x[v] = expf(x[v] - m);
+    x[v] = exp_below(x[v] - m);
     z += x[v];
   }
   return 1.0f / over_lanes<L>(z, Add{});
@@ -99,7 +109,7 @@ __device__ inline void finish_route(const RouteArgs& a, const float* p, const in
   float sum = 0.0f;
   int32_t count = 0;
   if (e < E) {
-#pragma unroll 4
+#pragma unroll 16
     for (int g = s; g < groups; g += split) {
       sum += p[(int64_t)g * E + e];
       count += n[(int64_t)g * (E + 1) + e];
@@ -185,7 +195,7 @@ __global__ __launch_bounds__(kRouteThreads) void ex_route_kernel(RouteArgs a) {
       }
     }
     // (a NaN is the largest, and makes the gates NaN as it does the probabilities)
-    float gate = expert >= 0 ? expf(of_key(mine) - top) * inv : 0.0f;
+    float gate = expert >= 0 ? exp_below(of_key(mine) - top) * inv : 0.0f;
     if (a.norm) {
       const float sum = over_lanes<L>(gate, Add{});
       if (expert >= 0) gate /= sum;
