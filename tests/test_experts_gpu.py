@@ -292,6 +292,35 @@ def test_adapters_sizes(size, dtype):
     _check_adapters(y, x, a, b, *_groups(sizes, T, K), s if T % 2 else None, d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("r", [8, 30, 64, 120])
+@pytest.mark.parametrize("T, sizes, K, N", [(8300, (3000, 0, 5200), 72, 136), (3500, (900, 1500, 1000), 264, 80),
+                                            (1100, (1000, 40), 520, 1032)], ids=str)
+def test_adapters_many_rows(T, sizes, K, N, r, dtype):
+    """Every way of sharing the rows out: tiles of 64 and of 32 places whose waves share a step, and
+    partial sums that are joined."""
+    y, x, a, b, d, s = _adapter_inputs(T, len(sizes), r, K, N, dtype, T + r)
+    _check_adapters(y, x, a, b, *_groups(sizes, T, r), s, d)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [8, 9, 63, 64, 65, 127, 128, 511, 1023])
+def test_adapters_every_end_of_the_wide_axis(K, dtype):
+    """The steps' ends, in both directions (K in, K out)."""
+    for T, sizes in ((20, (11, 9)), (8200, (4100, 4000))):
+        y, x, a, b, d, s = _adapter_inputs(T, 2, 20, K, K, dtype, K)
+        _check_adapters(y, x, a, b, *_groups(sizes, T, K), s, d)
+
+
+def test_adapters_of_many_requests():
+    """More groups than a wave looks at at once, most of them empty."""
+    sizes = [0] * 400
+    for i in (0, 63, 64, 65, 130, 255, 399):
+        sizes[i] = 1 + i % 40
+    y, x, a, b, d, s = _adapter_inputs(250, 400, 7, 40, 56, torch.bfloat16, 3)
+    _check_adapters(y, x, a, b, *_groups(sizes, 250, 3), s, d)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_adapters_rows_split_for_the_gradient(dtype):
     """One adapter with many rows: its gradients' rows are split over workgroups."""
@@ -763,3 +792,134 @@ def test_a_given_stream(call):
         torch.zeros(500, 700, device=DEV)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+# ---------------------------------------------------------------------- past 32-bit offsets
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 bytes and 2^31 elements: the last rows against the same rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T, N = 300000, 8192
+
+    def rows(cols):
+        return torch.randn(T, cols, generator=g, device=DEV, dtype=torch.float32).to(torch.bfloat16)
+    x, y = rows(N), rows(64)
+    assert x.numel() > 1 << 31
+    last = slice(T - 40, T)
+    # gated: x as gate and up; its gradient
+    leaf = x.requires_grad_()
+    h = tdb.gated_silu(leaf, checkpoint=True)
+    dx, = torch.autograd.grad(h, leaf, torch.ones_like(h))
+    few = x[last].detach().requires_grad_()
+    ref = tdb.gated_silu(few, checkpoint=True)
+    assert torch.equal(h[last], ref)
+    assert torch.equal(dx[last], torch.autograd.grad(ref, few, torch.ones_like(ref))[0])
+    del h, dx, ref
+    x = x.detach()
+    q, s = tdb.quantize_fp8(x)
+    back = tdb.dequantize_fp8(q, s)
+    assert torch.equal(back[last], tdb.dequantize_fp8(q[last], s[last]))
+    del q, s, back
+    # adapters: the wide axis in, and out
+    a, b = _randn(_gen(1), 2, 4, N, scale=0.01, dtype=torch.bfloat16), _randn(_gen(2), 2, 4, 64, dtype=torch.bfloat16)
+    order, offsets = torch.arange(T, device=DEV), torch.tensor([0, 1000, T], dtype=torch.int32, device=DEV)
+    few = (torch.arange(40, device=DEV), torch.tensor([0, 0, 40], dtype=torch.int32, device=DEV))
+    for ins, outs, p, r in ((x, y, a, b), (y, x, b, a)):
+        full = tdb.add_adapters(outs, ins, p, r, order, offsets)
+        ref = tdb.add_adapters(outs[last], ins[last], p, r, *few)
+        # (the contraction's order of sums depends on the rows: half a step of bf16 each)
+        assert float((full[last] - ref).abs().max()) <= 2.0 ** -8 * float(ref.abs().max())
+        del full
+    # router: 2^31 logits
+    z = x.view(-1, 1024)
+    gates, experts, _, _ = tdb.route_experts(z, 2)
+    ref = tdb.route_experts(z[-50:], 2)
+    assert torch.equal(gates[-50:], ref[0]) and torch.equal(experts[-50:], ref[1])
+
+
+# ------------------------------------------------------------------------------- as one layer
+def _plain_layer(layer, x, requests, valid):
+    """RoutedLayer without its shared layer in 64 bits, from elementary operations: (y, loss), of the
+    experts that the layer takes (they are compared on their own)."""
+    up = {n: getattr(layer, n).detach().double().cpu().requires_grad_() for n in ("router", "w_in", "w_out", "down", "up")}
+    z = x.detach().double().cpu().requires_grad_()
+    T, E, k = x.shape[0], layer.experts, layer.top
+    p = torch.softmax(z @ up["router"][0], 1)
+    with torch.no_grad():
+        logits = tdb.linear_grouped(x.detach().float(), layer.router.detach(), torch.tensor([0, T], dtype=torch.int32, device=DEV))
+        _, experts, counts, _ = tdb.route_experts(logits, k, valid=valid, renormalize=True)
+    experts, on = experts.cpu().long(), valid.cpu()
+    best = torch.topk(p.detach(), k, 1).values[:, -1]
+    assert (p.detach().gather(1, experts.clamp_min(0)).amin(1)[on] >= best[on] * (1 - 1e-4)).all()
+    g = p.gather(1, experts.clamp_min(0)) * on[:, None]
+    g = g / g.sum(1, keepdim=True).clamp_min(1e-300)
+    H = layer.w_out.shape[1]
+    y = torch.zeros_like(z)
+    for j in range(k):
+        e = experts[:, j].clamp_min(0)
+        h = torch.einsum("tk,tkn->tn", z, up["w_in"][e])
+        h = h[:, :H] * torch.sigmoid(h[:, :H]) * h[:, H:]
+        y = y + g[:, j, None] * torch.einsum("tk,tkn->tn", h, up["w_out"][e])
+    a = requests.cpu().clamp_min(0)
+    u = torch.einsum("tk,trk->tr", z, up["down"][a])
+    y = y + torch.einsum("tr,trn->tn", u, up["up"][a]) * (requests.cpu() >= 0)[:, None]
+    f = counts.cpu().double() / max(int(counts.sum()), 1)
+    loss = E * (f * (p * on[:, None]).sum(0)).sum() / int(on.sum())
+    return y, loss, z, up
+
+
+def test_routed_layer_as_a_whole():
+    """All operators together in FP32: results and every gradient against 64 bits.  Each is a chain of
+    at most six FP32 sums of up to 260 terms, and so within 6 * 2 * 260 u = 4e-4 of its norm even if
+    all roundings went one way."""
+    from tiled_double_buffered_amd.expert_layer import RoutedLayer
+    T, width, hidden = 90, 72, 130
+    layer = RoutedLayer(width, hidden, 6, DEV, top=2, adapters=3, rank=5, dtype=torch.float32, checkpoint=False)
+    with torch.no_grad():
+        layer.shared.zero_()
+    g = _gen(4)
+    x = _randn(g, T, width).requires_grad_()
+    requests = torch.randint(-1, 3, (T,), generator=g).to(DEV)
+    valid = (torch.arange(T) % 7 != 3).to(DEV)
+    dy = _randn(g, T, width)
+    y, loss = layer(x, requests, valid)
+    names = ("router", "w_in", "w_out", "down", "up")
+    got = torch.autograd.grad((y, loss), [x, *(getattr(layer, n) for n in names)], (dy, torch.tensor(3.0, device=DEV)))
+    ry, rloss, z, up = _plain_layer(layer, x, requests, valid)
+    ref = torch.autograd.grad((ry, rloss), [z, *(up[n] for n in names)], (dy.double().cpu(), torch.tensor(3.0, dtype=torch.float64)))
+    for name, a, b in zip(("y", "loss", "x", *names), (y, loss, *got), (ry, rloss, *ref)):
+        off = float((a.detach().double().cpu() - b.detach()).norm() / b.detach().norm())
+        assert off <= 4e-4, (name, off)
+
+
+def test_routed_layer_with_8_bit_checkpoints():
+    """The forward pass does not change; the gradients of what is kept move by the 8-bit rounding,
+    2^-4 of a value at most, twice (the hidden values' input, and they themselves)."""
+    from tiled_double_buffered_amd.expert_layer import RoutedLayer
+    x = _randn(_gen(1), 200, 256, dtype=torch.bfloat16)
+    requests = torch.randint(-1, 4, (200,), generator=_gen(2)).to(DEV)
+    res = []
+    for keep in (False, True):
+        layer = RoutedLayer(256, 192, 5, DEV, checkpoint=keep)
+        y, loss = layer(x, requests)
+        res.append((y, loss, *torch.autograd.grad((y.float().square().sum(), loss), layer.parameters())))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    for a, b in zip(res[0][2:], res[1][2:]):
+        assert float((a - b).float().norm() / a.float().norm()) <= 2 * 2.0 ** -4 + 2.0 ** -6
+
+
+def test_routed_layer_trains_and_serves():
+    from tiled_double_buffered_amd import expert_layer
+    layer = expert_layer.RoutedLayer(256, 128, 8, DEV, top=2)
+    losses, x, requests = expert_layer.train_routed(layer, 300, 256, 3, DEV)
+    assert len(losses) == 3 and all(math.isfinite(v) for pair in losses for v in pair)
+    serve = layer.served()
+    with torch.no_grad():
+        whole = serve(x, requests)
+        assert whole.shape == x.shape and torch.isfinite(whole.float()).all()
+        for n in (1, 7):
+            assert serve(x[:n], requests[:n]).shape == (n, 256)
+        # the experts and the adapters of one token are its own: a batch of it alone gives the same
+        # but for the tiles' order of sums
+        one = serve(x[5:6], requests[5:6]).float()
+        assert float((one - whole[5:6].float()).norm() / one.norm()) <= 2.0 ** -6
+    assert expert_layer.main(["--tokens", "64", "--width", "128", "--hidden", "64", "--experts", "4", "--steps", "2", "--top", "2"]) == 0

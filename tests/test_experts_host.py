@@ -52,6 +52,7 @@ def _route(rows=4, E=8, k=2, X=P[0], ldx=8, t=F32, valid=P[1], norm=0, gates=P[2
     (dict(loss=P[5]), tdb.ERR_ALIAS), (dict(counts=P[1]), tdb.ERR_ALIAS),
     (dict(rows=1 << 31), tdb.ERR_BAD_LD), (dict(ldx=1 << 61), tdb.ERR_TOO_LARGE),
     (dict(rows=1 << 31, n=1 << 40, ws=P[7]), tdb.ERR_TOO_LARGE),
+    (dict(rows=1 << 30, n=1 << 40, ws=P[7]), tdb.ERR_TOO_LARGE),  # counts past 32 bits
 ])
 def test_route_refusals(change, code):
     assert _route(**change) == code
@@ -240,6 +241,9 @@ def test_workspace_and_split_queries():
     assert tdb.gemm_adapters_grad_workspace(100000, 128, 16, 1, F32) > 0
     assert tdb.gemm_adapters_grad_workspace(-4, 128, 16, 1, F16) == tdb.ERR_NEGATIVE_DIM
     assert tdb.gemm_adapters_grad_workspace(4, 128, 16, 1, 3) == tdb.ERR_BAD_TYPE
+    most = (1 << 31) - 2000
+    assert tdb.gemm_adapters_grad_workspace(most, most, 128, most, F32) == 0  # one run each
+    assert 0 < tdb.gemm_adapters_grad_workspace(most, 16384, 128, most, F32) < 1 << 60
 
 
 def test_tensor_calls_refuse_what_they_cannot_take():

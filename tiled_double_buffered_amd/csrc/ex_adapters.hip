@@ -219,6 +219,7 @@ static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_
 #undef UP
 }
 
+// Bytes.  (Several runs there are only of 65536 columns or fewer, so that 64 bits hold them.)
 static int64_t grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
   const int64_t run = grad_run(rows, N, rank, bytes);
   return rows > run && N >= kLeastWide ? grad_runs(rows, E, run) * rank * N * 4 : 0;
@@ -255,7 +256,7 @@ static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
   // each expert's D has to end where the next begins, or it would be written twice
   if (E > 1 && (stride_d < 0 || (uint64_t)stride_d * b < (uint64_t)(one.hi - one.lo)))
     return GEMMF32_ERR_BAD_LD;
-  const int64_t need = grad_workspace(rows, N, rank, E, b);  // (fits: D's extent does)
+  const int64_t need = grad_workspace(rows, N, rank, E, b);
   if (workspace_bytes < need) return GEMMF32_ERR_BAD_LD;
   if (need && workspace == nullptr) return GEMMF32_ERR_NULL_PTR;
   if (need && !byte_range(workspace, 1, 0, 1, need, need, 1, &out[1])) return GEMMF32_ERR_TOO_LARGE;

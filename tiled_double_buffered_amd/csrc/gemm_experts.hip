@@ -80,7 +80,7 @@ static int run_route(int64_t rows, int64_t E, int64_t k, const void* X, int64_t 
   if (const int rc = route_sizes(rows, E, k, type)) return rc;
   const int64_t need = route_workspace(rows, E);
   if (ldx < E || workspace_bytes < need) return GEMMF32_ERR_BAD_LD;
-  if (rows > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (rows > kMaxDim / k) return GEMMF32_ERR_TOO_LARGE;  // (counts and their sum are 32-bit)
   if (counts == nullptr || sums == nullptr || loss == nullptr || (need && workspace == nullptr) ||
       (rows && (X == nullptr || gates == nullptr || experts == nullptr)))
     return GEMMF32_ERR_NULL_PTR;
@@ -117,7 +117,7 @@ static int run_route_grad(int64_t rows, int64_t E, int64_t k, const void* X, int
                           void* stream) {
   if (const int rc = route_sizes(rows, E, k, type)) return rc;
   if (ldx < E || lddx < E) return GEMMF32_ERR_BAD_LD;
-  if (rows > kMaxDim) return GEMMF32_ERR_TOO_LARGE;
+  if (rows > kMaxDim / k) return GEMMF32_ERR_TOO_LARGE;
   if (rows == 0) return GEMMF32_OK;
   if (X == nullptr || DX == nullptr || counts == nullptr || sums == nullptr ||
       (dgates && (gates == nullptr || experts == nullptr)))
