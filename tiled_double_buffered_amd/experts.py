@@ -424,19 +424,21 @@ def _unit_columns(w):
 
 # ------------------------------------------------------------------------------- gated unit
 def _gated(x, keep):
-    """(h, q, s): q and s None where nothing is kept."""
-    px, ldx = _matrix(x, "x", TYPES)
-    rows, N = x.shape[0], x.shape[1] // 2
+    """(h, q, s) of row-major x: q and s None where nothing is kept."""
+    rows, cols = x.shape
+    N = cols // 2
     h = x.new_empty((rows, N))
     q = s = pq = ps = None
     ldq = lds = 0
     if keep:
-        q = _rows16(rows, 2 * N, x.device)
+        q = _rows16(rows, cols, x.device)
         s = torch.empty((rows, 2 * _blocks(N)), dtype=torch.float32, device=x.device)
-        pq, ldq, ps, lds = q.data_ptr(), max(q.stride(0), 1), s.data_ptr(), max(s.shape[1], 1)
+        pq, ldq, ps, lds = q.data_ptr(), q.stride(0), s.data_ptr(), s.shape[1]
     if rows and N:
-        _check(load().gemm_gated(rows, N, px, max(ldx, 2 * N), TYPES[x.dtype], h.data_ptr(), N,
-                                 pq, ldq, ps, lds, _current(x)), "gemm_gated")
+        rc = load().gemm_gated(rows, N, x.data_ptr(), max(x.stride(0), cols), TYPES[x.dtype],
+                               h.data_ptr(), N, pq, ldq, ps, lds, _current(x))
+        if rc:
+            _check(rc, "gemm_gated")
     return h, q, s
 
 
@@ -444,24 +446,31 @@ class _Gated(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, keep):
         h, q, s = _gated(x, keep)
-        ctx.save_for_backward(None if keep else x, q, s)
+        if keep:
+            ctx.save_for_backward(q, s)
+        else:
+            ctx.save_for_backward(x)
         return h
 
     @staticmethod
     @_once
     def backward(ctx, dh):
-        x, q, s = ctx.saved_tensors
-        dh = dh if dh.is_contiguous() else _row_major(dh)
+        if not dh.is_contiguous():
+            dh = _row_major(dh)
         rows, N = dh.shape
         dx = dh.new_empty((rows, 2 * N))
         if rows and N:
-            ldd = max(dh.stride(0), N)  # (of one row, any)
-            if x is None:
+            kept = ctx.saved_tensors
+            if len(kept) == 2:
+                q, s = kept
                 kept = None, 0, q.data_ptr(), q.stride(0), s.data_ptr(), s.shape[1]
             else:
+                x, = kept
                 kept = x.data_ptr(), max(x.stride(0), 2 * N), None, 0, None, 0
-            _check(load().gemm_gated_grad(rows, N, *kept, dh.data_ptr(), ldd, dx.data_ptr(), 2 * N,
-                                          TYPES[dh.dtype], _current(dh)), "gemm_gated_grad")
+            rc = load().gemm_gated_grad(rows, N, *kept, dh.data_ptr(), max(dh.stride(0), N),
+                                        dx.data_ptr(), 2 * N, TYPES[dh.dtype], _current(dh))
+            if rc:
+                _check(rc, "gemm_gated_grad")
         return dx, None
 
 
@@ -480,13 +489,18 @@ def gated_silu(x, checkpoint=False):
         raise ValueError(f"x has {x.shape[-1]} columns: gate and up need as many each")
     if not x.is_cuda:
         raise ValueError("x must live on the GPU (the library takes device pointers)")
-    flat, keep = _row_major(_flat(x)), bool(checkpoint)
-    grads = x.requires_grad and torch.is_grad_enabled()
-    if _here(x, None):
-        h = _Gated.apply(flat, keep) if grads else _gated(flat, False)[0]
+    flat = x if x.dim() == 2 and x.is_contiguous() else _row_major(_flat(x))
+    if x.requires_grad and torch.is_grad_enabled():
+        if _here(x, None):
+            h = _Gated.apply(flat, bool(checkpoint))
+        else:
+            with _on(None, x):
+                h = _Gated.apply(flat, bool(checkpoint))
+    elif _here(x, None):
+        h = _gated(flat, False)[0]
     else:
         with _on(None, x):
-            h = _Gated.apply(flat, keep) if grads else _gated(flat, False)[0]
+            h = _gated(flat, False)[0]
     return h if x.dim() == 2 else h.view(*x.shape[:-1], x.shape[-1] // 2)
 
 
