@@ -12,6 +12,18 @@
 // FP32 instruction.  Both operands of these kernels lie across the contraction: a lane loads 8 k of
 // 8 neighbouring columns, which is all that its fragments need of either instruction, so that
 // nothing moves between lanes, and neighbouring lanes load and store neighbouring columns.
+//
+// Bound by memory, and by how evenly the groups fill the chip (bf16, each pass on other rows):
+//   down  8192 x 4096, rank 32: 17 us for 67 MB (3.9 TB/s); 25 with four uneven groups, whose 258
+//         tiles leave two for a second round; 4096 x 4096, rank 16: 10 us; one token each for 24
+//         adapters, rank 16: 4.9 us, the latency of three loads that wait for each other
+//   up    4096 x 11008, rank 16: 39 us for 180 MB (4.6 TB/s; a large copy reaches 5.0); 24 adapters
+//         of one token beside 4096 columns: 6.3 us
+//   grad  8192 x 4096, rank 32: 26 us for 67 MB and 4.3 for the sums: a workgroup lives 9 us, of
+//         which 3 are vector instructions (u's parts, turning) and most of the rest the chain from
+//         the offsets to the rows' numbers to the rows, and there are 2.25 rounds of workgroups
+// With one workgroup's loads guarded one by one (a branch each, at which all earlier ones have to
+// arrive) `up` took 84 us where it takes 39.
 #pragma once
 
 #include "ex_common.h"
@@ -227,7 +239,8 @@ constexpr int kWideThreads = 512;
 template <int RF>
 constexpr int kWideDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;
 template <class T, int RF, int RW>
-__global__ __launch_bounds__(kWideThreads, (RF <= 2 ? 4 : 2)) void ex_adapters_down_wide_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(kWideThreads, (RF <= 2 ? 4 : 2)) void ex_adapters_down_wide_kernel(
+    AdapterArgs a) {
   constexpr int PER = 16 / T::BYTES, STEP = kRowBytes / T::BYTES, DEEP = kWideDeep<RF>;
   constexpr int KG = 8 / RW, WROWS = RF * 16, LD = RF * 16 + 4;
   constexpr int OWN = (WROWS / 8 + RW - 1) / RW;  // loads of eight adapter rows a wave makes
