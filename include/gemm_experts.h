@@ -87,8 +87,10 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  *   take it as one split: for many rows, as they read U several times.
  * up: OUT[order[p]] = Y[order[p]] + (sum of U's splits)[p] B_e; places of no expert: Y alone.
  *   Y may be NULL (0).
- * grad: D_e (rank x N, row stride ldd, stride_d elements apart) = sum over the places p of e of
- *   U[p]^T X[order[p]]; an expert without rows gets zeros.
+ * grad: DA_e (rank x K, row stride ldda, stride_da elements apart) = sum over the places p of e of
+ *   V[p]^T X[order[p]], and DB_e (rank x N) = the same of U[p]^T DOUT[order[p]]; an expert without
+ *   rows gets zeros.  Where only one is wanted the other's K or N is 0 (and its other arguments are
+ *   not looked at).
  * gemm_adapters_splits: the number of splits that `down` should make, at least 1.
  * gemm_adapters_grad_workspace: bytes of workspace that `grad` needs, as in gemm_route. */
 int gemm_adapters_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t *order,
@@ -99,12 +101,15 @@ int gemm_adapters_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int
                      const int32_t *offsets, const float *U, int splits, const void *B,
                      int64_t ldb, int64_t stride_b, const void *Y, int64_t ldy, void *OUT,
                      int64_t ldo, int type, void *stream);
-int gemm_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_t *order,
-                       const int32_t *offsets, const float *U, int splits, const void *X,
-                       int64_t ldx, void *D, int64_t ldd, int64_t stride_d, void *workspace,
+int gemm_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_t *order,
+                       const int32_t *offsets, int64_t K, const float *V, int v_splits,
+                       const void *X, int64_t ldx, void *DA, int64_t ldda, int64_t stride_da,
+                       int64_t N, const float *U, int u_splits, const void *DOUT, int64_t ldd,
+                       void *DB, int64_t lddb, int64_t stride_db, void *workspace,
                        int64_t workspace_bytes, int type, void *stream);
 int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E);
-int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int type);
+int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t K, int64_t N, int64_t rank, int64_t E,
+                                     int type);
 
 /* H = silu(G) * U, silu(g) = g / (1 + exp(-g)): X is rows x 2N, G its first N columns and U the
  * others; H rows x N.  Q, S (both or neither): G and U in 8 bits as gemm_fp8_quantize gives them,

@@ -324,7 +324,7 @@ def test_adapters_of_many_requests():
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_adapters_rows_split_for_the_gradient(dtype):
     """One adapter with many rows: its gradients' rows are split over workgroups."""
-    assert tdb.gemm_adapters_grad_workspace(3001, 136, 24, 1, 0) > 0
+    assert tdb.gemm_adapters_grad_workspace(3001, 136, 200, 24, 1, 0) > 0
     y, x, a, b, d, s = _adapter_inputs(3001, 1, 24, 136, 200, dtype, 1)
     _check_adapters(y, x, a, b, *_groups((2900,), 3001, 3), s, d)
 

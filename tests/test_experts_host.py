@@ -138,25 +138,29 @@ def test_up_refusals(change, code):
     assert _up(**change) == code
 
 
-def _grad(rows=4, N=64, r=8, E=2, order=P[0], off=P[1], U=P[2], splits=1, X=P[3], ldx=64, D=P[4],
-          ldd=64, sD=512, ws=None, n=0, t=BF16):
-    return tdb.gemm_adapters_grad(rows, N, r, E, order, off, U, splits, X, ldx, D, ldd, sD, ws, n, t,
-                                  None)
+def _grad(rows=4, r=8, E=2, order=P[0], off=P[1], K=64, V=P[2], vs=1, X=P[3], ldx=64, DA=P[4], ldda=64,
+          sA=512, N=32, U=P[5], us=1, DO=P[6], ldd=32, DB=P[7], lddb=32, sB=256, ws=None, n=0, t=BF16):
+    return tdb.gemm_adapters_grad(rows, r, E, order, off, K, V, vs, X, ldx, DA, ldda, sA, N, U, us, DO,
+                                  ldd, DB, lddb, sB, ws, n, t, None)
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(E=-1), tdb.ERR_NEGATIVE_DIM), (dict(t=5), tdb.ERR_BAD_TYPE),
-    (dict(r=129), tdb.ERR_BAD_CONFIG), (dict(ldx=63), tdb.ERR_BAD_LD), (dict(ldd=63), tdb.ERR_BAD_LD),
-    (dict(sD=511), tdb.ERR_BAD_LD), (dict(sD=-512), tdb.ERR_TOO_LARGE),
+    (dict(E=-1), tdb.ERR_NEGATIVE_DIM), (dict(N=-1), tdb.ERR_NEGATIVE_DIM), (dict(t=5), tdb.ERR_BAD_TYPE),
+    (dict(r=129), tdb.ERR_BAD_CONFIG), (dict(vs=0), tdb.ERR_BAD_CONFIG), (dict(us=65), tdb.ERR_BAD_CONFIG),
+    (dict(ldx=63), tdb.ERR_BAD_LD), (dict(ldda=63), tdb.ERR_BAD_LD), (dict(ldd=31), tdb.ERR_BAD_LD),
+    (dict(sA=511), tdb.ERR_BAD_LD), (dict(sB=255), tdb.ERR_BAD_LD),
     (dict(rows=100000), tdb.ERR_BAD_LD), (dict(rows=100000, n=1 << 30), tdb.ERR_NULL_PTR),
-    (dict(D=None), tdb.ERR_NULL_PTR), (dict(X=None), tdb.ERR_NULL_PTR),
-    (dict(D=P[4] + 1), tdb.ERR_MISALIGNED), (dict(U=P[2] + 2), tdb.ERR_MISALIGNED),
-    (dict(D=P[3]), tdb.ERR_ALIAS), (dict(D=P[2]), tdb.ERR_ALIAS), (dict(D=P[1]), tdb.ERR_ALIAS),
+    (dict(DA=None), tdb.ERR_NULL_PTR), (dict(X=None), tdb.ERR_NULL_PTR), (dict(DB=None), tdb.ERR_NULL_PTR),
+    (dict(order=None), tdb.ERR_NULL_PTR), (dict(off=None), tdb.ERR_NULL_PTR),
+    (dict(DA=P[4] + 1), tdb.ERR_MISALIGNED), (dict(U=P[5] + 4), tdb.ERR_MISALIGNED),
+    (dict(order=P[0] + 4), tdb.ERR_MISALIGNED), (dict(DB=P[3]), tdb.ERR_ALIAS), (dict(DA=P[7]), tdb.ERR_ALIAS),
+    (dict(DA=P[2]), tdb.ERR_ALIAS), (dict(DB=P[1]), tdb.ERR_ALIAS),
     (dict(rows=100000, n=1 << 30, ws=P[4]), tdb.ERR_ALIAS), (dict(rows=1 << 31), tdb.ERR_TOO_LARGE),
+    (dict(K=0, N=0, order=None), tdb.OK), (dict(N=0, DA=None), tdb.ERR_NULL_PTR),
+    (dict(K=0, DA=None, X=None, V=None, DB=P[6]), tdb.ERR_ALIAS),
 ])
 def test_adapter_grad_refusals(change, code):
-    got = _grad(**change)
-    assert got == code or (change.get("sD") == -512 and got == tdb.ERR_BAD_LD)
+    assert _grad(**change) == code
 
 
 def _gated(rows=4, N=200, X=P[0], ldx=400, t=BF16, H=P[1], ldh=200, Q=P[2], ldq=400, S=P[3], lds=4):
@@ -216,7 +220,7 @@ def test_empty_calls_launch_nothing():
     assert _down(E=0, A=None) == tdb.OK
     assert _up(rows=0, O=None) == tdb.OK
     assert _up(N=0, O=None) == tdb.OK
-    assert _grad(r=0, D=None) == tdb.OK
+    assert _grad(r=0, DA=None) == tdb.OK
     assert _gated(rows=0, X=None) == tdb.OK
     assert _gated_grad(N=0, DX=None) == tdb.OK
     assert _dequantize(cols=0, Q=None) == tdb.OK
@@ -237,13 +241,13 @@ def test_workspace_and_split_queries():
     assert tdb.gemm_adapters_splits(100000, 4096, 16, 4) == 1
     assert tdb.gemm_adapters_splits(0, 0, 1, 0) == 1
     assert tdb.gemm_adapters_splits(1, 4096, 129, 4) == tdb.ERR_BAD_CONFIG
-    assert tdb.gemm_adapters_grad_workspace(4, 4096, 16, 4, BF16) == 0
-    assert tdb.gemm_adapters_grad_workspace(100000, 128, 16, 1, F32) > 0
-    assert tdb.gemm_adapters_grad_workspace(-4, 128, 16, 1, F16) == tdb.ERR_NEGATIVE_DIM
-    assert tdb.gemm_adapters_grad_workspace(4, 128, 16, 1, 3) == tdb.ERR_BAD_TYPE
+    assert tdb.gemm_adapters_grad_workspace(4, 4096, 4096, 16, 4, BF16) == 0
+    assert tdb.gemm_adapters_grad_workspace(100000, 128, 0, 16, 1, F32) > 0
+    assert tdb.gemm_adapters_grad_workspace(-4, 128, 128, 16, 1, F16) == tdb.ERR_NEGATIVE_DIM
+    assert tdb.gemm_adapters_grad_workspace(4, 128, 128, 16, 1, 3) == tdb.ERR_BAD_TYPE
     most = (1 << 31) - 2000
-    assert tdb.gemm_adapters_grad_workspace(most, most, 128, most, F32) == 0  # one run each
-    assert 0 < tdb.gemm_adapters_grad_workspace(most, 4096, 128, most, F32) < 1 << 60
+    assert tdb.gemm_adapters_grad_workspace(most, most, most, 128, most, F32) == 0  # one run each
+    assert 0 < tdb.gemm_adapters_grad_workspace(most, 4096, 1024, 128, most, F32) < 1 << 60
 
 
 def test_tensor_calls_refuse_what_they_cannot_take():

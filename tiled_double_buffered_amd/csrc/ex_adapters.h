@@ -535,6 +535,12 @@ __global__ __launch_bounds__(256) void ex_adapters_up_deep_kernel(AdapterArgs a)
 }
 
 // ------------------------------------------------------------------------------------ grad
+// One gradient, or both of a step in one launch: the first `wgs` workgroups have the first.
+struct GradArgs {
+  AdapterArgs set[2];
+  int wgs;
+};
+
 // 128 columns of RF * 16 rows of one adapter's gradient, from a run of its places.  The waves take
 // turns at 32 of these and add up through LDS.  An adapter with one run has its result; those of one
 // with several are added by another launch.  (Runs of one length, however the places are shared out:
@@ -622,7 +628,10 @@ __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int
   }
 }
 template <class T, int RF>
-__global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD) void ex_adapters_grad_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD) void
+ex_adapters_grad_kernel(GradArgs args) {
+  const bool second = (int)blockIdx.x >= args.wgs;
+  const AdapterArgs& a = args.set[second ? 1 : 0];
   constexpr int WAVES = GradShape<RF>::WAVES, N = RF * 8 * 4;
   __shared__ float red[WAVES / 2][N][64];
   constexpr int LD = GradShape<RF>::LD;
@@ -630,7 +639,7 @@ __global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD)
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   // workgroups: columns, then blocks of the rank, then runs
   const int rb = (a.rank + RF * 16 - 1) / (RF * 16);
-  int id = blockIdx.x;
+  int id = (int)blockIdx.x - (second ? args.wgs : 0);
   const int n0 = id % a.tiles_n * kWaveCols;
   id /= a.tiles_n;
   const int r0 = id % rb * (RF * 16);
@@ -682,11 +691,14 @@ __global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD)
 // The sums of the adapters that have several runs.  A workgroup has 2048 neighbouring values of one
 // adapter's gradient, a thread eight of one row.
 template <class T>
-__global__ __launch_bounds__(256) void ex_adapters_sum_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(256) void ex_adapters_sum_kernel(GradArgs args) {
+  const bool second = (int)blockIdx.x >= args.wgs;
+  const AdapterArgs& a = args.set[second ? 1 : 0];
+  const unsigned wg = blockIdx.x - (second ? args.wgs : 0);
   const int per = (a.N + 7) / 8;
   const int64_t blocks = ((int64_t)a.rank * per + 255) / 256;
-  const int e = (int)(blockIdx.x / blocks);
-  const int64_t i = (blockIdx.x - e * blocks) * 256 + threadIdx.x;
+  const int e = (int)(wg / blocks);
+  const int64_t i = (wg - e * blocks) * 256 + threadIdx.x;
   // its first run: the runs of the adapters before it
   int before = 0, runs = 0;
   for (int base = 0; base <= e; base += 64) {

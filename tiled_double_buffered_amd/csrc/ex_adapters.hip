@@ -56,10 +56,10 @@ static int64_t grad_blocks(int64_t N, int64_t rank, int bytes) {
   const int64_t per = 16 * grad_fragments(rank, bytes);
   return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per);
 }
-// Places of a run in `grad`: so many that there are two workgroups a CU, but 256 at least (a turn of
-// eight waves); and the most runs that there can be.
-static int64_t grad_run(int64_t rows, int64_t N, int64_t rank, int bytes) {
-  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(grad_blocks(N, rank, bytes), 1), 1);
+// Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
+// two workgroups a CU, but 256 at least (a turn of eight waves); and the most runs that there can be.
+static int64_t grad_run(int64_t rows, int64_t blocks) {
+  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 1);
   return std::max<int64_t>(((rows + per - 1) / per + 255) / 256 * 256, 256);
 }
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
@@ -219,78 +219,115 @@ static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_
 #undef UP
 }
 
-// Bytes.  (Several runs there are only of 65536 columns or fewer, so that 64 bits hold them.)
-static int64_t grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int bytes) {
-  const int64_t run = grad_run(rows, N, rank, bytes);
+// One of the gradients of a step, N columns wide.
+struct GradSide {
+  int64_t N;
+  const float* U;
+  int splits;
+  const void* X;
+  int64_t ldx;
+  void* D;
+  int64_t ldd, stride_d;
+  bool wide() const { return N >= kLeastWide; }
+};
+static int64_t side_blocks(int64_t N, int64_t rank, int bytes) {
+  return N >= kLeastWide ? grad_blocks(N, rank, bytes) : 0;
+}
+// Bytes of the runs of a gradient.  (Several runs there are only of 65536 columns or fewer, so that
+// 64 bits hold them.)
+static int64_t side_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int64_t run) {
   return rows > run && N >= kLeastWide ? grad_runs(rows, E, run) * rank * N * 4 : 0;
 }
 
-static int run_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E,
-                             const int64_t* order, const int32_t* offsets, const float* U,
-                             int splits, const void* X, int64_t ldx, void* D, int64_t ldd,
-                             int64_t stride_d, void* workspace, int64_t workspace_bytes, int type,
-                             void* stream) {
-  if (bad_dims(rows, N, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
+static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_t* order,
+                             const int32_t* offsets, const GradSide (&sides)[2], void* workspace,
+                             int64_t workspace_bytes, int type, void* stream) {
+  for (const GradSide& s : sides)
+    if (bad_dims(rows, s.N, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
-  if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS) return GEMMF32_ERR_BAD_CONFIG;
-  if (ldx < at_least_1(N) || ldd < at_least_1(N)) return GEMMF32_ERR_BAD_LD;
-  if (too_large(rows, N, E)) return GEMMF32_ERR_TOO_LARGE;
-  if (N == 0 || rank == 0 || E == 0) return GEMMF32_OK;
+  if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
+  if (rank == 0 || E == 0) return GEMMF32_OK;
   const int b = type_bytes(type);
   const bool reads = rows > 0;
   const int64_t ldu = u_columns((int)rank);
-  Range out[2], one, in[4];
-  if (D == nullptr || offsets == nullptr ||
-      (reads && (order == nullptr || U == nullptr || X == nullptr)))
-    return GEMMF32_ERR_NULL_PTR;
-  if (misaligned(D, b) || misaligned(X, b) || misaligned(U, 16) || misaligned(order, 8) ||
-      misaligned(offsets, 4) || misaligned(workspace, 8))
+  const int64_t run =
+      grad_run(rows, side_blocks(sides[0].N, rank, b) + side_blocks(sides[1].N, rank, b));
+  Range out[3], in[6];
+  int64_t need = 0;
+  for (int i = 0; i < 2; ++i) {
+    const GradSide& s = sides[i];
+    if (s.N == 0) continue;
+    if (s.splits < 1 || s.splits > GEMM_ADAPTERS_MAX_SPLITS) return GEMMF32_ERR_BAD_CONFIG;
+    if (s.ldx < s.N || s.ldd < s.N) return GEMMF32_ERR_BAD_LD;
+    if (too_large(rows, s.N, E)) return GEMMF32_ERR_TOO_LARGE;
+    if (s.D == nullptr || offsets == nullptr ||
+        (reads && (order == nullptr || s.U == nullptr || s.X == nullptr)))
+      return GEMMF32_ERR_NULL_PTR;
+    if (misaligned(s.D, b) || misaligned(s.X, b) || misaligned(s.U, 16))
+      return GEMMF32_ERR_MISALIGNED;
+    Range one;
+    if (!byte_range(s.D, E, s.stride_d, rank, s.N, s.ldd, b, &out[i]) ||
+        !byte_range(s.D, 1, 0, rank, s.N, s.ldd, b, &one) ||
+        (reads && (!byte_range(s.U, s.splits, rows * ldu, rows, ldu, ldu, 4, &in[2 * i]) ||
+                   !byte_range(s.X, 1, 0, rows, s.N, s.ldx, b, &in[2 * i + 1]))))
+      return GEMMF32_ERR_TOO_LARGE;
+    // each expert's D has to end where the next begins, or it would be written twice
+    if (E > 1 && (s.stride_d < 0 || (uint64_t)s.stride_d * b < (uint64_t)(one.hi - one.lo)))
+      return GEMMF32_ERR_BAD_LD;
+    need += side_workspace(rows, s.N, rank, E, run);
+  }
+  if (sides[0].N == 0 && sides[1].N == 0) return GEMMF32_OK;
+  if (misaligned(order, 8) || misaligned(offsets, 4) || misaligned(workspace, 8))
     return GEMMF32_ERR_MISALIGNED;
-  if (!byte_range(D, E, stride_d, rank, N, ldd, b, &out[0]) ||
-      !byte_range(D, 1, 0, rank, N, ldd, b, &one) ||
-      !byte_range(offsets, 1, 0, 1, E + 1, E + 1, 4, &in[0]) ||
-      (reads && (!byte_range(order, 1, 0, 1, rows, rows, 8, &in[1]) ||
-                 !byte_range(U, splits, rows * ldu, rows, ldu, ldu, 4, &in[2]) ||
-                 !byte_range(X, 1, 0, rows, N, ldx, b, &in[3]))))
-    return GEMMF32_ERR_TOO_LARGE;
-  // each expert's D has to end where the next begins, or it would be written twice
-  if (E > 1 && (stride_d < 0 || (uint64_t)stride_d * b < (uint64_t)(one.hi - one.lo)))
-    return GEMMF32_ERR_BAD_LD;
-  const int64_t need = grad_workspace(rows, N, rank, E, b);
   if (workspace_bytes < need) return GEMMF32_ERR_BAD_LD;
   if (need && workspace == nullptr) return GEMMF32_ERR_NULL_PTR;
-  if (need && !byte_range(workspace, 1, 0, 1, need, need, 1, &out[1])) return GEMMF32_ERR_TOO_LARGE;
-  if (overlap(out[0], out[1])) return GEMMF32_ERR_ALIAS;
-  for (const Range& r : in)
-    if (overlap(out[0], r) || overlap(out[1], r)) return GEMMF32_ERR_ALIAS;
-  AdapterArgs a{};
-  a.X = X, a.C = D, a.offsets = offsets, a.order = order, a.U = (float*)U;
-  a.part = (float*)workspace, a.ldx = ldx, a.ldc = ldd, a.stride_c = stride_d;
-  a.rows = (int)rows, a.N = (int)N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
-  a.splits = splits, a.tiles_n = (int)((N + kWaveCols - 1) / kWaveCols);
-  a.run = (int)grad_run(rows, N, rank, b);
-  a.runs = (int)std::min<int64_t>(grad_runs(rows, E, a.run), kMaxDim);
-  if (N < kLeastWide) {
-    if (!fits_grid(E * rank, 256)) return GEMMF32_ERR_TOO_LARGE;
-#define FEW(T) &ex_adapters_grad_few_kernel<T>
-    return launch(BY_TYPE(type, FEW), dim3((unsigned)(E * rank)), 256, &a, stream);
-#undef FEW
-  }
+  if ((need && !row_range(workspace, need, 1, &out[2])) || !row_range(offsets, E + 1, 4, &in[4]) ||
+      (reads && !row_range(order, rows, 8, &in[5])))
+    return GEMMF32_ERR_TOO_LARGE;
+  if (any_overlap(out, in)) return GEMMF32_ERR_ALIAS;
+
   const int fragments = grad_fragments(rank, b);
   const int threads = 64 * (fragments <= 2 ? GradShape<1>::WAVES : GradShape<4>::WAVES);
-  int64_t wgs;
-  if (__builtin_mul_overflow(grad_blocks(N, rank, b), grad_runs(rows, E, a.run), &wgs) ||
-      !fits_grid(wgs, threads))
+  GradArgs wide{};
+  int64_t wgs[2] = {}, sums[2] = {};
+  int count = 0;
+  float* part = (float*)workspace;
+  for (const GradSide& s : sides) {
+    if (s.N == 0) continue;
+    AdapterArgs a{};
+    a.X = s.X, a.C = s.D, a.offsets = offsets, a.order = order, a.U = (float*)s.U;
+    a.part = part, a.ldx = s.ldx, a.ldc = s.ldd, a.stride_c = s.stride_d;
+    a.rows = (int)rows, a.N = (int)s.N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
+    a.splits = s.splits, a.tiles_n = (int)((s.N + kWaveCols - 1) / kWaveCols);
+    a.run = (int)run, a.runs = (int)std::min<int64_t>(grad_runs(rows, E, run), kMaxDim);
+    if (s.wide()) {
+      if (__builtin_mul_overflow(side_blocks(s.N, rank, b), grad_runs(rows, E, run), &wgs[count]))
+        return GEMMF32_ERR_TOO_LARGE;
+      sums[count] = E * ((rank * ((s.N + 7) / 8) + 255) / 256);
+      part += side_workspace(rows, s.N, rank, E, run) / 4;
+      wide.set[count++] = a;
+      continue;
+    }
+    if (!fits_grid(E * rank, 256)) return GEMMF32_ERR_TOO_LARGE;
+#define FEW(T) &ex_adapters_grad_few_kernel<T>
+    if (const int rc = launch(BY_TYPE(type, FEW), dim3((unsigned)(E * rank)), 256, &a, stream))
+      return rc;
+#undef FEW
+  }
+  if (count == 0) return GEMMF32_OK;
+  if (wgs[0] > kMaxDim || wgs[1] > kMaxDim || !fits_grid(wgs[0] + wgs[1], threads) ||
+      !fits_grid(sums[0] + sums[1], 256))
     return GEMMF32_ERR_TOO_LARGE;
-  const int64_t sums = E * ((rank * ((N + 7) / 8) + 255) / 256);
-  if (!fits_grid(sums, 256)) return GEMMF32_ERR_TOO_LARGE;
+  wide.wgs = (int)wgs[0];
 #define GRAD(T) grad_kernel<T>(fragments)
-  if (const int rc = launch(BY_TYPE(type, GRAD), dim3((unsigned)wgs), threads, &a, stream)) return rc;
+  if (const int rc = launch(BY_TYPE(type, GRAD), dim3((unsigned)(wgs[0] + wgs[1])), threads, &wide,
+                            stream))
+    return rc;
 #undef GRAD
-  if (rows <= a.run) return GEMMF32_OK;  // (one run each)
-
+  if (rows <= run) return GEMMF32_OK;  // (one run each)
+  wide.wgs = (int)sums[0];
 #define SUM(T) &ex_adapters_sum_kernel<T>
-  return launch(BY_TYPE(type, SUM), dim3((unsigned)sums), 256, &a, stream);
+  return launch(BY_TYPE(type, SUM), dim3((unsigned)(sums[0] + sums[1])), 256, &wide, stream);
 #undef SUM
 }
 
@@ -314,12 +351,16 @@ int gemm_adapters_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int
                         ldo, type, stream);
 }
 
-int gemm_adapters_grad(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_t* order,
-                       const int32_t* offsets, const float* U, int splits, const void* X,
-                       int64_t ldx, void* D, int64_t ldd, int64_t stride_d, void* workspace,
+int gemm_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_t* order,
+                       const int32_t* offsets, int64_t K, const float* V, int v_splits,
+                       const void* X, int64_t ldx, void* DA, int64_t ldda, int64_t stride_da,
+                       int64_t N, const float* U, int u_splits, const void* DOUT, int64_t ldd,
+                       void* DB, int64_t lddb, int64_t stride_db, void* workspace,
                        int64_t workspace_bytes, int type, void* stream) {
-  return gemmlp::run_adapters_grad(rows, N, rank, E, order, offsets, U, splits, X, ldx, D, ldd,
-                                   stride_d, workspace, workspace_bytes, type, stream);
+  return gemmlp::run_adapters_grad(rows, rank, E, order, offsets,
+                                   {{K, V, v_splits, X, ldx, DA, ldda, stride_da},
+                                    {N, U, u_splits, DOUT, ldd, DB, lddb, stride_db}},
+                                   workspace, workspace_bytes, type, stream);
 }
 
 int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
@@ -329,12 +370,16 @@ int gemm_adapters_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
   return gemmlp::adapter_splits(rows, K, rank, E);
 }
 
-int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int type) {
-  if (gemmlp::bad_dims(rows, N, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
+int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t K, int64_t N, int64_t rank, int64_t E,
+                                     int type) {
+  using namespace gemmlp;
+  if (bad_dims(rows, K, rank, E) || N < 0) return GEMMF32_ERR_NEGATIVE_DIM;
+  if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
   if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
-  if (gemmlp::too_large(rows, N, E)) return GEMMF32_ERR_TOO_LARGE;
-  if (!gemmlp::known_type(type)) return GEMMF32_ERR_BAD_TYPE;
-  return gemmlp::grad_workspace(rows, N, rank, E, gemmlp::type_bytes(type));
+  if (too_large(rows, std::max(K, N), E)) return GEMMF32_ERR_TOO_LARGE;
+  const int b = type_bytes(type);
+  const int64_t run = grad_run(rows, side_blocks(K, rank, b) + side_blocks(N, rank, b));
+  return side_workspace(rows, K, rank, E, run) + side_workspace(rows, N, rank, E, run);
 }
 
 }  // extern "C"

@@ -58,21 +58,6 @@ static int route_sizes(int64_t rows, int64_t E, int64_t k, int type) {
   return GEMMF32_OK;
 }
 
-// Outputs against each other and against inputs; unused ranges are empty and overlap nothing.
-template <int OUTS, int INS>
-static bool any_overlap(const Range (&out)[OUTS], const Range (&in)[INS]) {
-  for (int i = 0; i < OUTS; ++i) {
-    for (const Range& r : in)
-      if (overlap(out[i], r)) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i], out[j])) return true;
-  }
-  return false;
-}
-static bool row_range(const void* p, int64_t count, int64_t bytes, Range* r) {
-  return byte_range(p, 1, 0, 1, count, count, bytes, r);
-}
-
 static int run_route(int64_t rows, int64_t E, int64_t k, const void* X, int64_t ldx, int type,
                      const uint8_t* valid, int renormalize, float* gates, int32_t* experts,
                      int32_t* counts, int32_t* sums, float* loss, void* workspace,

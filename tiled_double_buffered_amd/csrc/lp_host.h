@@ -29,6 +29,21 @@ static inline bool byte_range(const void* p, int64_t count, int64_t stride, int6
 }
 static inline bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// Outputs against each other and against inputs; unused ranges are empty and overlap nothing.
+template <int OUTS, int INS>
+static inline bool any_overlap(const Range (&out)[OUTS], const Range (&in)[INS]) {
+  for (int i = 0; i < OUTS; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+static inline bool row_range(const void* p, int64_t count, int64_t bytes, Range* r) {
+  return byte_range(p, 1, 0, 1, count, count, bytes, r);
+}
+
 static inline bool known_type(int t) { return t == GEMM_LP_BF16 || t == GEMM_LP_F16 || t == GEMM_LP_F32; }
 static inline bool misaligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) != 0; }
 static inline int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }

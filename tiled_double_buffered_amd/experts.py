@@ -40,10 +40,11 @@ SIGNATURES = {
                                   _vp, _vp, _int, _int, _int, _vp]),
     "gemm_adapters_up": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp,
                                 _i64, _vp, _i64, _int, _vp]),
-    "gemm_adapters_grad": (_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i64, _vp,
-                                  _i64, _i64, _vp, _i64, _int, _vp]),
+    "gemm_adapters_grad": (_int, [_i64, _i64, _i64, _vp, _vp] +
+                           2 * [_i64, _vp, _int, _vp, _i64, _vp, _i64, _i64] +
+                           [_vp, _i64, _int, _vp]),
     "gemm_adapters_splits": (_int, [_i64, _i64, _i64, _i64]),
-    "gemm_adapters_grad_workspace": (_i64, [_i64, _i64, _i64, _i64, _int]),
+    "gemm_adapters_grad_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64, _int]),
     "gemm_gated": (_int, [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
     "gemm_gated_grad": (_int, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                                _int, _vp]),
@@ -101,8 +102,8 @@ def gemm_adapters_splits(rows, K, rank, E) -> int:
     return load().gemm_adapters_splits(rows, K, rank, E)
 
 
-def gemm_adapters_grad_workspace(rows, N, rank, E, type_code) -> int:
-    return load().gemm_adapters_grad_workspace(rows, N, rank, E, type_code)
+def gemm_adapters_grad_workspace(rows, K, N, rank, E, type_code) -> int:
+    return load().gemm_adapters_grad_workspace(rows, K, N, rank, E, type_code)
 
 
 def gemm_gated(*args) -> int:
@@ -309,19 +310,35 @@ def _up(u, splits, b, y, order, offsets):
     return out
 
 
-def _adapter_grad(u, splits, rank, x, E, order, offsets):
-    """E x rank x N: u^T x over each adapter's rows."""
-    rows, N = x.shape
-    lib, code = load(), TYPES[x.dtype]
-    d = x.new_empty((E, rank, N))
-    need = _size(lib.gemm_adapters_grad_workspace(rows, N, rank, E, code),
+_NO_SIDE = 0, None, 1, None, 0, None, 0, 0
+
+
+def _adapter_grads(shape, order, offsets, *sides):
+    """E x rank x width: u^T x over each adapter's rows, for each (u, splits, x) of two sides; None
+    for a side that is None."""
+    E, rank = shape
+    lib, like = load(), next(s[2] for s in sides if s is not None)
+    rows, code = like.shape[0], TYPES[like.dtype]
+    grads, args, widths = [], [], []
+    for s in sides:
+        if s is None:
+            grads.append(None)
+            args += _NO_SIDE
+            widths.append(0)
+            continue
+        u, splits, x = s
+        width = x.shape[1]
+        d = x.new_empty((E, rank, width))
+        grads.append(d)
+        args += (width, u.data_ptr(), splits, x.data_ptr(), _ld(x), d.data_ptr(), max(width, 1),
+                 rank * width)
+        widths.append(width)
+    need = _size(lib.gemm_adapters_grad_workspace(rows, *widths, rank, E, code),
                  "gemm_adapters_grad_workspace")
-    hold, pw = _workspace(need, x.device)
-    _check(lib.gemm_adapters_grad(rows, N, rank, E, order.data_ptr(), offsets.data_ptr(),
-                                  u.data_ptr(), splits, x.data_ptr(), _ld(x), d.data_ptr(),
-                                  max(N, 1), rank * N, pw, need, code, _current(x)),
-           "gemm_adapters_grad")
-    return d
+    hold, pw = _workspace(need, like.device)
+    _check(lib.gemm_adapters_grad(rows, rank, E, order.data_ptr(), offsets.data_ptr(), *args, pw,
+                                  need, code, _current(like)), "gemm_adapters_grad")
+    return grads
 
 
 class _Adapters(torch.autograd.Function):
@@ -340,15 +357,14 @@ class _Adapters(torch.autograd.Function):
     def backward(ctx, dout):
         need_y, need_x, need_a, need_b = ctx.needs_input_grad[:4]
         x, a, b, u, order, offsets, scale = ctx.saved_tensors
-        E, rank = ctx.size
         dx = da = db = None
-        if need_x or need_a or need_b:
-            rows = _row_major(dout)
-            if need_x or need_a:
-                v, splits = _down(rows, b, order, offsets, scale)
-                dx = _up(v, splits, a, None, order, offsets) if need_x else None
-                da = _adapter_grad(v, splits, rank, x, E, order, offsets) if need_a else None
-            db = _adapter_grad(u, ctx.splits, rank, rows, E, order, offsets) if need_b else None
+        rows = _row_major(dout)
+        if need_x or need_a:
+            v, splits = _down(rows, b, order, offsets, scale)
+            dx = _up(v, splits, a, None, order, offsets) if need_x else None
+        if need_a or need_b:
+            da, db = _adapter_grads(ctx.size, order, offsets, (v, splits, x) if need_a else None,
+                                    (u, ctx.splits, rows) if need_b else None)
         return dout if need_y else None, dx, da, db, None, None, None
 
 
