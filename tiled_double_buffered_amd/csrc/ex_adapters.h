@@ -545,18 +545,17 @@ struct GradArgs {
 // turns at 32 of these and add up through LDS.  An adapter with one run has its result; those of one
 // with several are added by another launch.  (Runs of one length, however the places are shared out:
 // with as many for each adapter the largest one decides.)
-template <int RF>
+template <int RF, int WAVES>
 struct GradShape {
-  static constexpr int WAVES = RF <= 2 ? 8 : 4;
   static constexpr int LD = RF * 16 + 4;  // numbers of a place in LDS
   static constexpr int PER_SIMD = RF == 4 ? 1 : 2;  // waves
 };
 // What one wave adds of the places first + 32 wave, + 32 WAVES and so on.  u and the rows' numbers
 // come by whole lines, through LDS of the wave's own (lds: 32 LD numbers).
-template <class T, int RF>
+template <class T, int RF, int WAVES>
 __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int end, int c, int r0,
                                             float* lds, float4v (&acc)[RF][8]) {
-  constexpr int WAVES = GradShape<RF>::WAVES, LD = GradShape<RF>::LD;
+  constexpr int LD = GradShape<RF, WAVES>::LD;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int64_t u_step = (int64_t)a.rows * a.ldu;
   for (int i0 = first + (threadIdx.x >> 6) * 32; i0 < end; i0 += WAVES * 32) {
@@ -627,14 +626,14 @@ __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int
     __builtin_amdgcn_wave_barrier();
   }
 }
-template <class T, int RF>
-__global__ __launch_bounds__(GradShape<RF>::WAVES * 64, GradShape<RF>::PER_SIMD) void
+template <class T, int RF, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, (GradShape<RF, WAVES>::PER_SIMD)) void
 ex_adapters_grad_kernel(GradArgs args) {
   const bool second = (int)blockIdx.x >= args.wgs;
   const AdapterArgs& a = args.set[second ? 1 : 0];
-  constexpr int WAVES = GradShape<RF>::WAVES, N = RF * 8 * 4;
+  constexpr int N = RF * 8 * 4;
   __shared__ float red[WAVES / 2][N][64];
-  constexpr int LD = GradShape<RF>::LD;
+  constexpr int LD = GradShape<RF, WAVES>::LD;
   static_assert(WAVES * 32 * LD <= WAVES / 2 * N * 64, "the waves' u lies where their sums meet");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   // workgroups: columns, then blocks of the rank, then runs
@@ -655,7 +654,7 @@ ex_adapters_grad_kernel(GradArgs args) {
   float* const lds = (float*)red + wave * 32 * LD;
   // (columns past the last are computed once more as the last ones)
   const int c = min(n0 + 8 * l16, a.N - 8);
-  grad_places<T, RF>(a, first, end, c, r0, lds, acc);
+  grad_places<T, RF, WAVES>(a, first, end, c, r0, lds, acc);
   __syncthreads();
   for (int d = WAVES / 2; d > 0; d /= 2) {
     if (wave >= d && wave < 2 * d) {

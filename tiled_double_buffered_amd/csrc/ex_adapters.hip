@@ -56,11 +56,16 @@ static int64_t grad_blocks(int64_t N, int64_t rank, int bytes) {
   const int64_t per = 16 * grad_fragments(rank, bytes);
   return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per);
 }
+// Waves of a workgroup of `grad`: four past rank 32, where they have the registers of a SIMD, and
+// where the adapters have fewer places than eight take in a turn.
+static int grad_waves(int64_t rows, int64_t rank, int64_t E, int bytes) {
+  return grad_fragments(rank, bytes) == 4 || rows < 256 * E ? 4 : 8;
+}
 // Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
-// two workgroups a CU, but 256 at least (a turn of eight waves); and the most runs that there can be.
-static int64_t grad_run(int64_t rows, int64_t blocks) {
-  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 1);
-  return std::max<int64_t>(((rows + per - 1) / per + 255) / 256 * 256, 256);
+// two workgroups a CU, but a turn of the waves at least; and the most runs that there can be.
+static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
+  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 1), turn = 32 * waves;
+  return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
 
@@ -87,12 +92,15 @@ static const void* up_kernel(int64_t rank, int places) {
                         : (const void*)&ex_adapters_up_kernel<T, 16>;
 }
 template <class T>
-static const void* grad_kernel(int fragments) {
+static const void* grad_kernel(int fragments, int waves) {
   if constexpr (T::BYTES == 2) {
-    if (fragments == 4) return (const void*)&ex_adapters_grad_kernel<T, 4>;
+    if (fragments == 4) return (const void*)&ex_adapters_grad_kernel<T, 4, 4>;
   }
-  return fragments == 1 ? (const void*)&ex_adapters_grad_kernel<T, 1>
-                        : (const void*)&ex_adapters_grad_kernel<T, 2>;
+  if (waves == 4)
+    return fragments == 1 ? (const void*)&ex_adapters_grad_kernel<T, 1, 4>
+                          : (const void*)&ex_adapters_grad_kernel<T, 2, 4>;
+  return fragments == 1 ? (const void*)&ex_adapters_grad_kernel<T, 1, 8>
+                        : (const void*)&ex_adapters_grad_kernel<T, 2, 8>;
 }
 #define BY_TYPE(type, f)                                     \
   ((type) == GEMM_LP_BF16  ? (const void*)f(Bf16)            \
@@ -250,8 +258,9 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
   const int b = type_bytes(type);
   const bool reads = rows > 0;
   const int64_t ldu = u_columns((int)rank);
+  const int waves = grad_waves(rows, rank, E, b), threads = 64 * waves;
   const int64_t run =
-      grad_run(rows, side_blocks(sides[0].N, rank, b) + side_blocks(sides[1].N, rank, b));
+      grad_run(rows, side_blocks(sides[0].N, rank, b) + side_blocks(sides[1].N, rank, b), waves);
   Range out[3], in[6];
   int64_t need = 0;
   for (int i = 0; i < 2; ++i) {
@@ -287,7 +296,6 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
   if (any_overlap(out, in)) return GEMMF32_ERR_ALIAS;
 
   const int fragments = grad_fragments(rank, b);
-  const int threads = 64 * (fragments <= 2 ? GradShape<1>::WAVES : GradShape<4>::WAVES);
   GradArgs wide{};
   int64_t wgs[2] = {}, sums[2] = {};
   int count = 0;
@@ -319,7 +327,7 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
       !fits_grid(sums[0] + sums[1], 256))
     return GEMMF32_ERR_TOO_LARGE;
   wide.wgs = (int)wgs[0];
-#define GRAD(T) grad_kernel<T>(fragments)
+#define GRAD(T) grad_kernel<T>(fragments, waves)
   if (const int rc = launch(BY_TYPE(type, GRAD), dim3((unsigned)(wgs[0] + wgs[1])), threads, &wide,
                             stream))
     return rc;
@@ -378,7 +386,8 @@ int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t K, int64_t N, int64_t
   if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
   if (too_large(rows, std::max(K, N), E)) return GEMMF32_ERR_TOO_LARGE;
   const int b = type_bytes(type);
-  const int64_t run = grad_run(rows, side_blocks(K, rank, b) + side_blocks(N, rank, b));
+  const int64_t run = grad_run(rows, side_blocks(K, rank, b) + side_blocks(N, rank, b),
+                               grad_waves(rows, rank, E, b));
   return side_workspace(rows, K, rank, E, run) + side_workspace(rows, N, rank, E, run);
 }
 
