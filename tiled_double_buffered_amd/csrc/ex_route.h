@@ -61,14 +61,17 @@ __device__ __forceinline__ int column(int lane, int v) {
 template <class T, int L, int V>
 __device__ __forceinline__ void load_logits(const void* X, int64_t at, int E, int lane, float* x) {
   const typename T::type* row = (const typename T::type*)X + at;
-  if (V > 1 && E % 4 == 0) {
-    Raw<T, 4> r[(V + 3) / 4];
+  const bool wide = V > 1 && E % 4 == 0;
+  if constexpr (V > 1) {
+    if (wide) {
 #pragma unroll
-    for (int q = 0; q < V; q += 4)
-      r[q / 4] = load_raw<T, 4>(row + min(column<L, V>(lane, q), E - 4));
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = (float)r[v / 4][v % 4];
-  } else {
+      for (int q = 0; q < V; q += 4) {
+        const Raw<T, 4> r = load_raw<T, 4>(row + min(column<L, V>(lane, q), E - 4));
+        x[q] = (float)r[0], x[q + 1] = (float)r[1], x[q + 2] = (float)r[2], x[q + 3] = (float)r[3];
+      }
+    }
+  }
+  if (!wide) {
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = (float)row[min(column<L, V>(lane, v), E - 1)];
   }
@@ -171,13 +174,22 @@ __global__ __launch_bounds__(kRouteThreads) void ex_route_kernel(RouteArgs a) {
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = key_of(x[v]);
-    const bool valid = a.valid == nullptr || a.valid[t] != 0;
+    uint32_t most = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) most = max(most, key[v]);
+    most = over_lanes<L>(most, Most{});
+    const bool on = (a.valid == nullptr || a.valid[t] != 0) && most > kKeyNoExpert;
+    // (the probabilities are added before the search, which then has their registers)
     const float inv = exponentials<L, V>(x);
+    if (on) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
+      rows += lane == 0;
+    }
     // the j-th best of the row is kept by its lane j
+    const float top = of_key(most);
     uint32_t mine = 0;
     int expert = -1;
-    float top = 0.0f;
-    bool on = false;
     for (int j = 0; j < a.k; ++j) {
       uint32_t best = 0;
 #pragma unroll
@@ -190,10 +202,6 @@ __global__ __launch_bounds__(kRouteThreads) void ex_route_kernel(RouteArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (column<L, V>(lane, v) == at) key[v] = 0;
-      if (j == 0) {
-        on = valid && best > kKeyNoExpert;
-        top = of_key(best);
-      }
       if (lane == j && on && best > kKeyNoExpert) {
         mine = best;
         expert = at;
@@ -210,11 +218,6 @@ __global__ __launch_bounds__(kRouteThreads) void ex_route_kernel(RouteArgs a) {
       a.experts[t * a.k + lane] = expert;
     }
     if (expert >= 0) atomicAdd(&lds_n[expert], 1);
-    if (on) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
-      rows += lane == 0;
-    }
   }
   // the workgroup's sums: over the rows of a wave, then over the waves
 #pragma unroll
