@@ -91,6 +91,9 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  *   V[p]^T X[order[p]], and DB_e (rank x N) = the same of U[p]^T DOUT[order[p]]; an expert without
  *   rows gets zeros.  Where only one is wanted the other's K or N is 0 (and its other arguments are
  *   not looked at).
+ * Inf and NaN stay in their places' rows and their adapters.  In bf16 `up` and `grad` multiply U and V
+ *   in three parts, of which one may be 0: Inf in A or B, and for grad in X or DOUT, gives NaN where
+ *   the product is Inf.
  * gemm_adapters_splits: the number of splits that `down` should make, at least 1.
  * gemm_adapters_grad_workspace: bytes of workspace that `grad` needs, as in gemm_route. */
 int gemm_adapters_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t *order,

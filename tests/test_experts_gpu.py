@@ -394,6 +394,32 @@ def test_adapters_inf_and_nan_stay_in_their_rows(dtype):
     assert torch.equal(got[keep], clean[keep]) and torch.isnan(got[rows[2]]).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_adapters_inf_in_a_row(dtype):
+    """Inf in x: the row's results are what the formula gives, Inf or NaN; the others do not change.
+    Inf in an adapter: its rows alone are not finite."""
+    y, x, a, b, d, s = _adapter_inputs(24, 2, 5, 72, 40, dtype, 9)
+    order, offsets = _groups((12, 12), 24, 3)
+    a = a.abs()
+    b = torch.where(b.abs() < 0.1, torch.ones_like(b), b)
+    clean = tdb.add_adapters(y, x, a, b, order, offsets)
+    bad = x.clone()
+    bad[4, 3], bad[9, 70] = math.inf, -math.inf
+    got = tdb.add_adapters(y, bad, a, b, order, offsets)
+    _, ref, slack = xo.adapters(y, bad, a, b, order, offsets, None)[0]
+    xo.close(got, ref, torch.nan_to_num(slack, posinf=0.0), "inf in x")
+    keep = torch.ones(24, dtype=torch.bool, device=DEV)
+    keep[[4, 9]] = False
+    assert torch.equal(got[keep], clean[keep]) and not torch.isfinite(got[~keep]).any()
+    worse = b.clone()
+    worse[1, 2, 7] = math.inf
+    got = tdb.add_adapters(y, x, a, worse, order, offsets)
+    rows = order[offsets[1]:offsets[2]]
+    assert not torch.isfinite(got[rows, 7]).any()
+    got[rows, 7] = clean[rows, 7]
+    assert torch.equal(got, clean)
+
+
 def test_adapters_large_and_small_numbers_in_fp16():
     """x A^T beyond fp16's range and below its smallest step, with results inside it."""
     g = _gen(4)

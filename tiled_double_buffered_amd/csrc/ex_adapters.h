@@ -378,7 +378,8 @@ struct Block8 {
 };
 
 // The three bf16 parts of FP32 numbers, cut (not rounded) so that they add up exactly and no part
-// passes bf16's range; Inf and NaN are in the first.
+// passes bf16's range; Inf and NaN are in the first.  (A part may be 0, and 0 times Inf is NaN: an Inf
+// of the other operand does not come out as one.)
 __device__ __forceinline__ void three_parts(const float (&u)[8], bf168v (&part)[3]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
