@@ -295,10 +295,11 @@ def test_adapters_sizes(size, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("r", [8, 30, 64, 120])
 @pytest.mark.parametrize("T, sizes, K, N", [(8300, (3000, 0, 5200), 72, 136), (3500, (900, 1500, 1000), 264, 80),
-                                            (1100, (1000, 40), 520, 1032)], ids=str)
+                                            (1100, (1000, 40), 520, 1032), (2500, (900, 0, 1500), 1100, 72)],
+                         ids=str)
 def test_adapters_many_rows(T, sizes, K, N, r, dtype):
-    """Every way of sharing the rows out: tiles of 64 and of 32 places whose waves share a step, and
-    partial sums that are joined."""
+    """Every way of sharing the rows out: tiles of 64 places whose waves share a step, and partial sums
+    that are joined."""
     y, x, a, b, d, s = _adapter_inputs(T, len(sizes), r, K, N, dtype, T + r)
     _check_adapters(y, x, a, b, *_groups(sizes, T, r), s, d)
 

@@ -14,14 +14,16 @@
 // nothing moves between lanes, and neighbouring lanes load and store neighbouring columns.
 //
 // Bound by memory, and by how evenly the groups fill the chip (bf16, each pass on other rows):
-//   down  8192 x 4096, rank 32: 17 us for 67 MB (3.9 TB/s); 25 with four uneven groups, whose 258
-//         tiles leave two for a second round; 4096 x 4096, rank 16: 10 us; one token each for 24
-//         adapters, rank 16: 4.9 us, the latency of three loads that wait for each other
+//   down  8192 x 4096, rank 32: 22 us for 67 MB (3.0 TB/s), 3 of them the launch that joins the
+//         splits, which make it the same for even and uneven groups; 4096 x 4096, rank 16: 10 us;
+//         one token each for 24 adapters, rank 16: 4.9 us, the latency of three loads that wait for
+//         each other
 //   up    4096 x 11008, rank 16: 39 us for 180 MB (4.6 TB/s; a large copy reaches 5.0); 24 adapters
 //         of one token beside 4096 columns: 6.3 us
-//   grad  8192 x 4096, rank 32: 26 us for 67 MB and 4.3 for the sums: a workgroup lives 9 us, of
-//         which 3 are vector instructions (u's parts, turning) and most of the rest the chain from
-//         the offsets to the rows' numbers to the rows, and there are 2.25 rounds of workgroups
+//   grad  8192 x 4096, rank 32, both gradients in one launch: 43 us for 134 MB and 4.2 for the sums
+//         (in two launches 26 and 4.3 each): a workgroup lives 9 us, of which 3 are vector
+//         instructions (u's parts, turning) and most of the rest the chain from the offsets to the
+//         rows' numbers to the rows
 // With one workgroup's loads guarded one by one (a branch each, at which all earlier ones have to
 // arrive) `up` took 84 us where it takes 39.
 #pragma once
@@ -230,26 +232,25 @@ __global__ __launch_bounds__(kDownThreads) void ex_adapters_down_kernel(AdapterA
   }
 }
 
-// The same for 16 RW places, by eight waves: RW of them, a group, have 16 places each and share the
+// The same for 64 places, by eight waves: four of them, a group, have 16 places each and share the
 // adapter's part of a step, of which each loads its share, in two slots of LDS in turn with one
-// barrier a step; their own rows' part they turn by themselves.  The 8 / RW groups share the steps of
-// K.  (With a copy for each wave the adapter's bytes, from the L2, take longer than the rows' from
+// barrier a step; their own rows' part they turn by themselves.  The two groups share the steps of K.  (With a copy for each wave the adapter's bytes, from the L2, take longer than the rows' from
 // memory: rank 32 has two of them for each of the rows', and a CU gets 16 a cycle.)
-constexpr int kWideThreads = 512;
+constexpr int kWideThreads = 512, kWidePlaces = 64;
 template <int RF>
 constexpr int kWideDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;
-template <class T, int RF, int RW>
+template <class T, int RF>
 __global__ __launch_bounds__(kWideThreads, (RF <= 2 ? 4 : 2)) void ex_adapters_down_wide_kernel(
     AdapterArgs a) {
   constexpr int PER = 16 / T::BYTES, STEP = kRowBytes / T::BYTES, DEEP = kWideDeep<RF>;
-  constexpr int KG = 8 / RW, WROWS = RF * 16, LD = RF * 16 + 4;
+  constexpr int RW = kWidePlaces / 16, KG = 8 / RW, WROWS = RF * 16, LD = RF * 16 + 4;
   constexpr int OWN = (WROWS / 8 + RW - 1) / RW;  // loads of eight adapter rows a wave makes
   __shared__ int4v rows_tile[8][16 * 8];
   __shared__ int4v rank_tile[KG][2][WROWS * 8];
   using Vec = Raw<T, PER>;
   Places t;
   const int split = blockIdx.x % a.splits;
-  if (!find_places<true>(a, 16 * RW, blockIdx.x / a.splits, t) || t.e < 0) return;
+  if (!find_places<true>(a, kWidePlaces, blockIdx.x / a.splits, t) || t.e < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   const int rw = wave % RW, kg = wave / RW;
   const int r8 = lane >> 3, c8 = lane & 7, place0 = t.first + 16 * rw;

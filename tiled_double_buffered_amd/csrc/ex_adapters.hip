@@ -16,20 +16,20 @@ static int64_t place_tiles(int64_t rows, int64_t E, int bm) {
   return rows / bm + std::min<int64_t>(E + 2, rows);
 }
 
-// Waves of a workgroup of `down` with places of their own: four or two where that leaves a workgroup
-// for most CUs and the adapters have several such tiles; otherwise one, with a kernel of its own.
-// Past rank 64 four as soon as splits of K can make up for the workgroups (and never two, which would
-// need more registers than a wave has): there the adapter's bytes decide.
-static int down_waves(int64_t rows, int64_t rank, int64_t E) {
-  if (rank > 64) return rows >= 2048 && rows >= 128 * E ? 4 : 1;
-  for (int w = 4; w > 1; w /= 2)
-    if (rows >= 16 * w * (kCus * 3 / 4) && rows >= 32 * w * E) return w;
-  return 1;
+// Whether `down` takes 64 places a workgroup: where the adapters have several such tiles and splits of
+// K can make up for the workgroups; otherwise 16, with a kernel of its own.  A low rank needs more rows
+// for it, as the rows' bytes decide there and not the adapter's.  (bf16, with 64 and 16, in us with the
+// join: 8192 x 4096, rank 32, 22 and 26; 4096 x 8192, rank 64, 27 and 47; 4096 x 4096, rank 16, 13
+// and 10.)
+static bool down_wide(int64_t rows, int64_t rank, int64_t E) {
+  return rows >= (rank > 32 ? 2048 : 6144) && rows >= 128 * E;
+}
+static int64_t down_tiles(int64_t rows, int64_t rank, int64_t E) {
+  return place_tiles(rows, E, down_wide(rows, rank, E) ? kWidePlaces : 16);
 }
 // Splits of K: enough workgroups for two a CU where there are none for each, but 256 columns a split.
 static int adapter_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
-  const int64_t tiles =
-      std::max<int64_t>(place_tiles(rows, E, 16 * down_waves(rows, rank, E)), 1);
+  const int64_t tiles = std::max<int64_t>(down_tiles(rows, rank, E), 1);
   if (tiles >= kCus * 3 / 4) return 1;
   return (int)std::max<int64_t>(std::min<int64_t>({2 * kCus / tiles, K / 256, 8}), 1);
 }
@@ -69,16 +69,13 @@ static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
 }
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
 
-template <class T, int RW>
-static const void* down_wide_kernel(int64_t rank) {
-  return rank <= 16   ? (const void*)&ex_adapters_down_wide_kernel<T, 1, RW>
-         : rank <= 32 ? (const void*)&ex_adapters_down_wide_kernel<T, 2, RW>
-         : rank <= 64 ? (const void*)&ex_adapters_down_wide_kernel<T, 4, RW>
-                      : (const void*)&ex_adapters_down_wide_kernel<T, 8, 4>;
-}
 template <class T>
-static const void* down_kernel(int64_t rank, int waves) {
-  if (waves > 1) return waves == 4 ? down_wide_kernel<T, 4>(rank) : down_wide_kernel<T, 2>(rank);
+static const void* down_kernel(int64_t rank, bool wide) {
+  if (wide)
+    return rank <= 16   ? (const void*)&ex_adapters_down_wide_kernel<T, 1>
+           : rank <= 32 ? (const void*)&ex_adapters_down_wide_kernel<T, 2>
+           : rank <= 64 ? (const void*)&ex_adapters_down_wide_kernel<T, 4>
+                        : (const void*)&ex_adapters_down_wide_kernel<T, 8>;
   return rank <= 16   ? (const void*)&ex_adapters_down_kernel<T, 1>
          : rank <= 32 ? (const void*)&ex_adapters_down_kernel<T, 2>
          : rank <= 64 ? (const void*)&ex_adapters_down_kernel<T, 4>
@@ -154,8 +151,9 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
   // (a multiple of the steps that four waves take at once)
   const int64_t unit = 4 * 128 / b;
   a.k_chunk = (int)((K + splits * unit - 1) / (splits * unit) * unit);
-  const int waves = down_waves(rows, rank, E), threads = waves > 1 ? kWideThreads : kDownThreads;
-  const int64_t wgs = place_tiles(rows, E, 16 * waves) * splits;
+  const bool wide = down_wide(rows, rank, E);
+  const int threads = wide ? kWideThreads : kDownThreads;
+  const int64_t wgs = down_tiles(rows, rank, E) * splits;
   if (K < kLeastWide) {
     const int64_t few = place_tiles(rows, E, 16) * splits;
     if (!fits_grid(few, 256)) return GEMMF32_ERR_TOO_LARGE;
@@ -164,7 +162,7 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
 #undef FEW
   }
   if (!fits_grid(wgs, threads)) return GEMMF32_ERR_TOO_LARGE;
-#define DOWN(T) down_kernel<T>(rank, waves)
+#define DOWN(T) down_kernel<T>(rank, wide)
   if (const int rc = launch(BY_TYPE(type, DOWN), dim3((unsigned)wgs), threads, &a, stream)) return rc;
 #undef DOWN
   if (!join || splits == 1) return GEMMF32_OK;
