@@ -34,7 +34,6 @@ extern "C" {
 #define GEMM_GROUP_MAX_EXPERTS 4096
 #define GEMM_ADAPTERS_MAX_RANK 128
 #define GEMM_ADAPTERS_MAX_SPLITS 64
-#define GEMM_ADAPTERS_MAX_RANK 128
 
 /* The router of `rows` rows.  X: rows x E logits of `type`, row stride ldx.  valid: rows bytes, 0
  * for a row to be left out, or NULL.  A row counts if it is valid and has a logit above -Inf.
@@ -46,8 +45,9 @@ extern "C" {
  *   loss = E sum_e (counts[e] / sums[1]) (sum_t p[t][e] / sums[0]); 0 where no row counts
  * A NaN is taken before every number; it, or +Inf, makes its row's gates and the loss NaN.
  * E <= GEMM_ROUTE_MAX_EXPERTS and k <= GEMM_ROUTE_MAX_CHOSEN, else GEMMF32_ERR_BAD_CONFIG, as for
- * k < 1 or k > E; rows k below 2^31 - 1024, else GEMMF32_ERR_TOO_LARGE.  workspace: gemm_route_workspace(rows, E) bytes, 8-byte aligned (less is
- * GEMMF32_ERR_BAD_LD; where that is 0 it may be NULL); calls that overlap in time need one each. */
+ * k < 1 or k > E; rows k below 2^31 - 1024, else GEMMF32_ERR_TOO_LARGE.  workspace:
+ * gemm_route_workspace(rows, E) bytes, 8-byte aligned (less is GEMMF32_ERR_BAD_LD; where that is 0 it
+ * may be NULL); calls that overlap in time need one each. */
 int gemm_route(int64_t rows, int64_t E, int64_t k, const void *X, int64_t ldx, int type,
                const uint8_t *valid, int renormalize, float *gates, int32_t *experts,
                int32_t *counts, int32_t *sums, float *loss, void *workspace,

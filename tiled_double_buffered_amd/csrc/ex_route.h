@@ -12,7 +12,7 @@
 //
 // 16384 rows of 256 experts in FP32, k = 8: 17 us (16.8 MB; four rows a wave, whose eight searches of
 // 40 instructions and 16 exponentials are most of it), 8.4 for the sums of 256 workgroups (half a
-// megabyte that one CU reads), 21 for the gradient.  16 rows of 64 experts, k = 4: 4.9 us.  A call
+// megabyte that one CU reads), 21 for the gradient.  16 rows of 64 experts, k = 4: 5.1 us.  A call
 // takes the host 14 us, a step 100, of which autograd's own 37 are for a function that does nothing.
 #pragma once
 

@@ -204,7 +204,8 @@ def route_experts(logits, k, valid=None, renormalize=False):
       gates    T x k float32, their p, with renormalize over the sum of the row's
       counts   E int32, how often each expert was taken
       loss     float32: E sum_e f_e P_e, f_e the share of counts that is e's, P_e the mean of p_e
-               over the rows that count; 1 where all experts are used alike, E where one is
+               over the rows that count; 1 where all experts are used alike, E where one is, and 0
+               where no row counts
     An expert whose logit is -Inf is never taken.  Where a row has none left, its place holds -1
     with a gate of 0 (`group_rows` puts such places last); rows that are not valid, or have no
     logit above -Inf, hold nothing else and do not count.  NaN is taken before every number; it, or
