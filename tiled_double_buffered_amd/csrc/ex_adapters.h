@@ -362,10 +362,10 @@ __global__ __launch_bounds__(256) void ex_adapters_join_kernel(AdapterArgs a) {
 // l of fragment j is 8 l + j.  A lane loads the eight columns of its l at once, and holds these eight
 // of the result, of four rows.
 
-// What a lane has of one operand in 32 k: 8 k (8 g + i) of 8 neighbouring columns.
-template <class T>
+// What a lane has of one operand in 32 k: 8 k (8 g + i) of CF neighbouring columns.
+template <class T, int CF = 8>
 struct Block8 {
-  Raw<T, 8> v[8];  // v[i][j]: k = 8 g + i, column j; after turn(): v[j][i]
+  Raw<T, CF> v[8];  // v[i][j]: k = 8 g + i, column j; after turn(): v[j][i]
   __device__ __forceinline__ void turn() {
     if constexpr (T::BYTES == 2) {
       Block8 o;
@@ -396,9 +396,9 @@ __device__ __forceinline__ void three_parts(const float (&u)[8], bf168v (&part)[
 }
 
 // acc[j] += u x fragment j of `w` over 32 k, u the instruction's row l16.  bf16: w turned.
-template <class T>
-__device__ __forceinline__ void multiply_across(const Block8<T>& w, const float (&u)[8],
-                                                float4v (&acc)[8]) {
+template <class T, int CF>
+__device__ __forceinline__ void multiply_across(const Block8<T, CF>& w, const float (&u)[8],
+                                                float4v (&acc)[CF]) {
   if constexpr (std::is_same_v<T, Bf16>) {
     bf168v part[3];
     three_parts(u, part);
@@ -410,7 +410,7 @@ __device__ __forceinline__ void multiply_across(const Block8<T>& w, const float 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = mma32(u[i], (float)w.v[i][j], acc[j]);
+      for (int j = 0; j < CF; ++j) acc[j] = mma32(u[i], (float)w.v[i][j], acc[j]);
   }
 }
 
@@ -543,21 +543,30 @@ struct GradArgs {
   int wgs;
 };
 
-// 128 columns of RF * 16 rows of one adapter's gradient, from a run of its places.  The waves take
+// Columns of a workgroup: 64 past rank 32, as with 128 the sums take all registers of a SIMD's only
+// wave.  (8192 x 4096, bf16, rank 64, four and 64 even adapters: 57 and 124 us, 64 and 171 with 128; FP32,
+// 4096 x 4096 of eight, 55 and 71.  Up to rank 32 128 need fewer instructions: bf16, rank 16, 37 us, 40
+// with 64.)
+__host__ __device__ constexpr int grad_columns(int rank) { return rank <= 32 ? 128 : 64; }
+
+// These columns of RF * 16 rows of one adapter's gradient, from a run of its places.  The waves take
 // turns at 32 of these and add up through LDS.  An adapter with one run has its result; those of one
 // with several are added by another launch.  (Runs of one length, however the places are shared out:
 // with as many for each adapter the largest one decides.)
 template <int RF, int WAVES>
 struct GradShape {
-  static constexpr int LD = RF * 16 + 4;  // numbers of a place in LDS
-  static constexpr int PER_SIMD = RF == 4 ? 1 : 2;  // waves
+  static constexpr int CF = grad_columns(RF * 16) / 16;  // fragments of the columns
+  static constexpr int LD = RF * 16 + 4;                 // numbers of a place in LDS
+  static constexpr int N = RF * CF * 4;                  // numbers of a lane's sums
+  static constexpr int U = WAVES * 32 * LD, SUMS = WAVES / 2 * N * 64;
 };
 // What one wave adds of the places first + 32 wave, + 32 WAVES and so on.  u and the rows' numbers
 // come by whole lines, through LDS of the wave's own (lds: 32 LD numbers).
 template <class T, int RF, int WAVES>
 __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int end, int c, int r0,
-                                            float* lds, float4v (&acc)[RF][8]) {
-  constexpr int LD = GradShape<RF, WAVES>::LD;
+                                            float* lds,
+                                            float4v (&acc)[RF][GradShape<RF, WAVES>::CF]) {
+  constexpr int LD = GradShape<RF, WAVES>::LD, CF = GradShape<RF, WAVES>::CF;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int64_t u_step = (int64_t)a.rows * a.ldu;
   for (int i0 = first + (threadIdx.x >> 6) * 32; i0 < end; i0 += WAVES * 32) {
@@ -573,10 +582,10 @@ __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int
                                   (int64_t)min(i0 + j * PLACES + lane / LANES, end - 1) * a.ldu + ur);
     };
     load_u(0, part);
-    Block8<T> o;
+    Block8<T, CF> o;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      o.v[i] = load_raw<T, 8>((const typename T::type*)a.X +
+      o.v[i] = load_raw<T, CF>((const typename T::type*)a.X +
                               (int64_t)__shfl(row_of, 8 * g + i) * a.ldx + c);
     for (int s = 1; s < a.splits; ++s) {
       float4v more[32 / PLACES];
@@ -594,10 +603,28 @@ __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int
     if (i0 + 32 > end) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i0 + 8 * g + i >= end) o.v[i] = Raw<T, 8>{};
+        if (i0 + 8 * g + i >= end) o.v[i] = Raw<T, CF>{};
     }
     __builtin_amdgcn_wave_barrier();
-    if constexpr (std::is_same_v<T, Bf16>) {
+    if constexpr (std::is_same_v<T, Bf16> && RF == 4) {
+      bf168v w[CF];  // (the columns held, one fragment of u cut at a time)
+#pragma unroll
+      for (int j = 0; j < CF; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[j][i] = o.v[i][j];
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        float u[8];
+        bf168v parts[3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = lds[(8 * g + i) * LD + 16 * f + l16];
+        three_parts(u, parts);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int j = 0; j < CF; ++j) acc[f][j] = mma16(parts[p], w[j], acc[f][j]);
+      }
+    } else if constexpr (std::is_same_v<T, Bf16>) {
       bf168v parts[RF][3];
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
@@ -629,44 +656,45 @@ __device__ __forceinline__ void grad_places(const AdapterArgs& a, int first, int
   }
 }
 template <class T, int RF, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, (GradShape<RF, WAVES>::PER_SIMD)) void
-ex_adapters_grad_kernel(GradArgs args) {
+__global__ __launch_bounds__(WAVES * 64, 2) void ex_adapters_grad_kernel(
+    GradArgs args) {
   const bool second = (int)blockIdx.x >= args.wgs;
   const AdapterArgs& a = args.set[second ? 1 : 0];
-  constexpr int N = RF * 8 * 4;
-  __shared__ float red[WAVES / 2][N][64];
-  constexpr int LD = GradShape<RF, WAVES>::LD;
-  static_assert(WAVES * 32 * LD <= WAVES / 2 * N * 64, "the waves' u lies where their sums meet");
+  using Shape = GradShape<RF, WAVES>;
+  constexpr int N = Shape::N, LD = Shape::LD, CF = Shape::CF;
+  // (the waves' u, and then their sums)
+  __shared__ alignas(16) float shared[Shape::U > Shape::SUMS ? Shape::U : Shape::SUMS];
+  float (*const red)[N][64] = (float (*)[N][64])shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
   // workgroups: columns, then blocks of the rank, then runs
   const int rb = (a.rank + RF * 16 - 1) / (RF * 16);
   int id = (int)blockIdx.x - (second ? args.wgs : 0);
-  const int n0 = id % a.tiles_n * kWaveCols;
+  const int n0 = id % a.tiles_n * (16 * CF);
   id /= a.tiles_n;
   const int r0 = id % rb * (RF * 16);
   id /= rb;
   Places t;
   if (!find_places<false>(a, a.run, id, t)) return;
   const int first = t.first, end = t.end;
-  float4v acc[RF][8];
+  float4v acc[RF][CF];
 #pragma unroll
   for (int f = 0; f < RF; ++f)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[f][j] = float4v{0, 0, 0, 0};
-  float* const lds = (float*)red + wave * 32 * LD;
+    for (int j = 0; j < CF; ++j) acc[f][j] = float4v{0, 0, 0, 0};
+  float* const lds = shared + wave * 32 * LD;
   // (columns past the last are computed once more as the last ones)
-  const int c = min(n0 + 8 * l16, a.N - 8);
+  const int c = min(n0 + CF * l16, a.N - CF);
   grad_places<T, RF, WAVES>(a, first, end, c, r0, lds, acc);
   __syncthreads();
   for (int d = WAVES / 2; d > 0; d /= 2) {
     if (wave >= d && wave < 2 * d) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[wave - d][i][lane] = acc[i / 32][i / 4 % 8][i % 4];
+      for (int i = 0; i < N; ++i) red[wave - d][i][lane] = acc[i / (4 * CF)][i / 4 % CF][i % 4];
     }
     __syncthreads();
     if (wave < d) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i / 32][i / 4 % 8][i % 4] += red[wave][i][lane];
+      for (int i = 0; i < N; ++i) acc[i / (4 * CF)][i / 4 % CF][i % 4] += red[wave][i][lane];
     }
     __syncthreads();
   }
@@ -677,13 +705,13 @@ ex_adapters_grad_kernel(GradArgs args) {
     for (int q = 0; q < 4; ++q) {
       const int r = r0 + 16 * f + 4 * g + q;
       if (r >= a.rank) continue;
-      float v[8];
+      float v[CF];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[f][j][q];
+      for (int j = 0; j < CF; ++j) v[j] = acc[f][j][q];
       if (t.tiles > 1) {
-        store_row<8, GEMM_LP_F32>(a.part, ((int64_t)id * a.rank + r) * a.N + c, 8, GEMM_LP_F32, v);
+        store_row<CF, GEMM_LP_F32>(a.part, ((int64_t)id * a.rank + r) * a.N + c, CF, GEMM_LP_F32, v);
       } else {
-        store_row<8, T::CODE>(a.C, t.e * a.stride_c + r * a.ldc + c, 8, T::CODE, v);
+        store_row<CF, T::CODE>(a.C, t.e * a.stride_c + r * a.ldc + c, CF, T::CODE, v);
       }
     }
   }

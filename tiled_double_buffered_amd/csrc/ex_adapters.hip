@@ -49,22 +49,23 @@ static int up_places(int64_t rows, int64_t N, int64_t E) {
 }
 
 // Fragments of the rank of a workgroup of `grad`.
-static int grad_fragments(int64_t rank, int bytes) {
-  return rank <= 16 ? 1 : rank <= 32 || bytes == 4 ? 2 : 4;
+static int grad_fragments(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
+static int64_t grad_blocks(int64_t N, int64_t rank) {
+  const int64_t per = 16 * grad_fragments(rank), columns = grad_columns((int)rank);
+  return (N + columns - 1) / columns * ((rank + per - 1) / per);
 }
-static int64_t grad_blocks(int64_t N, int64_t rank, int bytes) {
-  const int64_t per = 16 * grad_fragments(rank, bytes);
-  return (N + kWaveCols - 1) / kWaveCols * ((rank + per - 1) / per);
-}
-// Waves of a workgroup of `grad`: four past rank 32, where they have the registers of a SIMD, and
-// where the adapters have fewer places than eight take in a turn.
-static int grad_waves(int64_t rows, int64_t rank, int64_t E, int bytes) {
-  return grad_fragments(rank, bytes) == 4 || rows < 256 * E ? 4 : 8;
+// Waves of a workgroup of `grad`: four past rank 32, two workgroups a CU, and where the adapters have
+// fewer places than eight take in a turn.
+static int grad_waves(int64_t rows, int64_t rank, int64_t E) {
+  return rank > 32 || rows < 256 * E ? 4 : 8;
 }
 // Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
-// two workgroups a CU, but a turn of the waves at least; and the most runs that there can be.
+// two workgroups a CU and four runs, but a turn of the waves at least; and the most runs that there
+// can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096 of eight uneven ones, rank
+// 128, 231 us, 255 without.)
 static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
-  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 1), turn = 32 * waves;
+  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
+  const int64_t turn = 32 * waves;
   return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
@@ -90,9 +91,7 @@ static const void* up_kernel(int64_t rank, int places) {
 }
 template <class T>
 static const void* grad_kernel(int fragments, int waves) {
-  if constexpr (T::BYTES == 2) {
-    if (fragments == 4) return (const void*)&ex_adapters_grad_kernel<T, 4, 4>;
-  }
+  if (fragments == 4) return (const void*)&ex_adapters_grad_kernel<T, 4, 4>;
   if (waves == 4)
     return fragments == 1 ? (const void*)&ex_adapters_grad_kernel<T, 1, 4>
                           : (const void*)&ex_adapters_grad_kernel<T, 2, 4>;
@@ -236,8 +235,8 @@ struct GradSide {
   int64_t ldd, stride_d;
   bool wide() const { return N >= kLeastWide; }
 };
-static int64_t side_blocks(int64_t N, int64_t rank, int bytes) {
-  return N >= kLeastWide ? grad_blocks(N, rank, bytes) : 0;
+static int64_t side_blocks(int64_t N, int64_t rank) {
+  return N >= kLeastWide ? grad_blocks(N, rank) : 0;
 }
 // Bytes of the runs of a gradient.  (Several runs there are only of 65536 columns or fewer, so that
 // 64 bits hold them.)
@@ -256,9 +255,9 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
   const int b = type_bytes(type);
   const bool reads = rows > 0;
   const int64_t ldu = u_columns((int)rank);
-  const int waves = grad_waves(rows, rank, E, b), threads = 64 * waves;
+  const int waves = grad_waves(rows, rank, E), threads = 64 * waves;
   const int64_t run =
-      grad_run(rows, side_blocks(sides[0].N, rank, b) + side_blocks(sides[1].N, rank, b), waves);
+      grad_run(rows, side_blocks(sides[0].N, rank) + side_blocks(sides[1].N, rank), waves);
   Range out[3], in[6];
   int64_t need = 0;
   for (int i = 0; i < 2; ++i) {
@@ -293,7 +292,7 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
     return GEMMF32_ERR_TOO_LARGE;
   if (any_overlap(out, in)) return GEMMF32_ERR_ALIAS;
 
-  const int fragments = grad_fragments(rank, b);
+  const int fragments = grad_fragments(rank), columns = grad_columns((int)rank);
   GradArgs wide{};
   int64_t wgs[2] = {}, sums[2] = {};
   int count = 0;
@@ -304,10 +303,10 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
     a.X = s.X, a.C = s.D, a.offsets = offsets, a.order = order, a.U = (float*)s.U;
     a.part = part, a.ldx = s.ldx, a.ldc = s.ldd, a.stride_c = s.stride_d;
     a.rows = (int)rows, a.N = (int)s.N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
-    a.splits = s.splits, a.tiles_n = (int)((s.N + kWaveCols - 1) / kWaveCols);
+    a.splits = s.splits, a.tiles_n = (int)((s.N + columns - 1) / columns);
     a.run = (int)run, a.runs = (int)std::min<int64_t>(grad_runs(rows, E, run), kMaxDim);
     if (s.wide()) {
-      if (__builtin_mul_overflow(side_blocks(s.N, rank, b), grad_runs(rows, E, run), &wgs[count]))
+      if (__builtin_mul_overflow(side_blocks(s.N, rank), grad_runs(rows, E, run), &wgs[count]))
         return GEMMF32_ERR_TOO_LARGE;
       sums[count] = E * ((rank * ((s.N + 7) / 8) + 255) / 256);
       part += side_workspace(rows, s.N, rank, E, run) / 4;
@@ -383,9 +382,8 @@ int64_t gemm_adapters_grad_workspace(int64_t rows, int64_t K, int64_t N, int64_t
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
   if (rank > GEMM_ADAPTERS_MAX_RANK) return GEMMF32_ERR_BAD_CONFIG;
   if (too_large(rows, std::max(K, N), E)) return GEMMF32_ERR_TOO_LARGE;
-  const int b = type_bytes(type);
-  const int64_t run = grad_run(rows, side_blocks(K, rank, b) + side_blocks(N, rank, b),
-                               grad_waves(rows, rank, E, b));
+  const int64_t run = grad_run(rows, side_blocks(K, rank) + side_blocks(N, rank),
+                               grad_waves(rows, rank, E));
   return side_workspace(rows, K, rank, E, run) + side_workspace(rows, N, rank, E, run);
 }
 
