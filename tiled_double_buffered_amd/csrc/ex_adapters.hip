@@ -60,11 +60,11 @@ static int grad_waves(int64_t rows, int64_t rank, int64_t E) {
   return rank > 32 || rows < 256 * E ? 4 : 8;
 }
 // Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
-// two workgroups a CU and four runs, but a turn of the waves at least; and the most runs that there
-// can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096 of eight uneven ones, rank
+// two workgroups a CU and four runs (one where a run has as many), but a turn of the waves at least;
+// and the most runs that there can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096 of eight uneven ones, rank
 // 128, 231 us, 255 without.)
 static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
-  const int64_t per = std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
+  const int64_t per = blocks > 2 * kCus ? 1 : std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
   const int64_t turn = 32 * waves;
   return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
