@@ -234,8 +234,9 @@ __global__ __launch_bounds__(kDownThreads) void ex_adapters_down_kernel(AdapterA
 
 // The same for 64 places, by eight waves: four of them, a group, have 16 places each and share the
 // adapter's part of a step, of which each loads its share, in two slots of LDS in turn with one
-// barrier a step; their own rows' part they turn by themselves.  The two groups share the steps of K.  (With a copy for each wave the adapter's bytes, from the L2, take longer than the rows' from
-// memory: rank 32 has two of them for each of the rows', and a CU gets 16 a cycle.)
+// barrier a step; their own rows' part they turn by themselves.  The two groups share the steps of K.
+// (With a copy for each wave the adapter's bytes, from the L2, take longer than the rows' from memory:
+// rank 32 has two of them for each of the rows', and a CU gets 16 a cycle.)
 constexpr int kWideThreads = 512, kWidePlaces = 64;
 template <int RF>
 constexpr int kWideDeep = RF <= 2 ? 4 : RF == 4 ? 3 : 2;

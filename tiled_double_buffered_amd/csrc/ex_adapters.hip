@@ -61,10 +61,11 @@ static int grad_waves(int64_t rows, int64_t rank, int64_t E) {
 }
 // Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
 // two workgroups a CU and four runs (one where a run has as many), but a turn of the waves at least;
-// and the most runs that there can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096 of eight uneven ones, rank
-// 128, 231 us, 255 without.)
+// and the most runs that there can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096
+// of eight uneven ones, rank 128, 231 us, 255 without.)
 static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
-  const int64_t per = blocks > 2 * kCus ? 1 : std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
+  const int64_t per =
+      blocks > 2 * kCus ? 1 : std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
   const int64_t turn = 32 * waves;
   return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
@@ -120,7 +121,8 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
                     int type, void* stream) {
   if (bad_dims(rows, K, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
-  if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS) return GEMMF32_ERR_BAD_CONFIG;
+  if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS)
+    return GEMMF32_ERR_BAD_CONFIG;
   if (ldx < at_least_1(K) || lda < at_least_1(K) || stride_a < 0) return GEMMF32_ERR_BAD_LD;
   if (too_large(rows, K, E)) return GEMMF32_ERR_TOO_LARGE;
   if (rows == 0 || rank == 0 || E == 0) return GEMMF32_OK;
@@ -176,7 +178,8 @@ static int run_up(int64_t rows, int64_t N, int64_t rank, int64_t E, const int64_
                   void* stream) {
   if (bad_dims(rows, N, rank, E)) return GEMMF32_ERR_NEGATIVE_DIM;
   if (!known_type(type)) return GEMMF32_ERR_BAD_TYPE;
-  if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS) return GEMMF32_ERR_BAD_CONFIG;
+  if (rank > GEMM_ADAPTERS_MAX_RANK || splits < 1 || splits > GEMM_ADAPTERS_MAX_SPLITS)
+    return GEMMF32_ERR_BAD_CONFIG;
   if (ldb < at_least_1(N) || stride_b < 0 || (Y && ldy < at_least_1(N)) || ldo < at_least_1(N))
     return GEMMF32_ERR_BAD_LD;
   if (too_large(rows, N, E)) return GEMMF32_ERR_TOO_LARGE;
