@@ -212,7 +212,7 @@ def _check_group(ids, count):
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("count", [0, 1, 2, 64, 255, 1024, 1025, 4096])
-@pytest.mark.parametrize("n", [0, 1, 63, 64, 65, 512, 1000, 8192, 8193, 40001])
+@pytest.mark.parametrize("n", [0, 1, 63, 64, 65, 512, 1000, 2048, 2049, 8192, 8193, 40001])
 def test_group_rows(n, count, dtype):
     ids = torch.randint(-1, count + 2, (n,), generator=_gen(n + count), dtype=dtype).to(DEV)
     _check_group(ids, count)

@@ -232,8 +232,8 @@ def test_workspace_and_split_queries():
     assert tdb.gemm_route_workspace(1 << 20, 64) == 256 * (2 * 64 + 1) * 4
     assert tdb.gemm_route_workspace(-1, 64) == tdb.ERR_NEGATIVE_DIM
     assert tdb.gemm_route_workspace(1, 2000) == tdb.ERR_BAD_CONFIG
-    assert tdb.gemm_group_rows_workspace(8192, 64) == 0
-    assert tdb.gemm_group_rows_workspace(8193, 64) == 5 * 65 * 4
+    assert tdb.gemm_group_rows_workspace(2048, 64) == 0
+    assert tdb.gemm_group_rows_workspace(2049, 64) == 16 * 65 * 4
     for n in (10000, 1 << 20, 1 << 30):  # a bounded number of workgroups, whatever the rows
         assert tdb.gemm_group_rows_workspace(n, 64) <= 128 * 65 * 4
     assert tdb.gemm_group_rows_workspace(1, 5000) == tdb.ERR_BAD_CONFIG
