@@ -122,7 +122,7 @@ int gemm_gated(int64_t rows, int64_t N, const void *X, int64_t ldx, int type, vo
                void *Q, int64_t ldq, float *S, int64_t lds, void *stream);
 
 /* DX (rows x 2N) = (DH U silu'(G), DH silu(G)), with G and U from X, or where X is NULL from Q and
- * S. */
+ * S (finite products past the type's range count as its largest number). */
 int gemm_gated_grad(int64_t rows, int64_t N, const void *X, int64_t ldx, const void *Q, int64_t ldq,
                     const float *S, int64_t lds, const void *DH, int64_t lddh, void *DX,
                     int64_t lddx, int type, void *stream);

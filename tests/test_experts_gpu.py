@@ -554,6 +554,25 @@ def test_gated_far_ends():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_gated_kept_values_at_the_ends_of_the_range(dtype):
+    """The type's largest and lowest numbers in 8 bits can round to more than the type has: they
+    count as its largest then, and the gradients are finite where those of x itself are."""
+    most = torch.finfo(dtype).max
+    g = torch.tensor([-most, most, 1.0, -2.0, -most, most, 0.0, 0.97 * most])
+    u = torch.tensor([1.0, 1.0, -most, most, most, -0.5, -most, 1.0])
+    # (a block of its own for each, so that every scale is its value's)
+    x = torch.stack([torch.cat([a.view(1), b.view(1)]) for a, b in zip(g, u)]).to(dtype).to(DEV).requires_grad_()
+    dh = torch.full((8, 1), 0.5, dtype=dtype, device=DEV)
+    h = tdb.gated_silu(x, checkpoint=True)
+    dx, = torch.autograd.grad(h, x, dh)
+    values = torch.cat([lo.values(*_quantized(half), 1) for half in x.detach().split(1, 1)], 1).clamp(-most, most)
+    (_, _), (rx, mx) = xo.gated(x, dh, values)
+    xo.close(dx, rx, mx, "dx")
+    plain, = torch.autograd.grad(tdb.gated_silu(x), x, dh)
+    assert torch.isfinite(plain).all() and torch.isfinite(dx).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_gated_views_and_leading_axes(dtype):
     big = _wide(41, 131, dtype, 3)
     dh = _wide(40, 61, dtype, 4)[:, 1:]

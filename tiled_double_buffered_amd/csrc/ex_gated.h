@@ -88,6 +88,21 @@ __device__ __forceinline__ void load8s(int n, PV... pv) {
   else load8_each<T>(n, pv...);
 }
 
+// Eight 8-bit values times their scale, as numbers of T's range: finite products past it become its
+// largest number (T's own largest can round up to such a product).
+template <class T>
+__device__ __forceinline__ void dequantized(uint2 q, float scale, float* v) {
+  constexpr float most = T::CODE == GEMM_LP_F16    ? 65504.0f
+                         : T::CODE == GEMM_LP_BF16 ? 3.3895313892515355e38f
+                                                   : 3.4028234663852886e38f;
+  from_fp8x8(q, scale, v);
+  if (fabsf(scale) < __builtin_inff()) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(v[i]) > most) v[i] = copysignf(most, v[i]);
+  }
+}
+
 // Which row, block and first column a thread has; false past the end (for whole 16 lanes).
 __device__ __forceinline__ bool block_at(int rows, int cols, int& row, int& block, int& c) {
   const int kb = (cols + kBlock - 1) / kBlock;
@@ -152,8 +167,8 @@ __global__ __launch_bounds__(256) void ex_gated_grad_kernel(GatedArgs p) {
       qg = load_bytes8(q, n), qu = load_bytes8(q + p.N, n);
       load8<T>(d, n, dh);
     }
-    from_fp8x8(qg, sg, g);
-    from_fp8x8(qu, su, u);
+    dequantized<T>(qg, sg, g);
+    dequantized<T>(qu, su, u);
   } else {
     const typename T::type* x = (const typename T::type*)p.X + row * p.ldx + c;
     load8s<T>(n, x, g, x + p.N, u, d, dh);
@@ -184,16 +199,8 @@ __global__ __launch_bounds__(256) void ex_dequantize_kernel(DequantArgs p) {
   if (!block_at(p.rows, p.cols, row, block, c)) return;
   const int n = p.cols - c;
   const float scale = p.S[(int64_t)(row >> p.shift) * p.lds + block];
-  const float most = T::CODE == GEMM_LP_F16   ? 65504.0f
-                     : T::CODE == GEMM_LP_BF16 ? 3.3895313892515355e38f
-                                               : 3.4028234663852886e38f;
-  float q[8], v[8];
-  from_fp8x8(load_bytes8(p.Q + row * p.ldq + c, n), 1.0f, q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = q[i] * scale;
-    if (fabsf(v[i]) > most && fabsf(scale) < __builtin_inff()) v[i] = copysignf(most, v[i]);
-  }
+  float v[8];
+  dequantized<T>(load_bytes8(p.Q + row * p.ldq + c, n), scale, v);
   store_row<8, T::CODE>(p.Y, row * p.ldy + c, n, T::CODE, v);
 }
 

@@ -500,8 +500,8 @@ def gated_silu(x, checkpoint=False):
 
     Differentiable.  With checkpoint the backward pass works on the 8-bit values that `quantize_fp8`
     has of gate and of up, by blocks of 1 x 128 each, and x itself need not be kept: 8 bits a value
-    and a scale for every 128, and a gradient of these values (NaN where x is Inf, which has no 8-bit
-    value); the forward result is x's own."""
+    and a scale for every 128, and a gradient of these values (of the type's largest number where x's
+    own rounds to more, NaN where x is Inf, which has no 8-bit value); the forward result is x's own."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in TYPES:
         raise TypeError(f"x must be a tensor of {_names(TYPES)}")
     if x.shape[-1] % 2:
