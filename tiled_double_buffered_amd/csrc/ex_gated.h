@@ -3,7 +3,9 @@
 // values turned back into numbers.
 //   dg = dh u s (1 + g (1 - s)),  du = dh g s
 // s and 1 - s both come from exp(-|g|), so that neither is a difference of near numbers and the
-// exponential never overflows.
+// exponential never overflows.  For g < 0 s = c^3 r, c = exp(-|g| / 3) and r = 1 / (1 + c^3), and its
+// three factors meet g, u and dh one by one: c is a normal number down to g = -262, where h is 0 for
+// every u (and dg below 2^-113 for every u and dh), whereas exp(-|g|) is one only down to -87.
 //
 // Bound by memory: everything is read once and written once.  16 lanes hold a block of 128 columns,
 // eight each, so that a block's scale needs four rotations.  16384 x 2048 in bf16, kept in 8 bits: 46
@@ -28,21 +30,23 @@ struct GatedArgs {
   int rows, N;
 };
 
-// s(g) and 1 - s(g).  FP32 results keep the exponential's and the quotient's full precision; 16-bit
-// ones, rounded at 2^-9 or 2^-12, take the instructions' (2^-22) for a third of the time.
+// s(g) = c^3 r and 1 - s(g) = rest; c = 1 for g >= 0.  FP32 results keep the exponential's and the
+// quotient's full precision; 16-bit ones, rounded at 2^-9 or 2^-12, take the instructions' (2^-22) for
+// a third of the time.
+struct Gate {
+  float c, r, rest;
+};
 template <class T>
-__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
-  float t, r;
+__device__ __forceinline__ Gate gate_of(float g) {
+  float c, r;
   if constexpr (T::BYTES == 4) {
-    t = expf(-fabsf(g));
-    r = 1.0f / (1.0f + t);
+    c = expf(-(1.0f / 3.0f) * fabsf(g));
+    r = 1.0f / (1.0f + c * c * c);
   } else {
-    t = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
-    r = __builtin_amdgcn_rcpf(1.0f + t);
+    c = __builtin_amdgcn_exp2f(-0.480898347f * fabsf(g));  // log2 e / 3
+    r = __builtin_amdgcn_rcpf(1.0f + c * c * c);
   }
-  s = g >= 0 ? r : t * r;
-  rest = g >= 0 ? t * r : r;
-  if (g != g) s = rest = g;
+  return g >= 0 ? Gate{1.0f, r, c * c * c * r} : Gate{c, r, r};
 }
 
 __device__ __forceinline__ void from_fp8x8(uint2 q, float scale, float* v) {
@@ -130,9 +134,8 @@ __global__ __launch_bounds__(256) void ex_gated_kernel(GatedArgs p) {
   load8s<T>(n, x, g, x + p.N, u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float s, rest;
-    sigmoid<T>(g[i], s, rest);
-    h[i] = g[i] * s * u[i];
+    const Gate t = gate_of<T>(g[i]);
+    h[i] = g[i] * t.c * t.r * (u[i] * t.c) * t.c;
   }
   store_row<8, T::CODE>(p.H, row * p.ldh + c, n, T::CODE, h);
   if constexpr (KEEP) {
@@ -175,11 +178,10 @@ __global__ __launch_bounds__(256) void ex_gated_grad_kernel(GatedArgs p) {
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float s, rest;
-    sigmoid<T>(g[i], s, rest);
-    const float gs = g[i] * s;
-    g[i] = dh[i] * u[i] * (s + gs * rest);
-    u[i] = dh[i] * gs;
+    const Gate t = gate_of<T>(g[i]);
+    const float slope = t.c * (t.r * (1.0f + g[i] * t.rest)), silu = g[i] * t.c * t.r;
+    g[i] = slope * dh[i] * (u[i] * t.c) * t.c;
+    u[i] = silu * (dh[i] * t.c) * t.c;
   }
   store_row<8, T::CODE>(p.DX, row * p.lddx + c, n, T::CODE, g);
   store_row<8, T::CODE>(p.DX, row * p.lddx + p.N + c, n, T::CODE, u);
