@@ -330,6 +330,20 @@ def test_adapters_rows_split_for_the_gradient(dtype):
     _check_adapters(y, x, a, b, *_groups((2900,), 3001, 3), s, d)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("r", [9, 40, 70])
+def test_adapters_with_many_rows_among_those_with_few(r, dtype):
+    """Gradients that several workgroups add up among such that one has whole, more adapters than a
+    wave looks at at once: the sums lie one after another, whichever adapters they are of."""
+    sizes = [(0, 1, 3)[i % 3] for i in range(150)]
+    for i, n in ((0, 300), (1, 129), (5, 128), (62, 700), (63, 257), (64, 1000), (65, 2), (100, 385),
+                 (127, 130), (128, 256), (149, 2000)):
+        sizes[i] = n
+    T, K, N = sum(sizes) + 7, 136, 200
+    y, x, a, b, d, s = _adapter_inputs(T, 150, r, K, N, dtype, r)
+    _check_adapters(y, x, a, b, *_groups(sizes, T, r), s, d)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_adapters_views(dtype):
     """Odd strides and starts, broadcast adapters, leading axes, transposed operands."""

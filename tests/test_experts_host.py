@@ -250,6 +250,19 @@ def test_workspace_and_split_queries():
     assert 0 < tdb.gemm_adapters_grad_workspace(most, 4096, 1024, 128, most, F32) < 1 << 60
 
 
+def test_gradient_workspace_goes_by_rows_and_not_by_adapters():
+    """Sums that another launch adds there are only of adapters with more rows than a run has: at
+    most twice as many as the rows fill, whatever the number of adapters."""
+    few = tdb.gemm_adapters_grad_workspace(8192, 4096, 4096, 64, 8, BF16)
+    assert few > 0
+    for E in (16, 512, 4096, 100000):
+        assert tdb.gemm_adapters_grad_workspace(8192, 4096, 4096, 64, E, BF16) <= few
+    for rows, E in ((8192, 4), (20000, 1000), (100000, 1), (1000, 1000)):
+        need = tdb.gemm_adapters_grad_workspace(rows, 4096, 4096, 64, E, BF16)
+        # (a run has 128 rows at least: the bytes of half of x's in FP32, a rank of 64 for its 128)
+        assert need <= 2 * 2 * rows // 128 * 64 * 4096 * 4, (rows, E)
+
+
 def test_tensor_calls_refuse_what_they_cannot_take():
     x = torch.zeros(4, 64)
     q = torch.zeros(4, 256, dtype=torch.uint8).view(torch.float8_e4m3fn)

@@ -41,14 +41,14 @@ struct AdapterArgs {
   const float* scale;
   const void* Y;
   float* U;              // [split][place][ldu], zeros past the rank
-  float* part;           // grad: [tile][rank][N] of the adapters with several tiles
+  float* part;           // grad: [slot][rank][N], a slot for each run of the adapters with several
   int64_t ldx, ldw, stride_w, ldc, stride_c, ldy;
   int rows, N, K, E;
   int rank, ldu;
   int splits;            // of U
   int tiles_n;           // up, grad: blocks of columns
   int k_chunk;           // down: columns of a split
-  int run, runs;         // grad: places of a run, and how many runs `part` has room for
+  int run, slots;        // grad: places of a run, and how many of them `part` has room for
 };
 
 // The columns of U: whole fragments of 16, so that its loads need no bounds.
@@ -66,10 +66,12 @@ __device__ __forceinline__ int64_t row_at(const AdapterArgs& a, int place) {
 struct Places {
   int e, first, end;
   int tile, tiles;  // which of its adapter's, and how many that has
+  int slot;         // (of the adapters alone) which of the tiles of those that have several
 };
 template <bool NONE>
 __device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places& t) {
   const int lane = threadIdx.x & 63, groups = NONE ? a.E + 2 : a.E;
+  int slots = 0;
   for (int base = 0; base < groups; base += 64) {
     // group g: from edge g to edge g + 1, of which the adapters have 0 .. E
     const int g = min(base + lane, groups - 1) - (NONE ? 1 : 0);
@@ -80,6 +82,7 @@ __device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places&
     hi = max(hi, lo);
     const int tiles = base + lane < groups ? max((hi - lo + bm - 1) / bm, NONE ? 0 : 1) : 0;
     const int upto = wave_scan(tiles);
+    const int several = !NONE && tiles > 1 ? tiles : 0, upto_slot = NONE ? 0 : wave_scan(several);
     const uint64_t past = __ballot(upto > id);
     if (past) {
       const int l = __builtin_ctzll(past);
@@ -87,11 +90,14 @@ __device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places&
       if (NONE && t.e >= a.E) t.e = -1;
       t.tiles = __builtin_amdgcn_readlane(tiles, l);
       t.tile = id - (__builtin_amdgcn_readlane(upto, l) - t.tiles);
+      if (!NONE)
+        t.slot = slots + t.tile + __builtin_amdgcn_readlane(upto_slot, l) - __builtin_amdgcn_readlane(several, l);
       t.first = __builtin_amdgcn_readlane(lo, l) + t.tile * bm;
       t.end = min(__builtin_amdgcn_readlane(hi, l), t.first + bm);
       return true;
     }
     id -= __builtin_amdgcn_readlane(upto, 63);
+    if (!NONE) slots += __builtin_amdgcn_readlane(upto_slot, 63);
   }
   return false;
 }
@@ -710,7 +716,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void ex_adapters_grad_kernel(
 #pragma unroll
       for (int j = 0; j < CF; ++j) v[j] = acc[f][j][q];
       if (t.tiles > 1) {
-        store_row<CF, GEMM_LP_F32>(a.part, ((int64_t)id * a.rank + r) * a.N + c, CF, GEMM_LP_F32, v);
+        // (offsets that overlap would give more slots than there are)
+        const int64_t slot = min(t.slot, a.slots - 1);
+        store_row<CF, GEMM_LP_F32>(a.part, (slot * a.rank + r) * a.N + c, CF, GEMM_LP_F32, v);
       } else {
         store_row<CF, T::CODE>(a.C, t.e * a.stride_c + r * a.ldc + c, CF, T::CODE, v);
       }
@@ -729,14 +737,15 @@ __global__ __launch_bounds__(256) void ex_adapters_sum_kernel(GradArgs args) {
   const int64_t blocks = ((int64_t)a.rank * per + 255) / 256;
   const int e = (int)(wg / blocks);
   const int64_t i = (wg - e * blocks) * 256 + threadIdx.x;
-  // its first run: the runs of the adapters before it
+  // its first slot: the runs of the adapters before it that have several
   int before = 0, runs = 0;
   for (int base = 0; base <= e; base += 64) {
     const int g = base + (threadIdx.x & 63);
     const int lo = clamped_offset(a.offsets, min(g, e), a.rows);
     const int len = max(clamped_offset(a.offsets, min(g, e) + 1, a.rows) - lo, 0);
     const int n = max((len + a.run - 1) / a.run, 1);
-    before += __builtin_amdgcn_readlane(wave_scan(g < e ? n : 0), 63);
+    // (offsets that overlap would count more slots than there are)
+    before = min(before + __builtin_amdgcn_readlane(wave_scan(g < e && n > 1 ? n : 0), 63), a.slots);
     runs = __builtin_amdgcn_readfirstlane(__shfl(n, e - base));  // (of the last turn)
   }
   if (runs == 1 || i >= (int64_t)a.rank * per) return;
@@ -744,8 +753,7 @@ __global__ __launch_bounds__(256) void ex_adapters_sum_kernel(GradArgs args) {
   float v[8] = {};
 #pragma unroll 4
   for (int s = 0; s < runs; ++s) {
-    // (offsets that overlap would count more runs than there are)
-    const int at = min(before + s, a.runs - 1);
+    const int at = min(before + s, a.slots - 1);
     const float* part = a.part + ((int64_t)at * a.rank + r) * a.N;
     const Raw<F32, 8> w = load_raw<F32, 8>(part + c);
 #pragma unroll

@@ -70,6 +70,11 @@ static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
   return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
+// Runs of the adapters that have several, the most that there can be: an adapter of more than `run`
+// places has fewer than twice as many runs as its places fill.
+static int64_t grad_slots(int64_t rows, int64_t E, int64_t run) {
+  return std::min(grad_runs(rows, E, run), 2 * rows / run);
+}
 
 template <class T>
 static const void* down_kernel(int64_t rank, bool wide) {
@@ -241,10 +246,10 @@ struct GradSide {
 static int64_t side_blocks(int64_t N, int64_t rank) {
   return N >= kLeastWide ? grad_blocks(N, rank) : 0;
 }
-// Bytes of the runs of a gradient.  (Several runs there are only of 65536 columns or fewer, so that
-// 64 bits hold them.)
+// Bytes of a gradient's slots: of the runs whose sums another launch adds.  (Several runs there are
+// only of 65536 columns or fewer, so that 64 bits hold them.)
 static int64_t side_workspace(int64_t rows, int64_t N, int64_t rank, int64_t E, int64_t run) {
-  return rows > run && N >= kLeastWide ? grad_runs(rows, E, run) * rank * N * 4 : 0;
+  return rows > run && N >= kLeastWide ? grad_slots(rows, E, run) * rank * N * 4 : 0;
 }
 
 static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_t* order,
@@ -307,7 +312,7 @@ static int run_adapters_grad(int64_t rows, int64_t rank, int64_t E, const int64_
     a.part = part, a.ldx = s.ldx, a.ldc = s.ldd, a.stride_c = s.stride_d;
     a.rows = (int)rows, a.N = (int)s.N, a.E = (int)E, a.rank = (int)rank, a.ldu = (int)ldu;
     a.splits = s.splits, a.tiles_n = (int)((s.N + columns - 1) / columns);
-    a.run = (int)run, a.runs = (int)std::min<int64_t>(grad_runs(rows, E, run), kMaxDim);
+    a.run = (int)run, a.slots = (int)grad_slots(rows, E, run);
     if (s.wide()) {
       if (__builtin_mul_overflow(side_blocks(s.N, rank), grad_runs(rows, E, run), &wgs[count]))
         return GEMMF32_ERR_TOO_LARGE;
