@@ -305,3 +305,26 @@ def test_tensor_calls_refuse_what_they_cannot_take():
     ):
         with pytest.raises(TypeError):
             call()
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A dual tensor does not require a gradient, and no call answers it without its tangent."""
+    from torch.autograd import forward_ad
+    x, y = torch.randn(4, 64), torch.zeros(4, 32)
+    a, b, scale = torch.zeros(2, 8, 64), torch.zeros(2, 8, 32), torch.ones(2)
+    order, off = torch.arange(4), torch.zeros(3, dtype=torch.int32)
+
+    def adapters(i, t):
+        ops = [y, x, a, b, scale]
+        ops[i] = t
+        return tdb.add_adapters(*ops[:4], order, off, scale=ops[4])
+    with forward_ad.dual_level():
+        for t, call in ((x, lambda d: tdb.gated_silu(d)), (x, lambda d: tdb.gated_silu(d, checkpoint=True)),
+                        (x, lambda d: tdb.route_experts(d, 2)),
+                        *((t, lambda d, i=i: adapters(i, d)) for i, t in enumerate((y, x, a, b, scale)))):
+            with pytest.raises(NotImplementedError):
+                call(forward_ad.make_dual(t, torch.ones_like(t)))
+            with pytest.raises(ValueError, match="GPU"):  # (no tangent: as outside)
+                call(t)
+    with pytest.raises(ValueError, match="GPU"):
+        tdb.gated_silu(x)

@@ -15,8 +15,8 @@ import math
 import torch
 
 from . import _binding
-from .lowp import (BLOCK, TYPES, _F8, _blocks, _check, _current, _here, _matrix, _names, _offsets,
-                   _on, _once, _out_type, _row_major, _rows16, _same_device)
+from .lowp import (BLOCK, TYPES, _F8, _blocks, _check, _current, _here, _matrix, _names, _no_tangents,
+                   _offsets, _on, _once, _out_type, _row_major, _rows16, _same_device)
 
 MAX_EXPERTS = 1024         # of a router; GEMM_ROUTE_MAX_EXPERTS
 MAX_CHOSEN = 16            # GEMM_ROUTE_MAX_CHOSEN
@@ -211,7 +211,8 @@ def route_experts(logits, k, valid=None, renormalize=False):
     logit above -Inf, hold nothing else and do not count.  NaN is taken before every number; it, or
     +Inf, makes the row's gates and the loss NaN.
 
-    Differentiable in logits through gates and loss; counts are constants in it, as usual."""
+    Differentiable (once, backward) in logits through gates and loss; counts are constants in it, as
+    usual."""
     if valid is not None:
         if not isinstance(valid, torch.Tensor) or valid.dtype != torch.bool or valid.dim() != 1:
             raise TypeError("valid must be a 1-D bool tensor")
@@ -221,6 +222,7 @@ def route_experts(logits, k, valid=None, renormalize=False):
         valid = valid.contiguous()
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in TYPES:
         raise TypeError(f"logits must be a 2-D tensor of {_names(TYPES)}")
+    _no_tangents("route_experts", logits)
     logits, k = _row_major(logits), int(k)
     if not (logits.requires_grad and torch.is_grad_enabled()):
         if _here(logits, None):
@@ -382,7 +384,7 @@ def add_adapters(y, x, a, b, order, offsets, scale=None):
     their rows and adapters (in bfloat16 Inf in b, and for the gradients in x, a or the incoming one,
     may come out as NaN).
 
-    Differentiable in y, x, a and b; adapters without rows get zeros."""
+    Differentiable (once, backward) in y, x, a and b; adapters without rows get zeros."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in TYPES:
         raise TypeError(f"x must be a tensor of {_names(TYPES)}")
     if not isinstance(y, torch.Tensor) or y.dim() < 1 or y.dtype != x.dtype:
@@ -409,6 +411,7 @@ def add_adapters(y, x, a, b, order, offsets, scale=None):
         _same_device(x, scale)
         if scale.requires_grad and torch.is_grad_enabled():
             raise ValueError("scale has no gradient here: detach it")
+    _no_tangents("add_adapters", y, x, a, b, scale)
     if not x.is_cuda:
         raise ValueError("x must live on the GPU (the library takes device pointers)")
     rows, base = _row_major(_flat(x)), _row_major(_flat(y))
@@ -498,7 +501,7 @@ def gated_silu(x, checkpoint=False):
     second (the two results of one product with twice the columns), of bfloat16, float16 or
     float32; sums and functions in float32, rounded once.
 
-    Differentiable.  With checkpoint the backward pass works on the 8-bit values that `quantize_fp8`
+    Differentiable (once, backward).  With checkpoint the backward pass works on the 8-bit values that `quantize_fp8`
     has of gate and of up, by blocks of 1 x 128 each, and x itself need not be kept: 8 bits a value
     and a scale for every 128, and a gradient of these values (of the type's largest number where x's
     own rounds to more, NaN where x is Inf, which has no 8-bit value); the forward result is x's own."""
@@ -506,6 +509,7 @@ def gated_silu(x, checkpoint=False):
         raise TypeError(f"x must be a tensor of {_names(TYPES)}")
     if x.shape[-1] % 2:
         raise ValueError(f"x has {x.shape[-1]} columns: gate and up need as many each")
+    _no_tangents("gated_silu", x)
     if not x.is_cuda:
         raise ValueError("x must live on the GPU (the library takes device pointers)")
     flat = x if x.dim() == 2 and x.is_contiguous() else _row_major(_flat(x))

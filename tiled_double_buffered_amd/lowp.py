@@ -18,6 +18,7 @@ import functools
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding
 from ._binding import GemmError
@@ -439,6 +440,17 @@ def _once(backward):
     def call(ctx, *grads):
         return (checked if torch.is_grad_enabled() else backward)(ctx, *grads)
     return call
+
+
+def _no_tangents(what, *tensors):
+    """Refuses dual tensors of forward-mode differentiation: they need not require a gradient, and a
+    call that goes round its autograd function for such would answer without their tangents, which
+    counts as a derivative of zero."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # (outside of it, without asking each: 1 us)
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 class _LinearFp8(torch.autograd.Function):
