@@ -1006,3 +1006,16 @@ def test_routed_layer_trains_and_serves():
         one = serve(x[5:6], requests[5:6]).float()
         assert float((one - whole[5:6].float()).norm() / one.norm()) <= 2.0 ** -6
     assert expert_layer.main(["--tokens", "64", "--width", "128", "--hidden", "64", "--experts", "4", "--steps", "2", "--top", "2"]) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_routed_layer_of_other_types_trains_and_serves(checkpoint, dtype):
+    from tiled_double_buffered_amd import expert_layer
+    layer = expert_layer.RoutedLayer(128, 72, 5, DEV, top=2, dtype=dtype, checkpoint=checkpoint)
+    losses, x, requests = expert_layer.train_routed(layer, 130, 128, 2, DEV)
+    assert x.dtype == dtype and len(losses) == 2
+    assert all(math.isfinite(v) for pair in losses for v in pair)
+    with torch.no_grad():
+        y = layer.served()(x, requests)
+    assert y.dtype == dtype and y.shape == x.shape and torch.isfinite(y.float()).all()

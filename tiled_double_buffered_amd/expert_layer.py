@@ -155,7 +155,8 @@ def train_routed(layer, tokens, width, steps, device, seed=1, rate=0.05, balance
     as many without an adapter; returns the loss and the balance loss of each step, the tokens and
     their requests."""
     teacher = RoutedLayer(width, layer.w_out.shape[1], layer.experts, device, layer.top,
-                          layer.adapters, layer.down.shape[1], seed=seed + 7)
+                          layer.adapters, layer.down.shape[1], seed=seed + 7,
+                          dtype=layer.shared.dtype, checkpoint=layer.checkpoint)
     g = torch.Generator(device="cpu").manual_seed(seed)
     x = torch.randn(tokens, width, generator=g).to(device=device, dtype=layer.shared.dtype)
     requests = torch.randint(0, layer.adapters, (tokens,), generator=g).to(device)
