@@ -78,6 +78,13 @@ def test_route_many_rows_for_each_workgroup(norm):
     _check_step(_logits(40000, 12, torch.bfloat16, 5), 3, None, norm)
 
 
+@pytest.mark.parametrize("T, E, k", [(70000, 12, 2), (17000, 300, 3)])
+def test_route_gradient_of_more_rows_than_its_workgroups(T, E, k):
+    """More rows than the gradient's workgroups take at once (65536 of up to 256 experts, 16384 of
+    more), so that each goes round twice."""
+    _check_step(_logits(T, E, torch.float32, 6), k, (torch.arange(T) % 9 != 4).to(DEV), k == 3)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("norm", [False, True])
 @pytest.mark.parametrize("size", [(29, 6, 6), (50, 40, 8), (30, 300, 16)], ids=str)
@@ -480,6 +487,67 @@ def test_adapters_wrong_plans_stay_in_bounds():
         assert out.shape == (T, N)
         torch.autograd.grad(out, leaves, d)
     torch.cuda.synchronize()
+
+
+class _Guarded:
+    """Buffers with 64 KiB of a pattern on both sides, which has to be there afterwards."""
+    PAD = 1 << 16
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, *shape, dtype=torch.float32):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((2 * self.PAD + (n + 255) // 256 * 256,), 0x5A, dtype=torch.uint8, device=DEV)
+        self.all.append((raw, n))
+        return raw[self.PAD:self.PAD + n].view(dtype).view(shape)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for raw, n in self.all:
+            assert (raw[:self.PAD] == 0x5A).all() and (raw[self.PAD + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("r", [4, 48])
+@pytest.mark.parametrize("T, plans", [
+    (30, ([0, 10, 20, 99], [5, 3, 50, 20], [-9, -3, 10, 30], [30, 20, 10, 0])),
+    (2000, ([0, 2000, 0, 2000], [0, 5000, -1, 1 << 30], [1999, 0, 2000, 3]))], ids=["few", "many"])
+def test_adapters_wrong_plans_leave_the_memory_around(T, plans, r, dtype):
+    """Through the C ABI: rows and offsets that are out of range, decrease or overlap write nothing
+    outside U, the results, the gradients and the workspace."""
+    E, K, N = 3, 200, 136
+    y, x, a, b, d, s = _adapter_inputs(T, E, r, K, N, dtype, 2)
+    order = torch.arange(T, device=DEV)
+    order[3], order[7], order[T - 1] = 1 << 40, -5, T
+    code, stream = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[dtype], torch.cuda.current_stream().cuda_stream
+    ldu = (r + 15) // 16 * 16
+    for plan in plans:
+        g = _Guarded()
+        o = torch.tensor(plan, dtype=torch.int32, device=DEV)
+        su, sv = tdb.gemm_adapters_splits(T, K, r, E), tdb.gemm_adapters_splits(T, N, r, E)
+        u, v, out, dx = g(su, T, ldu), g(sv, T, ldu), g(T, N, dtype=dtype), g(T, K, dtype=dtype)
+        da, db = g(E, r, K, dtype=dtype), g(E, r, N, dtype=dtype)
+        need = tdb.gemm_adapters_grad_workspace(T, K, N, r, E, code)
+        assert (need > 0) == (T == 2000)
+        ws = g(max(need, 8), dtype=torch.uint8)
+        for w in (u, v):
+            w.zero_()
+        at = order.data_ptr(), o.data_ptr()
+        for rc in (
+                tdb.gemm_adapters_down(T, K, r, E, *at, x.data_ptr(), K, a.data_ptr(), K, r * K,
+                                       s.data_ptr(), u.data_ptr(), su, 0, code, stream),
+                tdb.gemm_adapters_down(T, N, r, E, *at, d.data_ptr(), N, b.data_ptr(), N, r * N,
+                                       s.data_ptr(), v.data_ptr(), sv, 1, code, stream),
+                tdb.gemm_adapters_up(T, N, r, E, *at, u.data_ptr(), su, b.data_ptr(), N, r * N,
+                                     y.data_ptr(), N, out.data_ptr(), N, code, stream),
+                tdb.gemm_adapters_up(T, K, r, E, *at, v.data_ptr(), 1, a.data_ptr(), K, r * K, None, 0,
+                                     dx.data_ptr(), K, code, stream),
+                tdb.gemm_adapters_grad(T, r, E, *at, K, v.data_ptr(), 1, x.data_ptr(), K, da.data_ptr(), K,
+                                       r * K, N, u.data_ptr(), su, d.data_ptr(), N, db.data_ptr(), N, r * N,
+                                       ws.data_ptr(), need, code, stream)):
+            assert rc == tdb.OK
+        g.check()
 
 
 def test_adapter_gradients_against_differences():
