@@ -59,6 +59,15 @@ __device__ __forceinline__ int64_t row_at(const AdapterArgs& a, int place) {
   return min(max(r, (int64_t)0), (int64_t)a.rows - 1);
 }
 
+// Tiles of bm in a group of len places.  (Unsigned, as a run of the gradient can be so long that the
+// sum of the two passes 31 bits.)
+__host__ __device__ constexpr int tiles_of(int len, int bm) {
+  return (int)(((unsigned)len + (unsigned)bm - 1u) / (unsigned)bm);
+}
+static_assert(tiles_of(2147482623, 4194560) == 512 && tiles_of(2147482623, 2147482624) == 1 &&
+                  tiles_of(0, 16) == 0 && tiles_of(16, 16) == 1 && tiles_of(17, 16) == 2,
+              "also at the largest number of rows");
+
 // The places of tile `id` of bm: adapter e's are offsets[e] .. offsets[e+1] - 1, and -1 has those
 // before the first and from the last on.  Every wave looks for itself, 64 groups at a time; false
 // past the last tile.  NONE: with the places of no adapter; otherwise of the adapters alone, one
@@ -80,7 +89,7 @@ __device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places&
     if (NONE && g < 0) lo = 0;
     if (NONE && g >= a.E) hi = a.rows;
     hi = max(hi, lo);
-    const int tiles = base + lane < groups ? max((hi - lo + bm - 1) / bm, NONE ? 0 : 1) : 0;
+    const int tiles = base + lane < groups ? max(tiles_of(hi - lo, bm), NONE ? 0 : 1) : 0;
     const int upto = wave_scan(tiles);
     const int several = !NONE && tiles > 1 ? tiles : 0, upto_slot = NONE ? 0 : wave_scan(several);
     const uint64_t past = __ballot(upto > id);
@@ -93,7 +102,7 @@ __device__ inline bool find_places(const AdapterArgs& a, int bm, int id, Places&
       if (!NONE)
         t.slot = slots + t.tile + __builtin_amdgcn_readlane(upto_slot, l) - __builtin_amdgcn_readlane(several, l);
       t.first = __builtin_amdgcn_readlane(lo, l) + t.tile * bm;
-      t.end = min(__builtin_amdgcn_readlane(hi, l), t.first + bm);
+      t.end = t.first + min(__builtin_amdgcn_readlane(hi, l) - t.first, bm);
       return true;
     }
     id -= __builtin_amdgcn_readlane(upto, 63);
@@ -743,7 +752,7 @@ __global__ __launch_bounds__(256) void ex_adapters_sum_kernel(GradArgs args) {
     const int g = base + (threadIdx.x & 63);
     const int lo = clamped_offset(a.offsets, min(g, e), a.rows);
     const int len = max(clamped_offset(a.offsets, min(g, e) + 1, a.rows) - lo, 0);
-    const int n = max((len + a.run - 1) / a.run, 1);
+    const int n = max(tiles_of(len, a.run), 1);
     // (offsets that overlap would count more slots than there are)
     before = min(before + __builtin_amdgcn_readlane(wave_scan(g < e && n > 1 ? n : 0), 63), a.slots);
     runs = __builtin_amdgcn_readfirstlane(__shfl(n, e - base));  // (of the last turn)
