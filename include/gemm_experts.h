@@ -93,7 +93,7 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  *   not looked at).
  * Inf and NaN stay in their places' rows and their adapters.  In bf16 `up` and `grad` multiply U and V
  *   in three parts, of which one may be 0: Inf in A or B, and for grad in X or DOUT, gives NaN where
- *   the product is Inf.
+ *   the product is Inf; and of a U or V the bits below 2^-133, bf16's smallest step, are lost.
  * gemm_adapters_splits: the number of splits that `down` should make, at least 1.
  * gemm_adapters_grad_workspace: bytes of workspace that `grad` needs, as in gemm_route. */
 int gemm_adapters_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int64_t *order,

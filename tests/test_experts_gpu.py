@@ -455,6 +455,25 @@ def test_adapters_large_and_small_numbers_in_fp16():
             xo.close(tdb.add_adapters(y, x, a, b, *p), ref, slack, name)
 
 
+@pytest.mark.parametrize("exponent", [-100, -112, -124, -130])
+def test_adapters_small_contractions_in_bf16(exponent):
+    """x A^T near FP32's smallest normal number and below it, with results of ordinary size: nothing
+    is lost but the bits below bf16's smallest step, 2^-133, of each of the contraction's numbers."""
+    g = _gen(2)
+    T, r, K, N = 40, 6, 64, 72
+    half = exponent // 2
+    y = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV)
+    x = _randn(g, T, K, scale=2.0 ** half, dtype=torch.bfloat16)
+    a = _randn(g, 1, r, K, scale=2.0 ** (exponent - half), dtype=torch.bfloat16)
+    b = _randn(g, 1, r, N, scale=2.0 ** 100, dtype=torch.bfloat16)
+    order, offsets = _groups((T,), T, 1)
+    got = tdb.add_adapters(y, x, a, b, order, offsets)
+    (_, ref, slack), = xo.adapters(y, x, a, b, order, offsets, None)
+    # (of FP32's own steps, 2^-149: one for each product of the contraction)
+    lost = (2.0 ** -133 + K * 2.0 ** -149) * b[0].double().cpu().abs().sum(0)
+    xo.close(got, ref, slack + lost, "out")
+
+
 def test_adapters_rows_behind_are_left():
     """Through the C ABI: columns past N and places of no adapter keep what they hold."""
     T, E, r, K, N = 20, 2, 5, 48, 40

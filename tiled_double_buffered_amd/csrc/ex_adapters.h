@@ -7,8 +7,8 @@
 //
 // u and v stay in FP32 between the kernels.  `down` multiplies 16-bit values by the 16-bit matrix
 // instruction (exact products, FP32 sums).  In `up` and `grad` one operand is u or v: for bf16 it
-// is cut into three bf16 parts of 8 bits each, whose sum it is exactly, and multiplied part by part
-// by the 16-bit instruction; fp16, whose exponents end too early for such parts, and FP32 take the
+// is cut into three bf16 parts of 8 bits each, whose sum it is (but for what is below bf16's smallest
+// step, 2^-133), and multiplied part by part by the 16-bit instruction; fp16, whose exponents end too early for such parts, and FP32 take the
 // FP32 instruction.  Both operands of these kernels lie across the contraction: a lane loads 8 k of
 // 8 neighbouring columns, which is all that its fragments need of either instruction, so that
 // nothing moves between lanes, and neighbouring lanes load and store neighbouring columns.
@@ -394,8 +394,8 @@ struct Block8 {
   }
 };
 
-// The three bf16 parts of FP32 numbers, cut (not rounded) so that they add up exactly and no part
-// passes bf16's range; Inf and NaN are in the first.  (A part may be 0, and 0 times Inf is NaN: an Inf
+// The three bf16 parts of FP32 numbers, cut (not rounded) so that no part passes bf16's range.  They
+// add up exactly from 2^-110 on; below, what the last has no steps for is lost, less than 2^-133.  Inf and NaN are in the first.  (A part may be 0, and 0 times Inf is NaN: an Inf
 // of the other operand does not come out as one.)
 __device__ __forceinline__ void three_parts(const float (&u)[8], bf168v (&part)[3]) {
 #pragma unroll

@@ -380,9 +380,9 @@ def add_adapters(y, x, a, b, order, offsets, scale=None):
     to 128; all of one type, bfloat16, float16 or float32.  order (T int64) and offsets (E + 1
     int32) are `group_rows` of the rows' adapters, made once for all projections of a batch: order
     holds every row once.  scale is E float32 on the GPU, or None for 1.  Rows of no adapter keep y.
-    The contraction over K is kept in float32; all sums are, and are rounded once.  Inf and NaN stay in
-    their rows and adapters (in bfloat16 Inf in b, and for the gradients in x, a or the incoming one,
-    may come out as NaN).
+    The contraction over K is kept in float32 (in bfloat16 without its bits below 2^-133); all sums
+    are, and are rounded once.  Inf and NaN stay in their rows and adapters (in bfloat16 Inf in b, and
+    for the gradients in x, a or the incoming one, may come out as NaN).
 
     Differentiable (once, backward) in y, x, a and b; adapters without rows get zeros."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in TYPES:
