@@ -128,8 +128,9 @@ int gemm_gated_grad(int64_t rows, int64_t N, const void *X, int64_t ldx, const v
                     int64_t lddx, int type, void *stream);
 
 /* Y = Q S, Q rows x cols e4m3fn with one scale for each block_rows x 128 block (block_rows 1 or
- * 128), as gemm_fp8_quantize lays them out; one rounding to `type`.  Finite products past the
- * type's range become its largest number. */
+ * 128), as gemm_fp8_quantize lays them out.  The product is formed in FP32, which rounds it unless S
+ * is a power of two, as gemm_fp8_quantize's are, and is then rounded to `type`.  Finite products past
+ * the type's range become its largest number. */
 int gemm_fp8_dequantize(int64_t rows, int64_t cols, const void *Q, int64_t ldq, const float *S,
                         int64_t lds, int block_rows, void *Y, int64_t ldy, int type, void *stream);
 

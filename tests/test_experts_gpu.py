@@ -755,6 +755,15 @@ def test_dequantize(shape, block, dtype):
     xo.close(tdb.dequantize_fp8(q, odd, dtype), ref, ref.abs() * xo.U)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dequantize_forms_the_product_in_float32(dtype):
+    """Scales of 24 bits: the product rounded to FP32, then to the type, to the nearest each time."""
+    q, _ = tdb.quantize_fp8(_wide(64, 640, torch.float32, 3))
+    s = (torch.rand(64, 5, generator=_gen(4)) + 0.5).to(DEV)
+    ref = (q.float() * s.repeat_interleave(128, 1)).to(dtype)
+    assert torch.equal(tdb.dequantize_fp8(q, s, dtype), ref)
+
+
 def test_dequantize_every_value_and_the_ends():
     q = torch.arange(256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).view(2, 128)
     for s in (1.0, 2.0 ** -126, 256.0, 2.0 ** 100, 2.0 ** 120, 1e38):

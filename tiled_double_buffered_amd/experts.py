@@ -549,9 +549,11 @@ def _dequantize(q, s, out_dtype):
 
 
 def dequantize_fp8(q, s, out_dtype=torch.bfloat16, stream=None):
-    """The numbers q * s that `quantize_fp8`'s results stand for, rounded once to out_dtype: q is
-    2-D float8_e4m3fn, s float32 with one scale for each block of 1 x 128 or of 128 x 128, any
-    numbers.  Finite products past out_dtype's range become its largest number."""
+    """The numbers q * s that `quantize_fp8`'s results stand for, in out_dtype: q is 2-D
+    float8_e4m3fn, s float32 with one scale for each block of 1 x 128 or of 128 x 128.  s may be any
+    numbers: the product is formed in float32, which rounds it unless s is a power of two, as
+    `quantize_fp8`'s are, and then rounded to out_dtype.  Finite products past out_dtype's range become
+    its largest number."""
     if _here(q, stream):
         return _dequantize(q, s, out_dtype)
     with _on(stream, q, s):
