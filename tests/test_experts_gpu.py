@@ -320,6 +320,26 @@ def test_adapters_every_end_of_the_wide_axis(K, dtype):
         _check_adapters(y, x, a, b, *_groups(sizes, T, K), s, d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("r, K", [(r, K) for r in (9, 20) for K in (8, 9, 63, 64, 65, 127, 128, 511, 1023)] +
+                         [(r, K) for r in (50, 100) for K in (9, 65, 511)])
+def test_adapters_every_end_of_the_wide_axis_in_tiles_of_64(K, r, dtype):
+    """So many rows that a workgroup of the contraction takes 64 of them, whatever the columns."""
+    T = 10050 if r <= 64 else 5050
+    y, x, a, b, d, s = _adapter_inputs(T, 2, r, K, 40, dtype, K)
+    _check_adapters(y, x, a, b, *_groups((T // 2 + 17, T // 2 - 60), T, K), s, d)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T, sizes, r, K", [(1030, (400, 0, 600), 30, 2100), (1030, (1, 1000, 2), 50, 1030),
+                                            (1030, (65, 63, 64, 800), 100, 513), (5003, (4000, 900), 7, 2050),
+                                            (1200, (18,) * 64, 64, 1090)], ids=str)
+def test_adapters_few_rows_in_tiles_of_64(T, sizes, r, K, dtype):
+    """Columns and ranks whose bytes ask for tiles of 64 with few rows, splits of the columns among them."""
+    y, x, a, b, d, s = _adapter_inputs(T, len(sizes), r, K, 40, dtype, r)
+    _check_adapters(y, x, a, b, *_groups(sizes, T, r), s, d)
+
+
 def test_adapters_of_many_requests():
     """More groups than a wave looks at at once, most of them empty."""
     sizes = [0] * 400

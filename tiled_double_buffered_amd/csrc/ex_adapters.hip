@@ -16,20 +16,25 @@ static int64_t place_tiles(int64_t rows, int64_t E, int bm) {
   return rows / bm + std::min<int64_t>(E + 2, rows);
 }
 
-// Whether `down` takes 64 places a workgroup: where the adapters have several such tiles and splits of
-// K can make up for the workgroups; otherwise 16, with a kernel of its own.  A low rank needs more rows
-// for it, as the rows' bytes decide there and not the adapter's.  (bf16, with 64 and 16, in us with the
-// join: 8192 x 4096, rank 32, 22 and 26; 4096 x 8192, rank 64, 27 and 47; 4096 x 4096, rank 16, 13
-// and 10.)
-static bool down_wide(int64_t rows, int64_t rank, int64_t E) {
-  return rows >= (rank > 32 ? 2048 : 6144) && rows >= 128 * E;
+// Whether `down` takes 64 places a workgroup or 16: the adapter's lines are read for every tile, so that
+// few places pay where these are few: few columns, or a low rank, whose rows' own bytes decide.  From
+// 10000 rows on (5000 past rank 64) tiles of 64 fill the chip without splits of K and their join.
+// (Over 3104 sizes, 32 to 20000 rows, 256 to 11008 columns, ranks 16 to 128, 1 to 64 adapters, bf16 and FP32,
+// the choice is 1.8 % slower than the better one in the mean and 6 % or more for a tenth of them; always
+// 16 17 %, always 64 14 %.  bf16, with 16 and 64, in us with the join: 8192 x 4096, rank 32, four uneven adapters, 28 and 22; rank
+// 16 22 and 21; 4096 x 4096, rank 16, 14 and 17, rank 64 26 and 20; 8192 x 1024, rank 64, 12 and 14; 16384
+// x 1024 22 and 17; 1024 x 11008, rank 128, 34 and 21.)
+static bool down_wide(int64_t rows, int64_t K, int64_t rank) {
+  if (rows >= (rank > 64 ? 5000 : 10000)) return true;
+  const int64_t fragments = rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+  return rows >= (rank > 16 ? 1024 : 5000) && fragments * K > 65536;
 }
-static int64_t down_tiles(int64_t rows, int64_t rank, int64_t E) {
-  return place_tiles(rows, E, down_wide(rows, rank, E) ? kWidePlaces : 16);
+static int64_t down_tiles(int64_t rows, int64_t K, int64_t rank, int64_t E) {
+  return place_tiles(rows, E, down_wide(rows, K, rank) ? kWidePlaces : 16);
 }
 // Splits of K: enough workgroups for two a CU where there are none for each, but 256 columns a split.
 static int adapter_splits(int64_t rows, int64_t K, int64_t rank, int64_t E) {
-  const int64_t tiles = std::max<int64_t>(down_tiles(rows, rank, E), 1);
+  const int64_t tiles = std::max<int64_t>(down_tiles(rows, K, rank, E), 1);
   if (tiles >= kCus * 3 / 4) return 1;
   return (int)std::max<int64_t>(std::min<int64_t>({2 * kCus / tiles, K / 256, 8}), 1);
 }
@@ -157,9 +162,9 @@ static int run_down(int64_t rows, int64_t K, int64_t rank, int64_t E, const int6
   // (a multiple of the steps that four waves take at once)
   const int64_t unit = 4 * 128 / b;
   a.k_chunk = (int)((K + splits * unit - 1) / (splits * unit) * unit);
-  const bool wide = down_wide(rows, rank, E);
+  const bool wide = down_wide(rows, K, rank);
   const int threads = wide ? kWideThreads : kDownThreads;
-  const int64_t wgs = down_tiles(rows, rank, E) * splits;
+  const int64_t wgs = down_tiles(rows, K, rank, E) * splits;
   if (K < kLeastWide) {
     const int64_t few = place_tiles(rows, E, 16) * splits;
     if (!fits_grid(few, 256)) return GEMMF32_ERR_TOO_LARGE;
