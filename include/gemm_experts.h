@@ -44,6 +44,7 @@ extern "C" {
  *   counts[e]: how often e was taken;  sums[0]: rows that count, sums[1]: the total of counts
  *   loss = E sum_e (counts[e] / sums[1]) (sum_t p[t][e] / sums[0]); 0 where no row counts
  * A NaN is taken before every number; it, or +Inf, makes its row's gates and the loss NaN.
+ * Probabilities below 2^-126 may count as 0.
  * E <= GEMM_ROUTE_MAX_EXPERTS and k <= GEMM_ROUTE_MAX_CHOSEN, else GEMMF32_ERR_BAD_CONFIG, as for
  * k < 1 or k > E; rows k below 2^31 - 1024, else GEMMF32_ERR_TOO_LARGE.  workspace:
  * gemm_route_workspace(rows, E) bytes, 8-byte aligned (less is GEMMF32_ERR_BAD_LD; where that is 0 it

@@ -14,14 +14,15 @@
 // nothing moves between lanes, and neighbouring lanes load and store neighbouring columns.
 //
 // Bound by memory, and by how evenly the groups fill the chip (bf16, each pass on other rows):
-//   down  8192 x 4096, rank 32: 22 us for 67 MB (3.0 TB/s), 3 of them the launch that joins the
+//   down  8192 x 4096, rank 32: 22 us for 67 MB (3.0 TB/s) and 4 for the launch that joins the
 //         splits, which make it the same for even and uneven groups; 4096 x 4096, rank 16: 10 us;
-//         one token each for 24 adapters, rank 16: 4.9 us, the latency of three loads that wait for
+//         one token each for 24 adapters, rank 16: 5.1 us, the latency of three loads that wait for
 //         each other
 //   up    4096 x 11008, rank 16: 39 us for 180 MB (4.6 TB/s; a large copy reaches 5.0); 24 adapters
 //         of one token beside 4096 columns: 6.3 us
 //   grad  8192 x 4096, rank 32, both gradients in one launch: 43 us for 134 MB and 4.2 for the sums
-//         (in two launches 26 and 4.3 each): a workgroup lives 9 us, of which 3 are vector
+//         (in two launches 26 and 4.3 each): 170 registers leave room for one workgroup a CU, which
+//         lives 9 us, of which 3 are vector
 //         instructions (u's parts, turning) and most of the rest the chain from the offsets to the
 //         rows' numbers to the rows
 // With one workgroup's loads guarded one by one (a branch each, at which all earlier ones have to
@@ -560,8 +561,8 @@ struct GradArgs {
 };
 
 // Columns of a workgroup: 64 past rank 32, as with 128 the sums take all registers of a SIMD's only
-// wave.  (8192 x 4096, bf16, rank 64, four and 64 even adapters: 57 and 124 us, 64 and 171 with 128; FP32,
-// 4096 x 4096 of eight, 55 and 71.  Up to rank 32 128 need fewer instructions: bf16, rank 16, 37 us, 40
+// wave.  (8192 x 4096, bf16, rank 64, four and 64 even adapters, when it was chosen: 57 and 124 us, 64 and
+// 171 with 128; FP32, 4096 x 4096 of eight, 55 and 71.  Up to rank 32 128 need fewer instructions: bf16, rank 16, 37 us, 40
 // with 64.)
 __host__ __device__ constexpr int grad_columns(int rank) { return rank <= 32 ? 128 : 64; }
 

@@ -62,21 +62,22 @@ static int64_t grad_blocks(int64_t N, int64_t rank) {
   const int64_t per = 16 * grad_fragments(rank), columns = grad_columns((int)rank);
   return (N + columns - 1) / columns * ((rank + per - 1) / per);
 }
-// Waves of a workgroup of `grad`: four past rank 32, two workgroups a CU, and where the adapters have
+// Waves of a workgroup of `grad`: four past rank 32, of which two workgroups fit on a CU, and where the adapters have
 // fewer places than eight take in a turn.
 static int grad_waves(int64_t rows, int64_t rank, int64_t E) {
   return rank > 32 || rows < 256 * E ? 4 : 8;
 }
 // Places of a run in `grad` for gradients of so many workgroups a run together: so many that there are
-// two workgroups a CU and four runs (one where a run has as many), but a turn of the waves at least;
-// and the most runs that there can be.  (Four, as with fewer the longest adapter decides: 16384 x 4096
-// of eight uneven ones, rank 128, 231 us, 255 without.)
+// two workgroups for each CU and four runs (one where a run has as many), but a turn of the waves at
+// least.  (Four, as with fewer the longest adapter decides: 16384 x 4096 of eight uneven ones, rank 128,
+// 231 us, 255 without, when it was chosen.)
 static int64_t grad_run(int64_t rows, int64_t blocks, int waves) {
   const int64_t per =
       blocks > 2 * kCus ? 1 : std::max<int64_t>(2 * kCus / std::max<int64_t>(blocks, 1), 4);
   const int64_t turn = 32 * waves;
   return std::max<int64_t>(((rows + per - 1) / per + turn - 1) / turn * turn, turn);
 }
+// The most runs that there can be.
 static int64_t grad_runs(int64_t rows, int64_t E, int64_t run) { return rows / run + E; }
 // Runs of the adapters that have several, the most that there can be: an adapter of more than `run`
 // places has fewer than twice as many runs as its places fill.

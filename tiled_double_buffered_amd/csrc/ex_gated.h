@@ -8,9 +8,9 @@
 // every u (and dg below 2^-113 for every u and dh), whereas exp(-|g|) is one only down to -87.
 //
 // Bound by memory: everything is read once and written once.  16 lanes hold a block of 128 columns,
-// eight each, so that a block's scale needs four rotations.  16384 x 2048 in bf16, kept in 8 bits: 46
-// us for 268 MB forward (5.8 TB/s, a part of it from the caches; 67 with the loads of gate and up
-// behind a branch each), 41 us for as many backward; 16384 x 4096 values from 8 bits to bf16 38 us
+// eight each, so that a block's scale needs four rotations.  16384 x 2048 in bf16, kept in 8 bits: 48
+// us for 268 MB forward (5.6 TB/s, a part of it from the caches; 67 with the loads of gate and up
+// behind a branch each), 42 us for as many backward; from its input 36 and 54; 16384 x 4096 values from 8 bits to bf16 38 us
 // for 203 MB.
 #pragma once
 

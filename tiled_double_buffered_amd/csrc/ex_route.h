@@ -10,9 +10,10 @@
 // order does not matter); the sums of all workgroups are added by one more launch, in a fixed
 // order, or by the same workgroup where it is the only one.
 //
-// 16384 rows of 256 experts in FP32, k = 8: 17 us (16.8 MB; four rows a wave, whose eight searches of
+// 16384 rows of 256 experts in FP32, k = 8: 16 us (16.8 MB; four rows a wave, whose eight searches of
 // 40 instructions and 16 exponentials are most of it), 8.4 for the sums of 256 workgroups (half a
-// megabyte that one CU reads), 21 for the gradient.  16 rows of 64 experts, k = 4: 5.1 us.  A call
+// megabyte that one CU reads), 20 for the gradient (33.5 MB, 6.8 us of a copy; its counts are loaded one
+// after another before a row is).  16 rows of 64 experts, k = 4: 5.1 us.  A call
 // takes the host 14 us, a step 100, of which autograd's own 37 are for a function that does nothing.
 #pragma once
 

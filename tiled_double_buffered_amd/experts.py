@@ -209,7 +209,7 @@ def route_experts(logits, k, valid=None, renormalize=False):
     An expert whose logit is -Inf is never taken.  Where a row has none left, its place holds -1
     with a gate of 0 (`group_rows` puts such places last); rows that are not valid, or have no
     logit above -Inf, hold nothing else and do not count.  NaN is taken before every number; it, or
-    +Inf, makes the row's gates and the loss NaN.
+    +Inf, makes the row's gates and the loss NaN.  Probabilities below 2^-126 may count as 0.
 
     Differentiable (once, backward) in logits through gates and loss; counts are constants in it, as
     usual."""
