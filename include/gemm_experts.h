@@ -85,7 +85,7 @@ int64_t gemm_group_rows_workspace(int64_t n, int64_t E);
  *   over K, each rows x 16 ceil(rank / 16) with zeros past the rank, one after another and 16-byte
  *   aligned (places of no expert are left as they were).  scale may be NULL (1).  With `join` the
  *   first holds their sum in the end (of places of no expert what it may), so that `up` and `grad`
- *   take it as one split: for many rows, as they read U several times.
+ *   take it as one split: for many rows (about 1024 and more), as they read U several times.
  * up: OUT[order[p]] = Y[order[p]] + (sum of U's splits)[p] B_e; places of no expert: Y alone.
  *   Y may be NULL (0).
  * grad: DA_e (rank x K, row stride ldda, stride_da elements apart) = sum over the places p of e of
