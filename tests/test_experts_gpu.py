@@ -403,6 +403,26 @@ def test_adapters_shared_by_all_experts_add_their_gradients():
     xo.close(got, ref.sum(0), slack.sum(0) + ref.abs().sum(0) * 4 * xo.U, "shared")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_adapters_rows_of_none_keep_y(dtype):
+    """Bit for bit, zeros of either sign, Inf and the smallest numbers among them; every kernel, rows of
+    none before the first adapter's and behind the last one's.  Their dx is 0 (not -0)."""
+    ends = torch.tensor([0.0, -0.0, math.inf, -math.inf, torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal,
+                         -torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps])
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    for T, r, N in ((40, 5, 72), (40, 40, 72), (40, 5, 7), (5000, 12, 264)):
+        y, x, a, b, d, s = _adapter_inputs(T, 2, r, 24, N, dtype, r)
+        y = ends.repeat(T * N // 7 + 1)[:T * N].view(T, N).to(dtype).to(DEV)
+        order = torch.randperm(T, generator=_gen(T)).to(DEV)
+        offsets = torch.tensor([7, T // 2, T - 9], dtype=torch.int32, device=DEV)
+        x.requires_grad_()
+        out = tdb.add_adapters(y, x, a, b, order, offsets)
+        none = torch.cat([order[:7], order[T - 9:]])
+        assert torch.equal(out[none].view(bits), y[none].view(bits))
+        dx, = torch.autograd.grad(out, x, d)
+        assert (dx[none].view(bits) == 0).all()
+
+
 def test_adapters_missing_gradients():
     y, x, a, b, d, s = _adapter_inputs(20, 2, 4, 24, 40, torch.float32, 3)
     order, offsets = _groups((9, 8), 20, 4)

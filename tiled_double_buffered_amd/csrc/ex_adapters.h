@@ -490,9 +490,11 @@ struct UpColumns {
       for (int q = 0; q < 4; ++q)
         y[q] = load_raw<T, 8>((const typename T::type*)a.Y + row[q] * a.ldy + c);
     }
+    // (y + -0 is y, its sign too where it is 0)
+    const float none = a.Y != nullptr && t.e < 0 ? -0.0f : 0.0f;
     float4v acc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = float4v{0, 0, 0, 0};
+    for (int j = 0; j < 8; ++j) acc[j] = float4v{none, none, none, none};
     if (t.e >= 0) sum(acc);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -799,7 +801,7 @@ __global__ __launch_bounds__(256) void ex_adapters_up_few_kernel(AdapterArgs a) 
   for (int i = threadIdx.x; i < (t.end - t.first) * a.N; i += 256) {
     const int place = t.first + i / a.N, n = i % a.N;
     const int64_t row = row_at(a, place);
-    float v = 0.0f;
+    float v = a.Y != nullptr && t.e < 0 ? -0.0f : 0.0f;  // (as above)
     if (t.e >= 0) {
       for (int r = 0; r < a.rank; ++r) {
         float u = 0.0f;
