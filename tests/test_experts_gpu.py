@@ -340,6 +340,17 @@ def test_adapters_few_rows_in_tiles_of_64(T, sizes, r, K, dtype):
     _check_adapters(y, x, a, b, *_groups(sizes, T, r), s, d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_adapters_of_a_plan_that_begins_past_the_first_place(dtype):
+    """Places before the first adapter's, and x that is y too."""
+    T, r, K = 300, 9, 72
+    y, x, a, b, d, s = _adapter_inputs(T, 3, r, K, K, dtype, 1)
+    order = torch.randperm(T, generator=_gen(2)).to(DEV)
+    offsets = torch.tensor([11, 60, 60, 250], dtype=torch.int32, device=DEV)
+    _check_adapters(y, x, a, b, order, offsets, s, d)
+    assert torch.equal(tdb.add_adapters(y, y, a, b, order, offsets), tdb.add_adapters(y, y.clone(), a, b, order, offsets))
+
+
 def test_adapters_of_many_requests():
     """More groups than a wave looks at at once, most of them empty."""
     sizes = [0] * 400
@@ -991,6 +1002,44 @@ def test_graph_replays_follow_their_inputs(name):
         ref = call(fresh)
         for a, b in zip(out, ref):
             assert torch.equal(a, b), seed
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_two_graphs_at_once(name):
+    """Captured one after the other, replayed on two streams at once: each has its own workspace."""
+    make, call = _step_calls()[name]
+    v = [make(1), make(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ref = [[t.detach() for t in call(w)] for w in v]
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for w in v:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call(w)
+        graphs.append(graph), outs.append(out)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for out, r in zip(outs, ref):
+            assert all(torch.equal(a, b) for a, b in zip(out, r))
+
+
+@pytest.mark.parametrize("name", ["route", "adapters", "gated", "kept"])
+def test_saved_tensors_kept_on_the_host(name):
+    """What the backward pass gets back need not have the strides that were saved."""
+    make, call = _step_calls()[name]
+    v = make(1)
+    ref = call(v)
+    with torch.autograd.graph.save_on_cpu():
+        got = call(v)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
 @pytest.mark.parametrize("call", ["group", "dequantize"])
